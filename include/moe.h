@@ -111,7 +111,9 @@ typedef enum {
   MOE_OP_LAYER_FWD = 5,
   MOE_OP_LAYER_BWD = 6,
   MOE_OP_LAYER_FWD_FP8 = 7,
-  MOE_OP_LAYER_BWD_FP8 = 8
+  MOE_OP_LAYER_BWD_FP8 = 8,
+  MOE_OP_LAYER_DECODE = 9,
+  MOE_OP_LAYER_DECODE_FP8 = 10
 } moe_op;
 
 /* Per-expert capacity for a capacity factor: ceil(factor * T * k / E), the
@@ -367,6 +369,103 @@ moe_status moe_layer_bwd_fp8(const moe_dims* dims, const moe_bf16* x,
                              const void* saved, moe_bf16* dx, float* dWg,
                              float* dW1, float* dW3, float* dW2, void* ws,
                              size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------- a few tokens
+ * The whole layer for 1 <= T <= 128 tokens, as a serving loop calls it for the
+ * next token of each of its sequences.  The same mathematics as
+ * moe_layer_fwd:
+ *   l = x Wg (+ b);  the k largest logits (ties to the lower expert id);
+ *   gates = softmax over the chosen k;
+ *   y[t] = sum_j gates[t,j] (silu(x W1[e_j]) * (x W3[e_j])) W2[e_j]
+ * with fp32 sums throughout and H = silu(A) * B rounded once to bf16 (FC2's
+ * tensor-core operand); A, B, the experts' outputs and the gated sum stay in
+ * fp32 until y is rounded.  Only the chosen experts' weights are read, each
+ * once.  Nothing is kept for a backward pass.
+ *
+ * In: as moe_layer_fwd.  Out: y [T,h] bf16 and, where the pointers are not
+ * NULL, topk_idx [T,k] and gates [T,k].  dims.capacity > 0 drops assignments
+ * as moe_layer_fwd does.  Results do not depend on how blocks are scheduled:
+ * the same inputs give the same bits.
+ * MOE_ERR_UNSUPPORTED: T > 128, or dims.sar = 1 (there is no context).
+ * Workspace: moe_workspace_bytes(dims, MOE_OP_LAYER_DECODE). */
+moe_status moe_layer_decode(const moe_dims* dims, const moe_bf16* x,
+                            const float* Wg, const float* b,
+                            const moe_bf16* W1, const moe_bf16* W3,
+                            const moe_bf16* W2, moe_bf16* y,
+                            int32_t* topk_idx, float* gates, void* ws,
+                            size_t ws_bytes, moe_stream_t stream);
+
+/* moe_layer_decode on e4m3 weights: `qw` as moe_quantize_weights_fp8 writes it
+ * (256-byte aligned).  The arithmetic of moe_layer_fwd_fp8: x quantised with
+ * one scale for each token, H (from its bf16 value) with one for each row, the
+ * products of codes summed in fp32 and multiplied by the two scales.  h and f
+ * multiples of 128 (MOE_ERR_UNSUPPORTED otherwise).
+ * Workspace: moe_workspace_bytes(dims, MOE_OP_LAYER_DECODE_FP8). */
+moe_status moe_layer_decode_fp8(const moe_dims* dims, const moe_bf16* x,
+                                const float* Wg, const float* b,
+                                const void* qw, moe_bf16* y,
+                                int32_t* topk_idx, float* gates, void* ws,
+                                size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------- norms around the block
+ * What joins the layer to its residual stream r [T,h] (bf16, or fp32 with
+ * res_f32): an RMS norm of the block's output y, a gate, the residual scales,
+ * and the RMS norm that feeds the next block:
+ *   z     = y / rms(y) * w_post          (z = y where w_post is NULL)
+ *   r_out = alpha r + beta gate * z      (rounded once to r's type)
+ *   u     = r_out / rms(r_out) * w_pre   (bf16; of the stored r_out)
+ * with rms(v) = sqrt(mean(v^2) + eps) over a row, all in fp32.  gate: one
+ * number for each channel (fp32 [h]), for each token (fp32 [T]), or none.
+ * w_post, w_pre: fp32 [h]. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1,  /* gate [h] */
+  MOE_GATE_TOKEN = 2     /* gate [T] */
+} moe_gate_kind;
+
+typedef struct {
+  int32_t T;        /* rows */
+  int32_t h;        /* row length: a multiple of 8, at most 8192 */
+  int32_t res_f32;  /* 1: r, r_out, dr, dr_out are fp32; 0: bf16 */
+  int32_t gate;     /* moe_gate_kind */
+  float eps;        /* > 0 */
+  float alpha;      /* scale of the residual */
+  float beta;       /* scale of the block's output */
+} moe_norm_dims;
+
+/* Scratch bytes of moe_block_norm_bwd (0 on invalid dims). */
+size_t moe_norm_workspace_bytes(const moe_norm_dims* dims);
+
+/* The forward above in one pass over r and y.
+ *   y NULL:      the norm before the first block: u = r / rms(r) * w_pre only.
+ *                w_post and r_out must be NULL; gate, alpha, beta are unused.
+ *   w_pre NULL:  the end of the last block: r_out only; u must be NULL.
+ * gate is unused with MOE_GATE_NONE.  r_out may be r itself. */
+moe_status moe_block_norm_fwd(const moe_norm_dims* dims, const void* r,
+                              const moe_bf16* y, const float* w_post,
+                              const float* gate, const float* w_pre,
+                              void* r_out, moe_bf16* u, moe_stream_t stream);
+
+/* Its backward, from the gradients du of u and dr_out of r_out's other uses
+ * (NULL: none) with the same optional parts as the forward call:
+ *   G    = dr_out + J_pre^T (du * w_pre),  J_pre the Jacobian of r_out / rms
+ *   dr   = alpha G;   dz = beta gate * G;  dy = J_post^T (dz * w_post)
+ *   dw_pre [h] = sum_t du * r_out / rms;   dw_post [h] = sum_t dz * y / rms
+ *   dgate = beta G * z, summed over t (channel) or over the row (token)
+ * r_out is the stored output of the forward (r where y is NULL; then
+ * dr = G, and dy, dw_post, dgate must be NULL); it may be NULL without w_pre.
+ * Both row norms are computed again from r_out and y: nothing is kept from
+ * the forward.  dr may be dr_out itself.  Gradients are written, not
+ * accumulated, and every sum has a fixed order.
+ * Workspace: moe_norm_workspace_bytes(dims), 256-byte aligned; it needs no
+ * zeroing. */
+moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out,
+                              const moe_bf16* y, const float* w_post,
+                              const float* gate, const float* w_pre,
+                              const moe_bf16* du, const void* dr_out, void* dr,
+                              moe_bf16* dy, float* dw_post, float* dgate,
+                              float* dw_pre, void* ws, size_t ws_bytes,
+                              moe_stream_t stream);
 
 /* Whole layer backward from `saved`: writes dx [T,h] bf16 and the fp32
  * gradients dWg, dW1, dW3, dW2.  The router bias gets no gradient. */

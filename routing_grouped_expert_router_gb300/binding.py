@@ -23,7 +23,9 @@ MOE_ERR_DEVICE_TIMEOUT = 5
 MOE_ERR_DEVICE_INDEX = 6
 
 OP_ROUTE, OP_PERMUTE, OP_EXPERT_FFN_FWD, OP_EXPERT_FFN_BWD, OP_ROUTER_BWD, \
-    OP_LAYER_FWD, OP_LAYER_BWD, OP_LAYER_FWD_FP8, OP_LAYER_BWD_FP8 = range(9)
+    OP_LAYER_FWD, OP_LAYER_BWD, OP_LAYER_FWD_FP8, OP_LAYER_BWD_FP8, OP_LAYER_DECODE, \
+    OP_LAYER_DECODE_FP8 = range(11)
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = range(3)
 
 HEADER = os.path.join(_build.ROOT, "include", "moe.h")
 
@@ -50,6 +52,18 @@ def dims_of(cfg, has_bias=None, capacity=0, sar=False) -> moe_dims:
     return dims(cfg.T, cfg.h, cfg.f, cfg.E, cfg.k, hb, capacity, sar)
 
 
+class moe_norm_dims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("h", ctypes.c_int32), ("res_f32", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("beta", ctypes.c_float)]
+
+
+def norm_dims(T, h, res_f32=False, gate=GATE_NONE, eps=1e-5, alpha=1.0,
+              beta=1.0) -> moe_norm_dims:
+    return moe_norm_dims(int(T), int(h), int(bool(res_f32)), int(gate), float(eps), float(alpha),
+                         float(beta))
+
+
 def capacity_for(T, k, E, factor: float) -> int:
     """moe_capacity_for: the per-expert capacity for a capacity factor."""
     c = load().moe_capacity_for(int(T), int(k), int(E), float(factor))
@@ -63,6 +77,7 @@ _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _D = ctypes.POINTER(moe_dims)
+_ND = ctypes.POINTER(moe_norm_dims)
 
 _SIGS = {
     "moe_workspace_bytes": (_SZ, [_D, _I]),
@@ -98,6 +113,11 @@ _SIGS = {
     "moe_quantize_weights_fp8_bwd": (_I, [_D, _P, _P, _P, _P]),
     "moe_fp8_bwd_weight_view": (_P, [_D, _P, ctypes.c_char_p]),
     "moe_layer_bwd_fp8": (_I, [_D] + [_P] * 11 + [_P, _SZ, _P]),
+    "moe_layer_decode": (_I, [_D] + [_P] * 10 + [_SZ, _P]),
+    "moe_layer_decode_fp8": (_I, [_D] + [_P] * 8 + [_SZ, _P]),
+    "moe_norm_workspace_bytes": (_SZ, [_ND]),
+    "moe_block_norm_fwd": (_I, [_ND] + [_P] * 8),
+    "moe_block_norm_bwd": (_I, [_ND] + [_P] * 13 + [_SZ, _P]),
     "moe_version": (ctypes.c_char_p, []),
     "moe_capacity_for": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                           ctypes.c_double]),
@@ -340,3 +360,34 @@ def moe_layer_bwd_fp8(d, x, dy, Wg, W2, qwb, saved, dx, dWg, dW1, dW3, dW2, ws, 
                                     _addr(dW2), _addr(ws), ws_bytes, _stream(stream)),
            "moe_layer_bwd_fp8")
 
+
+def moe_layer_decode(d, x, Wg, b, W1, W3, W2, y, topk_idx, gates, ws, ws_bytes=None, stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check(load().moe_layer_decode(ctypes.byref(d), _addr(x), _addr(Wg), _addr(b), _addr(W1),
+                                   _addr(W3), _addr(W2), _addr(y), _addr(topk_idx), _addr(gates),
+                                   _addr(ws), ws_bytes, _stream(stream)), "moe_layer_decode")
+
+
+def moe_layer_decode_fp8(d, x, Wg, b, qw, y, topk_idx, gates, ws, ws_bytes=None, stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check(load().moe_layer_decode_fp8(ctypes.byref(d), _addr(x), _addr(Wg), _addr(b), _addr(qw),
+                                       _addr(y), _addr(topk_idx), _addr(gates), _addr(ws),
+                                       ws_bytes, _stream(stream)), "moe_layer_decode_fp8")
+
+
+def moe_norm_workspace_bytes(nd: moe_norm_dims) -> int:
+    return int(load().moe_norm_workspace_bytes(ctypes.byref(nd)))
+
+
+def moe_block_norm_fwd(nd, r, y, w_post, gate, w_pre, r_out, u, stream=None):
+    _check(load().moe_block_norm_fwd(ctypes.byref(nd), _addr(r), _addr(y), _addr(w_post),
+                                     _addr(gate), _addr(w_pre), _addr(r_out), _addr(u),
+                                     _stream(stream)), "moe_block_norm_fwd")
+
+
+def moe_block_norm_bwd(nd, r_out, y, w_post, gate, w_pre, du, dr_out, dr, dy, dw_post, dgate,
+                       dw_pre, ws, ws_bytes=None, stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    args = [r_out, y, w_post, gate, w_pre, du, dr_out, dr, dy, dw_post, dgate, dw_pre]
+    _check(load().moe_block_norm_bwd(ctypes.byref(nd), *[_addr(a) for a in args], _addr(ws),
+                                     ws_bytes, _stream(stream)), "moe_block_norm_bwd")

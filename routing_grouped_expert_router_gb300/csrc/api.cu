@@ -14,6 +14,7 @@
 
 #include "../../include/moe.h"
 #include "api_internal.h"
+#include "decode.cuh"
 #include "grouped_gemm.cuh"
 #include "kernels.cuh"
 
@@ -64,7 +65,8 @@ moe_status check_dims(const moe_dims* d, bool routed) {
 
 bool routed_op(int op) {
   return op == MOE_OP_ROUTE || op == MOE_OP_LAYER_FWD || op == MOE_OP_LAYER_BWD ||
-         op == MOE_OP_LAYER_FWD_FP8 || op == MOE_OP_LAYER_BWD_FP8;
+         op == MOE_OP_LAYER_FWD_FP8 || op == MOE_OP_LAYER_BWD_FP8 ||
+         op == MOE_OP_LAYER_DECODE || op == MOE_OP_LAYER_DECODE_FP8;
 }
 
 
@@ -440,6 +442,8 @@ const char* moe_version(void) { return "libmoe_gb300 0.1 (sm_103a, tcgen05 Group
 
 size_t moe_workspace_bytes(const moe_dims* dims, int op) {
   if (check_dims(dims, routed_op(op)) != MOE_OK) return 0;
+  if (op == MOE_OP_LAYER_DECODE || op == MOE_OP_LAYER_DECODE_FP8)
+    return moe::decode_workspace_bytes(*dims, op == MOE_OP_LAYER_DECODE_FP8);
   return ws_layout(*dims, op).total;
 }
 
