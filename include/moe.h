@@ -492,8 +492,8 @@ const char* moe_status_string(moe_status status);
  * MOE_ERR_CUDA if the synchronisation itself failed. */
 moe_status moe_read_device_status(void* ws, moe_stream_t stream);
 
-/* Zeroes the status word at the start of `ws` (asynchronous); ws = NULL: the
- * current device's status word of the calls without a workspace. */
+/* Zeroes the 256 bytes at the start of `ws`, the status word among them
+ * (asynchronous); ws = NULL: the current device's status word of the calls without a workspace. */
 moe_status moe_clear_device_status(void* ws, moe_stream_t stream);
 
 /* Failure-path self test: launches one thread that waits on an mbarrier

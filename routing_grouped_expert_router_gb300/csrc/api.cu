@@ -508,7 +508,9 @@ moe_status moe_clear_device_status(void* ws, moe_stream_t stream) {
   if (ws && !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
   int* word = ws ? static_cast<int*>(ws) : moe::nows_status_word();
   if (!word) return MOE_ERR_CUDA;
-  MOE_CU(cudaMemsetAsync(word, 0, sizeof(int), reinterpret_cast<cudaStream_t>(stream)));
+  // a workspace's whole header: the few-token layer keeps its barrier words there
+  MOE_CU(cudaMemsetAsync(word, 0, ws ? kAlign : sizeof(int),
+                         reinterpret_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

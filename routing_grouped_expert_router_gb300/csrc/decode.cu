@@ -1,172 +1,966 @@
-// decode.cu -- the whole MoE layer for a few tokens: moe_layer_decode and
-// moe_layer_decode_fp8.
+// decode.cu -- the whole MoE layer for a few tokens in one kernel:
+// moe_layer_decode and moe_layer_decode_fp8.
+//
+//   l = x Wg (+ b);  the k largest;  gates = softmax over them
+//   H[p] = silu(x W1[e]) * (x W3[e])     for each placed assignment p = (t, e)
+//   O[p] = H[p] W2[e];   y[t] = sum_j gates[t,j] O[p(t,j)]
+//
+// What bounds it: the weights of the chosen experts are read once, and with at
+// most 128 tokens they are nearly all the bytes and leave the tensor cores idle
+// most of the time (128 tokens x 2 slots over 8 experts: 32 MACs for each
+// weight, where a GB300 can do 280 in the time its 2 bytes take to arrive).  So
+// the kernel is built as a stream of weights:
+//   * one persistent cooperative kernel, one block for each SM, four phases
+//     (route, FC1, FC2, combine) with a grid barrier between them;
+//   * the products are taken transposed, weights as the 128-row operand A of
+//     tcgen05.mma and the tokens as its N columns (16 to 128), so that the
+//     smallest batch wastes columns of an idle tensor core, not bytes;
+//   * 32 KiB weight stages (two 128-column tiles x 64 rows of bf16, 128 of
+//     e4m3) flow through a ring of up to 6 stages that TMA fills, about 200 KiB
+//     in flight on each SM; nothing but the TMA and MMA units touches them;
+//   * each phase's k-steps, over all its tiles in a row, are cut into equal
+//     ranges, one for each block, whatever the tiles' borders: the number of
+//     experts hit decides the tiles, and a tile for each block would leave up
+//     to half of the SMs idle in the last wave.  A tile that two or more blocks
+//     share is joined in block order (FC1: by the block that comes last, since
+//     SwiGLU needs the whole sums; FC2: when y is combined), so the result does
+//     not depend on timing;
+//   * the weights of FC2's first stages are loaded before the barrier that
+//     makes H whole.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <climits>
 #include <cstdint>
+#include <cstring>
 
 #include "../../include/moe.h"
 #include "api_internal.h"
 #include "decode.cuh"
+#include "grouped_gemm.cuh"
 #include "kernels.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTok = 8;  // tokens of an expert summed at once
+constexpr int kThreads = 256;
+constexpr int kWBytes = 32768;     // weights of a stage
+constexpr int kMaxStages = 6;
+constexpr int kMaxRows = kDecodeMaxT * 8;  // placed assignments
+constexpr int kMaxE = 64;
+constexpr int kGroupTok = 8;       // tokens of a router work unit at most
+constexpr int kTimeoutCode = MOE_ERR_DEVICE_TIMEOUT;
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kSmemMax = 232448;
 
-struct Args {
+// The workspace's first 256 bytes: the status word, then words that are zero
+// between calls (every call leaves them so).
+constexpr int kBarWord = 16;    // arrivals at the grid barriers
+constexpr int kExitWord = 17;   // blocks that are done
+constexpr int kGroupWord = 32;  // router units done for each token group (16)
+
+struct Params {
   int T, h, f, E, k, capacity;
-  const int32_t* idx;
-  const float* gates;
-  // bf16
+  int n1;                   // T rounded up to 16: FC1's MMA columns
+  int stages;
+  int tok_group, groups, slices, slice_h;  // router work units
   const uint16_t* x;
-  const uint16_t *W1, *W3, *W2;
-  // e4m3
-  const uint8_t *xq, *W13q, *W2q, *Hq;
-  const float *sx, *sh, *s1, *s3, *s2;
-  uint16_t* H;  // [T*k, f]
-  float* O;     // [T*k, h]
+  const float *Wg, *b;
+  int32_t* idx;
+  float* gates;
+  float* logits;            // [slices, T, E]
+  uint16_t* H;              // [T*k, f]
+  float* O;                 // [T*k, h]
+  float* part1;             // [2 * blocks][2, T, 128]: FC1 sums of shared tiles
+  float* part2;             // [blocks][T, 256]: FC2 sums of tiles begun elsewhere
+  unsigned* tick1;          // [blocks]
   uint16_t* y;
+  // e4m3
+  uint8_t *xq, *Hq;
+  float* sx;
+  unsigned* amax;           // [T*k]: bits of max |H|
+  const float *s1, *s3, *s2;
+  int* status;
 };
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
-__device__ __forceinline__ float e4(uint8_t v) {
-  __nv_fp8_e4m3 q;
-  q.__x = v;
-  return static_cast<float>(q);
+struct Maps {
+  CUtensorMap x, w1, w3, h, w2;
+};
+
+struct alignas(16) Ctrl {
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], hready, drain;
+  uint32_t tmem_base;
+  int abort, flag, nact;
+  int off[kMaxE + 1];       // first row of each expert
+  int act[kMaxE];           // experts with rows
+  int act_of[kMaxE];        // its inverse
+  float gate[kMaxRows];     // by assignment
+  float sx[kDecodeMaxT];
+  int16_t pos[kMaxRows];    // assignment -> row, -1 dropped
+  uint8_t exp[kMaxRows];    // assignment -> expert
+  uint8_t tok[kMaxRows];    // row -> token
+  uint16_t hist[kMaxRows / 32][kMaxE];
+};
+
+// One phase's k-steps [0, total) cut into blocks' ranges.
+struct Cut {
+  unsigned total, blocks;
+  __device__ unsigned start(unsigned c) const { return c * total / blocks; }
+  __device__ unsigned block_of(unsigned q) const { return ((q + 1) * blocks - 1) / total; }
+};
+__device__ __forceinline__ Cut cut_of(unsigned total, unsigned grid) {
+  return Cut{total, total < grid ? total : grid};
 }
 
-// The assignments that expert e keeps, in ascending order, in list; returns
-// their number.
-__device__ int expert_list(const Args& a, int e, int* list, int* count) {
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int i = 0; i < a.T * a.k && n < a.capacity; ++i)
-      if (a.idx[i] == e) list[n++] = i;
-    *count = n;
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+// A barrier over the grid, by one thread of each block: everything that the
+// block's threads wrote before it (they are ordered before this thread by a
+// block barrier) is seen by every block after it.  `target` counts all
+// arrivals of the launch so far.
+__device__ __forceinline__ bool grid_barrier(unsigned* word, unsigned target, int* status) {
+  __threadfence();
+  atomicAdd(word, 1u);
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+    if (static_cast<int>(v - target) >= 0) break;
+    if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(status, kTimeoutCode);
+      return false;
+    }
+  }
+  __threadfence();
+  return true;
+}
+
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Accumulator columns [col, col + 16) of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// One column (no wait).
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait8(uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                 "+r"(a[6]), "+r"(a[7]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
+                 "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])::"memory");
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// The scale and codes of a quantised row, as fp8.cu makes them.
+__device__ __forceinline__ float scale_of(float amax) {
+  return amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+}
+__device__ __forceinline__ uint32_t quant2(uint32_t w, float s) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+      make_float2(__fdiv_rn(bf16_lo(w), s), __fdiv_rn(bf16_hi(w), s)), __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ uint2 quant8(const uint4& w, float s) {
+  return make_uint2(quant2(w.x, s) | quant2(w.y, s) << 16, quant2(w.z, s) | quant2(w.w, s) << 16);
+}
+__device__ __forceinline__ float amax8(const uint4& w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
+  return m;
+}
+
+// ------------------------------------------------------------------ route
+// Top-k of one token by a warp: lane l holds the logits of experts l and
+// l + 32.  k rounds of an arg-max (the larger logit, the lower id on ties; NaN
+// counts as the smallest), then the softmax over the chosen.
+__device__ void select_topk(const Params& p, int t, float l0, float l1, int lane) {
+  bool live0 = lane < p.E, live1 = lane + 32 < p.E;
+  float top = 0.f, mine = 0.f, sum = 0.f;
+  int chosen = 0;
+  for (int j = 0; j < p.k; ++j) {
+    float bv = -INFINITY;
+    int be = 1 << 30;
+    const float v0 = isnan(l0) ? -INFINITY : l0, v1 = isnan(l1) ? -INFINITY : l1;
+    if (live0) {
+      bv = v0;
+      be = lane;
+    }
+    if (live1 && (be > kMaxE || v1 > bv)) {
+      bv = v1;
+      be = lane + 32;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float ov = __shfl_xor_sync(kFull, bv, o);
+      const int oe = __shfl_xor_sync(kFull, be, o);
+      if (oe < kMaxE && (be > kMaxE || ov > bv || (ov == bv && oe < be))) {
+        bv = ov;
+        be = oe;
+      }
+    }
+    if (be == lane) live0 = false;
+    if (be == lane + 32) live1 = false;
+    const float lv = __shfl_sync(kFull, be < 32 ? l0 : l1, be & 31);
+    if (j == 0) top = lv;
+    const float ev = expf(lv - top);
+    sum += ev;
+    if (lane == j) {
+      chosen = be;
+      mine = ev;
+    }
+  }
+  if (lane < p.k) {
+    p.idx[t * p.k + lane] = chosen;
+    p.gates[t * p.k + lane] = mine / sum;
+  }
+}
+
+// A router unit is a group of tokens x a slice of h: fp32 partial logits.  The
+// block that finishes a group's last slice adds the slices in order and chooses
+// the experts of its tokens, one warp for each.
+__device__ void route(const Params& p, Ctrl& c, float* smem) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned* words = reinterpret_cast<unsigned*>(p.status);
+  for (int unit = blockIdx.x; unit < p.groups * p.slices; unit += gridDim.x) {
+    const int g = unit / p.slices, s = unit % p.slices;
+    const int t0 = g * p.tok_group, nt = min(p.tok_group, p.T - t0);
+    const int j0 = s * p.slice_h, nj = min(p.slice_h, p.h - j0);
+    float* xs = smem;                          // [nj][8]
+    float* red = smem + p.slice_h * kGroupTok;  // [kThreads][8]
+    __syncthreads();
+    for (int i = tid; i < nj * kGroupTok; i += kThreads) {
+      const int t = i / nj, j = i - t * nj;
+      xs[j * kGroupTok + t] =
+          t < nt ? bf16_lo(p.x[static_cast<size_t>(t0 + t) * p.h + j0 + j]) : 0.f;
+    }
+    __syncthreads();
+    const int parts = kThreads / p.E;
+    const int e = tid % p.E, part = tid / p.E;
+    float acc[kGroupTok] = {};
+    if (part < parts) {
+#pragma unroll 4
+      for (int j = part; j < nj; j += parts) {
+        const float w = __ldg(p.Wg + static_cast<size_t>(j0 + j) * p.E + e);
+        const float4 a = *reinterpret_cast<const float4*>(xs + j * kGroupTok);
+        const float4 b = *reinterpret_cast<const float4*>(xs + j * kGroupTok + 4);
+        acc[0] = fmaf(a.x, w, acc[0]);
+        acc[1] = fmaf(a.y, w, acc[1]);
+        acc[2] = fmaf(a.z, w, acc[2]);
+        acc[3] = fmaf(a.w, w, acc[3]);
+        acc[4] = fmaf(b.x, w, acc[4]);
+        acc[5] = fmaf(b.y, w, acc[5]);
+        acc[6] = fmaf(b.z, w, acc[6]);
+        acc[7] = fmaf(b.w, w, acc[7]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kGroupTok; ++t) red[t * kThreads + tid] = acc[t];
+    __syncthreads();
+    for (int i = tid; i < nt * p.E; i += kThreads) {
+      const int t = i / p.E, ee = i - t * p.E;
+      float v = 0.f;
+      for (int q = 0; q < parts; ++q) v += red[t * kThreads + q * p.E + ee];
+      p.logits[(static_cast<size_t>(s) * p.T + t0 + t) * p.E + ee] = v;
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      const unsigned n = atomicAdd(words + kGroupWord + g, 1u);
+      c.flag = n + 1 == static_cast<unsigned>(p.slices);
+      if (c.flag) words[kGroupWord + g] = 0;
+    }
+    __syncthreads();
+    if (!c.flag) continue;
+    __threadfence();
+    // the slices' sums, `parts` interleaved chains for each logit
+    float* logit = red + kThreads * kGroupTok;  // [8][kMaxE]
+#pragma unroll
+    for (int t = 0; t < kGroupTok; ++t) acc[t] = 0.f;
+    if (part < parts) {
+      const float* src = p.logits + static_cast<size_t>(t0) * p.E + e;
+#pragma unroll 4
+      for (int q = part; q < p.slices; q += parts)
+#pragma unroll
+        for (int t = 0; t < kGroupTok; ++t)
+          if (t < nt) acc[t] += __ldcg(src + (static_cast<size_t>(q) * p.T + t) * p.E);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kGroupTok; ++t) red[t * kThreads + tid] = acc[t];
+    __syncthreads();
+    for (int i = tid; i < nt * p.E; i += kThreads) {
+      const int t = i / p.E, ee = i - t * p.E;
+      float v = 0.f;
+      for (int q = 0; q < parts; ++q) v += red[t * kThreads + q * p.E + ee];
+      logit[t * kMaxE + ee] = p.b ? v + __ldg(p.b + ee) : v;
+    }
+    __syncthreads();
+    if (warp < nt)
+      select_topk(p, t0 + warp, lane < p.E ? logit[warp * kMaxE + lane] : 0.f,
+                  lane + 32 < p.E ? logit[warp * kMaxE + lane + 32] : 0.f, lane);
+  }
+}
+
+// x rows to e4m3, a block for each row.
+__device__ void quant_x(const Params& p, float* red) {
+  const int tid = threadIdx.x, n8 = p.h / 8;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    const uint4* row = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.h);
+    float m = 0.f;
+    for (int c = tid; c < n8; c += kThreads) m = fmaxf(m, amax8(row[c]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, red[w]);
+    const float s = scale_of(m);
+    if (tid == 0) p.sx[t] = s;
+    uint2* out = reinterpret_cast<uint2*>(p.xq + static_cast<size_t>(t) * p.h);
+    for (int c = tid; c < n8; c += kThreads) out[c] = quant8(row[c], s);
+  }
+}
+
+// --------------------------------------------------------------- dispatch
+// Every block builds the same lists from the chosen experts: the rows of each
+// expert in ascending assignment order, at most `capacity` of them.
+__device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int R = p.T * p.k, chunks = (R + 31) / 32;
+  for (int i = tid; i < chunks * kMaxE; i += kThreads) c.hist[i / kMaxE][i % kMaxE] = 0;
+  if (f8)
+    for (int t = tid; t < p.T; t += kThreads) c.sx[t] = __ldcg(p.sx + t);
+  __syncthreads();
+  int rank[kMaxRows / kThreads];  // of my assignments within their chunk of 32
+  for (int ch = warp, n = 0; ch < chunks; ch += kThreads / 32, ++n) {
+    const int a = ch * 32 + lane;
+    int e = a < R ? __ldcg(p.idx + a) : -1;
+    if (a < R) {
+      c.gate[a] = __ldcg(p.gates + a);
+      c.exp[a] = static_cast<uint8_t>(e);
+    }
+    const unsigned same = __match_any_sync(kFull, e);
+    rank[n] = __popc(same & ((1u << lane) - 1));
+    if (e >= 0 && rank[n] == 0) c.hist[ch][e] = static_cast<uint16_t>(__popc(same));
   }
   __syncthreads();
-  return *count;
+  if (tid < kMaxE) {  // hist: counts -> assignments of the expert before the chunk
+    int n = 0;
+    for (int ch = 0; ch < chunks; ++ch) {
+      const int v = c.hist[ch][tid];
+      c.hist[ch][tid] = static_cast<uint16_t>(n);
+      n += v;
+    }
+    c.act_of[tid] = min(n, p.capacity);
+  }
+  __syncthreads();
+  if (warp == 0) {  // offsets and the list of experts with rows
+    const int n0 = c.act_of[lane], n1 = c.act_of[lane + 32];
+    int s0 = n0, s1 = n1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u0 = __shfl_up_sync(kFull, s0, o), u1 = __shfl_up_sync(kFull, s1, o);
+      if (lane >= o) {
+        s0 += u0;
+        s1 += u1;
+      }
+    }
+    const int all0 = __shfl_sync(kFull, s0, 31);
+    if (lane == 0) c.off[0] = 0;
+    c.off[lane + 1] = s0;
+    c.off[lane + 33] = all0 + s1;
+    const unsigned m0 = __ballot_sync(kFull, n0 > 0), m1 = __ballot_sync(kFull, n1 > 0);
+    const unsigned below = (1u << lane) - 1;
+    const int i0 = __popc(m0 & below), i1 = __popc(m0) + __popc(m1 & below);
+    __syncwarp();
+    if (n0 > 0) c.act[i0] = lane;
+    if (n1 > 0) c.act[i1] = lane + 32;
+    c.act_of[lane] = i0;
+    c.act_of[lane + 32] = i1;
+    if (lane == 0) c.nact = __popc(m0) + __popc(m1);
+  }
+  __syncthreads();
+  for (int ch = warp, n = 0; ch < chunks; ch += kThreads / 32, ++n) {
+    const int a = ch * 32 + lane;
+    if (a >= R) break;
+    const int e = c.exp[a], r = c.hist[ch][e] + rank[n];
+    const bool placed = r < p.capacity;
+    const int row = c.off[e] + r;
+    c.pos[a] = static_cast<int16_t>(placed ? row : -1);
+    if (placed) c.tok[row] = static_cast<uint8_t>(a / p.k);
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------- FC1's ends
+// H of a row's column from its two sums.
+template <bool F8>
+__device__ __forceinline__ void store_h(const Params& p, const Ctrl& c, int row, int e, int col,
+                                        float a, float b, float w1, float w3, int lane) {
+  float m = 0.f;
+  if (col < p.f) {
+    if (F8) {
+      const float s = c.sx[c.tok[row]];
+      a *= s * w1;
+      b *= s * w3;
+    }
+    const __nv_bfloat16 hv = __float2bfloat16_rn(a / (1.f + expf(-a)) * b);
+    p.H[static_cast<size_t>(row) * p.f + col] = *reinterpret_cast<const uint16_t*>(&hv);
+    m = fabsf(__bfloat162float(hv));
+  }
+  if (F8) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if (lane == 0) atomicMax(p.amax + row, __float_as_uint(m));
+  }
 }
 
 template <bool F8>
-__global__ void decode_fc1_kernel(const Args a) {
-  __shared__ int list[kDecodeMaxT], count;
-  const int e = blockIdx.y, c = blockIdx.x * blockDim.x + threadIdx.x;
-  const int n = expert_list(a, e, list, &count);
-  if (c >= a.f) return;
-  for (int i0 = 0; i0 < n; i0 += kTok) {
-    float sa[kTok] = {}, sb[kTok] = {};
-    for (int j = 0; j < a.h; ++j) {
-      float w1, w3;
-      if (F8) {
-        const size_t r = (static_cast<size_t>(e) * 2 * a.f + (c / 128) * 256 + c % 128) * a.h + j;
-        w1 = e4(a.W13q[r]);
-        w3 = e4(a.W13q[r + static_cast<size_t>(128) * a.h]);
-      } else {
-        const size_t r = (static_cast<size_t>(e) * a.h + j) * a.f + c;
-        w1 = bf(a.W1[r]);
-        w3 = bf(a.W3[r]);
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int bbytes = p.n1 * 128;
+  const int stage_bytes = kWBytes + bbytes;
+  Ctrl& c = *reinterpret_cast<Ctrl*>(smem + p.stages * stage_bytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned G = gridDim.x;
+  unsigned* words = reinterpret_cast<unsigned*>(p.status);
+  volatile int* abort_flag = &c.abort;
+
+  if (tid == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(smem_u32(&c.full[s]), 1);
+      mbar_init(smem_u32(&c.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&c.tfull[b]), 1);
+      mbar_init(smem_u32(&c.tempty[b]), 128);
+    }
+    mbar_init(smem_u32(&c.hready), 1);
+    mbar_init(smem_u32(&c.drain), 1);
+    c.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.w1);
+    tma_prefetch_desc(&maps.w3);
+    tma_prefetch_desc(&maps.h);
+    tma_prefetch_desc(&maps.w2);
+    p.tick1[blockIdx.x] = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&c.tmem_base), 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  // ------------------------------------------------------------- route
+  if (F8) {
+    quant_x(p, reinterpret_cast<float*>(smem));
+    for (int i = blockIdx.x * kThreads + tid; i < p.T * p.k; i += G * kThreads) p.amax[i] = 0;
+  }
+  route(p, c, reinterpret_cast<float*>(smem));
+  fence_proxy_async_all();  // xq for TMA; and the ring's memory, used by route above
+  __syncthreads();
+  if (tid == 0 && !grid_barrier(words + kBarWord, G, p.status)) c.abort = 1;
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem_base;
+  if (!c.abort) {
+    dispatch(p, c, F8);
+    fence_proxy_async_all();
+
+    constexpr int KB = F8 ? 128 : 64;  // contraction indices of a stage
+    const unsigned ks1 = p.h / KB, nt1 = (p.f + 127) / 128;
+    const unsigned ks2 = p.f / KB, nt2 = (p.h + 255) / 256;
+    const Cut cut1 = cut_of(c.nact * nt1 * ks1, G), cut2 = cut_of(c.nact * nt2 * ks2, G);
+    const unsigned cta = blockIdx.x;
+    const unsigned a1 = cta < cut1.blocks ? cut1.start(cta) : cut1.total;
+    const unsigned b1 = cta < cut1.blocks ? cut1.start(cta + 1) : cut1.total;
+    const unsigned a2 = cta < cut2.blocks ? cut2.start(cta) : cut2.total;
+    const unsigned b2 = cta < cut2.blocks ? cut2.start(cta + 1) : cut2.total;
+    const uint32_t ring = smem_u32(smem);
+
+    if (warp == 0) {
+      // ---------------------------------------------------- TMA producer
+      if (lane == 0) {
+        int s = 0;        // next stage
+        uint32_t ph = 0;  // its use count's parity
+        int filled = 0;
+        bool ok = true;
+        auto claim = [&](unsigned bytes) {
+          if (*abort_flag ||
+              !mbar_wait(smem_u32(&c.empty[s]), ph ^ 1, p.status, kTimeoutCode)) {
+            *abort_flag = 1;
+            ok = false;
+            return;
+          }
+          mbar_expect_tx(smem_u32(&c.full[s]), bytes);
+          if (filled < p.stages) ++filled;
+        };
+        auto next = [&] {
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        };
+        unsigned item = a1 / ks1, ks = a1 - item * ks1;
+        unsigned ai = item / nt1, tile = item - ai * nt1;
+        for (unsigned q = a1; ok && q < b1; ++q) {
+          claim(kWBytes + bbytes);
+          if (!ok) break;
+          const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&c.full[s]);
+          const int e = c.act[ai], k0 = ks * KB;
+          if (F8) {
+            tma_load_3d(dst, &maps.w1, k0, tile * 256, e, bar);
+          } else {
+            tma_load_3d(dst, &maps.w1, 0, e * p.h + k0, tile * 2, bar);
+            tma_load_3d(dst + kWBytes / 2, &maps.w3, 0, e * p.h + k0, tile * 2, bar);
+          }
+          tma_load_2d(dst + kWBytes, &maps.x, k0, 0, bar);
+          next();
+          if (++ks == ks1) {
+            ks = 0;
+            if (++tile == nt1) {
+              tile = 0;
+              ++ai;
+            }
+          }
+        }
+        // FC2.  The first stages' weights are asked for at once; their rows of H
+        // follow when every block's are written.
+        item = a2 / ks2;
+        ks = a2 - item * ks2;
+        ai = item / nt2;
+        tile = item - ai * nt2;
+        unsigned hks = ks, hai = ai, htile = tile;  // where the H loads are
+        int hs = s;
+        const unsigned ahead = min(b2 - a2, static_cast<unsigned>(p.stages));
+        auto load_h = [&] {
+          const int e = c.act[hai], r0 = c.off[e], n = c.off[e + 1] - r0;
+          const uint32_t dst = ring + hs * stage_bytes + kWBytes, bar = smem_u32(&c.full[hs]);
+          for (int r = 0; r < n; r += 16)
+            tma_load_2d(dst + r * 128, &maps.h, hks * KB, r0 + r, bar);
+          if (++hs == p.stages) hs = 0;
+          if (++hks == ks2) {
+            hks = 0;
+            if (++htile == nt2) {
+              htile = 0;
+              ++hai;
+            }
+          }
+        };
+        unsigned waiting = 0;  // stages whose H is not yet asked for
+        bool ready = false;
+        for (unsigned q = a2; ok && q < b2; ++q) {
+          const int e = c.act[ai];
+          const int rows16 = (c.off[e + 1] - c.off[e] + 15) / 16 * 16;
+          claim(kWBytes + rows16 * 128);
+          if (!ok) break;
+          const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&c.full[s]);
+          if (F8)
+            tma_load_3d(dst, &maps.w2, ks * KB, tile * 256, e, bar);
+          else
+            tma_load_3d(dst, &maps.w2, 0, e * p.f + ks * KB, tile * 4, bar);
+          ++waiting;
+          next();
+          if (++ks == ks2) {
+            ks = 0;
+            if (++tile == nt2) {
+              tile = 0;
+              ++ai;
+            }
+          }
+          if (!ready && q + 1 - a2 < ahead) continue;
+          if (!ready) {
+            if (!mbar_wait(smem_u32(&c.hready), 0, p.status, kTimeoutCode)) {
+              *abort_flag = 1;
+              ok = false;
+            }
+            ready = true;
+            fence_proxy_async_all();
+          }
+          // on failure too: the stages' loads must all land before the block ends
+          for (; waiting > 0; --waiting) load_h();
+        }
+        if (!ok) {
+          for (; waiting > 0; --waiting) load_h();
+          for (int i = 0; i < filled; ++i) {
+            s = s == 0 ? p.stages - 1 : s - 1;
+            if (s == p.stages - 1) ph ^= 1;
+            mbar_wait(smem_u32(&c.full[s]), ph, p.status, kTimeoutCode);
+          }
+        }
       }
+    } else if (warp == 1) {
+      // ------------------------------------------------------ MMA issuer
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      auto phase = [&](unsigned q0, unsigned q1, unsigned ksn, unsigned tiles, bool fc1) {
+        unsigned item = q0 / ksn, ks = q0 - item * ksn;
+        for (unsigned q = q0; ok && q < q1; ++q) {
+          const int buf = it & 1;
+          const bool first = q == q0 || ks == 0, last = q + 1 == q1 || ks + 1 == ksn;
+          if (first && (*abort_flag || !mbar_wait(smem_u32(&c.tempty[buf]), ((it >> 1) & 1) ^ 1,
+                                                  p.status, kTimeoutCode)))
+            ok = false;
+          if (ok && (*abort_flag ||
+                     !mbar_wait(smem_u32(&c.full[s]), ph, p.status, kTimeoutCode)))
+            ok = false;
+          if (!ok) {
+            *abort_flag = 1;
+            break;
+          }
+          int n = p.n1;
+          if (!fc1) {
+            const int e = c.act[item / tiles];
+            n = (c.off[e + 1] - c.off[e] + 15) / 16 * 16;
+          }
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t idesc = F8 ? idesc_e4m3(128, n) : idesc_bf16(128, n, true, false);
+            const uint32_t ab = ring + s * stage_bytes, bb = ab + kWBytes;
+            const uint32_t acc = tmem + buf * 256;
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        const size_t t = list[min(i0 + i, n - 1)] / a.k;
-        const float xv = F8 ? e4(a.xq[t * a.h + j]) : bf(a.x[t * a.h + j]);
-        sa[i] = fmaf(xv, w1, sa[i]);
-        sb[i] = fmaf(xv, w3, sb[i]);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t bd = smem_desc(bb + kk * 32, 16, 1024);
+              const uint32_t add = !(first && kk == 0);
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                const uint32_t am = ab + m * (kWBytes / 2);
+                if (F8)
+                  umma_e4m3(acc + m * 128, smem_desc(am + kk * 32, 16, 1024), bd, idesc, add);
+                else
+                  umma_bf16(acc + m * 128, smem_desc(am + kk * 2048, 8192, 1024), bd, idesc, add);
+              }
+            }
+            umma_commit(smem_u32(&c.empty[s]));
+            if (last) umma_commit(smem_u32(&c.tfull[buf]));
+          }
+          __syncwarp();
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (last) ++it;
+          if (++ks == ksn) {
+            ks = 0;
+            ++item;
+          }
+        }
+      };
+      phase(a1, b1, ks1, nt1, true);
+      phase(a2, b2, ks2, nt2, false);
+      if (lane == 0) {  // every MMA must be done before tensor memory is freed
+        umma_commit(smem_u32(&c.drain));
+        mbar_wait(smem_u32(&c.drain), 0, p.status, kTimeoutCode);
+      }
+      __syncwarp();
+    } else if (warp >= 4) {
+      // -------------------------------------------------------- epilogue
+      const int r = (warp & 3) * 32 + lane;  // my row of the 128-row tiles
+      const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      int it = 0;
+      bool ok = true;
+      auto filled = [&](int buf) {
+        const bool got = !*abort_flag && mbar_wait(smem_u32(&c.tfull[buf]), (it >> 1) & 1,
+                                                   p.status, kTimeoutCode);
+        if (!__all_sync(kFull, got)) {
+          *abort_flag = 1;
+          ok = false;
+        }
+        tc_fence_after();
+        return ok;
+      };
+      // ---- FC1
+      for (unsigned q = a1; ok && q < b1;) {
+        const unsigned item = q / ks1, q_item = item * ks1;
+        const unsigned end = min(b1, q_item + ks1);
+        const int buf = it & 1;
+        if (!filled(buf)) break;
+        const int e = c.act[item / nt1], col = (item % nt1) * 128 + r;
+        const int row0 = c.off[e], n = c.off[e + 1] - row0;
+        const uint32_t acc = tl + buf * 256;
+        const bool whole = q == q_item && end == q_item + ks1;
+        float w1 = 0.f, w3 = 0.f;
+        if (F8 && col < p.f) {
+          w1 = __ldg(p.s1 + static_cast<size_t>(e) * p.f + col);
+          w3 = __ldg(p.s3 + static_cast<size_t>(e) * p.f + col);
+        }
+        // two slots for each block: a tile begun elsewhere, a tile begun here
+        const size_t slot = static_cast<size_t>(2) * p.T * 128;
+        float* mine = p.part1 + (2 * cta + (q == q_item)) * slot;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+          uint32_t ra[8], rb[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t t = c.tok[row0 + min(i0 + i, n - 1)];
+            tmem_ld1(acc + t, ra[i]);
+            tmem_ld1(acc + 128 + t, rb[i]);
+          }
+          tmem_wait8(ra, rb);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i0 + i >= n) break;
+            const float va = __uint_as_float(ra[i]), vb = __uint_as_float(rb[i]);
+            if (whole) {
+              store_h<F8>(p, c, row0 + i0 + i, e, col, va, vb, w1, w3, lane);
+            } else {
+              __stcg(mine + (i0 + i) * 256 + r, va);
+              __stcg(mine + (i0 + i) * 256 + 128 + r, vb);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&c.tempty[buf]));
+        ++it;
+        if (!whole) {
+          const unsigned c0 = cut1.block_of(q_item), c1 = cut1.block_of(q_item + ks1 - 1);
+          __threadfence();
+          epi_sync();
+          if (r == 0) c.flag = atomicAdd(p.tick1 + c0, 1u) == c1 - c0;
+          epi_sync();
+          if (c.flag) {
+            __threadfence();
+            const float* first = p.part1 + (2 * c0 + 1) * slot + r;
+            for (int i = 0; i < n; ++i) {
+              float va = __ldcg(first + i * 256), vb = __ldcg(first + i * 256 + 128);
+              for (unsigned o = c0 + 1; o <= c1; ++o) {
+                const float* src = p.part1 + 2 * o * slot + i * 256 + r;
+                va += __ldcg(src);
+                vb += __ldcg(src + 128);
+              }
+              store_h<F8>(p, c, row0 + i, e, col, va, vb, w1, w3, lane);
+            }
+          }
+          epi_sync();  // c.flag is free again
+        }
+        q = end;
+      }
+      // ---- H whole
+      fence_proxy_async_all();
+      epi_sync();
+      if (r == 0 && !grid_barrier(words + kBarWord, 2 * G, p.status)) *abort_flag = 1;
+      epi_sync();
+      if (F8 && !*abort_flag) {  // rows of H to e4m3, 8 values at a time over the whole grid
+        const int n8 = p.f / 8, all = c.off[kMaxE] * n8;
+        for (int i = cta * 128 + r; i < all; i += G * 128) {
+          const int row = i / n8;
+          const float s = scale_of(__uint_as_float(__ldcg(p.amax + row)));
+          const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p.H) + i);
+          reinterpret_cast<uint2*>(p.Hq)[i] = quant8(w, s);
+        }
+        fence_proxy_async_all();
+        epi_sync();
+        if (r == 0 && !grid_barrier(words + kBarWord, 3 * G, p.status)) *abort_flag = 1;
+        epi_sync();
+      }
+      fence_proxy_async_all();
+      if (r == 0) mbar_arrive(smem_u32(&c.hready));
+      if (*abort_flag) ok = false;
+      ok = __all_sync(kFull, ok);
+      // ---- FC2: rows of O where this block began the tile, else of part2
+      for (unsigned q = a2; ok && q < b2;) {
+        const unsigned item = q / ks2, q_item = item * ks2;
+        const unsigned end = min(b2, q_item + ks2);
+        const int buf = it & 1;
+        if (!filled(buf)) break;
+        const int e = c.act[item / nt2], col0 = (item % nt2) * 256;
+        const int row0 = c.off[e], n = c.off[e + 1] - row0;
+        const bool begun = q == q_item;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int col = col0 + m * 128 + r;
+          float w2 = 1.f;
+          if (F8 && col < p.h) w2 = __ldg(p.s2 + static_cast<size_t>(e) * p.h + col);
+          float* dst = begun ? p.O + static_cast<size_t>(row0) * p.h + col
+                             : p.part2 + static_cast<size_t>(cta) * p.T * 256 + m * 128 + r;
+          const size_t ld = begun ? p.h : 256;
+          for (int i0 = 0; i0 < n; i0 += 16) {
+            float v[16];
+            tmem_ld16(tl + buf * 256 + m * 128 + i0, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (i0 + i >= n || col >= p.h) break;
+              if (F8) v[i] *= scale_of(__uint_as_float(__ldcg(p.amax + row0 + i0 + i))) * w2;
+              __stcg(dst + (i0 + i) * ld, v[i]);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&c.tempty[buf]));
+        ++it;
+        q = end;
       }
     }
-    for (int i = 0; i < kTok && i0 + i < n; ++i) {
-      const int p = list[i0 + i];
-      float va = sa[i], vb = sb[i];
-      if (F8) {
-        const float s = a.sx[p / a.k];
-        va *= s * a.s1[static_cast<size_t>(e) * a.f + c];
-        vb *= s * a.s3[static_cast<size_t>(e) * a.f + c];
+    __syncthreads();
+    // ------------------------------------------------------------ combine
+    if (tid == 0 && (*abort_flag ||
+                     !grid_barrier(words + kBarWord, (F8 ? 4 : 3) * G, p.status)))
+      *abort_flag = 1;
+    __syncthreads();
+    if (!*abort_flag) {
+      const int n4 = p.h / 4;
+      for (int i = cta * kThreads + tid; i < p.T * n4; i += G * kThreads) {
+        const int t = i / n4, col = (i - t * n4) * 4;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < p.k; ++j) {
+          const int a = t * p.k + j, row = c.pos[a];
+          if (row < 0) continue;
+          const int e = c.exp[a];
+          const unsigned q = (c.act_of[e] * nt2 + col / 256) * ks2;
+          float4 v = __ldcg(reinterpret_cast<const float4*>(p.O + static_cast<size_t>(row) * p.h + col));
+          const unsigned c1 = cut2.block_of(q + ks2 - 1);
+          for (unsigned o = cut2.block_of(q) + 1; o <= c1; ++o) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(
+                p.part2 + (static_cast<size_t>(o) * p.T + row - c.off[e]) * 256 + col % 256));
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+          }
+          const float g = c.gate[a];
+          sum.x = fmaf(g, v.x, sum.x);
+          sum.y = fmaf(g, v.y, sum.y);
+          sum.z = fmaf(g, v.z, sum.z);
+          sum.w = fmaf(g, v.w, sum.w);
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z, sum.w);
+        uint2 out;
+        out.x = *reinterpret_cast<const uint32_t*>(&lo);
+        out.y = *reinterpret_cast<const uint32_t*>(&hi);
+        reinterpret_cast<uint2*>(p.y)[i] = out;
       }
-      const __nv_bfloat16 hv = __float2bfloat16_rn(va / (1.f + expf(-va)) * vb);
-      a.H[static_cast<size_t>(p) * a.f + c] = *reinterpret_cast<const uint16_t*>(&hv);
     }
+  }
+  // ------------------------------------------------------------- teardown
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  // the last block to finish leaves the header's words zero for the next call
+  if (tid == 0 && atomicAdd(words + kExitWord, 1u) == G - 1) {
+    words[kBarWord] = 0;
+    words[kExitWord] = 0;
+    for (int g = 0; g < 16; ++g) words[kGroupWord + g] = 0;
+    __threadfence();
   }
 }
 
-template <bool F8>
-__global__ void decode_fc2_kernel(const Args a) {
-  __shared__ int list[kDecodeMaxT], count;
-  const int e = blockIdx.y, c = blockIdx.x * blockDim.x + threadIdx.x;
-  const int n = expert_list(a, e, list, &count);
-  if (c >= a.h) return;
-  for (int i0 = 0; i0 < n; i0 += kTok) {
-    float s[kTok] = {};
-    for (int j = 0; j < a.f; ++j) {
-      const float w = F8 ? e4(a.W2q[(static_cast<size_t>(e) * a.h + c) * a.f + j])
-                         : bf(a.W2[(static_cast<size_t>(e) * a.f + j) * a.h + c]);
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        const size_t o = static_cast<size_t>(list[min(i0 + i, n - 1)]) * a.f + j;
-        s[i] = fmaf(F8 ? e4(a.Hq[o]) : bf(a.H[o]), w, s[i]);
-      }
-    }
-    for (int i = 0; i < kTok && i0 + i < n; ++i) {
-      const int p = list[i0 + i];
-      float v = s[i];
-      if (F8) v *= a.sh[p] * a.s2[static_cast<size_t>(e) * a.h + c];
-      a.O[static_cast<size_t>(p) * a.h + c] = v;
-    }
-  }
-}
-
-// y[t] = the gated sum of the token's placed slots, in slot order.
-__global__ void decode_combine_kernel(const Args a) {
-  const int t = blockIdx.y, c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= a.h) return;
-  float s = 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    const int p = t * a.k + j, e = a.idx[p];
-    int before = 0;
-    for (int i = 0; i < p; ++i) before += a.idx[i] == e;
-    if (before < a.capacity) s = fmaf(a.gates[p], a.O[static_cast<size_t>(p) * a.h + c], s);
-  }
-  const __nv_bfloat16 v = __float2bfloat16_rn(s);
-  a.y[static_cast<size_t>(t) * a.h + c] = *reinterpret_cast<const uint16_t*>(&v);
-}
+// ------------------------------------------------------------------- host
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-  size_t logits, idx, gates, H, O, xq, sx, Hq, sh, total;
+  size_t logits, idx, gates, H, O, part1, part2, tick1, xq, sx, Hq, amax, total;
 };
+
+struct Plan {
+  int n1, stages, smem;
+  int tok_group, groups, slices, slice_h;
+};
+
+// Blocks = SMs.  Router units: token groups x slices of h, about one for each
+// block; groups of up to 8 tokens so that 128 tokens make 16 groups, and single
+// tokens up to 16.
+Plan plan_of(const moe_dims& d, int blocks) {
+  Plan p = {};
+  p.n1 = (d.T + 15) / 16 * 16;
+  const int stage = kWBytes + p.n1 * 128;
+  p.stages = (kSmemMax - 1024 - static_cast<int>(sizeof(Ctrl))) / stage;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.smem = 1024 + p.stages * stage + static_cast<int>(sizeof(Ctrl));
+  p.tok_group = (d.T + 15) / 16;
+  p.groups = (d.T + p.tok_group - 1) / p.tok_group;
+  int n = blocks / p.groups;
+  if (n < 1) n = 1;
+  p.slice_h = ((d.h + n - 1) / n + 7) / 8 * 8;
+  if (p.slice_h < 32) p.slice_h = 32;  // a few long slices add up sooner than many short ones
+  // x of a slice as fp32, the threads' sums and the logits fit the ring
+  const int most = (p.stages * stage - (kThreads + kMaxE) * kGroupTok * 4) / (kGroupTok * 4) / 8 * 8;
+  if (p.slice_h > most) p.slice_h = most;
+  p.slices = (d.h + p.slice_h - 1) / p.slice_h;
+  return p;
+}
+
 Layout layout(const moe_dims& d, bool fp8) {
   const size_t R = static_cast<size_t>(d.T) * d.k, T = d.T, h = d.h, f = d.f;
+  const size_t blocks = moe_api::num_sms();
+  const Plan plan = d.T > 0 ? plan_of(d, static_cast<int>(blocks)) : Plan{};
   size_t off = 256;
   auto take = [&](size_t n) {
     const size_t o = off;
-    off += (n + 255) / 256 * 256;
+    off += up256(n);
     return o;
   };
   Layout L = {};
-  L.logits = take(router_partial_bytes(d.T, d.h, d.E));
+  L.logits = take(plan.slices * T * d.E * 4);
   L.idx = take(R * 4);
   L.gates = take(R * 4);
   L.H = take(R * f * 2);
   L.O = take(R * h * 4);
+  L.part1 = take(2 * blocks * 2 * T * 128 * 4);
+  L.part2 = take(blocks * T * 256 * 4);
+  L.tick1 = take(blocks * 4);
   if (fp8) {
     L.xq = take(T * h);
     L.sx = take(T * 4);
     L.Hq = take(R * f);
-    L.sh = take(R * 4);
+    L.amax = take(R * 4);
   }
   L.total = off;
   return L;
 }
 
+// k-step counts times blocks stay below 2^31 (Cut's arithmetic; such weights
+// would not fit the GPU's memory many times over).
 bool supported(const moe_dims& d, bool fp8) {
-  return d.T <= kDecodeMaxT && d.sar == 0 && (!fp8 || (d.h % 128 == 0 && d.f % 128 == 0));
+  if (d.T > kDecodeMaxT || d.sar != 0 || (fp8 && (d.h % 128 != 0 || d.f % 128 != 0))) return false;
+  const long long kb = fp8 ? 128 : 64, lim = (1ll << 31) / moe_api::num_sms();
+  const long long t1 = d.E * ((d.f + 127ll) / 128) * (d.h / kb);
+  const long long t2 = d.E * ((d.h + 255ll) / 256) * (d.f / kb);
+  return t1 < lim && t2 < lim && static_cast<long long>(d.E) * (d.h > d.f ? d.h : d.f) * 2 < (1ll << 31);
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool ptr_ok(const void* p) { return p && aligned(p, 16); }
+
+template <bool F8>
+cudaError_t launch(const Params& p, const Maps& m, int smem, int blocks, cudaStream_t s) {
+  const void* kern = reinterpret_cast<const void*>(decode_kernel<F8>);
+  const cudaError_t e = set_smem_once(kern, kSmemMax);
+  if (e != cudaSuccess) return e;
+  void* args[2] = {const_cast<Params*>(&p), const_cast<Maps*>(&m)};
+  const cudaError_t l = cudaLaunchCooperativeKernel(kern, dim3(blocks), dim3(kThreads), args,
+                                                    static_cast<size_t>(smem), s);
+  return l == cudaSuccess ? launched() : l;
+}
 
 moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, const float* b,
                   const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2, const void* qw,
@@ -187,66 +981,65 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (empty) return MOE_OK;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const int sms = moe_api::num_sms();
-  int32_t* idx = topk_idx ? topk_idx : reinterpret_cast<int32_t*>(w + L.idx);
-  float* g = gates ? gates : reinterpret_cast<float*>(w + L.gates);
-  Args a = {};
-  a.T = d.T;
-  a.h = d.h;
-  a.f = d.f;
-  a.E = d.E;
-  a.k = d.k;
-  a.capacity = d.capacity > 0 ? d.capacity : INT_MAX;
-  a.idx = idx;
-  a.gates = g;
-  a.x = x;
-  a.W1 = W1;
-  a.W3 = W3;
-  a.W2 = W2;
-  a.H = reinterpret_cast<uint16_t*>(w + L.H);
-  a.O = reinterpret_cast<float*>(w + L.O);
-  a.y = y;
-  auto run = [&](cudaError_t e, const char* name) {
-    return e == cudaSuccess && moe_api::note(stream, name);
-  };
-  if (!run(launch_router(x, Wg, d.has_bias ? b : nullptr, d.T, d.h, d.E, d.k, idx, g,
-                         reinterpret_cast<float*>(w + L.logits), sms, stream),
-           "router_topk"))
-    return MOE_ERR_CUDA;
-  const dim3 g1((d.f + 127) / 128, d.E), g2((d.h + 127) / 128, d.E), g3((d.h + 127) / 128, d.T);
+  const int blocks = moe_api::num_sms();
+  const Plan plan = plan_of(d, blocks);
+  Params p = {};
+  p.T = d.T;
+  p.h = d.h;
+  p.f = d.f;
+  p.E = d.E;
+  p.k = d.k;
+  p.capacity = d.capacity > 0 ? d.capacity : INT_MAX;
+  p.n1 = plan.n1;
+  p.stages = plan.stages;
+  p.tok_group = plan.tok_group;
+  p.groups = plan.groups;
+  p.slices = plan.slices;
+  p.slice_h = plan.slice_h;
+  p.x = x;
+  p.Wg = Wg;
+  p.b = d.has_bias ? b : nullptr;
+  p.idx = topk_idx ? topk_idx : reinterpret_cast<int32_t*>(w + L.idx);
+  p.gates = gates ? gates : reinterpret_cast<float*>(w + L.gates);
+  p.logits = reinterpret_cast<float*>(w + L.logits);
+  p.H = reinterpret_cast<uint16_t*>(w + L.H);
+  p.O = reinterpret_cast<float*>(w + L.O);
+  p.part1 = reinterpret_cast<float*>(w + L.part1);
+  p.part2 = reinterpret_cast<float*>(w + L.part2);
+  p.tick1 = reinterpret_cast<unsigned*>(w + L.tick1);
+  p.y = y;
+  p.status = reinterpret_cast<int*>(ws);
+  Maps m;
+  memset(&m, 0, sizeof(m));
+  const uint64_t R = static_cast<uint64_t>(d.T) * d.k, E = d.E, h = d.h, f = d.f;
+  cudaError_t e;
   if (fp8) {
     auto view = [&](const char* name) {
       return moe_fp8_weight_view(dims, const_cast<void*>(qw), name);
     };
-    uint8_t* xq = w + L.xq;
-    uint8_t* Hq = w + L.Hq;
-    float* sx = reinterpret_cast<float*>(w + L.sx);
-    float* sh = reinterpret_cast<float*>(w + L.sh);
-    a.W13q = static_cast<const uint8_t*>(view("W13q"));
-    a.W2q = static_cast<const uint8_t*>(view("W2q"));
-    a.s1 = static_cast<const float*>(view("s1"));
-    a.s3 = static_cast<const float*>(view("s3"));
-    a.s2 = static_cast<const float*>(view("s2"));
-    a.xq = xq;
-    a.sx = sx;
-    a.Hq = Hq;
-    a.sh = sh;
-    if (!run(launch_quant_rows(x, nullptr, 1, d.T, d.T, d.h, xq, sx, sms, stream), "quant_x"))
+    p.xq = w + L.xq;
+    p.sx = reinterpret_cast<float*>(w + L.sx);
+    p.Hq = w + L.Hq;
+    p.amax = reinterpret_cast<unsigned*>(w + L.amax);
+    p.s1 = static_cast<const float*>(view("s1"));
+    p.s3 = static_cast<const float*>(view("s3"));
+    p.s2 = static_cast<const float*>(view("s2"));
+    if (!make_map_kmajor(&m.x, p.xq, h, d.T, plan.n1, true) ||
+        !make_map_codes(&m.w1, view("W13q"), h, 2 * f, E, 256) ||
+        !make_map_kmajor(&m.h, p.Hq, f, R, 16, true) ||
+        !make_map_codes(&m.w2, view("W2q"), f, h, E, 256))
       return MOE_ERR_CUDA;
-    decode_fc1_kernel<true><<<g1, 128, 0, stream>>>(a);
-    if (!run(launched(), "decode_fc1")) return MOE_ERR_CUDA;
-    const long long R = static_cast<long long>(d.T) * d.k;
-    if (!run(launch_quant_rows(a.H, nullptr, 1, R, R, d.f, Hq, sh, sms, stream), "quant_h"))
-      return MOE_ERR_CUDA;
-    decode_fc2_kernel<true><<<g2, 128, 0, stream>>>(a);
+    m.w3 = m.w1;
+    e = launch<true>(p, m, plan.smem, blocks, stream);
   } else {
-    decode_fc1_kernel<false><<<g1, 128, 0, stream>>>(a);
-    if (!run(launched(), "decode_fc1")) return MOE_ERR_CUDA;
-    decode_fc2_kernel<false><<<g2, 128, 0, stream>>>(a);
+    if (!make_map_kmajor(&m.x, x, h, d.T, plan.n1, false) || !make_map_columns(&m.w1, W1, f, E * h, 2) ||
+        !make_map_columns(&m.w3, W3, f, E * h, 2) || !make_map_kmajor(&m.h, p.H, f, R, 16, false) ||
+        !make_map_columns(&m.w2, W2, h, E * f, 4))
+      return MOE_ERR_CUDA;
+    e = launch<false>(p, m, plan.smem, blocks, stream);
   }
-  if (!run(launched(), "decode_fc2")) return MOE_ERR_CUDA;
-  decode_combine_kernel<<<g3, 128, 0, stream>>>(a);
-  return run(launched(), "decode_combine") ? MOE_OK : MOE_ERR_CUDA;
+  if (e != cudaSuccess || !moe_api::note(stream, "layer_decode")) return MOE_ERR_CUDA;
+  return MOE_OK;
 }
 
 }  // namespace

@@ -1540,6 +1540,29 @@ uint32_t mn_chunks(int epi, int num_b) { return pair_for(epi) ? 2 : BN / num_b /
 
 }  // namespace
 
+bool make_map_kmajor(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
+                     uint32_t box_rows, bool bytes) {
+  return make_map(m, base, inner, rows, bytes ? 2 * BK : BK, box_rows, bytes);
+}
+
+bool make_map_columns(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
+                      uint32_t chunks) {
+  return make_map_mn(m, base, inner, rows, BK, chunks);
+}
+
+bool make_map_codes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
+                    uint64_t experts, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, rows, experts};
+  cuuint64_t strides[2] = {inner, inner * rows};
+  cuuint32_t box[3] = {2 * BK, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t gemm_fc1_fwd(const GemmProblem& g, const void* x_perm, const void* W1,
                          const void* W3, void* A, void* B, void* H, cudaStream_t s) {
   Maps m;

@@ -6,6 +6,7 @@
 // the device-resident `offsets` array, so no count ever travels to the host.
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace moe {
@@ -72,6 +73,19 @@ cudaError_t gemm_fc2_wgrad(const GemmProblem& p, const void* H, const void* dO, 
 // dW1[e] = X_e^T dA_e, dW3[e] = X_e^T dB_e.  fp32 [E, h, f].
 cudaError_t gemm_fc1_wgrad(const GemmProblem& p, const void* x_perm, const void* dA,
                            const void* dB, float* dW1, float* dW3, cudaStream_t s);
+
+// TMA maps of tcgen05 operands, 128-byte swizzle, zero fill out of range.
+//   K-major rows: [rows, inner] bf16 (or bytes), boxes of 128 bytes x box_rows.
+bool make_map_kmajor(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
+                     uint32_t box_rows, bool bytes);
+//   MN-major columns: [rows, inner] bf16 as {64, rows, inner / 64}, boxes of
+//   `chunks` 64-column chunks x 64 rows.
+bool make_map_columns(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
+                      uint32_t chunks);
+//   K-major codes of several experts: [experts, rows, inner] bytes, boxes of
+//   128 bytes x box_rows that do not run into the next expert.
+bool make_map_codes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
+                    uint64_t experts, uint32_t box_rows);
 
 // Kernel names, in launch order of a layer, for the measurement hook.
 extern const char* const kGemmNames[6];
