@@ -398,8 +398,10 @@ moe_status moe_layer_decode(const moe_dims* dims, const moe_bf16* x,
 /* moe_layer_decode on e4m3 weights: `qw` as moe_quantize_weights_fp8 writes it
  * (256-byte aligned).  The arithmetic of moe_layer_fwd_fp8: x quantised with
  * one scale for each token, H (from its bf16 value) with one for each row, the
- * products of codes summed in fp32 and multiplied by the two scales.  h and f
- * multiples of 128 (MOE_ERR_UNSUPPORTED otherwise).
+ * products of codes summed in fp32 and multiplied by the two scales.  The
+ * activations' scales are amax times the fp32 reciprocal of 448 (the layer
+ * divides: an ulp apart at most, which shows where a value lies exactly
+ * between two codes).  h and f multiples of 128 (MOE_ERR_UNSUPPORTED otherwise).
  * Workspace: moe_workspace_bytes(dims, MOE_OP_LAYER_DECODE_FP8). */
 moe_status moe_layer_decode_fp8(const moe_dims* dims, const moe_bf16* x,
                                 const float* Wg, const float* b,

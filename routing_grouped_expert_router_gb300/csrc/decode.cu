@@ -71,7 +71,7 @@ struct Params {
   const float *Wg, *b;
   int32_t* idx;
   float* gates;
-  float* logits;            // [slices, T, E]
+  float* logits;            // [groups, slices, tok_group, E]
   uint16_t* H;              // [T*k, f]
   float* O;                 // [T*k, h]
   float* part1;             // [2 * blocks][2, T, 128]: FC1 sums of shared tiles
@@ -91,7 +91,7 @@ struct Maps {
 };
 
 struct alignas(16) Ctrl {
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], hready, drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], hready, drain, rbar;
   uint32_t tmem_base;
   int abort, flag, nact;
   int off[kMaxE + 1];       // first row of each expert
@@ -174,9 +174,11 @@ __device__ __forceinline__ void tmem_wait8(uint32_t (&a)[8], uint32_t (&b)[8]) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// The scale and codes of a quantised row, as fp8.cu makes them.
+// The scale and codes of a quantised row.  The scale is amax times the fp32
+// reciprocal of 448, within an ulp of fp8.cu's quotient; where a value lies
+// exactly between two codes, that ulp can choose the other one.
 __device__ __forceinline__ float scale_of(float amax) {
-  return amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+  return amax > 0.f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
 }
 __device__ __forceinline__ uint32_t quant2(uint32_t w, float s) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
@@ -194,36 +196,26 @@ __device__ __forceinline__ float amax8(const uint4& w) {
 }
 
 // ------------------------------------------------------------------ route
+// A logit as an integer of the same order (-0 as 0, NaN as minus infinity).
+__device__ __forceinline__ unsigned order_of(float v) {
+  const unsigned u = __float_as_uint(isnan(v) ? -INFINITY : v + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
 // Top-k of one token by a warp: lane l holds the logits of experts l and
-// l + 32.  k rounds of an arg-max (the larger logit, the lower id on ties; NaN
-// counts as the smallest), then the softmax over the chosen.
+// l + 32.  k rounds of a warp maximum (ties to the lower id), then the softmax
+// over the chosen.
 __device__ void select_topk(const Params& p, int t, float l0, float l1, int lane) {
-  bool live0 = lane < p.E, live1 = lane + 32 < p.E;
+  // 0 is below every logit: an expert that is taken or does not exist
+  unsigned o0 = lane < p.E ? order_of(l0) : 0u, o1 = lane + 32 < p.E ? order_of(l1) : 0u;
   float top = 0.f, mine = 0.f, sum = 0.f;
   int chosen = 0;
   for (int j = 0; j < p.k; ++j) {
-    float bv = -INFINITY;
-    int be = 1 << 30;
-    const float v0 = isnan(l0) ? -INFINITY : l0, v1 = isnan(l1) ? -INFINITY : l1;
-    if (live0) {
-      bv = v0;
-      be = lane;
-    }
-    if (live1 && (be > kMaxE || v1 > bv)) {
-      bv = v1;
-      be = lane + 32;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(kFull, bv, o);
-      const int oe = __shfl_xor_sync(kFull, be, o);
-      if (oe < kMaxE && (be > kMaxE || ov > bv || (ov == bv && oe < be))) {
-        bv = ov;
-        be = oe;
-      }
-    }
-    if (be == lane) live0 = false;
-    if (be == lane + 32) live1 = false;
+    const unsigned best = __reduce_max_sync(kFull, max(o0, o1));
+    const unsigned m0 = __ballot_sync(kFull, o0 == best), m1 = __ballot_sync(kFull, o1 == best);
+    const int be = m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
+    if (be == lane) o0 = 0;
+    if (be == lane + 32) o1 = 0;
     const float lv = __shfl_sync(kFull, be < 32 ? l0 : l1, be & 31);
     if (j == 0) top = lv;
     const float ev = expf(lv - top);
@@ -239,53 +231,84 @@ __device__ void select_topk(const Params& p, int t, float l0, float l1, int lane
   }
 }
 
-// A router unit is a group of tokens x a slice of h: fp32 partial logits.  The
-// block that finishes a group's last slice adds the slices in order and chooses
-// the experts of its tokens, one warp for each.
-__device__ void route(const Params& p, Ctrl& c, float* smem) {
+// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// A router unit is a group of tokens x a slice of h: fp32 partial logits.  All
+// that a unit reads is asked for at once (the slice's rows of Wg are one
+// contiguous piece); what this phase costs is latency, and loads in the loop's
+// order took 14 us for one token and 25 us for 32 where this takes 4 to 5.
+// The block that finishes a group's last slice adds the slices in order and
+// chooses the experts of its tokens, one warp for each.
+__device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned* words = reinterpret_cast<unsigned*>(p.status);
+  const int parts = kThreads / p.E;
+  const int e = tid % p.E, part = tid / p.E;
+  float* wg = reinterpret_cast<float*>(smem);                          // [nj][E]
+  uint8_t* xs = smem + static_cast<size_t>(p.slice_h) * p.E * 4;       // [8][nj] bf16
+  float* red = reinterpret_cast<float*>(xs + p.slice_h * kGroupTok * 2);  // [8][kThreads]
+  float* logit = red + kThreads * kGroupTok;                           // [8][kMaxE]
+  const uint32_t bar = smem_u32(&c.rbar);
+  uint32_t ph = 0;
   for (int unit = blockIdx.x; unit < p.groups * p.slices; unit += gridDim.x) {
     const int g = unit / p.slices, s = unit % p.slices;
     const int t0 = g * p.tok_group, nt = min(p.tok_group, p.T - t0);
     const int j0 = s * p.slice_h, nj = min(p.slice_h, p.h - j0);
-    float* xs = smem;                          // [nj][8]
-    float* red = smem + p.slice_h * kGroupTok;  // [kThreads][8]
+    fence_proxy_async_all();
     __syncthreads();
-    for (int i = tid; i < nj * kGroupTok; i += kThreads) {
-      const int t = i / nj, j = i - t * nj;
-      xs[j * kGroupTok + t] =
-          t < nt ? bf16_lo(p.x[static_cast<size_t>(t0 + t) * p.h + j0 + j]) : 0.f;
+    if (tid == 0) {
+      mbar_expect_tx(bar, nj * (p.E * 4 + nt * 2));
+      bulk_load(smem_u32(wg), p.Wg + static_cast<size_t>(j0) * p.E, nj * p.E * 4, bar);
+      for (int t = 0; t < nt; ++t)
+        bulk_load(smem_u32(xs) + t * nj * 2, p.x + static_cast<size_t>(t0 + t) * p.h + j0, nj * 2,
+                  bar);
     }
-    __syncthreads();
-    const int parts = kThreads / p.E;
-    const int e = tid % p.E, part = tid / p.E;
+    if (!mbar_wait(bar, ph, p.status, kTimeoutCode)) c.abort = 1;
+    ph ^= 1;
     float acc[kGroupTok] = {};
-    if (part < parts) {
-#pragma unroll 4
-      for (int j = part; j < nj; j += parts) {
-        const float w = __ldg(p.Wg + static_cast<size_t>(j0 + j) * p.E + e);
-        const float4 a = *reinterpret_cast<const float4*>(xs + j * kGroupTok);
-        const float4 b = *reinterpret_cast<const float4*>(xs + j * kGroupTok + 4);
-        acc[0] = fmaf(a.x, w, acc[0]);
-        acc[1] = fmaf(a.y, w, acc[1]);
-        acc[2] = fmaf(a.z, w, acc[2]);
-        acc[3] = fmaf(a.w, w, acc[3]);
-        acc[4] = fmaf(b.x, w, acc[4]);
-        acc[5] = fmaf(b.y, w, acc[5]);
-        acc[6] = fmaf(b.z, w, acc[6]);
-        acc[7] = fmaf(b.w, w, acc[7]);
-      }
-    }
+    if (part < parts)
+      for (int j = part * 8; j < nj; j += parts * 8) {
+        float w[8];
 #pragma unroll
-    for (int t = 0; t < kGroupTok; ++t) red[t * kThreads + tid] = acc[t];
-    __syncthreads();
-    for (int i = tid; i < nt * p.E; i += kThreads) {
-      const int t = i / p.E, ee = i - t * p.E;
-      float v = 0.f;
-      for (int q = 0; q < parts; ++q) v += red[t * kThreads + q * p.E + ee];
-      p.logits[(static_cast<size_t>(s) * p.T + t0 + t) * p.E + ee] = v;
-    }
+        for (int i = 0; i < 8; ++i) w[i] = wg[(j + i) * p.E + e];
+#pragma unroll
+        for (int t = 0; t < kGroupTok; ++t) {
+          if (t >= nt) break;
+          const uint4 q = *reinterpret_cast<const uint4*>(xs + (t * nj + j) * 2);
+          acc[t] = fmaf(bf16_lo(q.x), w[0], acc[t]);
+          acc[t] = fmaf(bf16_hi(q.x), w[1], acc[t]);
+          acc[t] = fmaf(bf16_lo(q.y), w[2], acc[t]);
+          acc[t] = fmaf(bf16_hi(q.y), w[3], acc[t]);
+          acc[t] = fmaf(bf16_lo(q.z), w[4], acc[t]);
+          acc[t] = fmaf(bf16_hi(q.z), w[5], acc[t]);
+          acc[t] = fmaf(bf16_lo(q.w), w[6], acc[t]);
+          acc[t] = fmaf(bf16_hi(q.w), w[7], acc[t]);
+        }
+      }
+    auto add_parts = [&](float* out, int ld, const float* bias) {
+#pragma unroll
+      for (int t = 0; t < kGroupTok; ++t)
+        if (t < nt) red[t * kThreads + tid] = acc[t];
+      __syncthreads();
+      for (int i = tid; i < nt * p.E; i += kThreads) {
+        const int t = i / p.E, ee = i - t * p.E;
+        float v = 0.f;
+#pragma unroll 4
+        for (int q = 0; q < parts; ++q) v += red[t * kThreads + q * p.E + ee];
+        out[t * ld + ee] = bias ? v + __ldg(bias + ee) : v;
+      }
+    };
+    // [group][slice][token][expert]
+    float* mine = p.logits + static_cast<size_t>(unit) * p.tok_group * p.E;
+    add_parts(mine, p.E, nullptr);
     __threadfence();
     __syncthreads();
     if (tid == 0) {
@@ -296,28 +319,19 @@ __device__ void route(const Params& p, Ctrl& c, float* smem) {
     __syncthreads();
     if (!c.flag) continue;
     __threadfence();
-    // the slices' sums, `parts` interleaved chains for each logit
-    float* logit = red + kThreads * kGroupTok;  // [8][kMaxE]
+    const float* all = p.logits + static_cast<size_t>(g) * p.slices * p.tok_group * p.E;
+    const int n = p.slices * p.tok_group * p.E;
+#pragma unroll 8
+    for (int i = tid; i < n; i += kThreads) wg[i] = __ldcg(all + i);
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < kGroupTok; ++t) acc[t] = 0.f;
-    if (part < parts) {
-      const float* src = p.logits + static_cast<size_t>(t0) * p.E + e;
-#pragma unroll 4
+    if (part < parts)
       for (int q = part; q < p.slices; q += parts)
 #pragma unroll
         for (int t = 0; t < kGroupTok; ++t)
-          if (t < nt) acc[t] += __ldcg(src + (static_cast<size_t>(q) * p.T + t) * p.E);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < kGroupTok; ++t) red[t * kThreads + tid] = acc[t];
-    __syncthreads();
-    for (int i = tid; i < nt * p.E; i += kThreads) {
-      const int t = i / p.E, ee = i - t * p.E;
-      float v = 0.f;
-      for (int q = 0; q < parts; ++q) v += red[t * kThreads + q * p.E + ee];
-      logit[t * kMaxE + ee] = p.b ? v + __ldg(p.b + ee) : v;
-    }
+          if (t < nt) acc[t] += wg[(q * p.tok_group + t) * p.E + e];
+    add_parts(logit, kMaxE, p.b);
     __syncthreads();
     if (warp < nt)
       select_topk(p, t0 + warp, lane < p.E ? logit[warp * kMaxE + lane] : 0.f,
@@ -464,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&c.hready), 1);
     mbar_init(smem_u32(&c.drain), 1);
+    mbar_init(smem_u32(&c.rbar), 1);
     c.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.x);
@@ -483,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     quant_x(p, reinterpret_cast<float*>(smem));
     for (int i = blockIdx.x * kThreads + tid; i < p.T * p.k; i += G * kThreads) p.amax[i] = 0;
   }
-  route(p, c, reinterpret_cast<float*>(smem));
+  route(p, c, smem);
   fence_proxy_async_all();  // xq for TMA; and the ring's memory, used by route above
   __syncthreads();
   if (tid == 0 && !grid_barrier(words + kBarWord, G, p.status)) c.abort = 1;
@@ -748,14 +763,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c.flag) {
             __threadfence();
             const float* first = p.part1 + (2 * c0 + 1) * slot + r;
-            for (int i = 0; i < n; ++i) {
-              float va = __ldcg(first + i * 256), vb = __ldcg(first + i * 256 + 128);
-              for (unsigned o = c0 + 1; o <= c1; ++o) {
-                const float* src = p.part1 + 2 * o * slot + i * 256 + r;
-                va += __ldcg(src);
-                vb += __ldcg(src + 128);
+            for (int i0 = 0; i0 < n; i0 += 4) {  // 4 rows' loads in flight
+              float va[4], vb[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int o = min(i0 + i, n - 1) * 256;
+                va[i] = __ldcg(first + o);
+                vb[i] = __ldcg(first + o + 128);
               }
-              store_h<F8>(p, c, row0 + i, e, col, va, vb, w1, w3, lane);
+#pragma unroll 4
+              for (unsigned blk = c0 + 1; blk <= c1; ++blk) {
+                const float* src = p.part1 + 2 * blk * slot + r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int o = min(i0 + i, n - 1) * 256;
+                  va[i] += __ldcg(src + o);
+                  vb[i] += __ldcg(src + o + 128);
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (i0 + i < n) store_h<F8>(p, c, row0 + i0 + i, e, col, va[i], vb[i], w1, w3, lane);
             }
           }
           epi_sync();  // c.flag is free again
@@ -828,27 +856,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n4 = p.h / 4;
       for (int i = cta * kThreads + tid; i < p.T * n4; i += G * kThreads) {
         const int t = i / n4, col = (i - t * n4) * 4;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < p.k; ++j) {
-          const int a = t * p.k + j, row = c.pos[a];
-          if (row < 0) continue;
-          const int e = c.exp[a];
-          const unsigned q = (c.act_of[e] * nt2 + col / 256) * ks2;
-          float4 v = __ldcg(reinterpret_cast<const float4*>(p.O + static_cast<size_t>(row) * p.h + col));
-          const unsigned c1 = cut2.block_of(q + ks2 - 1);
-          for (unsigned o = cut2.block_of(q) + 1; o <= c1; ++o) {
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(
-                p.part2 + (static_cast<size_t>(o) * p.T + row - c.off[e]) * 256 + col % 256));
-            v.x += u.x;
-            v.y += u.y;
-            v.z += u.z;
-            v.w += u.w;
+        const unsigned tile = col / 256;
+        // the k slots' loads together: this, too, is latency
+        float4 v[8];
+        unsigned blk[8], end[8];
+        int row[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int a = t * p.k + j;
+          row[j] = j < p.k ? c.pos[a] : -1;
+          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          blk[j] = end[j] = 0;
+          if (row[j] >= 0) {
+            v[j] = __ldcg(
+                reinterpret_cast<const float4*>(p.O + static_cast<size_t>(row[j]) * p.h + col));
+            const int e = c.exp[a];
+            const unsigned q = (c.act_of[e] * nt2 + tile) * ks2;
+            blk[j] = cut2.block_of(q);
+            end[j] = cut2.block_of(q + ks2 - 1);
+            row[j] -= c.off[e];
           }
-          const float g = c.gate[a];
-          sum.x = fmaf(g, v.x, sum.x);
-          sum.y = fmaf(g, v.y, sum.y);
-          sum.z = fmaf(g, v.z, sum.z);
-          sum.w = fmaf(g, v.w, sum.w);
+        }
+        for (bool more = true; more;) {
+          more = false;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (blk[j] == end[j]) continue;
+            ++blk[j];
+            more = true;
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(
+                p.part2 + (static_cast<size_t>(blk[j]) * p.T + row[j]) * 256 + col % 256));
+            v[j].x += u.x;
+            v[j].y += u.y;
+            v[j].z += u.z;
+            v[j].w += u.w;
+          }
+        }
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (row[j] < 0) continue;
+          const float g = c.gate[t * p.k + j];
+          sum.x = fmaf(g, v[j].x, sum.x);
+          sum.y = fmaf(g, v[j].y, sum.y);
+          sum.z = fmaf(g, v[j].z, sum.z);
+          sum.w = fmaf(g, v[j].w, sum.w);
         }
         const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y);
         const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z, sum.w);
@@ -884,6 +936,7 @@ struct Layout {
 struct Plan {
   int n1, stages, smem;
   int tok_group, groups, slices, slice_h;
+  bool ok;
 };
 
 // Blocks = SMs.  Router units: token groups x slices of h, about one for each
@@ -902,10 +955,13 @@ Plan plan_of(const moe_dims& d, int blocks) {
   if (n < 1) n = 1;
   p.slice_h = ((d.h + n - 1) / n + 7) / 8 * 8;
   if (p.slice_h < 32) p.slice_h = 32;  // a few long slices add up sooner than many short ones
-  // x of a slice as fp32, the threads' sums and the logits fit the ring
-  const int most = (p.stages * stage - (kThreads + kMaxE) * kGroupTok * 4) / (kGroupTok * 4) / 8 * 8;
+  // a slice of Wg and x, the threads' sums and the logits fit the ring
+  const int room = p.stages * stage - (kThreads + kMaxE) * kGroupTok * 4;
+  const int most = room / (d.E * 4 + kGroupTok * 2) / 8 * 8;
   if (p.slice_h > most) p.slice_h = most;
   p.slices = (d.h + p.slice_h - 1) / p.slice_h;
+  // so do a group's partial logits of all slices, where h is not enormous
+  p.ok = p.slices * p.tok_group * d.E * 4 <= room;
   return p;
 }
 
@@ -920,7 +976,7 @@ Layout layout(const moe_dims& d, bool fp8) {
     return o;
   };
   Layout L = {};
-  L.logits = take(plan.slices * T * d.E * 4);
+  L.logits = take(static_cast<size_t>(plan.groups) * plan.slices * plan.tok_group * d.E * 4);
   L.idx = take(R * 4);
   L.gates = take(R * 4);
   L.H = take(R * f * 2);
@@ -943,6 +999,7 @@ Layout layout(const moe_dims& d, bool fp8) {
 bool supported(const moe_dims& d, bool fp8) {
   if (d.T > kDecodeMaxT || d.sar != 0 || (fp8 && (d.h % 128 != 0 || d.f % 128 != 0))) return false;
   const long long kb = fp8 ? 128 : 64, lim = (1ll << 31) / moe_api::num_sms();
+  if (d.T > 0 && !plan_of(d, moe_api::num_sms()).ok) return false;
   const long long t1 = d.E * ((d.f + 127ll) / 128) * (d.h / kb);
   const long long t2 = d.E * ((d.h + 255ll) / 256) * (d.f / kb);
   return t1 < lim && t2 < lim && static_cast<long long>(d.E) * (d.h > d.f ? d.h : d.f) * 2 < (1ll << 31);

@@ -118,6 +118,12 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[N * (kMaxT
     for (int i = 0; i < N; ++i) v[i] += s[w * N + i];
 }
 
+// 1 / rms of a row from its sum of squares, correctly rounded: its error would
+// shift a whole row, and one for each row costs nothing.
+__device__ __forceinline__ float inv_rms(float ss, const Args& a) {
+  return __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.h)) + a.eps);
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args a) {
   __shared__ float red[2][kMaxThreads / 32];
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss[0] = fmaf(z[i][j], z[i][j], ss[0]);
         block_sum<1>(ss, red, slot);
-        ry = rsqrtf(fmaf(ss[0], a.inv_h, a.eps));
+        ry = inv_rms(ss[0], a);
       }
       float s = a.beta;
       if (a.gate_kind == MOE_GATE_TOKEN) s *= __ldg(a.gate + t);
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
     block_sum<1>(ss, red, slot);
-    const float rv = rsqrtf(fmaf(ss[0], a.inv_h, a.eps));
+    const float rv = inv_rms(ss[0], a);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -246,9 +252,9 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args 
         for (int j = 0; j < 8; ++j) s3[2] = fmaf(n[i][j], n[i][j], s3[2]);
     }
     block_sum<3>(s3, red3, slot3);
-    const float rv = rsqrtf(fmaf(s3[0], a.inv_h, a.eps));
+    const float rv = inv_rms(s3[0], a);
     const float k1 = s3[1] * a.inv_h * rv * rv * rv;
-    const float ry = a.w_post ? rsqrtf(fmaf(s3[2], a.inv_h, a.eps)) : 1.f;
+    const float ry = a.w_post ? inv_rms(s3[2], a) : 1.f;
     const float gt = a.y && a.gate_kind == MOE_GATE_TOKEN ? __ldg(a.gate + t) : 1.f;
     float s1[1] = {0.f};
 #pragma unroll

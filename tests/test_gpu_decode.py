@@ -59,9 +59,11 @@ def kept(idx, E, capacity):
     return keep
 
 
-def quant_rows(v):
+def quant_rows(v, weights=False):
+    """Activations: scale amax * fp32(1 / 448); weights (as moe_quantize_weights_fp8 writes them): amax / 448."""
     v = v.float()
-    s = v.abs().amax(-1, keepdim=True) / 448.0
+    s = v.abs().amax(-1, keepdim=True)
+    s = s / 448.0 if weights else s * (torch.ones(()) / 448.0)
     s = torch.where(s > 0, s, torch.ones_like(s))
     return (v / s).to(torch.float8_e4m3fn).double() * s.double()
 
@@ -80,7 +82,7 @@ def layer64(inp, k, capacity=0, fp8=False):
         xe, W1, W3, W2 = x[t].double(), inp["W1"][e].double(), inp["W3"][e].double(), inp["W2"][e].double()
         if fp8:
             xe = quant_rows(x[t])
-            W1, W3, W2 = (quant_rows(inp[n][e].t().contiguous()).t() for n in ("W1", "W3", "W2"))
+            W1, W3, W2 = (quant_rows(inp[n][e].t().contiguous(), weights=True).t() for n in ("W1", "W3", "W2"))
         a, b = xe @ W1, xe @ W3
         h = a * torch.sigmoid(a) * b
         if fp8:
