@@ -11,22 +11,23 @@
 // weight, where a GB300 can do 280 in the time its 2 bytes take to arrive).  So
 // the kernel is built as a stream of weights:
 //   * one persistent cooperative kernel, one block for each SM, four phases
-//     (route, FC1, FC2, combine) with a grid barrier between them;
+//     (route, FC1, FC2, combine);
 //   * the products are taken transposed, weights as the 128-row operand A of
 //     tcgen05.mma and the tokens as its N columns (16 to 128), so that the
 //     smallest batch wastes columns of an idle tensor core, not bytes;
 //   * 32 KiB weight stages (two 128-column tiles x 64 rows of bf16, 128 of
 //     e4m3) flow through a ring of up to 6 stages that TMA fills, about 200 KiB
 //     in flight on each SM; nothing but the TMA and MMA units touches them;
-//   * each phase's k-steps, over all its tiles in a row, are cut into equal
-//     ranges, one for each block, whatever the tiles' borders: the number of
-//     experts hit decides the tiles, and a tile for each block would leave up
-//     to half of the SMs idle in the last wave.  A tile that two or more blocks
-//     share is joined in block order (FC1: by the block that comes last, since
-//     SwiGLU needs the whole sums; FC2: when y is combined), so the result does
-//     not depend on timing;
-//   * the weights of FC2's first stages are loaded before the barrier that
-//     makes H whole.
+//   * each phase's k-steps, over all its tiles in a row, are cut into pieces
+//     whatever the tiles' borders: the number of experts hit decides the tiles,
+//     and a tile for each block would leave up to half of the SMs idle in the
+//     last wave.  Every block starts on a piece of its own; in long phases the
+//     last sixth is cut smaller and taken by whoever is free (see Cut).  A tile
+//     that two or more pieces share is joined in the pieces' order, by the whole
+//     grid: FC1's after a barrier, since SwiGLU needs the whole sums, FC2's when
+//     y is combined.  So the result does not depend on timing;
+//   * FC2's first stages of weights are loaded before the barriers that make H
+//     whole (bringing more of them into L2 meanwhile gained nothing).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -46,9 +47,13 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+// Warp 0 feeds the ring, warp 1 issues the MMAs, warps 4 to 7 are the epilogue;
+// the others help where a phase's work is spread over all threads.
+constexpr int kThreads = 512;
+constexpr int kHelpers = kThreads - 64;
 constexpr int kWBytes = 32768;     // weights of a stage
 constexpr int kMaxStages = 6;
+constexpr int kQueue = 4;          // pieces between the producer and the others
 constexpr int kMaxRows = kDecodeMaxT * 8;  // placed assignments
 constexpr int kMaxE = 64;
 constexpr int kGroupTok = 8;       // tokens of a router work unit at most
@@ -74,9 +79,9 @@ struct Params {
   float* logits;            // [groups, slices, tok_group, E]
   uint16_t* H;              // [T*k, f]
   float* O;                 // [T*k, h]
-  float* part1;             // [2 * blocks][2, T, 128]: FC1 sums of shared tiles
-  float* part2;             // [blocks][T, 256]: FC2 sums of tiles begun elsewhere
-  unsigned* tick1;          // [blocks]
+  float* part;              // FC1 [2 * pieces][T, 2, 128]: sums of shared tiles;
+                            // FC2 [pieces][T, 256]: of tiles begun in another piece
+  unsigned* claim;          // [2]: pieces taken of FC1's and FC2's later rounds
   uint16_t* y;
   // e4m3
   uint8_t *xq, *Hq;
@@ -92,8 +97,10 @@ struct Maps {
 
 struct alignas(16) Ctrl {
   uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], hready, drain, rbar;
+  uint64_t qfull[kQueue], qempty[kQueue];
   uint32_t tmem_base;
-  int abort, flag, nact;
+  int abort, flag, nact, most;  // most: rows of the busiest expert
+  int piece[kQueue];        // the block's pieces in order, -1 at a phase's end
   int off[kMaxE + 1];       // first row of each expert
   int act[kMaxE];           // experts with rows
   int act_of[kMaxE];        // its inverse
@@ -105,18 +112,80 @@ struct alignas(16) Ctrl {
   uint16_t hist[kMaxRows / 32][kMaxE];
 };
 
-// One phase's k-steps [0, total) cut into blocks' ranges.
+// One phase's k-steps [0, total) cut into pieces, in up to kRounds rounds of one
+// piece for each block.  Piece b of round 0 is block b's; those of the later,
+// ever smaller rounds go to whoever comes first.  The SMs do not stream equally
+// fast: on GB300 whole groups of 16 to 20 were 10 to 17% behind the others,
+// which ones changing with the weights' addresses (16 tokens, 11 of 32 experts:
+// 345 us for the fastest SM's share of FC1, 389 us for the slowest's).  Below
+// kRoundsFrom k-steps for each block the phase is too short to gain by it.
+constexpr int kRounds = 4;
+constexpr unsigned kRoundsFrom = 96;
 struct Cut {
-  unsigned total, blocks;
-  __device__ unsigned start(unsigned c) const { return c * total / blocks; }
-  __device__ unsigned block_of(unsigned q) const { return ((q + 1) * blocks - 1) / total; }
+  unsigned total, blocks, rounds;
+  unsigned at[kRounds + 1];  // rounds' borders
+  // Later rounds of 8, 5 and 3% of a block's share, but of no fewer than `least`
+  // k-steps a piece: every piece of a tile is one more sum to add.
+  __device__ Cut(unsigned n, unsigned grid, unsigned tile_steps) : total(n) {
+    rounds = n >= kRoundsFrom * grid ? kRounds : 1;
+    blocks = n < grid ? n : grid;
+    const unsigned share = n / grid, least = max(8u, tile_steps / 16u);
+    at[0] = 0;
+    at[4] = n;
+    at[3] = rounds == 1 ? n : n - grid * max(least, share * 3u / 100u);
+    at[2] = rounds == 1 ? n : at[3] - grid * max(least, share * 5u / 100u);
+    at[1] = rounds == 1 ? n : at[2] - grid * max(least, share * 8u / 100u);
+  }
+  __device__ unsigned start(unsigned piece) const {
+    const unsigned r = piece / blocks, j = piece - r * blocks;
+    unsigned lo = at[0], hi = at[1];
+#pragma unroll
+    for (int i = 1; i < kRounds; ++i)
+      if (r >= i) {
+        lo = at[i];
+        hi = at[i + 1];
+      }
+    return lo + j * (hi - lo) / blocks;
+  }
+  __device__ unsigned end(unsigned piece) const {
+    return piece + 1 == rounds * blocks ? total : start(piece + 1);
+  }
+  __device__ unsigned piece_of(unsigned q) const {
+    unsigned r = 0, lo = at[0], hi = at[1];
+#pragma unroll
+    for (int i = 1; i < kRounds; ++i)
+      if (q >= at[i]) {
+        r = i;
+        lo = at[i];
+        hi = at[i + 1];
+      }
+    return r * blocks + ((q - lo + 1) * blocks - 1) / (hi - lo);
+  }
 };
-__device__ __forceinline__ Cut cut_of(unsigned total, unsigned grid) {
-  return Cut{total, total < grid ? total : grid};
-}
 
 __device__ __forceinline__ void fence_proxy_async_all() {
   asm volatile("fence.proxy.async;" ::: "memory");
+}
+
+// Waits (with a limit) until *word has reached `target`; what was written before
+// the words that took it there is then seen.
+__device__ __forceinline__ bool wait_count(const unsigned* word, unsigned target, int* status) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+    if (static_cast<int>(v - target) >= 0) break;
+    if ((i & 255u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        atomicExch(status, kTimeoutCode);
+        return false;
+      }
+    }
+  }
+  __threadfence();
+  return true;
 }
 
 // A barrier over the grid, by one thread of each block: everything that the
@@ -126,21 +195,13 @@ __device__ __forceinline__ void fence_proxy_async_all() {
 __device__ __forceinline__ bool grid_barrier(unsigned* word, unsigned target, int* status) {
   __threadfence();
   atomicAdd(word, 1u);
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
-    if (static_cast<int>(v - target) >= 0) break;
-    if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
-      atomicExch(status, kTimeoutCode);
-      return false;
-    }
-  }
-  __threadfence();
-  return true;
+  return wait_count(word, target, status);
 }
 
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// A barrier of all warps but 0 and 1.
+__device__ __forceinline__ void helper_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kHelpers) : "memory");
+}
 
 // Accumulator columns [col, col + 16) of this thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
@@ -415,7 +476,11 @@ __device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
     if (n1 > 0) c.act[i1] = lane + 32;
     c.act_of[lane] = i0;
     c.act_of[lane + 32] = i1;
-    if (lane == 0) c.nact = __popc(m0) + __popc(m1);
+    const int most = __reduce_max_sync(kFull, max(n0, n1));
+    if (lane == 0) {
+      c.nact = __popc(m0) + __popc(m1);
+      c.most = most;
+    }
   }
   __syncthreads();
   for (int ch = warp, n = 0; ch < chunks; ch += kThreads / 32, ++n) {
@@ -431,6 +496,10 @@ __device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
 }
 
 // ------------------------------------------------------------- FC1's ends
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
 // H of a row's column from its two sums.
 template <bool F8>
 __device__ __forceinline__ void store_h(const Params& p, const Ctrl& c, int row, int e, int col,
@@ -450,6 +519,125 @@ __device__ __forceinline__ void store_h(const Params& p, const Ctrl& c, int row,
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     if (lane == 0) atomicMax(p.amax + row, __float_as_uint(m));
+  }
+}
+
+// The same of four columns (f is a multiple of 64: all in range or none).
+template <bool F8>
+__device__ __forceinline__ void store_h4(const Params& p, const Ctrl& c, int row, int col, float4 a,
+                                         float4 b, float4 w1, float4 w3, int lane) {
+  float m = 0.f;
+  if (col < p.f) {
+    if (F8) {
+      const float s = c.sx[c.tok[row]];
+      a = make_float4(a.x * (s * w1.x), a.y * (s * w1.y), a.z * (s * w1.z), a.w * (s * w1.w));
+      b = make_float4(b.x * (s * w3.x), b.y * (s * w3.y), b.z * (s * w3.z), b.w * (s * w3.w));
+    }
+    const __nv_bfloat162 lo =
+        __floats2bfloat162_rn(a.x / (1.f + expf(-a.x)) * b.x, a.y / (1.f + expf(-a.y)) * b.y);
+    const __nv_bfloat162 hi =
+        __floats2bfloat162_rn(a.z / (1.f + expf(-a.z)) * b.z, a.w / (1.f + expf(-a.w)) * b.w);
+    uint2 out;
+    out.x = *reinterpret_cast<const uint32_t*>(&lo);
+    out.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p.H + static_cast<size_t>(row) * p.f + col) = out;
+    m = fmaxf(fmaxf(fabsf(bf16_lo(out.x)), fabsf(bf16_hi(out.x))),
+              fmaxf(fabsf(bf16_lo(out.y)), fabsf(bf16_hi(out.y))));
+  }
+  if (F8) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if (lane == 0) atomicMax(p.amax + row, __float_as_uint(m));
+  }
+}
+
+// y: 128 columns of a token to a warp.  Lane j first looks up slot j's row and
+// the pieces that its tile went through (done by every thread for every slot, the
+// divisions alone cost 4 us).  Then eight chains of loads run side by side, since this is latency: LANES of them for each of up
+// to 8 / LANES slots, the slot's row of O and the parts that other pieces left
+// of it dealt out to them in turn.
+template <int LANES>
+__device__ void combine(const Params& p, const Ctrl& c, const Cut& cut, unsigned tiles,
+                        unsigned ksn) {
+  const int lane = threadIdx.x & 31, blocks = (p.h + 127) / 128;
+  const size_t stride = static_cast<size_t>(LANES) * p.T * 64;  // float4s
+  for (int i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < p.T * blocks;
+       i += gridDim.x * (kThreads / 32)) {
+    const int t = i / blocks, b = i - t * blocks, col = b * 128 + lane * 4;
+    const bool in = col < p.h;
+    int my_row = -1, my_n = 0;   // its row; further parts
+    unsigned my_at = 0;          // its row in the first piece's part
+    float my_gate = 0.f;
+    if (lane < p.k) {
+      const int a = t * p.k + lane;
+      my_row = c.pos[a];
+      if (my_row >= 0) {
+        my_gate = c.gate[a];
+        const int e = c.exp[a];
+        const unsigned q = (c.act_of[e] * tiles + b / 2) * ksn, first = cut.piece_of(q);
+        my_n = cut.piece_of(q + ksn - 1) - first;
+        my_at = first * p.T + my_row - c.off[e];
+      }
+    }
+    float4 v[8];
+    const float4* src[8];
+    int left[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      constexpr int kLanes = LANES;
+      const int j = w / kLanes, u = w % kLanes;
+      const int row = __shfl_sync(kFull, my_row, j), n = __shfl_sync(kFull, my_n, j);
+      const unsigned at = __shfl_sync(kFull, my_at, j);
+      v[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+      left[w] = row >= 0 && n >= u ? (n - u) / kLanes + 1 : 0;
+      src[w] = reinterpret_cast<const float4*>(p.part) +
+               (static_cast<size_t>(at + u * p.T) * 64 + (col & 255) / 4);
+      if (u == 0 && row >= 0) {
+        if (in)
+          v[w] = __ldcg(
+              reinterpret_cast<const float4*>(p.O + static_cast<size_t>(row) * p.h + col));
+        src[w] += stride;
+        --left[w];
+      }
+    }
+    for (bool any = true; any;) {
+      any = false;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (left[w] == 0) continue;
+        any = true;
+        const float4 x = __ldcg(src[w]);
+        src[w] += stride;
+        --left[w];
+        v[w].x += x.x;
+        v[w].y += x.y;
+        v[w].z += x.z;
+        v[w].w += x.w;
+      }
+    }
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 8 / LANES; ++j) {
+      float4 o = v[j * LANES];
+#pragma unroll
+      for (int u = 1; u < LANES; ++u) {
+        const float4 x = v[j * LANES + u];
+        o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+      }
+      const float g = __shfl_sync(kFull, my_gate, j);
+      if (__shfl_sync(kFull, my_row, j) < 0) continue;
+      sum.x = fmaf(g, o.x, sum.x);
+      sum.y = fmaf(g, o.y, sum.y);
+      sum.z = fmaf(g, o.z, sum.z);
+      sum.w = fmaf(g, o.w, sum.w);
+    }
+    if (!in) continue;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z, sum.w);
+    uint2 out;
+    out.x = *reinterpret_cast<const uint32_t*>(&lo);
+    out.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t) * p.h + col) = out;
   }
 }
 
@@ -479,6 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&c.hready), 1);
     mbar_init(smem_u32(&c.drain), 1);
     mbar_init(smem_u32(&c.rbar), 1);
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(smem_u32(&c.qfull[i]), 1);
+      mbar_init(smem_u32(&c.qempty[i]), 5);  // the MMA warp and four epilogue warps
+    }
     c.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.x);
@@ -486,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.w3);
     tma_prefetch_desc(&maps.h);
     tma_prefetch_desc(&maps.w2);
-    p.tick1[blockIdx.x] = 0;
+    if (blockIdx.x == 0) p.claim[0] = p.claim[1] = 0;
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&c.tmem_base), 512);
@@ -512,12 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KB = F8 ? 128 : 64;  // contraction indices of a stage
     const unsigned ks1 = p.h / KB, nt1 = (p.f + 127) / 128;
     const unsigned ks2 = p.f / KB, nt2 = (p.h + 255) / 256;
-    const Cut cut1 = cut_of(c.nact * nt1 * ks1, G), cut2 = cut_of(c.nact * nt2 * ks2, G);
+    const Cut cut1(c.nact * nt1 * ks1, G, ks1), cut2(c.nact * nt2 * ks2, G, ks2);
     const unsigned cta = blockIdx.x;
-    const unsigned a1 = cta < cut1.blocks ? cut1.start(cta) : cut1.total;
-    const unsigned b1 = cta < cut1.blocks ? cut1.start(cta + 1) : cut1.total;
-    const unsigned a2 = cta < cut2.blocks ? cut2.start(cta) : cut2.total;
-    const unsigned b2 = cta < cut2.blocks ? cut2.start(cta + 1) : cut2.total;
     const uint32_t ring = smem_u32(smem);
 
     if (warp == 0) {
@@ -526,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0;        // next stage
         uint32_t ph = 0;  // its use count's parity
         int filled = 0;
+        int published = 0;
         bool ok = true;
         auto claim = [&](unsigned bytes) {
           if (*abort_flag ||
@@ -543,85 +732,116 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1;
           }
         };
-        unsigned item = a1 / ks1, ks = a1 - item * ks1;
-        unsigned ai = item / nt1, tile = item - ai * nt1;
-        for (unsigned q = a1; ok && q < b1; ++q) {
-          claim(kWBytes + bbytes);
-          if (!ok) break;
-          const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&c.full[s]);
-          const int e = c.act[ai], k0 = ks * KB;
-          if (F8) {
-            tma_load_3d(dst, &maps.w1, k0, tile * 256, e, bar);
-          } else {
-            tma_load_3d(dst, &maps.w1, 0, e * p.h + k0, tile * 2, bar);
-            tma_load_3d(dst + kWBytes / 2, &maps.w3, 0, e * p.h + k0, tile * 2, bar);
+        auto publish = [&](int piece) {
+          const int i = published % kQueue;
+          if (!ok || *abort_flag ||
+              !mbar_wait(smem_u32(&c.qempty[i]), ((published / kQueue) & 1) ^ 1, p.status,
+                         kTimeoutCode)) {
+            *abort_flag = 1;
+            ok = false;
+            return;
           }
-          tma_load_2d(dst + kWBytes, &maps.x, k0, 0, bar);
-          next();
-          if (++ks == ks1) {
-            ks = 0;
-            if (++tile == nt1) {
-              tile = 0;
-              ++ai;
+          c.piece[i] = piece;
+          mbar_arrive(smem_u32(&c.qfull[i]));
+          ++published;
+        };
+        // the block's next piece of a phase, -1 when there is none
+        auto more = [&](const Cut& cut, unsigned* taken) {
+          if (cut.rounds == 1) return -1;
+          const unsigned i = cut.blocks + atomicAdd(taken, 1u);
+          return i < cut.rounds * cut.blocks ? static_cast<int>(i) : -1;
+        };
+        unsigned ks, ai, tile;  // where the weights' loads are
+        auto seek = [&](unsigned q, unsigned ksn, unsigned tiles) {
+          const unsigned item = q / ksn;
+          ks = q - item * ksn;
+          ai = item / tiles;
+          tile = item - ai * tiles;
+        };
+        auto step = [&](unsigned ksn, unsigned tiles) {
+          if (++ks < ksn) return;
+          ks = 0;
+          if (++tile < tiles) return;
+          tile = 0;
+          ++ai;
+        };
+        int piece = cta < cut1.blocks ? static_cast<int>(cta) : -1;
+        for (; ok && piece >= 0; piece = more(cut1, p.claim)) {
+          publish(piece);
+          const unsigned q1 = cut1.end(piece);
+          unsigned q = cut1.start(piece);
+          seek(q, ks1, nt1);
+          for (; ok && q < q1; ++q) {
+            claim(kWBytes + bbytes);
+            if (!ok) break;
+            const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&c.full[s]);
+            const int e = c.act[ai], k0 = ks * KB;
+            if (F8) {
+              tma_load_3d(dst, &maps.w1, k0, tile * 256, e, bar);
+            } else {
+              tma_load_3d(dst, &maps.w1, 0, e * p.h + k0, tile * 2, bar);
+              tma_load_3d(dst + kWBytes / 2, &maps.w3, 0, e * p.h + k0, tile * 2, bar);
             }
+            tma_load_2d(dst + kWBytes, &maps.x, k0, 0, bar);
+            next();
+            step(ks1, nt1);
           }
         }
+        publish(-1);
         // FC2.  The first stages' weights are asked for at once; their rows of H
         // follow when every block's are written.
-        item = a2 / ks2;
-        ks = a2 - item * ks2;
-        ai = item / nt2;
-        tile = item - ai * nt2;
-        unsigned hks = ks, hai = ai, htile = tile;  // where the H loads are
+        unsigned hks = 0, hai = 0, htile = 0;  // where the H loads are
         int hs = s;
-        const unsigned ahead = min(b2 - a2, static_cast<unsigned>(p.stages));
         auto load_h = [&] {
           const int e = c.act[hai], r0 = c.off[e], n = c.off[e + 1] - r0;
           const uint32_t dst = ring + hs * stage_bytes + kWBytes, bar = smem_u32(&c.full[hs]);
           for (int r = 0; r < n; r += 16)
             tma_load_2d(dst + r * 128, &maps.h, hks * KB, r0 + r, bar);
           if (++hs == p.stages) hs = 0;
-          if (++hks == ks2) {
-            hks = 0;
-            if (++htile == nt2) {
-              htile = 0;
-              ++hai;
-            }
-          }
+          if (++hks < ks2) return;
+          hks = 0;
+          if (++htile < nt2) return;
+          htile = 0;
+          ++hai;
         };
         unsigned waiting = 0;  // stages whose H is not yet asked for
         bool ready = false;
-        for (unsigned q = a2; ok && q < b2; ++q) {
-          const int e = c.act[ai];
-          const int rows16 = (c.off[e + 1] - c.off[e] + 15) / 16 * 16;
-          claim(kWBytes + rows16 * 128);
-          if (!ok) break;
-          const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&c.full[s]);
-          if (F8)
-            tma_load_3d(dst, &maps.w2, ks * KB, tile * 256, e, bar);
-          else
-            tma_load_3d(dst, &maps.w2, 0, e * p.f + ks * KB, tile * 4, bar);
-          ++waiting;
-          next();
-          if (++ks == ks2) {
-            ks = 0;
-            if (++tile == nt2) {
-              tile = 0;
-              ++ai;
+        piece = cta < cut2.blocks ? static_cast<int>(cta) : -1;
+        for (; ok && piece >= 0; piece = more(cut2, p.claim + 1)) {
+          publish(piece);
+          const unsigned q0 = cut2.start(piece), q1 = cut2.end(piece);
+          const unsigned ahead = min(q1 - q0, static_cast<unsigned>(p.stages));
+          seek(q0, ks2, nt2);
+          hks = ks;
+          hai = ai;
+          htile = tile;
+          for (unsigned q = q0; ok && q < q1; ++q) {
+            const int e = c.act[ai];
+            const int rows16 = (c.off[e + 1] - c.off[e] + 15) / 16 * 16;
+            claim(kWBytes + rows16 * 128);
+            if (!ok) break;
+            const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&c.full[s]);
+            if (F8)
+              tma_load_3d(dst, &maps.w2, ks * KB, tile * 256, e, bar);
+            else
+              tma_load_3d(dst, &maps.w2, 0, e * p.f + ks * KB, tile * 4, bar);
+            ++waiting;
+            next();
+            step(ks2, nt2);
+            if (!ready && q + 1 - q0 < ahead) continue;
+            if (!ready) {
+              if (!mbar_wait(smem_u32(&c.hready), 0, p.status, kTimeoutCode)) {
+                *abort_flag = 1;
+                ok = false;
+              }
+              ready = true;
+              fence_proxy_async_all();
             }
+            // on failure too: the stages' loads must all land before the block ends
+            for (; waiting > 0; --waiting) load_h();
           }
-          if (!ready && q + 1 - a2 < ahead) continue;
-          if (!ready) {
-            if (!mbar_wait(smem_u32(&c.hready), 0, p.status, kTimeoutCode)) {
-              *abort_flag = 1;
-              ok = false;
-            }
-            ready = true;
-            fence_proxy_async_all();
-          }
-          // on failure too: the stages' loads must all land before the block ends
-          for (; waiting > 0; --waiting) load_h();
         }
+        publish(-1);
         if (!ok) {
           for (; waiting > 0; --waiting) load_h();
           for (int i = 0; i < filled; ++i) {
@@ -636,6 +856,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, it = 0;
       uint32_t ph = 0;
       bool ok = true;
+      int popped = 0;
+      auto pop = [&] {
+        const int i = popped % kQueue;
+        if (*abort_flag || !mbar_wait(smem_u32(&c.qfull[i]), (popped / kQueue) & 1, p.status,
+                                      kTimeoutCode)) {
+          *abort_flag = 1;
+          ok = false;
+        }
+        const int v = c.piece[i];
+        __syncwarp();
+        ++popped;
+        if (lane == 0) mbar_arrive(smem_u32(&c.qempty[i]));
+        ok = __all_sync(kFull, ok);
+        return ok ? v : -1;
+      };
       auto phase = [&](unsigned q0, unsigned q1, unsigned ksn, unsigned tiles, bool fc1) {
         unsigned item = q0 / ksn, ks = q0 - item * ksn;
         for (unsigned q = q0; ok && q < q1; ++q) {
@@ -689,15 +924,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      phase(a1, b1, ks1, nt1, true);
-      phase(a2, b2, ks2, nt2, false);
+      for (int i; (i = pop()) >= 0 && ok;) phase(cut1.start(i), cut1.end(i), ks1, nt1, true);
+      if (ok)
+        for (int i; (i = pop()) >= 0 && ok;) phase(cut2.start(i), cut2.end(i), ks2, nt2, false);
       if (lane == 0) {  // every MMA must be done before tensor memory is freed
         umma_commit(smem_u32(&c.drain));
         mbar_wait(smem_u32(&c.drain), 0, p.status, kTimeoutCode);
       }
       __syncwarp();
-    } else if (warp >= 4) {
-      // -------------------------------------------------------- epilogue
+    } else {
+      // ------------------------------------------- epilogue and helpers
+      const bool epilogue = warp >= 4 && warp < 8;
       const int r = (warp & 3) * 32 + lane;  // my row of the 128-row tiles
       const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       int it = 0;
@@ -712,10 +949,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return ok;
       };
+      int popped = 0;
+      unsigned q = 0, q_end = 0;
+      int piece = -1;
+      auto pop = [&](const Cut& cut) {  // the next piece's range, false at the phase's end
+        const int i = popped % kQueue;
+        const bool got = !*abort_flag && mbar_wait(smem_u32(&c.qfull[i]), (popped / kQueue) & 1,
+                                                   p.status, kTimeoutCode);
+        piece = c.piece[i];
+        ++popped;
+        if (!__all_sync(kFull, got)) {
+          *abort_flag = 1;
+          ok = false;
+          return false;
+        }
+        if (lane == 0) mbar_arrive(smem_u32(&c.qempty[i]));
+        if (piece < 0) return false;
+        q = cut.start(piece);
+        q_end = cut.end(piece);
+        return true;
+      };
       // ---- FC1
-      for (unsigned q = a1; ok && q < b1;) {
+      while (epilogue && ok && (q < q_end || pop(cut1))) {
         const unsigned item = q / ks1, q_item = item * ks1;
-        const unsigned end = min(b1, q_item + ks1);
+        const unsigned end = min(q_end, q_item + ks1);
         const int buf = it & 1;
         if (!filled(buf)) break;
         const int e = c.act[item / nt1], col = (item % nt1) * 128 + r;
@@ -727,9 +984,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           w1 = __ldg(p.s1 + static_cast<size_t>(e) * p.f + col);
           w3 = __ldg(p.s3 + static_cast<size_t>(e) * p.f + col);
         }
-        // two slots for each block: a tile begun elsewhere, a tile begun here
+        // two slots for each piece: a tile begun before it, a tile begun in it
         const size_t slot = static_cast<size_t>(2) * p.T * 128;
-        float* mine = p.part1 + (2 * cta + (q == q_item)) * slot;
+        float* mine = p.part + (2 * piece + (q == q_item)) * slot;
         for (int i0 = 0; i0 < n; i0 += 8) {
           uint32_t ra[8], rb[8];
 #pragma unroll
@@ -754,68 +1011,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(smem_u32(&c.tempty[buf]));
         ++it;
-        if (!whole) {
-          const unsigned c0 = cut1.block_of(q_item), c1 = cut1.block_of(q_item + ks1 - 1);
-          __threadfence();
-          epi_sync();
-          if (r == 0) c.flag = atomicAdd(p.tick1 + c0, 1u) == c1 - c0;
-          epi_sync();
-          if (c.flag) {
-            __threadfence();
-            const float* first = p.part1 + (2 * c0 + 1) * slot + r;
-            for (int i0 = 0; i0 < n; i0 += 4) {  // 4 rows' loads in flight
-              float va[4], vb[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int o = min(i0 + i, n - 1) * 256;
-                va[i] = __ldcg(first + o);
-                vb[i] = __ldcg(first + o + 128);
-              }
-#pragma unroll 4
-              for (unsigned blk = c0 + 1; blk <= c1; ++blk) {
-                const float* src = p.part1 + 2 * blk * slot + r;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int o = min(i0 + i, n - 1) * 256;
-                  va[i] += __ldcg(src + o);
-                  vb[i] += __ldcg(src + o + 128);
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (i0 + i < n) store_h<F8>(p, c, row0 + i0 + i, e, col, va[i], vb[i], w1, w3, lane);
-            }
-          }
-          epi_sync();  // c.flag is free again
-        }
         q = end;
       }
-      // ---- H whole
-      fence_proxy_async_all();
-      epi_sync();
-      if (r == 0 && !grid_barrier(words + kBarWord, 2 * G, p.status)) *abort_flag = 1;
-      epi_sync();
+      unsigned arrived = G;
+      auto grid_sync = [&] {
+        fence_proxy_async_all();
+        helper_sync();
+        arrived += G;
+        if (tid == 64 && !grid_barrier(words + kBarWord, arrived, p.status)) *abort_flag = 1;
+        helper_sync();
+      };
+      grid_sync();
+      // The tiles that pieces share, each in the order of its pieces: a tile goes
+      // with the first border inside it, two of its rows to a warp, four columns
+      // to a lane.
+      if (!*abort_flag) {
+        const size_t slot = static_cast<size_t>(2) * p.T * 128;
+        const unsigned pairs = (c.most + 1) / 2, work = cut1.rounds * cut1.blocks * pairs;
+        for (unsigned w = cta * (kHelpers / 32) + warp - 2; w < work; w += G * (kHelpers / 32)) {
+          const unsigned i = w / pairs, i0 = (w - i * pairs) * 2, begin = cut1.start(i);
+          const unsigned item = begin / ks1, q_item = item * ks1, ai = item / nt1;
+          const int e = c.act[ai], col = (item - ai * nt1) * 128 + lane * 4;
+          const unsigned row0 = c.off[e], n = c.off[e + 1] - row0;
+          if (i0 >= n || begin == q_item || cut1.piece_of(q_item) != i - 1) continue;
+          const unsigned last = cut1.piece_of(q_item + ks1 - 1), odd = i0 + 1 < n ? 64 : 0;
+          const float4* src =
+              reinterpret_cast<const float4*>(p.part + (2 * i - 1) * slot + i0 * 256) + lane;
+          float4 va = __ldcg(src), vb = __ldcg(src + 32);
+          float4 ua = __ldcg(src + odd), ub = __ldcg(src + odd + 32);
+          src += slot / 4;
+#pragma unroll 4
+          for (unsigned o = i; o <= last; ++o, src += slot / 2) {
+            va = add4(va, __ldcg(src));
+            vb = add4(vb, __ldcg(src + 32));
+            ua = add4(ua, __ldcg(src + odd));
+            ub = add4(ub, __ldcg(src + odd + 32));
+          }
+          float4 w1 = make_float4(0.f, 0.f, 0.f, 0.f), w3 = w1;
+          if (F8) {
+            w1 = __ldg(reinterpret_cast<const float4*>(p.s1 + static_cast<size_t>(e) * p.f + col));
+            w3 = __ldg(reinterpret_cast<const float4*>(p.s3 + static_cast<size_t>(e) * p.f + col));
+          }
+          store_h4<F8>(p, c, row0 + i0, col, va, vb, w1, w3, lane);
+          if (odd) store_h4<F8>(p, c, row0 + i0 + 1, col, ua, ub, w1, w3, lane);
+        }
+      }
+      grid_sync();
       if (F8 && !*abort_flag) {  // rows of H to e4m3, 8 values at a time over the whole grid
         const int n8 = p.f / 8, all = c.off[kMaxE] * n8;
-        for (int i = cta * 128 + r; i < all; i += G * 128) {
+        for (int i = cta * kHelpers + tid - 64; i < all; i += G * kHelpers) {
           const int row = i / n8;
           const float s = scale_of(__uint_as_float(__ldcg(p.amax + row)));
           const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p.H) + i);
           reinterpret_cast<uint2*>(p.Hq)[i] = quant8(w, s);
         }
-        fence_proxy_async_all();
-        epi_sync();
-        if (r == 0 && !grid_barrier(words + kBarWord, 3 * G, p.status)) *abort_flag = 1;
-        epi_sync();
+        grid_sync();
       }
       fence_proxy_async_all();
-      if (r == 0) mbar_arrive(smem_u32(&c.hready));
+      if (tid == 64) mbar_arrive(smem_u32(&c.hready));
       if (*abort_flag) ok = false;
       ok = __all_sync(kFull, ok);
-      // ---- FC2: rows of O where this block began the tile, else of part2
-      for (unsigned q = a2; ok && q < b2;) {
+      // ---- FC2: rows of O where this piece begins the tile, else of its part
+      q = q_end = 0;
+      while (epilogue && ok && (q < q_end || pop(cut2))) {
         const unsigned item = q / ks2, q_item = item * ks2;
-        const unsigned end = min(b2, q_item + ks2);
+        const unsigned end = min(q_end, q_item + ks2);
         const int buf = it & 1;
         if (!filled(buf)) break;
         const int e = c.act[item / nt2], col0 = (item % nt2) * 256;
@@ -827,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float w2 = 1.f;
           if (F8 && col < p.h) w2 = __ldg(p.s2 + static_cast<size_t>(e) * p.h + col);
           float* dst = begun ? p.O + static_cast<size_t>(row0) * p.h + col
-                             : p.part2 + static_cast<size_t>(cta) * p.T * 256 + m * 128 + r;
+                             : p.part + static_cast<size_t>(piece) * p.T * 256 + m * 128 + r;
           const size_t ld = begun ? p.h : 256;
           for (int i0 = 0; i0 < n; i0 += 16) {
             float v[16];
@@ -849,66 +1109,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     // ------------------------------------------------------------ combine
     if (tid == 0 && (*abort_flag ||
-                     !grid_barrier(words + kBarWord, (F8 ? 4 : 3) * G, p.status)))
+                     !grid_barrier(words + kBarWord, (F8 ? 5 : 4) * G, p.status)))
       *abort_flag = 1;
     __syncthreads();
     if (!*abort_flag) {
-      const int n4 = p.h / 4;
-      for (int i = cta * kThreads + tid; i < p.T * n4; i += G * kThreads) {
-        const int t = i / n4, col = (i - t * n4) * 4;
-        const unsigned tile = col / 256;
-        // the k slots' loads together: this, too, is latency
-        float4 v[8];
-        unsigned blk[8], end[8];
-        int row[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int a = t * p.k + j;
-          row[j] = j < p.k ? c.pos[a] : -1;
-          v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          blk[j] = end[j] = 0;
-          if (row[j] >= 0) {
-            v[j] = __ldcg(
-                reinterpret_cast<const float4*>(p.O + static_cast<size_t>(row[j]) * p.h + col));
-            const int e = c.exp[a];
-            const unsigned q = (c.act_of[e] * nt2 + tile) * ks2;
-            blk[j] = cut2.block_of(q);
-            end[j] = cut2.block_of(q + ks2 - 1);
-            row[j] -= c.off[e];
-          }
-        }
-        for (bool more = true; more;) {
-          more = false;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (blk[j] == end[j]) continue;
-            ++blk[j];
-            more = true;
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(
-                p.part2 + (static_cast<size_t>(blk[j]) * p.T + row[j]) * 256 + col % 256));
-            v[j].x += u.x;
-            v[j].y += u.y;
-            v[j].z += u.z;
-            v[j].w += u.w;
-          }
-        }
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (row[j] < 0) continue;
-          const float g = c.gate[t * p.k + j];
-          sum.x = fmaf(g, v[j].x, sum.x);
-          sum.y = fmaf(g, v[j].y, sum.y);
-          sum.z = fmaf(g, v[j].z, sum.z);
-          sum.w = fmaf(g, v[j].w, sum.w);
-        }
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z, sum.w);
-        uint2 out;
-        out.x = *reinterpret_cast<const uint32_t*>(&lo);
-        out.y = *reinterpret_cast<const uint32_t*>(&hi);
-        reinterpret_cast<uint2*>(p.y)[i] = out;
-      }
+      if (p.k == 1)
+        combine<8>(p, c, cut2, nt2, ks2);
+      else if (p.k == 2)
+        combine<4>(p, c, cut2, nt2, ks2);
+      else if (p.k <= 4)
+        combine<2>(p, c, cut2, nt2, ks2);
+      else
+        combine<1>(p, c, cut2, nt2, ks2);
     }
   }
   // ------------------------------------------------------------- teardown
@@ -930,19 +1142,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-  size_t logits, idx, gates, H, O, part1, part2, tick1, xq, sx, Hq, amax, total;
+  size_t logits, idx, gates, H, O, part, claim, xq, sx, Hq, amax, total;
 };
 
 struct Plan {
   int n1, stages, smem;
   int tok_group, groups, slices, slice_h;
+  size_t pieces;
   bool ok;
 };
+
+// The most k-steps that a phase can have, with every expert that can be hit.
+long long most_steps(const moe_dims& d, bool fp8) {
+  const long long kb = fp8 ? 128 : 64;
+  const long long e = static_cast<long long>(d.T) * d.k < d.E ? d.T * d.k : d.E;
+  const long long t1 = e * ((d.f + 127ll) / 128) * (d.h / kb);
+  const long long t2 = e * ((d.h + 255ll) / 256) * (d.f / kb);
+  return t1 > t2 ? t1 : t2;
+}
 
 // Blocks = SMs.  Router units: token groups x slices of h, about one for each
 // block; groups of up to 8 tokens so that 128 tokens make 16 groups, and single
 // tokens up to 16.
-Plan plan_of(const moe_dims& d, int blocks) {
+Plan plan_of(const moe_dims& d, int blocks, bool fp8) {
   Plan p = {};
   p.n1 = (d.T + 15) / 16 * 16;
   const int stage = kWBytes + p.n1 * 128;
@@ -960,6 +1182,8 @@ Plan plan_of(const moe_dims& d, int blocks) {
   const int most = room / (d.E * 4 + kGroupTok * 2) / 8 * 8;
   if (p.slice_h > most) p.slice_h = most;
   p.slices = (d.h + p.slice_h - 1) / p.slice_h;
+  p.pieces = static_cast<size_t>(blocks) *
+             (most_steps(d, fp8) >= static_cast<long long>(kRoundsFrom) * blocks ? kRounds : 1);
   // so do a group's partial logits of all slices, where h is not enormous
   p.ok = p.slices * p.tok_group * d.E * 4 <= room;
   return p;
@@ -968,7 +1192,7 @@ Plan plan_of(const moe_dims& d, int blocks) {
 Layout layout(const moe_dims& d, bool fp8) {
   const size_t R = static_cast<size_t>(d.T) * d.k, T = d.T, h = d.h, f = d.f;
   const size_t blocks = moe_api::num_sms();
-  const Plan plan = d.T > 0 ? plan_of(d, static_cast<int>(blocks)) : Plan{};
+  const Plan plan = d.T > 0 ? plan_of(d, static_cast<int>(blocks), fp8) : Plan{};
   size_t off = 256;
   auto take = [&](size_t n) {
     const size_t o = off;
@@ -981,9 +1205,8 @@ Layout layout(const moe_dims& d, bool fp8) {
   L.gates = take(R * 4);
   L.H = take(R * f * 2);
   L.O = take(R * h * 4);
-  L.part1 = take(2 * blocks * 2 * T * 128 * 4);
-  L.part2 = take(blocks * T * 256 * 4);
-  L.tick1 = take(blocks * 4);
+  L.part = take(2 * plan.pieces * 2 * T * 128 * 4);
+  L.claim = take(8);
   if (fp8) {
     L.xq = take(T * h);
     L.sx = take(T * 4);
@@ -994,15 +1217,13 @@ Layout layout(const moe_dims& d, bool fp8) {
   return L;
 }
 
-// k-step counts times blocks stay below 2^31 (Cut's arithmetic; such weights
-// would not fit the GPU's memory many times over).
+// k-steps times blocks, and times 100, stay below 2^32 (Cut's arithmetic).
 bool supported(const moe_dims& d, bool fp8) {
   if (d.T > kDecodeMaxT || d.sar != 0 || (fp8 && (d.h % 128 != 0 || d.f % 128 != 0))) return false;
-  const long long kb = fp8 ? 128 : 64, lim = (1ll << 31) / moe_api::num_sms();
-  if (d.T > 0 && !plan_of(d, moe_api::num_sms()).ok) return false;
-  const long long t1 = d.E * ((d.f + 127ll) / 128) * (d.h / kb);
-  const long long t2 = d.E * ((d.h + 255ll) / 256) * (d.f / kb);
-  return t1 < lim && t2 < lim && static_cast<long long>(d.E) * (d.h > d.f ? d.h : d.f) * 2 < (1ll << 31);
+  // (a k-step is 32 KiB of weights: 14 million of them are 450 GB)
+  if (most_steps(d, fp8) >= (1ll << 31) / moe_api::num_sms()) return false;
+  if (d.T > 0 && !plan_of(d, moe_api::num_sms(), fp8).ok) return false;
+  return static_cast<long long>(d.E) * (d.h > d.f ? d.h : d.f) * 2 < (1ll << 31);
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -1039,7 +1260,7 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
   if (empty) return MOE_OK;
   uint8_t* w = static_cast<uint8_t*>(ws);
   const int blocks = moe_api::num_sms();
-  const Plan plan = plan_of(d, blocks);
+  const Plan plan = plan_of(d, blocks, fp8);
   Params p = {};
   p.T = d.T;
   p.h = d.h;
@@ -1061,9 +1282,8 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
   p.logits = reinterpret_cast<float*>(w + L.logits);
   p.H = reinterpret_cast<uint16_t*>(w + L.H);
   p.O = reinterpret_cast<float*>(w + L.O);
-  p.part1 = reinterpret_cast<float*>(w + L.part1);
-  p.part2 = reinterpret_cast<float*>(w + L.part2);
-  p.tick1 = reinterpret_cast<unsigned*>(w + L.tick1);
+  p.part = reinterpret_cast<float*>(w + L.part);
+  p.claim = reinterpret_cast<unsigned*>(w + L.claim);
   p.y = y;
   p.status = reinterpret_cast<int*>(ws);
   Maps m;
