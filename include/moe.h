@@ -58,7 +58,7 @@
  *     skipped (an assignment not placed, a zero row, a slot that adds
  *     nothing), so nothing is read or written out of bounds.  The calls that
  *     take no workspace (moe_combine, moe_unpermute, moe_quantize_rows_fp8,
- *     moe_permute_noalloc) record into one status word per device that the
+ *     moe_permute_noalloc, moe_block_norm_fwd) record into one status word per device that the
  *     library keeps (its address is looked up on the first such call on a
  *     device and kept until the process exits); moe_read_device_status(NULL,
  *     stream) reports that one.
@@ -459,8 +459,7 @@ moe_status moe_block_norm_fwd(const moe_norm_dims* dims, const void* r,
  * Both row norms are computed again from r_out and y: nothing is kept from
  * the forward.  dr may be dr_out itself.  Gradients are written, not
  * accumulated, and every sum has a fixed order.
- * Workspace: moe_norm_workspace_bytes(dims), 256-byte aligned; it needs no
- * zeroing. */
+ * Workspace: moe_norm_workspace_bytes(dims), 256-byte aligned. */
 moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out,
                               const moe_bf16* y, const float* w_post,
                               const float* gate, const float* w_pre,
@@ -489,8 +488,8 @@ const char* moe_status_string(moe_status status);
 
 /* Synchronises `stream`, returns the status word at the start of `ws` and
  * clears it.  ws = NULL: the status word of the calls that take no workspace
- * (moe_combine, moe_unpermute, moe_quantize_rows_fp8, moe_permute_noalloc) on
- * the current device.
+ * (moe_combine, moe_unpermute, moe_quantize_rows_fp8, moe_permute_noalloc,
+ * moe_block_norm_fwd) on the current device.
  * MOE_ERR_CUDA if the synchronisation itself failed. */
 moe_status moe_read_device_status(void* ws, moe_stream_t stream);
 

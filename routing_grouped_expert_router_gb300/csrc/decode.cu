@@ -292,16 +292,6 @@ __device__ void select_topk(const Params& p, int t, float l0, float l1, int lane
   }
 }
 
-// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // A router unit is a group of tokens x a slice of h: fp32 partial logits.  All
 // that a unit reads is asked for at once (the slice's rows of Wg are one
 // contiguous piece); what this phase costs is latency, and loads in the loop's
@@ -553,9 +543,9 @@ __device__ __forceinline__ void store_h4(const Params& p, const Ctrl& c, int row
 
 // y: 128 columns of a token to a warp.  Lane j first looks up slot j's row and
 // the pieces that its tile went through (done by every thread for every slot, the
-// divisions alone cost 4 us).  Then eight chains of loads run side by side, since this is latency: LANES of them for each of up
-// to 8 / LANES slots, the slot's row of O and the parts that other pieces left
-// of it dealt out to them in turn.
+// divisions alone cost 4 us).  Then eight chains of loads run side by side, since
+// this is latency: LANES of them for each of up to 8 / LANES slots, the slot's
+// row of O and the parts that other pieces left of it dealt out to them in turn.
 template <int LANES>
 __device__ void combine(const Params& p, const Ctrl& c, const Cut& cut, unsigned tiles,
                         unsigned ksn) {

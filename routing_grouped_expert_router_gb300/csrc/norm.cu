@@ -6,9 +6,12 @@
 //
 // Both directions are bound by HBM: the forward reads r and y and writes r_out
 // and u (8 bytes for each element with a bf16 residual), the backward reads
-// r_out, y, du and dr_out and writes dr and dy (12 bytes).  So a row is read
-// once and stays in the registers of one block, two 16-byte pieces for each
-// thread, through both of its row sums.
+// r_out, y, du and dr_out and writes dr and dy (12 bytes).  Each row is read
+// once.  A row has two sums in a chain, and a block that waits for its loads and
+// then for its sums leaves HBM idle (a block for each row: 4.5 TB/s forward), so
+// the blocks stay, each with a ring of the next rows in shared memory that bulk
+// copies fill, and keep the channel weights in registers: two 8-element pieces
+// of the row to a thread, the same columns for every row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -18,6 +21,7 @@
 #include "../../include/moe.h"
 #include "api_internal.h"
 #include "kernels.cuh"
+#include "ptx.cuh"
 
 namespace {
 
@@ -26,21 +30,25 @@ constexpr int kMaxH = 8192;
 constexpr int kMaxThreads = 512;
 constexpr int kPieces = 2;  // 8-element pieces of a row for each thread
 
+constexpr int kMaxSlots = 4;
+
 struct Args {
-  const void* r;        // fwd: r; bwd: r_out
-  const uint4* y;
+  const void* r;        // fwd: r; bwd: r_out (NULL without w_pre)
+  const uint16_t* y;
   const float* w_post;
   const float* gate;
   const float* w_pre;
-  const uint4* du;
+  const uint16_t* du;
   const void* dr_out;
   void* out_r;          // fwd: r_out; bwd: dr
   uint4* out_u;         // fwd: u; bwd: dy
   float* dgate;         // bwd, token gate
   float* partial;       // bwd: column sums of each block
+  int* status;
   int T, h;
   int gate_kind;
-  float eps, alpha, beta, inv_h;
+  int slots, slot_bytes;
+  float eps, alpha, beta;
 };
 
 __device__ __forceinline__ void unpack8(const uint4& q, float* v) {
@@ -95,27 +103,32 @@ __device__ __forceinline__ void load_w(const float* w, int c, float* v) {
 
 // Sums of N values over the block, in every thread.  The order is fixed:
 // butterflies within warps, then the warps in order.  `slot` alternates so
-// that one barrier for each call is enough.
+// that one barrier for each call is enough.  Returns whether `ok` held in
+// every thread.
 template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (*red)[N * (kMaxThreads / 32)],
-                                          int& slot) {
+__device__ __forceinline__ bool block_sum(float (&v)[N], float (*red)[N * (kMaxThreads / 32)],
+                                          int& slot, bool ok) {
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
   const int nw = blockDim.x >> 5;
-  if (nw == 1) return;
+  if (nw == 1) {
+    __syncwarp();
+    return __all_sync(kFull, ok);
+  }
   float* s = red[slot];
   slot ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) s[(threadIdx.x >> 5) * N + i] = v[i];
-  __syncthreads();
+  ok = __syncthreads_and(ok);
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
   for (int w = 0; w < nw; ++w)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += s[w * N + i];
+  return ok;
 }
 
 // 1 / rms of a row from its sum of squares, correctly rounded: its error would
@@ -124,75 +137,137 @@ __device__ __forceinline__ float inv_rms(float ss, const Args& a) {
   return __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.h)) + a.eps);
 }
 
+// The block's ring of rows.  Row number n of the block (token blockIdx.x + n *
+// gridDim.x) goes through slot n % slots; a slot holds `streams` arrays' rows,
+// one after another.
+constexpr int kMaxStreams = 4;
+struct Ring {
+  const uint8_t* src[kMaxStreams];
+  uint32_t bytes[kMaxStreams];  // of a row; 0: not read
+  uint32_t total;
+};
+__device__ __forceinline__ void ring_load(const Args& a, const Ring& g, uint64_t* full,
+                                          uint8_t* smem, int n) {
+  const long long t = blockIdx.x + static_cast<long long>(n) * gridDim.x;
+  if (t >= a.T) return;
+  const int s = n % a.slots;
+  const uint32_t bar = moe::smem_u32(&full[s]);
+  uint32_t dst = moe::smem_u32(smem) + s * a.slot_bytes;
+  moe::mbar_expect_tx(bar, g.total);
+#pragma unroll
+  for (int i = 0; i < kMaxStreams; ++i)
+    if (g.bytes[i]) {
+      moe::bulk_load(dst, g.src[i] + t * g.bytes[i], g.bytes[i], bar);
+      dst += g.bytes[i];
+    }
+}
+__device__ __forceinline__ bool ring_wait(const Args& a, uint64_t* full, int n) {
+  return moe::mbar_wait(moe::smem_u32(&full[n % a.slots]), (n / a.slots) & 1, a.status,
+                        MOE_ERR_DEVICE_TIMEOUT);
+}
+// After a wait ran out: the rows asked for land before the block ends.
+__device__ __forceinline__ void ring_drain(const Args& a, uint64_t* full, int n) {
+  if (threadIdx.x == 0)
+    for (int i = 1; i < a.slots; ++i)
+      if (blockIdx.x + static_cast<long long>(n + i) * gridDim.x < a.T) ring_wait(a, full, n + i);
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kMaxSlots];
   __shared__ float red[2][kMaxThreads / 32];
-  int slot = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  int half = 0;
+  Ring g;
+  g.src[0] = static_cast<const uint8_t*>(a.r);
+  g.src[1] = reinterpret_cast<const uint8_t*>(a.y);
+  g.bytes[0] = a.h * (F32 ? 4 : 2);
+  g.bytes[1] = a.y ? a.h * 2 : 0;
+  g.bytes[2] = g.bytes[3] = 0;
+  g.total = g.bytes[0] + g.bytes[1];
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.slots; ++s) moe::mbar_init(moe::smem_u32(&full[s]), 1);
+    moe::fence_mbar_init();
+    for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
+  }
+  // the scale of each of my columns of y, and of u
+  float wz[kPieces][8], wu[kPieces][8];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = (threadIdx.x + i * blockDim.x) * 8;
+    if (c >= a.h) continue;
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wz[i][j] = a.beta;
+    if (a.gate_kind == MOE_GATE_CHANNEL) {
+      load_w(a.gate, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wz[i][j] *= w[j];
+    }
+    if (a.w_post) {
+      load_w(a.w_post, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wz[i][j] *= w[j];
+    }
+    if (a.w_pre) load_w(a.w_pre, c, wu[i]);
+  }
+  __syncthreads();
+  int n = 0;
+  for (int t = blockIdx.x; t < a.T; ++n) {
     const size_t row = static_cast<size_t>(t) * a.h;
+    float s = 1.f;
+    if (a.gate_kind == MOE_GATE_TOKEN) s = __ldg(a.gate + t);
+    bool ok = ring_wait(a, full, n);
+    const uint8_t* slot = smem + (n % a.slots) * a.slot_bytes;
     float v[kPieces][8], z[kPieces][8];
     float ss[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c < a.h) {
-        load_res<F32>(a.r, row + c, v[i]);
-        if (a.y) unpack8(a.y[(row + c) >> 3], z[i]);
-      }
+      if (c >= a.h) continue;
+      load_res<F32>(slot, c, v[i]);
+      if (!a.y) continue;
+      unpack8(*reinterpret_cast<const uint4*>(slot + g.bytes[0] + c * 2), z[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss[0] = fmaf(z[i][j], z[i][j], ss[0]);
     }
+    // the barrier of this sum also ends the reads of the slot
+    ok = block_sum<1>(ss, red, half, ok);
+    if (threadIdx.x == 0 && ok) ring_load(a, g, full, smem, n + a.slots);
+    if (!ok) break;
     if (a.y) {
-      float ry = 1.f;
-      if (a.w_post) {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          if ((threadIdx.x + i * blockDim.x) * 8 < a.h)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss[0] = fmaf(z[i][j], z[i][j], ss[0]);
-        block_sum<1>(ss, red, slot);
-        ry = inv_rms(ss[0], a);
-      }
-      float s = a.beta;
-      if (a.gate_kind == MOE_GATE_TOKEN) s *= __ldg(a.gate + t);
-      ss[0] = 0.f;
+      if (a.w_post) s *= inv_rms(ss[0], a);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
-        float w[8];
-        if (a.w_post) {
-          load_w(a.w_post, c, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z[i][j] *= ry * w[j];
-        }
-        if (a.gate_kind == MOE_GATE_CHANNEL) {
-          load_w(a.gate, c, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[i][j] *= w[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = fmaf(s, z[i][j], a.alpha * v[i][j]);
+        for (int j = 0; j < 8; ++j) v[i][j] = fmaf(s * z[i][j], wz[i][j], a.alpha * v[i][j]);
         store_res<F32>(a.out_r, row + c, v[i]);
       }
     }
-    if (!a.w_pre) continue;
+    if (a.w_pre) {
+      ss[0] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if ((threadIdx.x + i * blockDim.x) * 8 < a.h)
+      for (int i = 0; i < kPieces; ++i)
+        if ((threadIdx.x + i * blockDim.x) * 8 < a.h)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
-    block_sum<1>(ss, red, slot);
-    const float rv = inv_rms(ss[0], a);
+          for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+      block_sum<1>(ss, red, half, true);
+      const float rv = inv_rms(ss[0], a);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c >= a.h) continue;
-      float w[8];
-      load_w(a.w_pre, c, w);
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        if (c >= a.h) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= rv * w[j];
-      a.out_u[(row + c) >> 3] = pack8(v[i]);
+        for (int j = 0; j < 8; ++j) v[i][j] *= rv * wu[i][j];
+        a.out_u[(row + c) >> 3] = pack8(v[i]);
+      }
     }
+    if (a.T - t <= static_cast<int>(gridDim.x)) return;
+    t += gridDim.x;
   }
+  if (n > 0 || static_cast<int>(blockIdx.x) < a.T) ring_drain(a, full, n);
 }
 
 // The backward of a row, with v = r_out, rv = 1 / rms(v), n = y / rms(y) (n = y
@@ -206,148 +281,189 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
 // blocks in order.
 template <bool F32>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kMaxSlots];
   __shared__ float red3[2][3 * (kMaxThreads / 32)];
   __shared__ float red1[2][kMaxThreads / 32];
-  int slot3 = 0, slot1 = 0;
+  int half3 = 0, half1 = 0;
+  const uint32_t res = a.h * (F32 ? 4 : 2), row16 = a.h * 2;
+  Ring g;
+  g.src[0] = static_cast<const uint8_t*>(a.r);
+  g.src[1] = reinterpret_cast<const uint8_t*>(a.du);
+  g.src[2] = reinterpret_cast<const uint8_t*>(a.y);
+  g.src[3] = static_cast<const uint8_t*>(a.dr_out);
+  g.bytes[0] = a.w_pre ? res : 0;
+  g.bytes[1] = a.w_pre ? row16 : 0;
+  g.bytes[2] = a.y ? row16 : 0;
+  g.bytes[3] = a.dr_out ? res : 0;
+  g.total = g.bytes[0] + g.bytes[1] + g.bytes[2] + g.bytes[3];
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.slots; ++s) moe::mbar_init(moe::smem_u32(&full[s]), 1);
+    moe::fence_mbar_init();
+    for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
+  }
+  // w_pre, and the factor of beta G in dz's product with w_post
+  float wu[kPieces][8], wz[kPieces][8];
   float P[kPieces][8], Q[kPieces][8];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i)
+  for (int i = 0; i < kPieces; ++i) {
+    const int c = (threadIdx.x + i * blockDim.x) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) P[i][j] = Q[i][j] = 0.f;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (int j = 0; j < 8; ++j) {
+      P[i][j] = Q[i][j] = 0.f;
+      wz[i][j] = 1.f;
+      wu[i][j] = 0.f;
+    }
+    if (c >= a.h) continue;
+    float w[8];
+    if (a.w_pre) load_w(a.w_pre, c, wu[i]);
+    if (a.gate_kind == MOE_GATE_CHANNEL) load_w(a.gate, c, wz[i]);
+    if (a.w_post) {
+      load_w(a.w_post, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wz[i][j] *= w[j];
+    }
+  }
+  const float al = a.y ? a.alpha : 1.f;
+  __syncthreads();
+  int n = 0;
+  bool ok = true;
+  for (int t = blockIdx.x; t < a.T; ++n) {
     const size_t row = static_cast<size_t>(t) * a.h;
-    float v[kPieces][8], g[kPieces][8], n[kPieces][8], du[kPieces][8];
+    float gt = 1.f;
+    if (a.gate_kind == MOE_GATE_TOKEN) gt = __ldg(a.gate + t);
+    ok = ring_wait(a, full, n);
+    const uint8_t* sv = smem + (n % a.slots) * a.slot_bytes;
+    const uint8_t* sdu = sv + g.bytes[0];
+    const uint8_t* sy = sdu + g.bytes[1];
+    const uint8_t* sdr = sy + g.bytes[2];
     float s3[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
       if (c >= a.h) continue;
+      float v[8], d[8];
       if (a.w_pre) {
-        load_res<F32>(a.r, row + c, v[i]);
-        unpack8(a.du[(row + c) >> 3], du[i]);
-      }
-      if (a.y) unpack8(a.y[(row + c) >> 3], n[i]);
-      if (a.dr_out) {
-        load_res<F32>(a.dr_out, row + c, g[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[i][j] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c >= a.h) continue;
-      float w[8];
-      if (a.w_pre) {
-        load_w(a.w_pre, c, w);
+        load_res<F32>(sv, c, v);
+        unpack8(*reinterpret_cast<const uint4*>(sdu + c * 2), d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          s3[0] = fmaf(v[i][j], v[i][j], s3[0]);
-          s3[1] = fmaf(du[i][j] * w[j], v[i][j], s3[1]);
+          s3[0] = fmaf(v[j], v[j], s3[0]);
+          s3[1] = fmaf(d[j] * wu[i][j], v[j], s3[1]);
         }
       }
-      if (a.w_post)
+      if (a.w_post) {
+        unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s3[2] = fmaf(n[i][j], n[i][j], s3[2]);
+        for (int j = 0; j < 8; ++j) s3[2] = fmaf(v[j], v[j], s3[2]);
+      }
     }
-    block_sum<3>(s3, red3, slot3);
-    const float rv = inv_rms(s3[0], a);
-    const float k1 = s3[1] * a.inv_h * rv * rv * rv;
+    ok = block_sum<3>(s3, red3, half3, ok);
+    if (!ok) break;
+    const float rv = a.w_pre ? inv_rms(s3[0], a) : 0.f;
+    const float k1 = s3[1] / static_cast<float>(a.h) * rv * rv * rv;
     const float ry = a.w_post ? inv_rms(s3[2], a) : 1.f;
-    const float gt = a.y && a.gate_kind == MOE_GATE_TOKEN ? __ldg(a.gate + t) : 1.f;
+    float G[kPieces][8], y[kPieces][8];
     float s1[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
       if (c >= a.h) continue;
-      float w[8], dr[8];
+      float v[8], d[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) G[i][j] = 0.f;
+      if (a.dr_out) load_res<F32>(sdr, c, G[i]);
       if (a.w_pre) {
-        load_w(a.w_pre, c, w);
+        load_res<F32>(sv, c, v);
+        unpack8(*reinterpret_cast<const uint4*>(sdu + c * 2), d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          P[i][j] = fmaf(du[i][j], v[i][j] * rv, P[i][j]);
-          g[i][j] += rv * du[i][j] * w[j] - k1 * v[i][j];
+          P[i][j] = fmaf(d[j], v[j] * rv, P[i][j]);
+          G[i][j] += rv * d[j] * wu[i][j] - k1 * v[j];
         }
       }
-      const float al = a.y ? a.alpha : 1.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dr[j] = al * g[i][j];
-      store_res<F32>(a.out_r, row + c, dr);
+      for (int j = 0; j < 8; ++j) v[j] = al * G[i][j];
+      store_res<F32>(a.out_r, row + c, v);
       if (!a.y) continue;
+      unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), y[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        n[i][j] *= ry;
-        g[i][j] *= a.beta;
-        Q[i][j] = fmaf(gt * g[i][j], n[i][j], Q[i][j]);
+        y[i][j] *= ry;
+        G[i][j] *= a.beta;
+        Q[i][j] = fmaf(gt * G[i][j], y[i][j], Q[i][j]);
+        G[i][j] *= wz[i][j];
+        s1[0] = fmaf(G[i][j], y[i][j], s1[0]);
       }
-      if (a.gate_kind == MOE_GATE_CHANNEL) {
-        load_w(a.gate, c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[i][j] *= w[j];
-      }
-      if (a.w_post) {
-        load_w(a.w_post, c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[i][j] *= w[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s1[0] = fmaf(g[i][j], n[i][j], s1[0]);
     }
-    if (!a.y) continue;
     // the projection of dy on y's row, which without the token's gate is also
-    // that gate's gradient
-    if (a.w_post || a.gate_kind == MOE_GATE_TOKEN) block_sum<1>(s1, red1, slot1);
-    const float k2 = a.w_post ? s1[0] * a.inv_h : 0.f;
+    // that gate's gradient; the barrier ends the reads of the slot
+    block_sum<1>(s1, red1, half1, true);
+    if (threadIdx.x == 0) ring_load(a, g, full, smem, n + a.slots);
+    if (a.y) {
+      const float k2 = a.w_post ? s1[0] / static_cast<float>(a.h) : 0.f;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c >= a.h) continue;
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        if (c >= a.h) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[i][j] = gt * ry * (g[i][j] - n[i][j] * k2);
-      a.out_u[(row + c) >> 3] = pack8(g[i]);
+        for (int j = 0; j < 8; ++j) G[i][j] = gt * ry * (G[i][j] - y[i][j] * k2);
+        a.out_u[(row + c) >> 3] = pack8(G[i]);
+      }
+      if (a.dgate && threadIdx.x == 0) a.dgate[t] = s1[0];
     }
-    if (a.dgate && threadIdx.x == 0) a.dgate[t] = s1[0];
+    if (a.T - t <= static_cast<int>(gridDim.x)) break;
+    t += gridDim.x;
   }
+  if (!ok) ring_drain(a, full, n);
   float* part = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.h;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
     if (c >= a.h) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      part[c + j] = P[i][j];
-      part[a.h + c + j] = Q[i][j];
+    for (int j = 0; j < 8; j += 4) {
+      *reinterpret_cast<float4*>(part + c + j) =
+          make_float4(P[i][j], P[i][j + 1], P[i][j + 2], P[i][j + 3]);
+      *reinterpret_cast<float4*>(part + a.h + c + j) =
+          make_float4(Q[i][j], Q[i][j + 1], Q[i][j + 2], Q[i][j + 3]);
     }
   }
 }
 
-// The column gradients from the blocks' sums, a fixed order for each column:
-// 8 interleaved chains, then those in order.
-__global__ void __launch_bounds__(256) block_norm_cols_kernel(const float* partial, int nblk, int h,
-                                                              const float* w_post,
-                                                              const float* gate, float* dw_pre,
-                                                              float* dw_post, float* dgate) {
-  __shared__ float sp[8][32], sq[8][32];
+// The column gradients from the blocks' sums, a fixed order for each column: 32
+// interleaved chains, then those in order.
+constexpr int kColGroups = 32;
+__global__ void __launch_bounds__(32 * kColGroups)
+    block_norm_cols_kernel(const float* partial, int nblk, int h, const float* w_post,
+                           const float* gate, float* dw_pre, float* dw_post, float* dgate) {
+  __shared__ float sp[kColGroups][33], sq[kColGroups][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float p = 0.f, q = 0.f;
-  if (c < h)
-    for (int b = g; b < nblk; b += 8) {
-      p += partial[static_cast<size_t>(b) * 2 * h + c];
-      q += partial[static_cast<size_t>(b) * 2 * h + h + c];
+  if (c < h) {
+#pragma unroll 8
+    for (int b = g; b < nblk; b += kColGroups) {
+      p += __ldcg(partial + static_cast<size_t>(b) * 2 * h + c);
+      q += __ldcg(partial + static_cast<size_t>(b) * 2 * h + h + c);
     }
+  }
   sp[g][lane] = p;
   sq[g][lane] = q;
   __syncthreads();
-  if (g != 0 || c >= h) return;
-  for (int i = 1; i < 8; ++i) {
-    p += sp[i][lane];
-    q += sq[i][lane];
+  // warp g adds up column g: lane i holds chain i
+  const int col = blockIdx.x * 32 + g;
+  p = sp[lane][g];
+  q = sq[lane][g];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    p += __shfl_xor_sync(kFull, p, o);
+    q += __shfl_xor_sync(kFull, q, o);
   }
-  if (dw_pre) dw_pre[c] = p;
-  if (dw_post) dw_post[c] = gate ? gate[c] * q : q;
-  if (dgate) dgate[c] = w_post ? w_post[c] * q : q;
+  if (lane != 0 || col >= h) return;
+  if (dw_pre) dw_pre[col] = p;
+  if (dw_post) dw_post[col] = gate ? gate[col] * q : q;
+  if (dgate) dgate[col] = w_post ? w_post[col] * q : q;
 }
 
 constexpr size_t kAlign = 256;
@@ -357,12 +473,38 @@ int threads_for(int h) {
   return (need + 31) / 32 * 32;
 }
 
-// Blocks of the backward: each keeps column sums, so only as many as run at
-// once.
-int bwd_blocks(const moe_norm_dims& d) {
-  const int per_sm = 1024 / threads_for(d.h) > 8 ? 8 : 1024 / threads_for(d.h);
+// Blocks on an SM, and the rows that each keeps on their way: about 512 threads
+// (the registers for the weights and column sums allow no more), and at least
+// two slots for each block within the shared memory.
+struct Plan {
+  int threads, blocks, slots, slot_bytes, smem;
+};
+Plan plan_of(const moe_norm_dims& d, bool bwd) {
+  constexpr int kSmem = 216 << 10;
+  Plan p;
+  p.threads = threads_for(d.h);
+  const int res = d.res_f32 ? 4 : 2;
+  p.slot_bytes = d.h * (bwd ? 2 * res + 4 : res + 2);
+  int per_sm = 512 / p.threads;
+  if (per_sm * 2 * p.slot_bytes > kSmem) per_sm = kSmem / (2 * p.slot_bytes);
+  if (per_sm < 1) per_sm = 1;
+  p.slots = kSmem / (per_sm * p.slot_bytes);
+  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+  p.smem = p.slots * p.slot_bytes;
   const int n = moe_api::num_sms() * per_sm;
-  return d.T < n ? d.T : n;
+  p.blocks = d.T < n ? d.T : n;
+  return p;
+}
+
+template <bool F32, bool BWD>
+cudaError_t launch(Args& a, const Plan& p, cudaStream_t s) {
+  auto kern = BWD ? block_norm_bwd_kernel<F32> : block_norm_fwd_kernel<F32>;
+  const cudaError_t e = moe::set_smem_once(reinterpret_cast<const void*>(kern), 216 << 10);
+  if (e != cudaSuccess) return e;
+  a.slots = p.slots;
+  a.slot_bytes = p.slot_bytes;
+  kern<<<p.blocks, p.threads, p.smem, s>>>(a);
+  return moe::launched();
 }
 
 moe_status check(const moe_norm_dims* d) {
@@ -384,7 +526,7 @@ Args args_of(const moe_norm_dims& d, const void* r, const moe_bf16* y, const flo
              const float* gate, const float* w_pre) {
   Args a = {};
   a.r = r;
-  a.y = reinterpret_cast<const uint4*>(y);
+  a.y = y;
   a.w_post = w_post;
   a.gate_kind = y ? d.gate : MOE_GATE_NONE;
   a.gate = a.gate_kind ? gate : nullptr;
@@ -394,7 +536,6 @@ Args args_of(const moe_norm_dims& d, const void* r, const moe_bf16* y, const flo
   a.eps = d.eps;
   a.alpha = d.alpha;
   a.beta = d.beta;
-  a.inv_h = 1.0f / static_cast<float>(d.h);
   return a;
 }
 
@@ -404,7 +545,7 @@ extern "C" {
 
 size_t moe_norm_workspace_bytes(const moe_norm_dims* dims) {
   if (check(dims) != MOE_OK) return 0;
-  const size_t n = static_cast<size_t>(bwd_blocks(*dims)) * 2 * dims->h * sizeof(float);
+  const size_t n = static_cast<size_t>(plan_of(*dims, true).blocks) * 2 * dims->h * sizeof(float);
   return kAlign + (n + kAlign - 1) / kAlign * kAlign;
 }
 
@@ -424,13 +565,11 @@ moe_status moe_block_norm_fwd(const moe_norm_dims* dims, const void* r, const mo
   Args a = args_of(d, r, y, w_post, gate, w_pre);
   a.out_r = r_out;
   a.out_u = reinterpret_cast<uint4*>(u);
-  const int threads = threads_for(d.h);
-  if (d.res_f32)
-    block_norm_fwd_kernel<true><<<d.T, threads, 0, s>>>(a);
-  else
-    block_norm_fwd_kernel<false><<<d.T, threads, 0, s>>>(a);
-  if (moe::launched() != cudaSuccess || !moe_api::note(s, "block_norm_fwd")) return MOE_ERR_CUDA;
-  return MOE_OK;
+  a.status = moe::nows_status_word();
+  if (!a.status) return MOE_ERR_CUDA;
+  const Plan p = plan_of(d, false);
+  const cudaError_t e = d.res_f32 ? launch<true, false>(a, p, s) : launch<false, false>(a, p, s);
+  return e == cudaSuccess && moe_api::note(s, "block_norm_fwd") ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, const moe_bf16* y,
@@ -461,23 +600,21 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_norm_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
   Args a = args_of(d, r_out, y, w_post, gate, w_pre);
-  a.du = reinterpret_cast<const uint4*>(du);
+  a.du = du;
   a.dr_out = dr_out;
   a.out_r = dr;
   a.out_u = reinterpret_cast<uint4*>(dy);
   a.dgate = a.gate_kind == MOE_GATE_TOKEN ? dgate : nullptr;
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAlign);
-  const int threads = threads_for(d.h), blocks = bwd_blocks(d);
-  if (d.res_f32)
-    block_norm_bwd_kernel<true><<<blocks, threads, 0, s>>>(a);
-  else
-    block_norm_bwd_kernel<false><<<blocks, threads, 0, s>>>(a);
-  if (moe::launched() != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
+  a.status = static_cast<int*>(ws);
+  const Plan p = plan_of(d, true);
+  const cudaError_t e = d.res_f32 ? launch<true, true>(a, p, s) : launch<false, true>(a, p, s);
+  if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (dw_pre || dw_post || channel) {
-    block_norm_cols_kernel<<<(d.h + 31) / 32, 256, 0, s>>>(a.partial, blocks, d.h, w_post,
-                                                           channel ? gate : nullptr, dw_pre,
-                                                           dw_post, channel ? dgate : nullptr);
+    block_norm_cols_kernel<<<(d.h + 31) / 32, 32 * kColGroups, 0, s>>>(
+        a.partial, p.blocks, d.h, w_post, channel ? gate : nullptr, dw_pre, dw_post,
+        channel ? dgate : nullptr);
     if (moe::launched() != cudaSuccess || !moe_api::note(s, "block_norm_cols")) return MOE_ERR_CUDA;
   }
   return MOE_OK;
