@@ -158,10 +158,28 @@ def _addr(t) -> int | None:
     return t.data_ptr()
 
 
+_RAW_STREAM = None    # torch's lookup of a device's current stream by index
+
+
+def _current_stream() -> int:
+    """The current stream's handle, without building a torch.cuda.Stream for every call (2 us of
+    the few that a small kernel takes)."""
+    global _RAW_STREAM
+    if _RAW_STREAM is None:
+        import torch
+        handle = torch.cuda.current_stream().cuda_stream    # also initialises CUDA
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if raw is None or device is None:
+            return handle
+        _RAW_STREAM = (raw, device)
+    raw, device = _RAW_STREAM
+    return raw(device())
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -48,93 +48,137 @@ struct Args {
   int T, h;
   int gate_kind;
   int slots, slot_bytes;
-  float eps, alpha, beta;
+  float eps, alpha, beta, inv_h;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& q, float* v) {
+// Pairs of fp32 values for Blackwell's packed arithmetic: these kernels issue
+// about 20 instructions for each element otherwise, which bounded them.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ float sum2(f2 v) {
+  const float2 s = split(v);
+  return s.x + s.y;
+}
+
+// Eight bf16 values as four pairs, and back.
+__device__ __forceinline__ void unpack8(const uint4& q, f2* v) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float* v) {
+__device__ __forceinline__ uint4 pack8(const f2* v) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    const float2 s = split(v[i]);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(s.x, s.y);
     w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight fp32 values, as the residual stream and the channel weights have them.
+__device__ __forceinline__ void load8(const float* p, f2* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = pair(a.x, a.y);
+  v[1] = pair(a.z, a.w);
+  v[2] = pair(b.x, b.y);
+  v[3] = pair(b.z, b.w);
+}
+__device__ __forceinline__ void store8(float* p, const f2* v) {
+  const float2 a = split(v[0]), b = split(v[1]), c = split(v[2]), d = split(v[3]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+}
 // Eight values of the residual stream at element offset o.
 template <bool F32>
-__device__ __forceinline__ void load_res(const void* p, size_t o, float* v) {
-  if (F32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + o);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
+__device__ __forceinline__ void load_res(const void* p, size_t o, f2* v) {
+  if (F32)
+    load8(static_cast<const float*>(p) + o, v);
+  else
     unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + o), v);
-  }
 }
 // Stores eight values in the residual's type and leaves the stored ones in v.
 template <bool F32>
-__device__ __forceinline__ void store_res(void* p, size_t o, float* v) {
+__device__ __forceinline__ void store_res(void* p, size_t o, f2* v) {
   if (F32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + o);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    store8(static_cast<float*>(p) + o, v);
   } else {
     const uint4 q = pack8(v);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + o) = q;
     unpack8(q, v);
   }
 }
-__device__ __forceinline__ void load_w(const float* w, int c, float* v) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w + c));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
 
-// Sums of N values over the block, in every thread.  The order is fixed:
-// butterflies within warps, then the warps in order.  `slot` alternates so
-// that one barrier for each call is enough.  Returns whether `ok` held in
-// every thread.
-template <int N>
-__device__ __forceinline__ bool block_sum(float (&v)[N], float (*red)[N * (kMaxThreads / 32)],
-                                          int& slot, bool ok) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
-  const int nw = blockDim.x >> 5;
-  if (nw == 1) {
-    __syncwarp();
-    return __all_sync(kFull, ok);
+// Sums over the block, in every thread.  The order is fixed: a butterfly within
+// each warp, then the warps in order.  red[..][warp] of the warps that do not
+// exist is zero.  `half` alternates so that one barrier for each call is enough.
+// Returns whether `ok` held in every thread.
+__device__ __forceinline__ float sum_warps(const float* s) {
+  const float4* q = reinterpret_cast<const float4*>(s);
+  const float4 a = q[0], b = q[1];
+  float v = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+  if (blockDim.x > 256) {
+    const float4 c = q[2], d = q[3];
+    v += ((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w));
   }
-  float* s = red[slot];
-  slot ^= 1;
-  if ((threadIdx.x & 31) == 0)
+  return v;
+}
+typedef float Red1[2][16];
+typedef float Red3[2][4][16];
+__device__ __forceinline__ bool block_sum(float& v, Red1& red, int& half, bool ok) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[(threadIdx.x >> 5) * N + i] = v[i];
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if ((threadIdx.x & 31) == 0) red[half][threadIdx.x >> 5] = v;
+  ok = __syncthreads_and(ok);
+  v = sum_warps(red[half]);
+  half ^= 1;
+  return ok;
+}
+// Three sums: each exchange halves what a lane holds, so that 6 shuffles do
+// instead of 15; lanes 0, 8 and 16 end up with one sum each.
+__device__ __forceinline__ bool block_sum3(float (&v)[3], Red3& red, int& half, bool ok) {
+  const int lane = threadIdx.x & 31;
+  const bool hi = lane & 16, mid = lane & 8;
+  float x0 = (hi ? v[2] : v[0]) + __shfl_xor_sync(kFull, hi ? v[0] : v[2], 16);
+  float x1 = (hi ? 0.f : v[1]) + __shfl_xor_sync(kFull, hi ? v[1] : 0.f, 16);
+  x0 = (mid ? x1 : x0) + __shfl_xor_sync(kFull, mid ? x0 : x1, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x0 += __shfl_xor_sync(kFull, x0, o);
+  if ((lane & 7) == 0) red[half][lane >> 3][threadIdx.x >> 5] = x0;
   ok = __syncthreads_and(ok);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int w = 0; w < nw; ++w)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += s[w * N + i];
+  for (int i = 0; i < 3; ++i) v[i] = sum_warps(red[half][i]);
+  half ^= 1;
   return ok;
 }
 
-// 1 / rms of a row from its sum of squares, correctly rounded: its error would
-// shift a whole row, and one for each row costs nothing.
+// 1 / rms of a row from its sum of squares: the fast reciprocal root and one
+// Newton step, within about an ulp (0 where the sum overflowed).
 __device__ __forceinline__ float inv_rms(float ss, const Args& a) {
-  return __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(a.h)) + a.eps);
+  const float x = fmaf(ss, a.inv_h, a.eps), y = rsqrtf(x);
+  return x < INFINITY ? fmaf(0.5f * y, fmaf(-x * y, y, 1.f), y) : y;
 }
 
 // The block's ring of rows.  Row number n of the block (token blockIdx.x + n *
@@ -176,8 +220,9 @@ template <bool F32>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxSlots];
-  __shared__ float red[2][kMaxThreads / 32];
+  __shared__ __align__(16) Red1 red;
   int half = 0;
+  if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
   Ring g;
   g.src[0] = static_cast<const uint8_t*>(a.r);
   g.src[1] = reinterpret_cast<const uint8_t*>(a.y);
@@ -191,25 +236,25 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
     for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
   }
   // the scale of each of my columns of y, and of u
-  float wz[kPieces][8], wu[kPieces][8];
+  f2 wz[kPieces][4], wu[kPieces][4];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
     if (c >= a.h) continue;
-    float w[8];
+    f2 w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) wz[i][j] = a.beta;
+    for (int j = 0; j < 4; ++j) wz[i][j] = both(a.beta);
     if (a.gate_kind == MOE_GATE_CHANNEL) {
-      load_w(a.gate, c, w);
+      load8(a.gate + c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wz[i][j] *= w[j];
+      for (int j = 0; j < 4; ++j) wz[i][j] = mul2(wz[i][j], w[j]);
     }
     if (a.w_post) {
-      load_w(a.w_post, c, w);
+      load8(a.w_post + c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wz[i][j] *= w[j];
+      for (int j = 0; j < 4; ++j) wz[i][j] = mul2(wz[i][j], w[j]);
     }
-    if (a.w_pre) load_w(a.w_pre, c, wu[i]);
+    if (a.w_pre) load8(a.w_pre + c, wu[i]);
   }
   __syncthreads();
   int n = 0;
@@ -219,8 +264,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
     if (a.gate_kind == MOE_GATE_TOKEN) s = __ldg(a.gate + t);
     bool ok = ring_wait(a, full, n);
     const uint8_t* slot = smem + (n % a.slots) * a.slot_bytes;
-    float v[kPieces][8], z[kPieces][8];
-    float ss[1] = {0.f};
+    f2 v[kPieces][4], z[kPieces][4], acc = 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -229,38 +273,42 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
       if (!a.y) continue;
       unpack8(*reinterpret_cast<const uint4*>(slot + g.bytes[0] + c * 2), z[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss[0] = fmaf(z[i][j], z[i][j], ss[0]);
+      for (int j = 0; j < 4; ++j) acc = fma2(z[i][j], z[i][j], acc);
     }
     // the barrier of this sum also ends the reads of the slot
-    ok = block_sum<1>(ss, red, half, ok);
+    float ss = sum2(acc);
+    ok = block_sum(ss, red, half, ok);
     if (threadIdx.x == 0 && ok) ring_load(a, g, full, smem, n + a.slots);
     if (!ok) break;
     if (a.y) {
-      if (a.w_post) s *= inv_rms(ss[0], a);
+      if (a.w_post) s *= inv_rms(ss, a);
+      const f2 s2 = both(s), al = both(a.alpha);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = fmaf(s * z[i][j], wz[i][j], a.alpha * v[i][j]);
+        for (int j = 0; j < 4; ++j)
+          v[i][j] = fma2(mul2(s2, z[i][j]), wz[i][j], mul2(al, v[i][j]));
         store_res<F32>(a.out_r, row + c, v[i]);
       }
     }
     if (a.w_pre) {
-      ss[0] = 0.f;
+      acc = 0;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
         if ((threadIdx.x + i * blockDim.x) * 8 < a.h)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
-      block_sum<1>(ss, red, half, true);
-      const float rv = inv_rms(ss[0], a);
+          for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
+      ss = sum2(acc);
+      block_sum(ss, red, half, true);
+      const f2 rv = both(inv_rms(ss, a));
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= rv * wu[i][j];
+        for (int j = 0; j < 4; ++j) v[i][j] = mul2(mul2(rv, v[i][j]), wu[i][j]);
         a.out_u[(row + c) >> 3] = pack8(v[i]);
       }
     }
@@ -274,18 +322,20 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
 // without w_post), and the row sums S:
 //   G  = dr_out + rv (du w_pre - v rv^2 S(du w_pre v) / h)
 //   q  = beta gate G;  dy = (q w_post - n S(q w_post n) / h) / rms(y)
-// Column sums: P = sum_t du v rv (dw_pre) and Q = sum_t beta g_t G n, from which
-// dw_post = gate_c Q and the channel gate's gradient = w_post Q, so one sum
-// serves both (g_t: the token gate, else 1).  Each block keeps P and Q of its
+// Column sums: P = sum_t du v rv (dw_pre) and Q = sum_t g_t G n, from which
+// dw_post = beta gate_c Q and the channel gate's gradient = beta w_post Q, so one
+// sum serves both (g_t: the token gate, else 1).  Each block keeps P and Q of its
 // rows in registers and writes them once; block_norm_cols_kernel adds the
 // blocks in order.
 template <bool F32>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxSlots];
-  __shared__ float red3[2][3 * (kMaxThreads / 32)];
-  __shared__ float red1[2][kMaxThreads / 32];
+  __shared__ __align__(16) Red3 red3;
+  __shared__ __align__(16) Red1 red1;
   int half3 = 0, half1 = 0;
+  for (int i = threadIdx.x; i < 2 * 4 * 16; i += blockDim.x) (&red3[0][0][0])[i] = 0.f;
+  if (threadIdx.x < 32) red1[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
   const uint32_t res = a.h * (F32 ? 4 : 2), row16 = a.h * 2;
   Ring g;
   g.src[0] = static_cast<const uint8_t*>(a.r);
@@ -302,132 +352,134 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args 
     moe::fence_mbar_init();
     for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
   }
-  // w_pre, and the factor of beta G in dz's product with w_post
-  float wu[kPieces][8], wz[kPieces][8];
-  float P[kPieces][8], Q[kPieces][8];
+  // w_pre, and the factor of G in dz's product with w_post
+  f2 wu[kPieces][4], wz[kPieces][4];
+  f2 P[kPieces][4], Q[kPieces][4];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      P[i][j] = Q[i][j] = 0.f;
-      wz[i][j] = 1.f;
-      wu[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      P[i][j] = Q[i][j] = wu[i][j] = 0;
+      wz[i][j] = both(a.beta);
     }
     if (c >= a.h) continue;
-    float w[8];
-    if (a.w_pre) load_w(a.w_pre, c, wu[i]);
-    if (a.gate_kind == MOE_GATE_CHANNEL) load_w(a.gate, c, wz[i]);
-    if (a.w_post) {
-      load_w(a.w_post, c, w);
+    f2 w[4];
+    if (a.w_pre) load8(a.w_pre + c, wu[i]);
+    if (a.gate_kind == MOE_GATE_CHANNEL) {
+      load8(a.gate + c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wz[i][j] *= w[j];
+      for (int j = 0; j < 4; ++j) wz[i][j] = mul2(wz[i][j], w[j]);
+    }
+    if (a.w_post) {
+      load8(a.w_post + c, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wz[i][j] = mul2(wz[i][j], w[j]);
     }
   }
   const float al = a.y ? a.alpha : 1.f;
+  const bool token = a.gate_kind == MOE_GATE_TOKEN;
   __syncthreads();
   int n = 0;
   bool ok = true;
   for (int t = blockIdx.x; t < a.T; ++n) {
     const size_t row = static_cast<size_t>(t) * a.h;
     float gt = 1.f;
-    if (a.gate_kind == MOE_GATE_TOKEN) gt = __ldg(a.gate + t);
+    if (token) gt = __ldg(a.gate + t);
     ok = ring_wait(a, full, n);
     const uint8_t* sv = smem + (n % a.slots) * a.slot_bytes;
     const uint8_t* sdu = sv + g.bytes[0];
     const uint8_t* sy = sdu + g.bytes[1];
     const uint8_t* sdr = sy + g.bytes[2];
-    float s3[3] = {0.f, 0.f, 0.f};
+    f2 acc[3] = {0, 0, 0};
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
       if (c >= a.h) continue;
-      float v[8], d[8];
+      f2 v[4], d[4];
       if (a.w_pre) {
         load_res<F32>(sv, c, v);
         unpack8(*reinterpret_cast<const uint4*>(sdu + c * 2), d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s3[0] = fmaf(v[j], v[j], s3[0]);
-          s3[1] = fmaf(d[j] * wu[i][j], v[j], s3[1]);
+        for (int j = 0; j < 4; ++j) {
+          acc[0] = fma2(v[j], v[j], acc[0]);
+          acc[1] = fma2(mul2(d[j], wu[i][j]), v[j], acc[1]);
         }
       }
       if (a.w_post) {
         unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s3[2] = fmaf(v[j], v[j], s3[2]);
+        for (int j = 0; j < 4; ++j) acc[2] = fma2(v[j], v[j], acc[2]);
       }
     }
-    ok = block_sum<3>(s3, red3, half3, ok);
+    float s3[3] = {sum2(acc[0]), sum2(acc[1]), sum2(acc[2])};
+    ok = block_sum3(s3, red3, half3, ok);
     if (!ok) break;
-    const float rv = a.w_pre ? inv_rms(s3[0], a) : 0.f;
-    const float k1 = s3[1] / static_cast<float>(a.h) * rv * rv * rv;
-    const float ry = a.w_post ? inv_rms(s3[2], a) : 1.f;
-    float G[kPieces][8], y[kPieces][8];
-    float s1[1] = {0.f};
+    const float rvs = a.w_pre ? inv_rms(s3[0], a) : 0.f;
+    const float rys = a.w_post ? inv_rms(s3[2], a) : 1.f;
+    const f2 rv = both(rvs), k1 = both(-s3[1] * a.inv_h * rvs * rvs * rvs);
+    const f2 ry = both(rys), al2 = both(al), gt2 = both(gt);
+    f2 G[kPieces][4], y[kPieces][4], dot = 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
       if (c >= a.h) continue;
-      float v[8], d[8];
+      f2 v[4], d[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) G[i][j] = 0.f;
+      for (int j = 0; j < 4; ++j) G[i][j] = 0;
       if (a.dr_out) load_res<F32>(sdr, c, G[i]);
       if (a.w_pre) {
         load_res<F32>(sv, c, v);
         unpack8(*reinterpret_cast<const uint4*>(sdu + c * 2), d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          P[i][j] = fmaf(d[j], v[j] * rv, P[i][j]);
-          G[i][j] += rv * d[j] * wu[i][j] - k1 * v[j];
+        for (int j = 0; j < 4; ++j) {
+          const f2 dn = mul2(rv, d[j]);
+          P[i][j] = fma2(dn, v[j], P[i][j]);
+          G[i][j] = fma2(dn, wu[i][j], fma2(k1, v[j], G[i][j]));
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = al * G[i][j];
+      for (int j = 0; j < 4; ++j) v[j] = mul2(al2, G[i][j]);
       store_res<F32>(a.out_r, row + c, v);
       if (!a.y) continue;
       unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), y[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        y[i][j] *= ry;
-        G[i][j] *= a.beta;
-        Q[i][j] = fmaf(gt * G[i][j], y[i][j], Q[i][j]);
-        G[i][j] *= wz[i][j];
-        s1[0] = fmaf(G[i][j], y[i][j], s1[0]);
+      for (int j = 0; j < 4; ++j) {
+        y[i][j] = mul2(ry, y[i][j]);
+        Q[i][j] = fma2(token ? mul2(gt2, G[i][j]) : G[i][j], y[i][j], Q[i][j]);
+        G[i][j] = mul2(G[i][j], wz[i][j]);
+        dot = fma2(G[i][j], y[i][j], dot);
       }
     }
     // the projection of dy on y's row, which without the token's gate is also
     // that gate's gradient; the barrier ends the reads of the slot
-    block_sum<1>(s1, red1, half1, true);
+    float s1 = sum2(dot);
+    block_sum(s1, red1, half1, true);
     if (threadIdx.x == 0) ring_load(a, g, full, smem, n + a.slots);
     if (a.y) {
-      const float k2 = a.w_post ? s1[0] / static_cast<float>(a.h) : 0.f;
+      const f2 k2 = both(a.w_post ? -s1 * a.inv_h : 0.f), scale = both(gt * rys);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) G[i][j] = gt * ry * (G[i][j] - y[i][j] * k2);
+        for (int j = 0; j < 4; ++j) G[i][j] = mul2(scale, fma2(k2, y[i][j], G[i][j]));
         a.out_u[(row + c) >> 3] = pack8(G[i]);
       }
-      if (a.dgate && threadIdx.x == 0) a.dgate[t] = s1[0];
+      if (a.dgate && threadIdx.x == 0) a.dgate[t] = s1;
     }
     if (a.T - t <= static_cast<int>(gridDim.x)) break;
     t += gridDim.x;
   }
+  cudaTriggerProgrammaticLaunchCompletion();
   if (!ok) ring_drain(a, full, n);
   float* part = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.h;
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
     if (c >= a.h) continue;
-#pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      *reinterpret_cast<float4*>(part + c + j) =
-          make_float4(P[i][j], P[i][j + 1], P[i][j + 2], P[i][j + 3]);
-      *reinterpret_cast<float4*>(part + a.h + c + j) =
-          make_float4(Q[i][j], Q[i][j + 1], Q[i][j + 2], Q[i][j + 3]);
-    }
+    store8(part + c, P[i]);
+    store8(part + a.h + c, Q[i]);
   }
 }
 
@@ -436,7 +488,10 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args 
 constexpr int kColGroups = 32;
 __global__ void __launch_bounds__(32 * kColGroups)
     block_norm_cols_kernel(const float* partial, int nblk, int h, const float* w_post,
-                           const float* gate, float* dw_pre, float* dw_post, float* dgate) {
+                           const float* gate, float beta, float* dw_pre, float* dw_post,
+                           float* dgate) {
+  // this kernel is launched while the rows' kernel still runs
+  cudaGridDependencySynchronize();
   __shared__ float sp[kColGroups][33], sq[kColGroups][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -461,6 +516,7 @@ __global__ void __launch_bounds__(32 * kColGroups)
     q += __shfl_xor_sync(kFull, q, o);
   }
   if (lane != 0 || col >= h) return;
+  q *= beta;
   if (dw_pre) dw_pre[col] = p;
   if (dw_post) dw_post[col] = gate ? gate[col] * q : q;
   if (dgate) dgate[col] = w_post ? w_post[col] * q : q;
@@ -536,6 +592,7 @@ Args args_of(const moe_norm_dims& d, const void* r, const moe_bf16* y, const flo
   a.eps = d.eps;
   a.alpha = d.alpha;
   a.beta = d.beta;
+  a.inv_h = 1.0f / static_cast<float>(d.h);
   return a;
 }
 
@@ -612,9 +669,20 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
   if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (dw_pre || dw_post || channel) {
-    block_norm_cols_kernel<<<(d.h + 31) / 32, 32 * kColGroups, 0, s>>>(
-        a.partial, p.blocks, d.h, w_post, channel ? gate : nullptr, dw_pre, dw_post,
-        channel ? dgate : nullptr);
+    // launched ahead of the rows' kernel's end, which it waits for itself
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((d.h + 31) / 32, 1, 1);
+    cfg.blockDim = dim3(32 * kColGroups, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, block_norm_cols_kernel, static_cast<const float*>(a.partial),
+                           p.blocks, d.h, w_post, channel ? gate : nullptr, d.beta, dw_pre,
+                           dw_post, channel ? dgate : nullptr) != cudaSuccess)
+      return MOE_ERR_CUDA;
     if (moe::launched() != cudaSuccess || !moe_api::note(s, "block_norm_cols")) return MOE_ERR_CUDA;
   }
   return MOE_OK;
