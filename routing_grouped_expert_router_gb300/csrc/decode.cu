@@ -51,6 +51,7 @@ namespace {
 // the others help where a phase's work is spread over all threads.
 constexpr int kThreads = 512;
 constexpr int kHelpers = kThreads - 64;
+constexpr int kIdleWarps = kThreads / 32 - 6;  // neither of those roles
 constexpr int kWBytes = 32768;     // weights of a stage
 constexpr int kMaxStages = 6;
 constexpr int kQueue = 4;          // pieces between the producer and the others
@@ -120,7 +121,7 @@ struct alignas(16) Ctrl {
 // 345 us for the fastest SM's share of FC1, 389 us for the slowest's).  Below
 // kRoundsFrom k-steps for each block the phase is too short to gain by it.
 constexpr int kRounds = 4;
-constexpr unsigned kRoundsFrom = 96;
+constexpr unsigned kRoundsFrom = 48;
 struct Cut {
   unsigned total, blocks, rounds;
   unsigned at[kRounds + 1];  // rounds' borders
@@ -129,7 +130,7 @@ struct Cut {
   __device__ Cut(unsigned n, unsigned grid, unsigned tile_steps) : total(n) {
     rounds = n >= kRoundsFrom * grid ? kRounds : 1;
     blocks = n < grid ? n : grid;
-    const unsigned share = n / grid, least = max(8u, tile_steps / 16u);
+    const unsigned share = n / grid, least = max(4u, tile_steps / 16u);
     at[0] = 0;
     at[4] = n;
     at[3] = rounds == 1 ? n : n - grid * max(least, share * 3u / 100u);
@@ -184,17 +185,15 @@ __device__ __forceinline__ bool wait_count(const unsigned* word, unsigned target
       }
     }
   }
-  __threadfence();
   return true;
 }
 
-// A barrier over the grid, by one thread of each block: everything that the
-// block's threads wrote before it (they are ordered before this thread by a
-// block barrier) is seen by every block after it.  `target` counts all
+// A barrier over the grid, by one thread of each block between two barriers of
+// the block: everything that its threads wrote before is seen by every block
+// after.  Release and acquire carry that; full fences made it 0.4 us slower.  `target` counts all
 // arrivals of the launch so far.
 __device__ __forceinline__ bool grid_barrier(unsigned* word, unsigned target, int* status) {
-  __threadfence();
-  atomicAdd(word, 1u);
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(word) : "memory");
   return wait_count(word, target, status);
 }
 
@@ -360,16 +359,18 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
     // [group][slice][token][expert]
     float* mine = p.logits + static_cast<size_t>(unit) * p.tok_group * p.E;
     add_parts(mine, p.E, nullptr);
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
-      const unsigned n = atomicAdd(words + kGroupWord + g, 1u);
+      unsigned n;
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                   : "=r"(n)
+                   : "l"(words + kGroupWord + g)
+                   : "memory");
       c.flag = n + 1 == static_cast<unsigned>(p.slices);
       if (c.flag) words[kGroupWord + g] = 0;
     }
     __syncthreads();
     if (!c.flag) continue;
-    __threadfence();
     const float* all = p.logits + static_cast<size_t>(g) * p.slices * p.tok_group * p.E;
     const int n = p.slices * p.tok_group * p.E;
 #pragma unroll 8
@@ -541,94 +542,124 @@ __device__ __forceinline__ void store_h4(const Params& p, const Ctrl& c, int row
   }
 }
 
-// y: 128 columns of a token to a warp.  Lane j first looks up slot j's row and
-// the pieces that its tile went through (done by every thread for every slot, the
-// divisions alone cost 4 us).  Then eight chains of loads run side by side, since
-// this is latency: LANES of them for each of up to 8 / LANES slots, the slot's
-// row of O and the parts that other pieces left of it dealt out to them in turn.
-template <int LANES>
-__device__ void combine(const Params& p, const Ctrl& c, const Cut& cut, unsigned tiles,
-                        unsigned ksn) {
-  const int lane = threadIdx.x & 31, blocks = (p.h + 127) / 128;
-  const size_t stride = static_cast<size_t>(LANES) * p.T * 64;  // float4s
-  for (int i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < p.T * blocks;
-       i += gridDim.x * (kThreads / 32)) {
-    const int t = i / blocks, b = i - t * blocks, col = b * 128 + lane * 4;
-    const bool in = col < p.h;
-    int my_row = -1, my_n = 0;   // its row; further parts
-    unsigned my_at = 0;          // its row in the first piece's part
-    float my_gate = 0.f;
-    if (lane < p.k) {
-      const int a = t * p.k + lane;
-      my_row = c.pos[a];
-      if (my_row >= 0) {
-        my_gate = c.gate[a];
-        const int e = c.exp[a];
-        const unsigned q = (c.act_of[e] * tiles + b / 2) * ksn, first = cut.piece_of(q);
-        my_n = cut.piece_of(q + ksn - 1) - first;
-        my_at = first * p.T + my_row - c.off[e];
-      }
+// y: 64 columns of a token to a warp, four to a lane, each half of the warp
+// with every second sum.  This is latency: lane j of the first 8 looks up slot
+// j's row and the pieces that its tile went through (a warp that waits for the
+// end of FC2 does so ahead), then eight chains of loads run side by side, LANES
+// of them for each of up to 8 / LANES slots, with the slot's row of O and the
+// parts that other pieces left of it dealt out to them and the halves in turn.
+struct Look {
+  int row, n;      // the slot's row; how many further parts
+  unsigned at;     // the row's place in the first piece's part
+  float gate;
+};
+__device__ __forceinline__ Look look_of(const Params& p, const Ctrl& c, const Cut& cut,
+                                        unsigned tiles, unsigned ksn, int t, int b, int lane) {
+  Look l = {-1, 0, 0, 0.f};
+  if (lane < p.k) {
+    const int a = t * p.k + lane;
+    l.row = c.pos[a];
+    if (l.row >= 0) {
+      l.gate = c.gate[a];
+      const int e = c.exp[a];
+      const unsigned q = (c.act_of[e] * tiles + b / 4) * ksn, first = cut.piece_of(q);
+      l.n = cut.piece_of(q + ksn - 1) - first;
+      l.at = first * p.T + l.row - c.off[e];
     }
-    float4 v[8];
-    const float4* src[8];
-    int left[8];
+  }
+  return l;
+}
+template <int LANES>
+__device__ __forceinline__ void combine(const Params& p, const Look& l, int t, int b, int lane) {
+  constexpr int kStep = 2 * LANES;
+  const int half = lane >> 4, col = b * 64 + (lane & 15) * 4;
+  const size_t stride = static_cast<size_t>(kStep) * p.T * 64;  // float4s
+  float4 v[8];
+  const float4* src[8];
+  int left[8];
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const int j = w / LANES, u = (w % LANES) * 2 + half;  // u: the first sum of this chain
+    const int row = __shfl_sync(kFull, l.row, j), n = __shfl_sync(kFull, l.n, j);
+    const unsigned at = __shfl_sync(kFull, l.at, j);
+    v[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+    left[w] = row >= 0 && n >= u ? (n - u) / kStep + 1 : 0;
+    src[w] = reinterpret_cast<const float4*>(p.part) +
+             (static_cast<size_t>(at + u * p.T) * 64 + (col & 255) / 4);
+    if (u == 0 && row >= 0) {
+      v[w] = __ldcg(reinterpret_cast<const float4*>(p.O + static_cast<size_t>(row) * p.h + col));
+      src[w] += stride;
+      --left[w];
+    }
+  }
+  for (bool any = true; any;) {
+    any = false;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      constexpr int kLanes = LANES;
-      const int j = w / kLanes, u = w % kLanes;
-      const int row = __shfl_sync(kFull, my_row, j), n = __shfl_sync(kFull, my_n, j);
-      const unsigned at = __shfl_sync(kFull, my_at, j);
-      v[w] = make_float4(0.f, 0.f, 0.f, 0.f);
-      left[w] = row >= 0 && n >= u ? (n - u) / kLanes + 1 : 0;
-      src[w] = reinterpret_cast<const float4*>(p.part) +
-               (static_cast<size_t>(at + u * p.T) * 64 + (col & 255) / 4);
-      if (u == 0 && row >= 0) {
-        if (in)
-          v[w] = __ldcg(
-              reinterpret_cast<const float4*>(p.O + static_cast<size_t>(row) * p.h + col));
-        src[w] += stride;
-        --left[w];
-      }
+      if (left[w] == 0) continue;
+      any = true;
+      v[w] = add4(v[w], __ldcg(src[w]));
+      src[w] += stride;
+      --left[w];
     }
-    for (bool any = true; any;) {
-      any = false;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        if (left[w] == 0) continue;
-        any = true;
-        const float4 x = __ldcg(src[w]);
-        src[w] += stride;
-        --left[w];
-        v[w].x += x.x;
-        v[w].y += x.y;
-        v[w].z += x.z;
-        v[w].w += x.w;
-      }
-    }
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < 8 / LANES; ++j) {
-      float4 o = v[j * LANES];
-#pragma unroll
-      for (int u = 1; u < LANES; ++u) {
-        const float4 x = v[j * LANES + u];
-        o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-      }
-      const float g = __shfl_sync(kFull, my_gate, j);
-      if (__shfl_sync(kFull, my_row, j) < 0) continue;
-      sum.x = fmaf(g, o.x, sum.x);
-      sum.y = fmaf(g, o.y, sum.y);
-      sum.z = fmaf(g, o.z, sum.z);
-      sum.w = fmaf(g, o.w, sum.w);
-    }
-    if (!in) continue;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z, sum.w);
-    uint2 out;
-    out.x = *reinterpret_cast<const uint32_t*>(&lo);
-    out.y = *reinterpret_cast<const uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t) * p.h + col) = out;
   }
+  __syncwarp();
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < 8 / LANES; ++j) {
+    float4 o = v[j * LANES];
+#pragma unroll
+    for (int u = 1; u < LANES; ++u) o = add4(o, v[j * LANES + u]);
+    const float g = __shfl_sync(kFull, l.gate, j);
+    if (__shfl_sync(kFull, l.row, j) < 0) continue;
+    sum.x = fmaf(g, o.x, sum.x);
+    sum.y = fmaf(g, o.y, sum.y);
+    sum.z = fmaf(g, o.z, sum.z);
+    sum.w = fmaf(g, o.w, sum.w);
+  }
+  sum.x += __shfl_xor_sync(kFull, sum.x, 16);
+  sum.y += __shfl_xor_sync(kFull, sum.y, 16);
+  sum.z += __shfl_xor_sync(kFull, sum.z, 16);
+  sum.w += __shfl_xor_sync(kFull, sum.w, 16);
+  if (half) return;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(sum.z, sum.w);
+  uint2 out;
+  out.x = *reinterpret_cast<const uint32_t*>(&lo);
+  out.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t) * p.h + col) = out;
+}
+
+// Two rows of a tile of FC1 that pieces share: the sum left by the piece that
+// began it, then the parts of the pieces after it, in order.
+struct Join {
+  unsigned work;
+  int e, row, rows, col;
+  unsigned parts;
+  const float4* src;
+};
+template <bool F8>
+__device__ __forceinline__ void join_rows(const Params& p, const Ctrl& c, const Join& j, int lane) {
+  const size_t slot = static_cast<size_t>(p.T) * 64;  // float4s
+  const unsigned odd = j.rows > 1 ? 64 : 0;
+  const float4* src = j.src;
+  float4 va = __ldcg(src), vb = __ldcg(src + 32);
+  float4 ua = __ldcg(src + odd), ub = __ldcg(src + odd + 32);
+  src += slot;
+#pragma unroll 4
+  for (unsigned o = 0; o < j.parts; ++o, src += 2 * slot) {
+    va = add4(va, __ldcg(src));
+    vb = add4(vb, __ldcg(src + 32));
+    ua = add4(ua, __ldcg(src + odd));
+    ub = add4(ub, __ldcg(src + odd + 32));
+  }
+  float4 w1 = make_float4(0.f, 0.f, 0.f, 0.f), w3 = w1;
+  if (F8) {
+    w1 = __ldg(reinterpret_cast<const float4*>(p.s1 + static_cast<size_t>(j.e) * p.f + j.col));
+    w3 = __ldg(reinterpret_cast<const float4*>(p.s3 + static_cast<size_t>(j.e) * p.f + j.col));
+  }
+  store_h4<F8>(p, c, j.row, j.col, va, vb, w1, w3, lane);
+  if (odd) store_h4<F8>(p, c, j.row + 1, j.col, ua, ub, w1, w3, lane);
 }
 
 template <bool F8>
@@ -1003,6 +1034,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++it;
         q = end;
       }
+      // The tiles that pieces share are joined after the barrier below, by the
+      // warps that have nothing to do before it and so look up their first one:
+      // a tile goes with the first border inside it, two of its rows to a warp,
+      // four columns to a lane.
+      Join join = {};
+      const unsigned pairs = (c.most + 1) / 2, works = cut1.rounds * cut1.blocks * pairs;
+      auto look_up = [&] {
+        join.rows = 0;
+        if (join.work >= works) return;
+        const unsigned i = join.work / pairs, i0 = (join.work - i * pairs) * 2;
+        const unsigned begin = cut1.start(i), item = begin / ks1, ai = item / nt1;
+        join.e = c.act[ai];
+        const unsigned n = c.off[join.e + 1] - c.off[join.e];
+        if (i0 >= n || begin == item * ks1 || cut1.piece_of(item * ks1) != i - 1) return;
+        join.row = c.off[join.e] + i0;
+        join.rows = min(n - i0, 2u);
+        join.col = (item - ai * nt1) * 128 + lane * 4;
+        join.parts = cut1.piece_of((item + 1) * ks1 - 1) - i + 1;
+        join.src = reinterpret_cast<const float4*>(
+                       p.part + (2 * i - 1) * (static_cast<size_t>(2) * p.T * 128) + i0 * 256) +
+                   lane;
+      };
+      const int idle = warp < 4 ? warp - 2 : warp - 6;  // 0 .. kIdleWarps - 1
+      join.work = works;
+      if (!epilogue) {
+        join.work = cta + idle * G;
+        look_up();
+      }
       unsigned arrived = G;
       auto grid_sync = [&] {
         fence_proxy_async_all();
@@ -1012,38 +1071,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         helper_sync();
       };
       grid_sync();
-      // The tiles that pieces share, each in the order of its pieces: a tile goes
-      // with the first border inside it, two of its rows to a warp, four columns
-      // to a lane.
       if (!*abort_flag) {
-        const size_t slot = static_cast<size_t>(2) * p.T * 128;
-        const unsigned pairs = (c.most + 1) / 2, work = cut1.rounds * cut1.blocks * pairs;
-        for (unsigned w = cta * (kHelpers / 32) + warp - 2; w < work; w += G * (kHelpers / 32)) {
-          const unsigned i = w / pairs, i0 = (w - i * pairs) * 2, begin = cut1.start(i);
-          const unsigned item = begin / ks1, q_item = item * ks1, ai = item / nt1;
-          const int e = c.act[ai], col = (item - ai * nt1) * 128 + lane * 4;
-          const unsigned row0 = c.off[e], n = c.off[e + 1] - row0;
-          if (i0 >= n || begin == q_item || cut1.piece_of(q_item) != i - 1) continue;
-          const unsigned last = cut1.piece_of(q_item + ks1 - 1), odd = i0 + 1 < n ? 64 : 0;
-          const float4* src =
-              reinterpret_cast<const float4*>(p.part + (2 * i - 1) * slot + i0 * 256) + lane;
-          float4 va = __ldcg(src), vb = __ldcg(src + 32);
-          float4 ua = __ldcg(src + odd), ub = __ldcg(src + odd + 32);
-          src += slot / 4;
-#pragma unroll 4
-          for (unsigned o = i; o <= last; ++o, src += slot / 2) {
-            va = add4(va, __ldcg(src));
-            vb = add4(vb, __ldcg(src + 32));
-            ua = add4(ua, __ldcg(src + odd));
-            ub = add4(ub, __ldcg(src + odd + 32));
-          }
-          float4 w1 = make_float4(0.f, 0.f, 0.f, 0.f), w3 = w1;
-          if (F8) {
-            w1 = __ldg(reinterpret_cast<const float4*>(p.s1 + static_cast<size_t>(e) * p.f + col));
-            w3 = __ldg(reinterpret_cast<const float4*>(p.s3 + static_cast<size_t>(e) * p.f + col));
-          }
-          store_h4<F8>(p, c, row0 + i0, col, va, vb, w1, w3, lane);
-          if (odd) store_h4<F8>(p, c, row0 + i0 + 1, col, ua, ub, w1, w3, lane);
+        while (join.work < works) {
+          if (join.rows > 0) join_rows<F8>(p, c, join, lane);
+          join.work += G * kIdleWarps;
+          look_up();
         }
       }
       grid_sync();
@@ -1096,21 +1128,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         q = end;
       }
     }
-    __syncthreads();
     // ------------------------------------------------------------ combine
+    // the first rounds of tasks go to the idle warps, the rest to all
+    const int blocks = p.h / 64, tasks = p.T * blocks;
+    const bool waits = warp >= 2 && (warp < 4 || warp >= 8);
+    int task = waits ? cta + (warp < 4 ? warp - 2 : warp - 6) * G : tasks;
+    Look look = {};
+    if (task < tasks)
+      look = look_of(p, c, cut2, nt2, ks2, task / blocks, task % blocks, lane);
+    __syncthreads();
     if (tid == 0 && (*abort_flag ||
                      !grid_barrier(words + kBarWord, (F8 ? 5 : 4) * G, p.status)))
       *abort_flag = 1;
     __syncthreads();
     if (!*abort_flag) {
-      if (p.k == 1)
-        combine<8>(p, c, cut2, nt2, ks2);
-      else if (p.k == 2)
-        combine<4>(p, c, cut2, nt2, ks2);
-      else if (p.k <= 4)
-        combine<2>(p, c, cut2, nt2, ks2);
-      else
-        combine<1>(p, c, cut2, nt2, ks2);
+      const int rest = static_cast<int>(G * kIdleWarps + cta) + warp * static_cast<int>(G);
+      if (task >= tasks) task = -1;
+      for (int next = rest;;) {
+        if (task >= 0) {
+          const int t = task / blocks, b = task % blocks;
+          if (p.k <= 2)
+            combine<4>(p, look, t, b, lane);
+          else if (p.k <= 4)
+            combine<2>(p, look, t, b, lane);
+          else
+            combine<1>(p, look, t, b, lane);
+        }
+        if (next >= tasks) break;
+        task = next;
+        next += static_cast<int>(G) * (kThreads / 32);
+        look = look_of(p, c, cut2, nt2, ks2, task / blocks, task % blocks, lane);
+      }
     }
   }
   // ------------------------------------------------------------- teardown
