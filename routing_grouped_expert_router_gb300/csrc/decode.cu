@@ -892,66 +892,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(kFull, ok);
         return ok ? v : -1;
       };
+      // All that a k-step needs is worked out by the whole warp, and only the
+      // instructions are issued by one thread: the eight MMAs take the
+      // descriptors from uniform registers, which code under `lane == 0` has to
+      // fill one by one.  That and the look-ups for each step took 0.77 us, more
+      // than the 0.7 us in which a step's 32 KiB arrive.
+      constexpr uint32_t kA = F8 ? 2 : 128;  // 16-byte units from one MMA's A to the next
+      const uint64_t a_ring = smem_desc(0, F8 ? 16 : 8192, 1024) + (ring >> 4);
+      const uint64_t b_ring = smem_desc(0, 16, 1024) + ((ring + kWBytes) >> 4);
+      const uint32_t stage16 = stage_bytes >> 4;
       auto phase = [&](unsigned q0, unsigned q1, unsigned ksn, unsigned tiles, bool fc1) {
-        unsigned item = q0 / ksn, ks = q0 - item * ksn;
-        for (unsigned q = q0; ok && q < q1; ++q) {
-          const int buf = it & 1;
-          const bool first = q == q0 || ks == 0, last = q + 1 == q1 || ks + 1 == ksn;
-          if (first && (*abort_flag || !mbar_wait(smem_u32(&c.tempty[buf]), ((it >> 1) & 1) ^ 1,
-                                                  p.status, kTimeoutCode)))
-            ok = false;
-          if (ok && (*abort_flag ||
-                     !mbar_wait(smem_u32(&c.full[s]), ph, p.status, kTimeoutCode)))
-            ok = false;
-          if (!ok) {
-            *abort_flag = 1;
-            break;
-          }
+        unsigned item = q0 / ksn;
+        for (unsigned q = q0; q < q1; ++item) {
+          const unsigned end = min(q1, (item + 1) * ksn);
           int n = p.n1;
           if (!fc1) {
             const int e = c.act[item / tiles];
             n = (c.off[e + 1] - c.off[e] + 15) / 16 * 16;
           }
-          if (lane == 0) {
-            tc_fence_after();
-            const uint32_t idesc = F8 ? idesc_e4m3(128, n) : idesc_bf16(128, n, true, false);
-            const uint32_t ab = ring + s * stage_bytes, bb = ab + kWBytes;
-            const uint32_t acc = tmem + buf * 256;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t bd = smem_desc(bb + kk * 32, 16, 1024);
-              const uint32_t add = !(first && kk == 0);
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                const uint32_t am = ab + m * (kWBytes / 2);
-                if (F8)
-                  umma_e4m3(acc + m * 128, smem_desc(am + kk * 32, 16, 1024), bd, idesc, add);
-                else
-                  umma_bf16(acc + m * 128, smem_desc(am + kk * 2048, 8192, 1024), bd, idesc, add);
-              }
+          const uint32_t idesc = F8 ? idesc_e4m3(128, n) : idesc_bf16(128, n, true, false);
+          const int buf = it & 1;
+          const uint32_t acc = tmem + buf * 256;
+          ok = !*abort_flag && mbar_wait(smem_u32(&c.tempty[buf]), ((it >> 1) & 1) ^ 1, p.status,
+                                         kTimeoutCode);
+          uint32_t add = 0;
+          for (; q < end; ++q) {
+            // the whole warp goes on or stops
+            ok = __all_sync(kFull, ok && mbar_wait(smem_u32(&c.full[s]), ph, p.status,
+                                                   kTimeoutCode));
+            if (!ok) {
+              *abort_flag = 1;
+              return;
             }
-            umma_commit(smem_u32(&c.empty[s]));
-            if (last) umma_commit(smem_u32(&c.tfull[buf]));
+            tc_fence_after();
+            const uint64_t ad = a_ring + s * stage16, bd = b_ring + s * stage16;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                  const uint64_t am = ad + kk * kA + m * (kWBytes / 32);
+                  if (F8)
+                    umma_e4m3(acc + m * 128, am, bd + kk * 2, idesc, kk ? 1u : add);
+                  else
+                    umma_bf16(acc + m * 128, am, bd + kk * 2, idesc, kk ? 1u : add);
+                }
+              }
+              umma_commit(smem_u32(&c.empty[s]));
+              if (q + 1 == end) umma_commit(smem_u32(&c.tfull[buf]));
+            }
+            add = 1;
+            if (++s == p.stages) {
+              s = 0;
+              ph ^= 1;
+            }
           }
-          __syncwarp();
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1;
-          }
-          if (last) ++it;
-          if (++ks == ksn) {
-            ks = 0;
-            ++item;
-          }
+          ++it;
         }
       };
       for (int i; (i = pop()) >= 0 && ok;) phase(cut1.start(i), cut1.end(i), ks1, nt1, true);
       if (ok)
         for (int i; (i = pop()) >= 0 && ok;) phase(cut2.start(i), cut2.end(i), ks2, nt2, false);
-      if (lane == 0) {  // every MMA must be done before tensor memory is freed
-        umma_commit(smem_u32(&c.drain));
-        mbar_wait(smem_u32(&c.drain), 0, p.status, kTimeoutCode);
-      }
+      // every MMA must be done before tensor memory is freed
+      if (elect_one()) umma_commit(smem_u32(&c.drain));
+      mbar_wait(smem_u32(&c.drain), 0, p.status, kTimeoutCode);
       __syncwarp();
     } else {
       // ------------------------------------------- epilogue and helpers
