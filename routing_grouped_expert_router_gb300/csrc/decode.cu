@@ -57,6 +57,7 @@ constexpr int kMaxStages = 6;
 constexpr int kQueue = 4;          // pieces between the producer and the others
 constexpr int kMaxRows = kDecodeMaxT * 8;  // placed assignments
 constexpr int kMaxE = 64;
+constexpr int kMaxPieces = 640, kMaxTiles = 1024;
 constexpr int kGroupTok = 8;       // tokens of a router work unit at most
 constexpr int kTimeoutCode = MOE_ERR_DEVICE_TIMEOUT;
 constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -110,7 +111,14 @@ struct alignas(16) Ctrl {
   int16_t pos[kMaxRows];    // assignment -> row, -1 dropped
   uint8_t exp[kMaxRows];    // assignment -> expert
   uint8_t tok[kMaxRows];    // row -> token
-  uint16_t hist[kMaxRows / 32][kMaxE];
+  int joins;
+  uint32_t tile[kMaxTiles]; // FC2 tile -> its first piece | further pieces << 16
+  union {
+    uint16_t hist[kMaxRows / 32][kMaxE];  // dispatch
+    // FC1 tiles to join: the piece after the one that begins it | parts << 16;
+    // its expert among the active ones << 16 | its number
+    uint2 join[kMaxPieces];
+  };
 };
 
 // One phase's k-steps [0, total) cut into pieces, in up to kRounds rounds of one
@@ -130,7 +138,7 @@ struct Cut {
   __device__ Cut(unsigned n, unsigned grid, unsigned tile_steps) : total(n) {
     rounds = n >= kRoundsFrom * grid ? kRounds : 1;
     blocks = n < grid ? n : grid;
-    const unsigned share = n / grid, least = max(4u, tile_steps / 16u);
+    const unsigned share = n / grid, least = max(4u, tile_steps / 8u);
     at[0] = 0;
     at[4] = n;
     at[3] = rounds == 1 ? n : n - grid * max(least, share * 3u / 100u);
@@ -544,8 +552,9 @@ __device__ __forceinline__ void store_h4(const Params& p, const Ctrl& c, int row
 
 // y: 64 columns of a token to a warp, four to a lane, each half of the warp
 // with every second sum.  This is latency: lane j of the first 8 looks up slot
-// j's row and the pieces that its tile went through (a warp that waits for the
-// end of FC2 does so ahead), then eight chains of loads run side by side, LANES
+// j's row and the pieces that its tile went through (divisions for each slot in
+// every thread cost 4 us; the idle warps make a table of them during FC2), then
+// eight chains of loads run side by side, LANES
 // of them for each of up to 8 / LANES slots, with the slot's row of O and the
 // parts that other pieces left of it dealt out to them and the halves in turn.
 struct Look {
@@ -562,8 +571,16 @@ __device__ __forceinline__ Look look_of(const Params& p, const Ctrl& c, const Cu
     if (l.row >= 0) {
       l.gate = c.gate[a];
       const int e = c.exp[a];
-      const unsigned q = (c.act_of[e] * tiles + b / 4) * ksn, first = cut.piece_of(q);
-      l.n = cut.piece_of(q + ksn - 1) - first;
+      const unsigned i = c.act_of[e] * tiles + b / 4;
+      unsigned first, n;
+      if (i < kMaxTiles) {
+        first = c.tile[i] & 0xFFFFu;
+        n = c.tile[i] >> 16;
+      } else {
+        first = cut.piece_of(i * ksn);
+        n = cut.piece_of(i * ksn + ksn - 1) - first;
+      }
+      l.n = n;
       l.at = first * p.T + l.row - c.off[e];
     }
   }
@@ -630,24 +647,19 @@ __device__ __forceinline__ void combine(const Params& p, const Look& l, int t, i
   *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(t) * p.h + col) = out;
 }
 
-// Two rows of a tile of FC1 that pieces share: the sum left by the piece that
-// began it, then the parts of the pieces after it, in order.
-struct Join {
-  unsigned work;
-  int e, row, rows, col;
-  unsigned parts;
-  const float4* src;
-};
+// Two rows of a tile of FC1 that pieces share: at src, what the piece that began
+// it left, then the parts of the pieces after it, in order.
 template <bool F8>
-__device__ __forceinline__ void join_rows(const Params& p, const Ctrl& c, const Join& j, int lane) {
+__device__ __forceinline__ void join_rows(const Params& p, const Ctrl& c, const float4* src,
+                                          unsigned parts, int e, int row, int rows, int col,
+                                          int lane) {
   const size_t slot = static_cast<size_t>(p.T) * 64;  // float4s
-  const unsigned odd = j.rows > 1 ? 64 : 0;
-  const float4* src = j.src;
+  const unsigned odd = rows > 1 ? 64 : 0;
   float4 va = __ldcg(src), vb = __ldcg(src + 32);
   float4 ua = __ldcg(src + odd), ub = __ldcg(src + odd + 32);
   src += slot;
 #pragma unroll 4
-  for (unsigned o = 0; o < j.parts; ++o, src += 2 * slot) {
+  for (unsigned o = 0; o < parts; ++o, src += 2 * slot) {
     va = add4(va, __ldcg(src));
     vb = add4(vb, __ldcg(src + 32));
     ua = add4(ua, __ldcg(src + odd));
@@ -655,11 +667,11 @@ __device__ __forceinline__ void join_rows(const Params& p, const Ctrl& c, const 
   }
   float4 w1 = make_float4(0.f, 0.f, 0.f, 0.f), w3 = w1;
   if (F8) {
-    w1 = __ldg(reinterpret_cast<const float4*>(p.s1 + static_cast<size_t>(j.e) * p.f + j.col));
-    w3 = __ldg(reinterpret_cast<const float4*>(p.s3 + static_cast<size_t>(j.e) * p.f + j.col));
+    w1 = __ldg(reinterpret_cast<const float4*>(p.s1 + static_cast<size_t>(e) * p.f + col));
+    w3 = __ldg(reinterpret_cast<const float4*>(p.s3 + static_cast<size_t>(e) * p.f + col));
   }
-  store_h4<F8>(p, c, j.row, j.col, va, vb, w1, w3, lane);
-  if (odd) store_h4<F8>(p, c, j.row + 1, j.col, ua, ub, w1, w3, lane);
+  store_h4<F8>(p, c, row, col, va, vb, w1, w3, lane);
+  if (odd) store_h4<F8>(p, c, row + 1, col, ua, ub, w1, w3, lane);
 }
 
 template <bool F8>
@@ -960,6 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------- epilogue and helpers
       const bool epilogue = warp >= 4 && warp < 8;
+      const int idle = warp < 4 ? warp - 2 : warp - 6;  // 0 .. kIdleWarps - 1
       const int r = (warp & 3) * 32 + lane;  // my row of the 128-row tiles
       const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       int it = 0;
@@ -1038,33 +1051,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++it;
         q = end;
       }
-      // The tiles that pieces share are joined after the barrier below, by the
-      // warps that have nothing to do before it and so look up their first one:
-      // a tile goes with the first border inside it, two of its rows to a warp,
-      // four columns to a lane.
-      Join join = {};
-      const unsigned pairs = (c.most + 1) / 2, works = cut1.rounds * cut1.blocks * pairs;
-      auto look_up = [&] {
-        join.rows = 0;
-        if (join.work >= works) return;
-        const unsigned i = join.work / pairs, i0 = (join.work - i * pairs) * 2;
-        const unsigned begin = cut1.start(i), item = begin / ks1, ai = item / nt1;
-        join.e = c.act[ai];
-        const unsigned n = c.off[join.e + 1] - c.off[join.e];
-        if (i0 >= n || begin == item * ks1 || cut1.piece_of(item * ks1) != i - 1) return;
-        join.row = c.off[join.e] + i0;
-        join.rows = min(n - i0, 2u);
-        join.col = (item - ai * nt1) * 128 + lane * 4;
-        join.parts = cut1.piece_of((item + 1) * ks1 - 1) - i + 1;
-        join.src = reinterpret_cast<const float4*>(
-                       p.part + (2 * i - 1) * (static_cast<size_t>(2) * p.T * 128) + i0 * 256) +
-                   lane;
-      };
-      const int idle = warp < 4 ? warp - 2 : warp - 6;  // 0 .. kIdleWarps - 1
-      join.work = works;
-      if (!epilogue) {
-        join.work = cta + idle * G;
-        look_up();
+      // The tiles of FC1 that pieces share, listed by an idle warp (in the same
+      // order in every block): a tile goes with the first border inside it.
+      if (warp == 2) {
+        const unsigned pieces = cut1.rounds * cut1.blocks;
+        int listed = 0;
+        for (unsigned i0 = 0; i0 < pieces; i0 += 32) {
+          const unsigned i = i0 + lane;
+          unsigned parts = 0, item = 0;
+          if (i > 0 && i < pieces) {
+            const unsigned begin = cut1.start(i);
+            item = begin / ks1;
+            if (begin != item * ks1 && cut1.piece_of(item * ks1) == i - 1)
+              parts = cut1.piece_of(item * ks1 + ks1 - 1) - i + 1;
+          }
+          const unsigned some = __ballot_sync(kFull, parts > 0);
+          if (parts > 0)
+            c.join[listed + __popc(some & ((1u << lane) - 1))] =
+                make_uint2(i | parts << 16, (item / nt1) << 16 | item % nt1);
+          listed += __popc(some);
+        }
+        if (lane == 0) c.joins = listed;
       }
       unsigned arrived = G;
       auto grid_sync = [&] {
@@ -1075,11 +1082,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         helper_sync();
       };
       grid_sync();
-      if (!*abort_flag) {
-        while (join.work < works) {
-          if (join.rows > 0) join_rows<F8>(p, c, join, lane);
-          join.work += G * kIdleWarps;
-          look_up();
+      if (!*abort_flag) {  // two rows to a warp, four columns to a lane
+        const unsigned pairs = (c.most + 1) / 2, works = c.joins * pairs;
+        for (unsigned w = cta + (warp - 2) * G; w < works; w += G * (kHelpers / 32)) {
+          const unsigned at = w / pairs, i0 = (w - at * pairs) * 2;
+          const uint2 j = c.join[at];
+          const unsigned i = j.x & 0xFFFFu, parts = j.x >> 16;
+          const int e = c.act[j.y >> 16], row = c.off[e] + i0, rows = c.off[e + 1] - row;
+          if (rows > 0)
+            join_rows<F8>(p, c,
+                          reinterpret_cast<const float4*>(
+                              p.part + (2 * i - 1) * (static_cast<size_t>(2) * p.T * 128) +
+                              i0 * 256) + lane,
+                          parts, e, row, rows, (j.y & 0xFFFFu) * 128 + lane * 4, lane);
         }
       }
       grid_sync();
@@ -1097,6 +1112,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid == 64) mbar_arrive(smem_u32(&c.hready));
       if (*abort_flag) ok = false;
       ok = __all_sync(kFull, ok);
+      if (!epilogue) {  // for the combine: the pieces that each tile goes through
+        const unsigned tiles = min(c.nact * nt2, static_cast<unsigned>(kMaxTiles));
+        for (unsigned i = idle * 32 + lane; i < tiles; i += kIdleWarps * 32) {
+          const unsigned first = cut2.piece_of(i * ks2);
+          c.tile[i] = first | (cut2.piece_of(i * ks2 + ks2 - 1) - first) << 16;
+        }
+      }
       // ---- FC2: rows of O where this piece begins the tile, else of its part
       q = q_end = 0;
       while (epilogue && ok && (q < q_end || pop(cut2))) {
@@ -1133,35 +1155,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ------------------------------------------------------------ combine
-    // the first rounds of tasks go to the idle warps, the rest to all
-    const int blocks = p.h / 64, tasks = p.T * blocks;
-    const bool waits = warp >= 2 && (warp < 4 || warp >= 8);
-    int task = waits ? cta + (warp < 4 ? warp - 2 : warp - 6) * G : tasks;
-    Look look = {};
-    if (task < tasks)
-      look = look_of(p, c, cut2, nt2, ks2, task / blocks, task % blocks, lane);
     __syncthreads();
     if (tid == 0 && (*abort_flag ||
                      !grid_barrier(words + kBarWord, (F8 ? 5 : 4) * G, p.status)))
       *abort_flag = 1;
     __syncthreads();
     if (!*abort_flag) {
-      const int rest = static_cast<int>(G * kIdleWarps + cta) + warp * static_cast<int>(G);
-      if (task >= tasks) task = -1;
-      for (int next = rest;;) {
-        if (task >= 0) {
-          const int t = task / blocks, b = task % blocks;
-          if (p.k <= 2)
-            combine<4>(p, look, t, b, lane);
-          else if (p.k <= 4)
-            combine<2>(p, look, t, b, lane);
-          else
-            combine<1>(p, look, t, b, lane);
-        }
-        if (next >= tasks) break;
-        task = next;
-        next += static_cast<int>(G) * (kThreads / 32);
-        look = look_of(p, c, cut2, nt2, ks2, task / blocks, task % blocks, lane);
+      const int blocks = p.h / 64, tasks = p.T * blocks;
+      for (int i = cta + warp * G; i < tasks; i += G * (kThreads / 32)) {
+        const int t = i / blocks, b = i - t * blocks;
+        const Look look = look_of(p, c, cut2, nt2, ks2, t, b, lane);
+        if (p.k <= 2)
+          combine<4>(p, look, t, b, lane);
+        else if (p.k <= 4)
+          combine<2>(p, look, t, b, lane);
+        else
+          combine<1>(p, look, t, b, lane);
       }
     }
   }
@@ -1264,7 +1273,9 @@ bool supported(const moe_dims& d, bool fp8) {
   if (d.T > kDecodeMaxT || d.sar != 0 || (fp8 && (d.h % 128 != 0 || d.f % 128 != 0))) return false;
   // (a k-step is 32 KiB of weights: 14 million of them are 450 GB)
   if (most_steps(d, fp8) >= (1ll << 31) / moe_api::num_sms()) return false;
+  if (moe_api::num_sms() * kRounds > kMaxPieces) return false;
   if (d.T > 0 && !plan_of(d, moe_api::num_sms(), fp8).ok) return false;
+  if (d.f > (1 << 22)) return false;  // Ctrl::join's tile numbers
   return static_cast<long long>(d.E) * (d.h > d.f ? d.h : d.f) * 2 < (1ll << 31);
 }
 
