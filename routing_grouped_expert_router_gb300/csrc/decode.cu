@@ -134,11 +134,12 @@ struct Cut {
   unsigned total, blocks, rounds;
   unsigned at[kRounds + 1];  // rounds' borders
   // Later rounds of 8, 5 and 3% of a block's share, but of no fewer than `least`
-  // k-steps a piece: every piece of a tile is one more sum to add.
+  // k-steps a piece: every piece of a tile is one more sum to add.  Round 0 is
+  // half of all at the least.
   __device__ Cut(unsigned n, unsigned grid, unsigned tile_steps) : total(n) {
-    rounds = n >= kRoundsFrom * grid ? kRounds : 1;
-    blocks = n < grid ? n : grid;
     const unsigned share = n / grid, least = max(4u, tile_steps / 8u);
+    rounds = share >= max(kRoundsFrom, 2u * (kRounds - 1) * least) ? kRounds : 1;
+    blocks = n < grid ? n : grid;
     at[0] = 0;
     at[4] = n;
     at[3] = rounds == 1 ? n : n - grid * max(least, share * 3u / 100u);

@@ -345,3 +345,35 @@ def test_agrees_with_the_layer_call():
     # the layer call also rounds A, B's product chain and O: one more rounding than this one
     assert rel_l2(run.y.double().cpu(), y.double().cpu()) <= TOL_Y + 2.0 ** -9
     assert math.isfinite(float(run.y.float().sum()))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_tiles_in_few_pieces(fp8):
+    """Few tiles of very many k-steps (FC2: 4 for each expert, 912 steps of 64 each): the phase is long, but its pieces
+    are short against its tiles.  The reference runs on the GPU in 64 bits; TOL_Y as above."""
+    T, h, f, E, k = 2, 1024, 58368, 2, 2
+    g = torch.Generator("cuda").manual_seed(71)
+    n = lambda shape, std: torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, std, generator=g)  # noqa: E731
+    x, W1, W3, W2 = n((T, h), 1.0), n((E, h, f), h ** -0.5), n((E, h, f), h ** -0.5), n((E, f, h), f ** -0.5)
+    Wg = torch.randn(h, E, generator=g, device="cuda") * h ** -0.5
+    d = mb.dims(T, h, f, E, k)
+    ws = torch.zeros(mb.moe_workspace_bytes(d, mb.OP_LAYER_DECODE_FP8 if fp8 else mb.OP_LAYER_DECODE),
+                     dtype=torch.uint8, device="cuda")
+    y = torch.empty_like(x)
+    if fp8:
+        qw = torch.zeros(mb.moe_fp8_weight_bytes(d), dtype=torch.uint8, device="cuda")
+        mb.moe_quantize_weights_fp8(d, W1, W3, W2, qw)
+        mb.moe_layer_decode_fp8(d, x, Wg, None, qw, y, None, None, ws)
+    else:
+        mb.moe_layer_decode(d, x, Wg, None, W1, W3, W2, y, None, None, ws)
+    torch.cuda.synchronize()
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK
+    p = torch.softmax(x.double() @ Wg.double(), -1)  # k = E: every expert, with its probability
+    ref = torch.zeros(T, h, dtype=torch.float64, device="cuda")
+    q = (lambda v, w=False: quant_rows(v.cpu(), w).cuda()) if fp8 else (lambda v, w=False: v.double())
+    for e in range(E):
+        w1, w3, w2 = (q(w[e].t().contiguous(), True).t() if fp8 else w[e].double() for w in (W1, W3, W2))
+        a, b = q(x) @ w1, q(x) @ w3
+        hh = a * torch.sigmoid(a) * b
+        ref += p[:, e:e + 1] * ((q(hh.to(torch.bfloat16)) if fp8 else hh) @ w2)
+    assert rel_l2(y.double().cpu(), ref.cpu()) <= (TOL_Y_F8 if fp8 else TOL_Y)
