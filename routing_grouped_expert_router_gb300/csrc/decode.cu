@@ -74,6 +74,7 @@ struct Params {
   int n1;                   // T rounded up to 16: FC1's MMA columns
   int stages;
   int tok_group, groups, slices, slice_h;  // router work units
+  int red_at;
   const uint16_t* x;
   const float *Wg, *b;
   int32_t* idx;
@@ -313,7 +314,9 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
   const int e = tid % p.E, part = tid / p.E;
   float* wg = reinterpret_cast<float*>(smem);                          // [nj][E]
   uint8_t* xs = smem + static_cast<size_t>(p.slice_h) * p.E * 4;       // [8][nj] bf16
-  float* red = reinterpret_cast<float*>(xs + p.slice_h * kGroupTok * 2);  // [8][kThreads]
+  // [8][kThreads], after those and after the partial logits that are read back
+  // into wg's place
+  float* red = reinterpret_cast<float*>(smem + p.red_at);
   float* logit = red + kThreads * kGroupTok;                           // [8][kMaxE]
   const uint32_t bar = smem_u32(&c.rbar);
   uint32_t ph = 0;
@@ -1199,7 +1202,7 @@ struct Layout {
 
 struct Plan {
   int n1, stages, smem;
-  int tok_group, groups, slices, slice_h;
+  int tok_group, groups, slices, slice_h, red_at;
   size_t pieces;
   bool ok;
 };
@@ -1237,7 +1240,10 @@ Plan plan_of(const moe_dims& d, int blocks, bool fp8) {
   p.pieces = static_cast<size_t>(blocks) *
              (most_steps(d, fp8) >= static_cast<long long>(kRoundsFrom) * blocks ? kRounds : 1);
   // so do a group's partial logits of all slices, where h is not enormous
-  p.ok = p.slices * p.tok_group * d.E * 4 <= room;
+  const int slice = p.slice_h * (d.E * 4 + kGroupTok * 2);
+  const int back = (p.slices * p.tok_group * d.E * 4 + 15) / 16 * 16;
+  p.red_at = slice > back ? slice : back;
+  p.ok = p.red_at <= room;
   return p;
 }
 
@@ -1328,6 +1334,7 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
   p.groups = plan.groups;
   p.slices = plan.slices;
   p.slice_h = plan.slice_h;
+  p.red_at = plan.red_at;
   p.x = x;
   p.Wg = Wg;
   p.b = d.has_bias ? b : nullptr;

@@ -377,3 +377,22 @@ def test_long_tiles_in_few_pieces(fp8):
         hh = a * torch.sigmoid(a) * b
         ref += p[:, e:e + 1] * ((q(hh.to(torch.bfloat16)) if fp8 else hh) @ w2)
     assert rel_l2(y.double().cpu(), ref.cpu()) <= (TOL_Y_F8 if fp8 else TOL_Y)
+
+
+@pytest.mark.parametrize("T,E", [(1, 8), (1, 64), (3, 33), (40, 64)])
+def test_routing_holds_over_many_calls(T, E):
+    """The router's shared-memory phases follow each other closely: 300 calls on one input give the same bits, those of
+    the formula."""
+    cfg, inp = inputs(T=T, h=4096, f=64, E=E, k=min(E, 4), seed=72 + E + T)
+    run = Run(cfg, inp)
+    got = []
+    for i in range(300):
+        run.idx.fill_(-1)
+        run.gates.fill_(-1.0)
+        run.call()
+        got.append((run.idx.clone(), run.gates.clone()))
+    assert run.ok()
+    idx, gates = route64(inp["x"], inp["Wg"], None, cfg.k)
+    for a, b in got:
+        assert torch.equal(a, got[0][0]) and torch.equal(b, got[0][1])
+    assert (got[0][0].cpu() == idx).all() and (got[0][1].double().cpu() - gates).abs().max() <= TOL_GATE
