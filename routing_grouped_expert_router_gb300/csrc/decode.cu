@@ -16,7 +16,7 @@
 //     tcgen05.mma and the tokens as its N columns (16 to 128), so that the
 //     smallest batch wastes columns of an idle tensor core, not bytes;
 //   * 32 KiB weight stages (two 128-column tiles x 64 rows of bf16, 128 of
-//     e4m3) flow through a ring of up to 6 stages that TMA fills, about 200 KiB
+//     e4m3) flow through a ring of up to 5 stages that TMA fills, about 170 KiB
 //     in flight on each SM; nothing but the TMA and MMA units touches them;
 //   * each phase's k-steps, over all its tiles in a row, are cut into pieces
 //     whatever the tiles' borders: the number of experts hit decides the tiles,
@@ -53,7 +53,7 @@ constexpr int kThreads = 512;
 constexpr int kHelpers = kThreads - 64;
 constexpr int kIdleWarps = kThreads / 32 - 6;  // neither of those roles
 constexpr int kWBytes = 32768;     // weights of a stage
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 5;
 constexpr int kQueue = 4;          // pieces between the producer and the others
 constexpr int kMaxRows = kDecodeMaxT * 8;  // placed assignments
 constexpr int kMaxE = 64;

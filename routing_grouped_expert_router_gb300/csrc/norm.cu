@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args 
 
 // The column gradients from the blocks' sums, a fixed order for each column: 32
 // interleaved chains, then those in order.
-constexpr int kColGroups = 32;
+constexpr int kColGroups = 32;  // a warp adds up each of the block's 32 columns
 __global__ void __launch_bounds__(32 * kColGroups)
     block_norm_cols_kernel(const float* partial, int nblk, int h, const float* w_post,
                            const float* gate, float beta, float* dw_pre, float* dw_post,
@@ -549,6 +549,11 @@ Plan plan_of(const moe_norm_dims& d, bool bwd) {
   p.smem = p.slots * p.slot_bytes;
   const int n = moe_api::num_sms() * per_sm;
   p.blocks = d.T < n ? d.T : n;
+  // no more blocks than the same number of rounds needs: each leaves its sums
+  if (bwd && d.T > 0) {
+    const int rounds = (d.T - 1) / n + 1;
+    p.blocks = (d.T - 1) / rounds + 1;
+  }
   return p;
 }
 
