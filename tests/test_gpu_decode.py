@@ -396,3 +396,32 @@ def test_routing_holds_over_many_calls(T, E):
     for a, b in got:
         assert torch.equal(a, got[0][0]) and torch.equal(b, got[0][1])
     assert (got[0][0].cpu() == idx).all() and (got[0][1].double().cpu() - gates).abs().max() <= TOL_GATE
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with a workspace of its own, overlap as they like."""
+    runs = []
+    for seed in (81, 82):
+        cfg, inp = inputs(T=24, h=512, f=1024, E=8, k=2, seed=seed)
+        runs.append((cfg, inp, Run(cfg, inp), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _, _, run, s in runs:
+            run.call(stream=s)
+    torch.cuda.synchronize()
+    for cfg, inp, run, _ in runs:
+        assert run.ok()
+        check(cfg, inp, run)
+
+
+def test_after_a_launch_failure_on_the_host():
+    """The injected failure reports MOE_ERR_CUDA; the workspace serves the next call."""
+    cfg, inp = inputs(T=6, h=128, f=128, E=4, k=2, seed=83)
+    run = Run(cfg, inp)
+    mb.moe_test_fail_launch_after(1)
+    with pytest.raises(mb.MoeError):
+        run.call()
+    torch.cuda.synchronize()
+    run.call()
+    assert run.ok()
+    check(cfg, inp, run)
