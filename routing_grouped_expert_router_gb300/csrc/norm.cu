@@ -216,6 +216,14 @@ __device__ __forceinline__ void ring_drain(const Args& a, uint64_t* full, int n)
       if (blockIdx.x + static_cast<long long>(n + i) * gridDim.x < a.T) ring_wait(a, full, n + i);
 }
 
+// These kernels are launched before the stream's work ahead of them has ended,
+// which they wait for here: a step of a few rows is shorter than a launch.
+// Nothing that another kernel wrote is read, and nothing is written, before.
+__device__ __forceinline__ void after_stream() {
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -233,8 +241,10 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.slots; ++s) moe::mbar_init(moe::smem_u32(&full[s]), 1);
     moe::fence_mbar_init();
-    for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
   }
+  after_stream();
+  if (threadIdx.x == 0)
+    for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
   // the scale of each of my columns of y, and of u
   f2 wz[kPieces][4], wu[kPieces][4];
 #pragma unroll
@@ -350,8 +360,10 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.slots; ++s) moe::mbar_init(moe::smem_u32(&full[s]), 1);
     moe::fence_mbar_init();
-    for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
   }
+  after_stream();
+  if (threadIdx.x == 0)
+    for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
   // w_pre, and the factor of G in dz's product with w_post
   f2 wu[kPieces][4], wz[kPieces][4];
   f2 P[kPieces][4], Q[kPieces][4];
@@ -471,7 +483,6 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args 
     if (a.T - t <= static_cast<int>(gridDim.x)) break;
     t += gridDim.x;
   }
-  cudaTriggerProgrammaticLaunchCompletion();
   if (!ok) ring_drain(a, full, n);
   float* part = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.h;
 #pragma unroll
@@ -490,8 +501,7 @@ __global__ void __launch_bounds__(32 * kColGroups)
     block_norm_cols_kernel(const float* partial, int nblk, int h, const float* w_post,
                            const float* gate, float beta, float* dw_pre, float* dw_post,
                            float* dgate) {
-  // this kernel is launched while the rows' kernel still runs
-  cudaGridDependencySynchronize();
+  after_stream();
   __shared__ float sp[kColGroups][33], sq[kColGroups][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
@@ -557,6 +567,25 @@ Plan plan_of(const moe_norm_dims& d, bool bwd) {
   return p;
 }
 
+template <class... P, class... A>
+cudaError_t launch_early(void (*kern)(P...), int blocks, int threads, int smem, cudaStream_t s,
+                         A... args) {
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaSuccess) return moe::launched();
+  cudaGetLastError();  // reported here, not by the next launch
+  return e;
+}
+
 template <bool F32, bool BWD>
 cudaError_t launch(Args& a, const Plan& p, cudaStream_t s) {
   auto kern = BWD ? block_norm_bwd_kernel<F32> : block_norm_fwd_kernel<F32>;
@@ -564,8 +593,7 @@ cudaError_t launch(Args& a, const Plan& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   a.slots = p.slots;
   a.slot_bytes = p.slot_bytes;
-  kern<<<p.blocks, p.threads, p.smem, s>>>(a);
-  return moe::launched();
+  return launch_early(kern, p.blocks, p.threads, p.smem, s, a);
 }
 
 moe_status check(const moe_norm_dims* d) {
@@ -674,21 +702,11 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
   if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (dw_pre || dw_post || channel) {
-    // launched ahead of the rows' kernel's end, which it waits for itself
-    cudaLaunchAttribute early = {};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((d.h + 31) / 32, 1, 1);
-    cfg.blockDim = dim3(32 * kColGroups, 1, 1);
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, block_norm_cols_kernel, static_cast<const float*>(a.partial),
-                           p.blocks, d.h, w_post, channel ? gate : nullptr, d.beta, dw_pre,
-                           dw_post, channel ? dgate : nullptr) != cudaSuccess)
+    if (launch_early(block_norm_cols_kernel, (d.h + 31) / 32, 32 * kColGroups, 0, s, a.partial,
+                     p.blocks, d.h, w_post, channel ? gate : nullptr, d.beta, dw_pre, dw_post,
+                     channel ? dgate : nullptr) != cudaSuccess ||
+        !moe_api::note(s, "block_norm_cols"))
       return MOE_ERR_CUDA;
-    if (moe::launched() != cudaSuccess || !moe_api::note(s, "block_norm_cols")) return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }
