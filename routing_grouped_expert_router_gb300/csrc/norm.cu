@@ -28,6 +28,7 @@ namespace {
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kMaxH = 8192;
 constexpr int kMaxThreads = 512;
+constexpr int kFwdThreads = 1024;  // of the forward's blocks on an SM
 constexpr int kPieces = 2;  // 8-element pieces of a row for each thread
 
 constexpr int kMaxSlots = 4;
@@ -146,7 +147,6 @@ __device__ __forceinline__ float sum_warps(const float* s) {
   return v;
 }
 typedef float Red1[2][16];
-typedef float Red3[2][4][16];
 __device__ __forceinline__ bool block_sum(float& v, Red1& red, int& half, bool ok) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -156,20 +156,44 @@ __device__ __forceinline__ bool block_sum(float& v, Red1& red, int& half, bool o
   half ^= 1;
   return ok;
 }
-// Three sums: each exchange halves what a lane holds, so that 6 shuffles do
-// instead of 15; lanes 0, 8 and 16 end up with one sum each.
-__device__ __forceinline__ bool block_sum3(float (&v)[3], Red3& red, int& half, bool ok) {
+// The same for R rows at once.
+template <int R>
+struct RedRows {
+  float one[2][R][16], three[2][R][3][16];
+};
+template <int R>
+__device__ __forceinline__ void block_sum(float (&v)[R], RedRows<R>& red, int& half) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[r] += __shfl_xor_sync(kFull, v[r], o);
+    if ((threadIdx.x & 31) == 0) red.one[half][r][threadIdx.x >> 5] = v[r];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) v[r] = sum_warps(red.one[half][r]);
+  half ^= 1;
+}
+// Three sums of each row: each exchange halves what a lane holds, so that 6
+// shuffles do instead of 15; lanes 0, 8 and 16 end up with one sum each.
+template <int R>
+__device__ __forceinline__ bool block_sum3(float (&v)[R][3], RedRows<R>& red, int& half, bool ok) {
   const int lane = threadIdx.x & 31;
   const bool hi = lane & 16, mid = lane & 8;
-  float x0 = (hi ? v[2] : v[0]) + __shfl_xor_sync(kFull, hi ? v[0] : v[2], 16);
-  float x1 = (hi ? 0.f : v[1]) + __shfl_xor_sync(kFull, hi ? v[1] : 0.f, 16);
-  x0 = (mid ? x1 : x0) + __shfl_xor_sync(kFull, mid ? x0 : x1, 8);
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) x0 += __shfl_xor_sync(kFull, x0, o);
-  if ((lane & 7) == 0) red[half][lane >> 3][threadIdx.x >> 5] = x0;
+  for (int r = 0; r < R; ++r) {
+    float x0 = (hi ? v[r][2] : v[r][0]) + __shfl_xor_sync(kFull, hi ? v[r][0] : v[r][2], 16);
+    float x1 = (hi ? 0.f : v[r][1]) + __shfl_xor_sync(kFull, hi ? v[r][1] : 0.f, 16);
+    x0 = (mid ? x1 : x0) + __shfl_xor_sync(kFull, mid ? x0 : x1, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) x0 += __shfl_xor_sync(kFull, x0, o);
+    if ((lane & 7) == 0 && lane < 24) red.three[half][r][lane >> 3][threadIdx.x >> 5] = x0;
+  }
   ok = __syncthreads_and(ok);
 #pragma unroll
-  for (int i = 0; i < 3; ++i) v[i] = sum_warps(red[half][i]);
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[r][i] = sum_warps(red.three[half][r][i]);
   half ^= 1;
   return ok;
 }
@@ -224,8 +248,11 @@ __device__ __forceinline__ void after_stream() {
   cudaTriggerProgrammaticLaunchCompletion();
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args a) {
+// KEEP: a thread keeps its pieces of r and y between the two sums and the slot is
+// free after the first; otherwise it reads y again, with registers to spare for
+// twice the threads on an SM.
+template <bool F32, bool KEEP>
+__global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxSlots];
   __shared__ __align__(16) Red1 red;
@@ -274,44 +301,88 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
     if (a.gate_kind == MOE_GATE_TOKEN) s = __ldg(a.gate + t);
     bool ok = ring_wait(a, full, n);
     const uint8_t* slot = smem + (n % a.slots) * a.slot_bytes;
-    f2 v[kPieces][4], z[kPieces][4], acc = 0;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c >= a.h) continue;
-      load_res<F32>(slot, c, v[i]);
-      if (!a.y) continue;
-      unpack8(*reinterpret_cast<const uint4*>(slot + g.bytes[0] + c * 2), z[i]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc = fma2(z[i][j], z[i][j], acc);
-    }
-    // the barrier of this sum also ends the reads of the slot
-    float ss = sum2(acc);
-    ok = block_sum(ss, red, half, ok);
-    if (threadIdx.x == 0 && ok) ring_load(a, g, full, smem, n + a.slots);
-    if (!ok) break;
-    if (a.y) {
-      if (a.w_post) s *= inv_rms(ss, a);
-      const f2 s2 = both(s), al = both(a.alpha);
+    const uint8_t* sy = slot + g.bytes[0];
+    const f2 al = both(a.alpha);
+    f2 v[kPieces][4], acc = 0;
+    float ss = 0.f;
+    if (KEEP) {
+      f2 z[kPieces][4];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
+        load_res<F32>(slot, c, v[i]);
+        if (!a.y) continue;
+        unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), z[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[i][j] = fma2(mul2(s2, z[i][j]), wz[i][j], mul2(al, v[i][j]));
-        store_res<F32>(a.out_r, row + c, v[i]);
+        for (int j = 0; j < 4; ++j) acc = fma2(z[i][j], z[i][j], acc);
       }
-    }
-    if (a.w_pre) {
+      // the barrier of this sum also ends the reads of the slot
+      ss = sum2(acc);
+      ok = block_sum(ss, red, half, ok);
+      if (threadIdx.x == 0 && ok) ring_load(a, g, full, smem, n + a.slots);
+      if (!ok) break;
+      if (a.y) {
+        if (a.w_post) s *= inv_rms(ss, a);
+        const f2 s2 = both(s);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int c = (threadIdx.x + i * blockDim.x) * 8;
+          if (c >= a.h) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[i][j] = fma2(mul2(s2, z[i][j]), wz[i][j], mul2(al, v[i][j]));
+          store_res<F32>(a.out_r, row + c, v[i]);
+        }
+      }
+      if (a.w_pre) {
+        acc = 0;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          if ((threadIdx.x + i * blockDim.x) * 8 < a.h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
+        ss = sum2(acc);
+        block_sum(ss, red, half, true);
+      }
+    } else {
+      f2 z[4];
+      if (a.w_post) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int c = (threadIdx.x + i * blockDim.x) * 8;
+          if (c >= a.h) continue;
+          unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), z);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc = fma2(z[j], z[j], acc);
+        }
+        ss = sum2(acc);
+        ok = block_sum(ss, red, half, ok);
+        s *= inv_rms(ss, a);
+      }
+      const f2 s2 = both(s);
       acc = 0;
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        if ((threadIdx.x + i * blockDim.x) * 8 < a.h)
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        if (c >= a.h) continue;
+        load_res<F32>(slot, c, v[i]);
+        if (a.y) {
+          unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), z);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
+          for (int j = 0; j < 4; ++j)
+            v[i][j] = fma2(mul2(s2, z[j]), wz[i][j], mul2(al, v[i][j]));
+          store_res<F32>(a.out_r, row + c, v[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
+      }
       ss = sum2(acc);
-      block_sum(ss, red, half, true);
+      ok = block_sum(ss, red, half, ok);
+      if (!ok) break;
+      if (threadIdx.x == 0) ring_load(a, g, full, smem, n + a.slots);
+    }
+    if (a.w_pre) {
       const f2 rv = both(inv_rms(ss, a));
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
@@ -337,15 +408,18 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_fwd_kernel(const Args 
 // sum serves both (g_t: the token gate, else 1).  Each block keeps P and Q of its
 // rows in registers and writes them once; block_norm_cols_kernel adds the
 // blocks in order.
-template <bool F32>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args a) {
+// R rows go through these steps side by side: two where one block alone fits an
+// SM (rows of more than 4096) and a thread may have the registers for it.
+constexpr int kPairThreads = 384;
+template <bool F32, int R>
+__global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
+    block_norm_bwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxSlots];
-  __shared__ __align__(16) Red3 red3;
-  __shared__ __align__(16) Red1 red1;
+  __shared__ __align__(16) RedRows<R> red;
   int half3 = 0, half1 = 0;
-  for (int i = threadIdx.x; i < 2 * 4 * 16; i += blockDim.x) (&red3[0][0][0])[i] = 0.f;
-  if (threadIdx.x < 32) red1[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x)
+    reinterpret_cast<float*>(&red)[i] = 0.f;
   const uint32_t res = a.h * (F32 ? 4 : 2), row16 = a.h * 2;
   Ring g;
   g.src[0] = static_cast<const uint8_t*>(a.r);
@@ -391,97 +465,116 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_bwd_kernel(const Args 
   }
   const float al = a.y ? a.alpha : 1.f;
   const bool token = a.gate_kind == MOE_GATE_TOKEN;
+  const uint32_t at_y = g.bytes[0] + g.bytes[1], at_dr = at_y + g.bytes[2];
   __syncthreads();
   int n = 0;
   bool ok = true;
-  for (int t = blockIdx.x; t < a.T; ++n) {
-    const size_t row = static_cast<size_t>(t) * a.h;
-    float gt = 1.f;
-    if (token) gt = __ldg(a.gate + t);
-    ok = ring_wait(a, full, n);
-    const uint8_t* sv = smem + (n % a.slots) * a.slot_bytes;
-    const uint8_t* sdu = sv + g.bytes[0];
-    const uint8_t* sy = sdu + g.bytes[1];
-    const uint8_t* sdr = sy + g.bytes[2];
-    f2 acc[3] = {0, 0, 0};
+  for (long long t0 = blockIdx.x; t0 < a.T; t0 += static_cast<long long>(R) * gridDim.x, n += R) {
+    int t[R];
+    bool live[R];
+    float gt[R], s3[R][3];
+    const uint8_t* sv[R];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c >= a.h) continue;
-      f2 v[4], d[4];
-      if (a.w_pre) {
-        load_res<F32>(sv, c, v);
-        unpack8(*reinterpret_cast<const uint4*>(sdu + c * 2), d);
+    for (int r = 0; r < R; ++r) {
+      live[r] = t0 + r * gridDim.x < a.T;
+      t[r] = static_cast<int>(live[r] ? t0 + r * gridDim.x : t0);
+      gt[r] = token ? __ldg(a.gate + t[r]) : 1.f;
+      sv[r] = smem + ((n + r) % a.slots) * a.slot_bytes;
+      if (live[r]) ok = ring_wait(a, full, n + r) && ok;
+      f2 acc[3] = {0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[0] = fma2(v[j], v[j], acc[0]);
-          acc[1] = fma2(mul2(d[j], wu[i][j]), v[j], acc[1]);
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        if (c >= a.h || !live[r]) continue;
+        f2 v[4], d[4];
+        if (a.w_pre) {
+          load_res<F32>(sv[r], c, v);
+          unpack8(*reinterpret_cast<const uint4*>(sv[r] + g.bytes[0] + c * 2), d);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[0] = fma2(v[j], v[j], acc[0]);
+            acc[1] = fma2(mul2(d[j], wu[i][j]), v[j], acc[1]);
+          }
+        }
+        if (a.w_post) {
+          unpack8(*reinterpret_cast<const uint4*>(sv[r] + at_y + c * 2), v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[2] = fma2(v[j], v[j], acc[2]);
         }
       }
-      if (a.w_post) {
-        unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[2] = fma2(v[j], v[j], acc[2]);
-      }
+      for (int i = 0; i < 3; ++i) s3[r][i] = sum2(acc[i]);
     }
-    float s3[3] = {sum2(acc[0]), sum2(acc[1]), sum2(acc[2])};
-    ok = block_sum3(s3, red3, half3, ok);
+    ok = block_sum3<R>(s3, red, half3, ok);
     if (!ok) break;
-    const float rvs = a.w_pre ? inv_rms(s3[0], a) : 0.f;
-    const float rys = a.w_post ? inv_rms(s3[2], a) : 1.f;
-    const f2 rv = both(rvs), k1 = both(-s3[1] * a.inv_h * rvs * rvs * rvs);
-    const f2 ry = both(rys), al2 = both(al), gt2 = both(gt);
-    f2 G[kPieces][4], y[kPieces][4], dot = 0;
+    f2 G[R][kPieces][4];
+    uint4 y[R][kPieces];
+    float s1[R], rys[R];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c >= a.h) continue;
-      f2 v[4], d[4];
+    for (int r = 0; r < R; ++r) {
+      const float rvs = a.w_pre ? inv_rms(s3[r][0], a) : 0.f;
+      rys[r] = a.w_post ? inv_rms(s3[r][2], a) : 1.f;
+      const f2 rv = both(rvs), k1 = both(-s3[r][1] * a.inv_h * rvs * rvs * rvs);
+      const f2 al2 = both(al), gy = both(gt[r] * rys[r]);
+      const size_t row = static_cast<size_t>(t[r]) * a.h;
+      f2 dot = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) G[i][j] = 0;
-      if (a.dr_out) load_res<F32>(sdr, c, G[i]);
-      if (a.w_pre) {
-        load_res<F32>(sv, c, v);
-        unpack8(*reinterpret_cast<const uint4*>(sdu + c * 2), d);
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = (threadIdx.x + i * blockDim.x) * 8;
+        if (c >= a.h || !live[r]) continue;
+        f2 v[4], d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) G[r][i][j] = 0;
+        if (a.dr_out) load_res<F32>(sv[r] + at_dr, c, G[r][i]);
+        if (a.w_pre) {
+          load_res<F32>(sv[r], c, v);
+          unpack8(*reinterpret_cast<const uint4*>(sv[r] + g.bytes[0] + c * 2), d);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f2 dn = mul2(rv, d[j]);
+            P[i][j] = fma2(dn, v[j], P[i][j]);
+            G[r][i][j] = fma2(dn, wu[i][j], fma2(k1, v[j], G[r][i][j]));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = mul2(al2, G[r][i][j]);
+        store_res<F32>(a.out_r, row + c, v);
+        if (!a.y) continue;
+        y[r][i] = *reinterpret_cast<const uint4*>(sv[r] + at_y + c * 2);
+        unpack8(y[r][i], v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f2 dn = mul2(rv, d[j]);
-          P[i][j] = fma2(dn, v[j], P[i][j]);
-          G[i][j] = fma2(dn, wu[i][j], fma2(k1, v[j], G[i][j]));
+          Q[i][j] = fma2(mul2(gy, G[r][i][j]), v[j], Q[i][j]);
+          G[r][i][j] = mul2(G[r][i][j], wz[i][j]);
+          dot = fma2(G[r][i][j], v[j], dot);
         }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = mul2(al2, G[i][j]);
-      store_res<F32>(a.out_r, row + c, v);
-      if (!a.y) continue;
-      unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), y[i]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[i][j] = mul2(ry, y[i][j]);
-        Q[i][j] = fma2(token ? mul2(gt2, G[i][j]) : G[i][j], y[i][j], Q[i][j]);
-        G[i][j] = mul2(G[i][j], wz[i][j]);
-        dot = fma2(G[i][j], y[i][j], dot);
-      }
+      s1[r] = sum2(dot) * rys[r];
     }
     // the projection of dy on y's row, which without the token's gate is also
-    // that gate's gradient; the barrier ends the reads of the slot
-    float s1 = sum2(dot);
-    block_sum(s1, red1, half1, true);
-    if (threadIdx.x == 0) ring_load(a, g, full, smem, n + a.slots);
-    if (a.y) {
-      const f2 k2 = both(a.w_post ? -s1 * a.inv_h : 0.f), scale = both(gt * rys);
+    // that gate's gradient; the barrier ends the reads of the slots
+    block_sum<R>(s1, red, half1);
+    if (threadIdx.x == 0)
+#pragma unroll
+      for (int r = 0; r < R; ++r) ring_load(a, g, full, smem, n + r + a.slots);
+    if (!a.y) continue;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!live[r]) break;
+      const size_t row = static_cast<size_t>(t[r]) * a.h;
+      const f2 k2 = both(a.w_post ? -s1[r] * a.inv_h * rys[r] : 0.f), gy = both(gt[r] * rys[r]);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
+        f2 v[4];
+        unpack8(y[r][i], v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) G[i][j] = mul2(scale, fma2(k2, y[i][j], G[i][j]));
-        a.out_u[(row + c) >> 3] = pack8(G[i]);
+        for (int j = 0; j < 4; ++j) v[j] = mul2(gy, fma2(k2, v[j], G[r][i][j]));
+        a.out_u[(row + c) >> 3] = pack8(v);
       }
-      if (a.dgate && threadIdx.x == 0) a.dgate[t] = s1;
+      if (a.dgate && threadIdx.x == 0) a.dgate[t[r]] = s1[r];
     }
-    if (a.T - t <= static_cast<int>(gridDim.x)) break;
-    t += gridDim.x;
   }
   if (!ok) ring_drain(a, full, n);
   float* part = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.h;
@@ -539,11 +632,13 @@ int threads_for(int h) {
   return (need + 31) / 32 * 32;
 }
 
-// Blocks on an SM, and the rows that each keeps on their way: about 512 threads
-// (the registers for the weights and column sums allow no more), and at least
-// two slots for each block within the shared memory.
+// Blocks on an SM, and the rows that each keeps on their way: as many threads
+// as the registers allow (of a forward thread 64, of a backward one 128: the
+// weights and column sums), and at least two slots for each block within the
+// shared memory.
 struct Plan {
-  int threads, blocks, slots, slot_bytes, smem;
+  int threads, blocks, rows, slots, slot_bytes, smem;  // rows: side by side in a block
+  bool keep;
 };
 Plan plan_of(const moe_norm_dims& d, bool bwd) {
   constexpr int kSmem = 216 << 10;
@@ -551,18 +646,27 @@ Plan plan_of(const moe_norm_dims& d, bool bwd) {
   p.threads = threads_for(d.h);
   const int res = d.res_f32 ? 4 : 2;
   p.slot_bytes = d.h * (bwd ? 2 * res + 4 : res + 2);
-  int per_sm = 512 / p.threads;
+  // Forward: a row's pieces are kept where 512 threads hold enough columns at
+  // once.  Share of HBM over 2^25 elements, kept / read again, bf16 residual:
+  // h 512 82 / 64%, 2048 83 / 76, 4096 91 / 78, 8192 86 / 78; but 768 67 / 72,
+  // 2816 64 / 80, 4608 59 / 83, 5120 64 / 82, 6400 73 / 82; fp32: 768 80 / 74,
+  // 3328 91 / 82, 4096 90 / 80, 6400 81 / 81; but 2816 70 / 80, 4608 75 / 80.
+  p.keep = kMaxThreads / p.threads * d.h >= (d.res_f32 ? 5700 : 7000);
+  int per_sm = (bwd || p.keep ? kMaxThreads : kFwdThreads) / p.threads;
+  if (per_sm > 16) per_sm = 16;
   if (per_sm * 2 * p.slot_bytes > kSmem) per_sm = kSmem / (2 * p.slot_bytes);
   if (per_sm < 1) per_sm = 1;
   p.slots = kSmem / (per_sm * p.slot_bytes);
   if (p.slots > kMaxSlots) p.slots = kMaxSlots;
   p.smem = p.slots * p.slot_bytes;
+  // two rows need four slots; 9000 x 4608 bf16: 137 us with one, 125 with two
+  p.rows = bwd && per_sm == 1 && p.slots == kMaxSlots && p.threads <= kPairThreads ? 2 : 1;
   const int n = moe_api::num_sms() * per_sm;
   p.blocks = d.T < n ? d.T : n;
   // no more blocks than the same number of rounds needs: each leaves its sums
   if (bwd && d.T > 0) {
-    const int rounds = (d.T - 1) / n + 1;
-    p.blocks = (d.T - 1) / rounds + 1;
+    const int rounds = (d.T - 1) / (n * p.rows) + 1;
+    p.blocks = (d.T - 1) / (rounds * p.rows) + 1;
   }
   return p;
 }
@@ -586,9 +690,7 @@ cudaError_t launch_early(void (*kern)(P...), int blocks, int threads, int smem, 
   return e;
 }
 
-template <bool F32, bool BWD>
-cudaError_t launch(Args& a, const Plan& p, cudaStream_t s) {
-  auto kern = BWD ? block_norm_bwd_kernel<F32> : block_norm_fwd_kernel<F32>;
+cudaError_t launch(void (*kern)(Args), Args& a, const Plan& p, cudaStream_t s) {
   const cudaError_t e = moe::set_smem_once(reinterpret_cast<const void*>(kern), 216 << 10);
   if (e != cudaSuccess) return e;
   a.slots = p.slots;
@@ -658,7 +760,11 @@ moe_status moe_block_norm_fwd(const moe_norm_dims* dims, const void* r, const mo
   a.status = moe::nows_status_word();
   if (!a.status) return MOE_ERR_CUDA;
   const Plan p = plan_of(d, false);
-  const cudaError_t e = d.res_f32 ? launch<true, false>(a, p, s) : launch<false, false>(a, p, s);
+  const cudaError_t e =
+      launch(p.keep ? (d.res_f32 ? block_norm_fwd_kernel<true, true> : block_norm_fwd_kernel<false, true>)
+                    : (d.res_f32 ? block_norm_fwd_kernel<true, false>
+                                 : block_norm_fwd_kernel<false, false>),
+             a, p, s);
   return e == cudaSuccess && moe_api::note(s, "block_norm_fwd") ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -698,7 +804,10 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAlign);
   a.status = static_cast<int*>(ws);
   const Plan p = plan_of(d, true);
-  const cudaError_t e = d.res_f32 ? launch<true, true>(a, p, s) : launch<false, true>(a, p, s);
+  const cudaError_t e = launch(
+      p.rows == 1 ? (d.res_f32 ? block_norm_bwd_kernel<true, 1> : block_norm_bwd_kernel<false, 1>)
+                  : (d.res_f32 ? block_norm_bwd_kernel<true, 2> : block_norm_bwd_kernel<false, 2>),
+      a, p, s);
   if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (dw_pre || dw_post || channel) {
