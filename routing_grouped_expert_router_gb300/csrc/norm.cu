@@ -410,13 +410,18 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
 // blocks in order.
 // R rows go through these steps side by side: two where one block alone fits an
 // SM (rows of more than 4096) and a thread may have the registers for it.
+// ALL: every optional part is there (the training step's call), so the loops over a
+// row's pieces hold no branch on one, and the two pieces overlap (2^25 elements,
+// bf16, share of HBM without / with: h 1288 63 / 74%, 4096 80 / 88, 6400 64 / 73).
 constexpr int kPairThreads = 384;
-template <bool F32, int R>
+template <bool F32, int R, bool ALL>
 __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
     block_norm_bwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxSlots];
   __shared__ __align__(16) RedRows<R> red;
+  const bool has_y = ALL || a.y, has_dr = ALL || a.dr_out;
+  const bool post = ALL || a.w_post, pre = ALL || a.w_pre;
   int half3 = 0, half1 = 0;
   for (int i = threadIdx.x; i < static_cast<int>(sizeof(red) / 4); i += blockDim.x)
     reinterpret_cast<float*>(&red)[i] = 0.f;
@@ -480,14 +485,14 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
       t[r] = static_cast<int>(live[r] ? t0 + r * gridDim.x : t0);
       gt[r] = token ? __ldg(a.gate + t[r]) : 1.f;
       sv[r] = smem + ((n + r) % a.slots) * a.slot_bytes;
-      if (live[r]) ok = ring_wait(a, full, n + r) && ok;
+      if (R == 1 || live[r]) ok = ring_wait(a, full, n + r) && ok;
       f2 acc[3] = {0, 0, 0};
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
-        if (c >= a.h || !live[r]) continue;
+        if (c >= a.h || (R > 1 && !live[r])) continue;
         f2 v[4], d[4];
-        if (a.w_pre) {
+        if (pre) {
           load_res<F32>(sv[r], c, v);
           unpack8(*reinterpret_cast<const uint4*>(sv[r] + g.bytes[0] + c * 2), d);
 #pragma unroll
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
             acc[1] = fma2(mul2(d[j], wu[i][j]), v[j], acc[1]);
           }
         }
-        if (a.w_post) {
+        if (post) {
           unpack8(*reinterpret_cast<const uint4*>(sv[r] + at_y + c * 2), v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[2] = fma2(v[j], v[j], acc[2]);
@@ -512,8 +517,8 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
     float s1[R], rys[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float rvs = a.w_pre ? inv_rms(s3[r][0], a) : 0.f;
-      rys[r] = a.w_post ? inv_rms(s3[r][2], a) : 1.f;
+      const float rvs = pre ? inv_rms(s3[r][0], a) : 0.f;
+      rys[r] = post ? inv_rms(s3[r][2], a) : 1.f;
       const f2 rv = both(rvs), k1 = both(-s3[r][1] * a.inv_h * rvs * rvs * rvs);
       const f2 al2 = both(al), gy = both(gt[r] * rys[r]);
       const size_t row = static_cast<size_t>(t[r]) * a.h;
@@ -521,12 +526,12 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
-        if (c >= a.h || !live[r]) continue;
+        if (c >= a.h || (R > 1 && !live[r])) continue;
         f2 v[4], d[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) G[r][i][j] = 0;
-        if (a.dr_out) load_res<F32>(sv[r] + at_dr, c, G[r][i]);
-        if (a.w_pre) {
+        if (has_dr) load_res<F32>(sv[r] + at_dr, c, G[r][i]);
+        if (pre) {
           load_res<F32>(sv[r], c, v);
           unpack8(*reinterpret_cast<const uint4*>(sv[r] + g.bytes[0] + c * 2), d);
 #pragma unroll
@@ -539,7 +544,7 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = mul2(al2, G[r][i][j]);
         store_res<F32>(a.out_r, row + c, v);
-        if (!a.y) continue;
+        if (!has_y) continue;
         y[r][i] = *reinterpret_cast<const uint4*>(sv[r] + at_y + c * 2);
         unpack8(y[r][i], v);
 #pragma unroll
@@ -557,12 +562,12 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
     if (threadIdx.x == 0)
 #pragma unroll
       for (int r = 0; r < R; ++r) ring_load(a, g, full, smem, n + r + a.slots);
-    if (!a.y) continue;
+    if (!has_y) continue;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (!live[r]) break;
+      if (R > 1 && !live[r]) break;
       const size_t row = static_cast<size_t>(t[r]) * a.h;
-      const f2 k2 = both(a.w_post ? -s1[r] * a.inv_h * rys[r] : 0.f), gy = both(gt[r] * rys[r]);
+      const f2 k2 = both(post ? -s1[r] * a.inv_h * rys[r] : 0.f), gy = both(gt[r] * rys[r]);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -658,9 +663,14 @@ Plan plan_of(const moe_norm_dims& d, bool bwd) {
   if (per_sm < 1) per_sm = 1;
   p.slots = kSmem / (per_sm * p.slot_bytes);
   if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-  p.smem = p.slots * p.slot_bytes;
   // two rows need four slots; 9000 x 4608 bf16: 137 us with one, 125 with two
   p.rows = bwd && per_sm == 1 && p.slots == kMaxSlots && p.threads <= kPairThreads ? 2 : 1;
+  // Backward, one row at a time: the row that is worked on and the next.  More of
+  // them under way draw less from HBM (2^25 elements, bf16, share with four / two:
+  // h 1024 77 / 81%, 1288 70 / 74, 3328 80 / 82, 4096 85 / 88, 8192 83 / 83;
+  // 16384 x 4096: 138 us with four, 128 with two).
+  if (bwd && p.rows == 1) p.slots = 2;
+  p.smem = p.slots * p.slot_bytes;
   const int n = moe_api::num_sms() * per_sm;
   p.blocks = d.T < n ? d.T : n;
   // no more blocks than the same number of rounds needs: each leaves its sums
@@ -688,6 +698,13 @@ cudaError_t launch_early(void (*kern)(P...), int blocks, int threads, int smem, 
   if (e == cudaSuccess) return moe::launched();
   cudaGetLastError();  // reported here, not by the next launch
   return e;
+}
+
+template <bool F32>
+auto bwd_kernel(int rows, bool all) {
+  if (rows == 1)
+    return all ? block_norm_bwd_kernel<F32, 1, true> : block_norm_bwd_kernel<F32, 1, false>;
+  return all ? block_norm_bwd_kernel<F32, 2, true> : block_norm_bwd_kernel<F32, 2, false>;
 }
 
 cudaError_t launch(void (*kern)(Args), Args& a, const Plan& p, cudaStream_t s) {
@@ -804,10 +821,9 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAlign);
   a.status = static_cast<int*>(ws);
   const Plan p = plan_of(d, true);
-  const cudaError_t e = launch(
-      p.rows == 1 ? (d.res_f32 ? block_norm_bwd_kernel<true, 1> : block_norm_bwd_kernel<false, 1>)
-                  : (d.res_f32 ? block_norm_bwd_kernel<true, 2> : block_norm_bwd_kernel<false, 2>),
-      a, p, s);
+  const bool all = y && w_post && w_pre && dr_out;
+  const cudaError_t e =
+      launch(d.res_f32 ? bwd_kernel<true>(p.rows, all) : bwd_kernel<false>(p.rows, all), a, p, s);
   if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (dw_pre || dw_post || channel) {
