@@ -592,42 +592,49 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
   }
 }
 
-// The column gradients from the blocks' sums, a fixed order for each column: 32
-// interleaved chains, then those in order.
-constexpr int kColGroups = 32;  // a warp adds up each of the block's 32 columns
-__global__ void __launch_bounds__(32 * kColGroups)
+// The column gradients from the blocks' sums, a fixed order for each column:
+// interleaved chains, then those in order.  COLS columns to a block: 8 where two
+// blocks of 8 for each SM hold all, else 16 (1021 x 2056: 13.9 us in all
+// with 32 or 16, 12.9 with 8; 16384 x 4096: 128.6 with 32, 128.0 with 16, 131 with 8).
+constexpr int kColThreads = 1024;
+template <int COLS>
+__global__ void __launch_bounds__(kColThreads)
     block_norm_cols_kernel(const float* partial, int nblk, int h, const float* w_post,
                            const float* gate, float beta, float* dw_pre, float* dw_post,
                            float* dgate) {
+  constexpr int kChains = kColThreads / COLS;
   after_stream();
-  __shared__ float sp[kColGroups][33], sq[kColGroups][33];
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  __shared__ float sums[2][kChains][COLS + 1];
+  const int g = threadIdx.x / COLS, i = threadIdx.x % COLS;
+  const int c = blockIdx.x * COLS + i;
   float p = 0.f, q = 0.f;
   if (c < h) {
 #pragma unroll 8
-    for (int b = g; b < nblk; b += kColGroups) {
+    for (int b = g; b < nblk; b += kChains) {
       p += __ldcg(partial + static_cast<size_t>(b) * 2 * h + c);
       q += __ldcg(partial + static_cast<size_t>(b) * 2 * h + h + c);
     }
   }
-  sp[g][lane] = p;
-  sq[g][lane] = q;
+  sums[0][g][i] = p;
+  sums[1][g][i] = q;
   __syncthreads();
-  // warp g adds up column g: lane i holds chain i
-  const int col = blockIdx.x * 32 + g;
-  p = sp[lane][g];
-  q = sq[lane][g];
+  // a warp for each of the two sums of each column
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= 2 * COLS) return;
+  const int which = warp / COLS, col = blockIdx.x * COLS + warp % COLS;
+  float v = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    p += __shfl_xor_sync(kFull, p, o);
-    q += __shfl_xor_sync(kFull, q, o);
-  }
+  for (int n = lane; n < kChains; n += 32) v += sums[which][n][warp % COLS];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   if (lane != 0 || col >= h) return;
-  q *= beta;
-  if (dw_pre) dw_pre[col] = p;
-  if (dw_post) dw_post[col] = gate ? gate[col] * q : q;
-  if (dgate) dgate[col] = w_post ? w_post[col] * q : q;
+  if (which == 0) {
+    if (dw_pre) dw_pre[col] = v;
+    return;
+  }
+  v *= beta;
+  if (dw_post) dw_post[col] = gate ? gate[col] * v : v;
+  if (dgate) dgate[col] = w_post ? w_post[col] * v : v;
 }
 
 constexpr size_t kAlign = 256;
@@ -827,8 +834,10 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
   if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (dw_pre || dw_post || channel) {
-    if (launch_early(block_norm_cols_kernel, (d.h + 31) / 32, 32 * kColGroups, 0, s, a.partial,
-                     p.blocks, d.h, w_post, channel ? gate : nullptr, d.beta, dw_pre, dw_post,
+    const int cols = d.h > 16 * moe_api::num_sms() ? 16 : 8;
+    if (launch_early(cols == 8 ? block_norm_cols_kernel<8> : block_norm_cols_kernel<16>,
+                     (d.h + cols - 1) / cols, kColThreads, 0, s, a.partial, p.blocks, d.h, w_post,
+                     channel ? gate : nullptr, d.beta, dw_pre, dw_post,
                      channel ? dgate : nullptr) != cudaSuccess ||
         !moe_api::note(s, "block_norm_cols"))
       return MOE_ERR_CUDA;
