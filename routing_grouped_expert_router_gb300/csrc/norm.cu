@@ -408,14 +408,17 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
 // sum serves both (g_t: the token gate, else 1).  Each block keeps P and Q of its
 // rows in registers and writes them once; block_norm_cols_kernel adds the
 // blocks in order.
-// R rows go through these steps side by side: two where one block alone fits an
-// SM (rows of more than 4096) and a thread may have the registers for it.
+// R rows go through these steps side by side: two where a block is alone on
+// its SM (long rows) and a thread may have the registers for it.
 // ALL: every optional part is there (the training step's call), so the loops over a
 // row's pieces hold no branch on one, and the two pieces overlap (2^25 elements,
 // bf16, share of HBM without / with: h 1288 63 / 74%, 4096 80 / 88, 6400 64 / 73).
-constexpr int kPairThreads = 384;
-template <bool F32, int R, bool ALL>
-__global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
+// N pieces of the row to a thread: three (12 warps on an SM, 168 registers) where
+// that holds more columns on an SM than two (16 warps).
+constexpr int kPairThreads = 384, kThreeThreads = 192;
+template <bool F32, int R, bool ALL, int N>
+__global__ void __launch_bounds__(R == 2 ? kPairThreads : N == 3 ? kThreeThreads : kMaxThreads,
+                                  N == 3 ? 2 : 1)
     block_norm_bwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxSlots];
@@ -444,10 +447,10 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
   if (threadIdx.x == 0)
     for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
   // w_pre, and the factor of G in dz's product with w_post
-  f2 wu[kPieces][4], wz[kPieces][4];
-  f2 P[kPieces][4], Q[kPieces][4];
+  f2 wu[N][4], wz[N][4];
+  f2 P[N][4], Q[N][4];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
       if (R == 1 || live[r]) ok = ring_wait(a, full, n + r) && ok;
       f2 acc[3] = {0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      for (int i = 0; i < N; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h || (R > 1 && !live[r])) continue;
         f2 v[4], d[4];
@@ -512,8 +515,8 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
     }
     ok = block_sum3<R>(s3, red, half3, ok);
     if (!ok) break;
-    f2 G[R][kPieces][4];
-    uint4 y[R][kPieces];
+    f2 G[R][N][4];
+    uint4 y[R][N];
     float s1[R], rys[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
       const size_t row = static_cast<size_t>(t[r]) * a.h;
       f2 dot = 0;
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      for (int i = 0; i < N; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h || (R > 1 && !live[r])) continue;
         f2 v[4], d[4];
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
       const size_t row = static_cast<size_t>(t[r]) * a.h;
       const f2 k2 = both(post ? -s1[r] * a.inv_h * rys[r] : 0.f), gy = both(gt[r] * rys[r]);
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      for (int i = 0; i < N; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
         f2 v[4];
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(R == 1 ? kMaxThreads : kPairThreads)
   if (!ok) ring_drain(a, full, n);
   float* part = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.h;
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
     if (c >= a.h) continue;
     store8(part + c, P[i]);
@@ -639,8 +642,8 @@ __global__ void __launch_bounds__(kColThreads)
 
 constexpr size_t kAlign = 256;
 
-int threads_for(int h) {
-  const int need = (h / 8 + kPieces - 1) / kPieces;
+int threads_for(int h, int pieces) {
+  const int need = (h / 8 + pieces - 1) / pieces;
   return (need + 31) / 32 * 32;
 }
 
@@ -649,13 +652,14 @@ int threads_for(int h) {
 // weights and column sums), and at least two slots for each block within the
 // shared memory.
 struct Plan {
-  int threads, blocks, rows, slots, slot_bytes, smem;  // rows: side by side in a block
+  int threads, blocks, pieces, rows, slots, slot_bytes, smem;  // rows: side by side in a block
   bool keep;
 };
 Plan plan_of(const moe_norm_dims& d, bool bwd) {
   constexpr int kSmem = 216 << 10;
   Plan p;
-  p.threads = threads_for(d.h);
+  p.threads = threads_for(d.h, kPieces);
+  p.pieces = kPieces;
   const int res = d.res_f32 ? 4 : 2;
   p.slot_bytes = d.h * (bwd ? 2 * res + 4 : res + 2);
   // Forward: a row's pieces are kept where 512 threads hold enough columns at
@@ -665,12 +669,28 @@ Plan plan_of(const moe_norm_dims& d, bool bwd) {
   // 3328 91 / 82, 4096 90 / 80, 6400 81 / 81; but 2816 70 / 80, 4608 75 / 80.
   p.keep = kMaxThreads / p.threads * d.h >= (d.res_f32 ? 5700 : 7000);
   int per_sm = (bwd || p.keep ? kMaxThreads : kFwdThreads) / p.threads;
+  // Backward, bf16 residual: three pieces to a thread where blocks of two hold few
+  // columns on an SM and blocks of three more.  Share of HBM over 2^25 elements,
+  // two / three: h 768 74 / 81%, 1288 76 / 82, 2056 79 / 87, 2816 78 / 86, 4352 63 /
+  // 87, 4608 64 / 85; but 1536 (7680 columns with two) 86 / 82, and of fp32 rows
+  // 768 81 / 65, 2816 92 / 79, 4352 85 / 79.
+  const int per_sm3 = 2 * kThreeThreads / threads_for(d.h, 3);
+  if (bwd && !d.res_f32 && per_sm * d.h < 7000 && per_sm3 > per_sm) {
+    p.pieces = 3;
+    p.threads = threads_for(d.h, 3);
+    per_sm = per_sm3;
+  }
   if (per_sm > 16) per_sm = 16;
-  if (per_sm * 2 * p.slot_bytes > kSmem) per_sm = kSmem / (2 * p.slot_bytes);
+  // The backward's rows on their way to an SM: 160 KiB at most.  More of them draw
+  // less from HBM (fp32, 216 / 160 KiB: h 512 74 / 79%, 1024 78 / 85, 2048 80 / 84,
+  // 4096 80 / 89, other sizes the same).
+  const int most = bwd ? 160 << 10 : kSmem;
+  if (per_sm * 2 * p.slot_bytes > most) per_sm = most / (2 * p.slot_bytes);
   if (per_sm < 1) per_sm = 1;
   p.slots = kSmem / (per_sm * p.slot_bytes);
   if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-  // two rows need four slots; 9000 x 4608 bf16: 137 us with one, 125 with two
+  // Two rows need four slots (one row / two, fp32: h 3584 62 / 83%, 4096 67 / 89;
+  // bf16: 5120 66 / 68).
   p.rows = bwd && per_sm == 1 && p.slots == kMaxSlots && p.threads <= kPairThreads ? 2 : 1;
   // Backward, one row at a time: the row that is worked on and the next.  More of
   // them under way draw less from HBM (2^25 elements, bf16, share with four / two:
@@ -707,11 +727,16 @@ cudaError_t launch_early(void (*kern)(P...), int blocks, int threads, int smem, 
   return e;
 }
 
+template <bool F32, bool ALL>
+auto bwd_kernel(const Plan& p) {
+  if (p.rows == 2) return block_norm_bwd_kernel<F32, 2, ALL, 2>;
+  if constexpr (!F32)
+    if (p.pieces == 3) return block_norm_bwd_kernel<F32, 1, ALL, 3>;
+  return block_norm_bwd_kernel<F32, 1, ALL, 2>;
+}
 template <bool F32>
-auto bwd_kernel(int rows, bool all) {
-  if (rows == 1)
-    return all ? block_norm_bwd_kernel<F32, 1, true> : block_norm_bwd_kernel<F32, 1, false>;
-  return all ? block_norm_bwd_kernel<F32, 2, true> : block_norm_bwd_kernel<F32, 2, false>;
+auto bwd_kernel(const Plan& p, bool all) {
+  return all ? bwd_kernel<F32, true>(p) : bwd_kernel<F32, false>(p);
 }
 
 cudaError_t launch(void (*kern)(Args), Args& a, const Plan& p, cudaStream_t s) {
@@ -830,7 +855,7 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
   const Plan p = plan_of(d, true);
   const bool all = y && w_post && w_pre && dr_out;
   const cudaError_t e =
-      launch(d.res_f32 ? bwd_kernel<true>(p.rows, all) : bwd_kernel<false>(p.rows, all), a, p, s);
+      launch(d.res_f32 ? bwd_kernel<true>(p, all) : bwd_kernel<false>(p, all), a, p, s);
   if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (dw_pre || dw_post || channel) {
