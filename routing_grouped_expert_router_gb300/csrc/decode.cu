@@ -80,7 +80,6 @@ struct Params {
   int n1;                   // T rounded up to 16: FC1's MMA columns
   int stages;
   int tok_group, groups, slices, slice_h;  // router work units
-  int red_at;
   const uint16_t* x;
   const float *Wg, *b;
   int32_t* idx;
@@ -307,6 +306,18 @@ __device__ void select_topk(const Params& p, int t, float l0, float l1, int lane
   }
 }
 
+// s[0] + s[stride] + ... (n of them): four chains in a fixed order.
+__device__ __forceinline__ float add_up(const float* s, int n, int stride) {
+  float v[4] = {};
+  int i = 0;
+#pragma unroll 2
+  for (; i + 4 <= n; i += 4)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] += s[(i + u) * stride];
+  for (; i < n; ++i) v[0] += s[i * stride];
+  return (v[0] + v[1]) + (v[2] + v[3]);
+}
+
 // A router unit is a group of tokens x a slice of h: fp32 partial logits.  All
 // that a unit reads is asked for at once (the slice's rows of Wg are one
 // contiguous piece); what this phase costs is latency, and loads in the loop's
@@ -320,9 +331,8 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
   const int e = tid % p.E, part = tid / p.E;
   float* wg = reinterpret_cast<float*>(smem);                          // [nj][E]
   uint8_t* xs = smem + static_cast<size_t>(p.slice_h) * p.E * 4;       // [8][nj] bf16
-  // [8][kThreads], after those and after the partial logits that are read back
-  // into wg's place
-  float* red = reinterpret_cast<float*>(smem + p.red_at);
+  float* red = reinterpret_cast<float*>(smem + static_cast<size_t>(p.slice_h) *
+                                                  (p.E * 4 + kGroupTok * 2));  // [8][kThreads]
   float* logit = red + kThreads * kGroupTok;                           // [8][kMaxE]
   const uint32_t bar = smem_u32(&c.rbar);
   uint32_t ph = 0;
@@ -361,22 +371,17 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
           acc[t] = fmaf(bf16_hi(q.w), w[7], acc[t]);
         }
       }
-    auto add_parts = [&](float* out, int ld, const float* bias) {
 #pragma unroll
-      for (int t = 0; t < kGroupTok; ++t)
-        if (t < nt) red[t * kThreads + tid] = acc[t];
-      __syncthreads();
-      for (int i = tid; i < nt * p.E; i += kThreads) {
-        const int t = i / p.E, ee = i - t * p.E;
-        float v = 0.f;
-#pragma unroll 4
-        for (int q = 0; q < parts; ++q) v += red[t * kThreads + q * p.E + ee];
-        out[t * ld + ee] = bias ? v + __ldg(bias + ee) : v;
-      }
-    };
+    for (int t = 0; t < kGroupTok; ++t)
+      if (t < nt) red[t * kThreads + tid] = acc[t];
+    __syncthreads();
     // [group][slice][token][expert]
-    float* mine = p.logits + static_cast<size_t>(unit) * p.tok_group * p.E;
-    add_parts(mine, p.E, nullptr);
+    const int pairs = p.tok_group * p.E;  // 512 at most
+    float* mine = p.logits + static_cast<size_t>(unit) * pairs;
+    for (int i = tid; i < nt * p.E; i += kThreads) {
+      const int t = i / p.E;
+      mine[i] = add_up(red + t * kThreads + i - t * p.E, parts, p.E);
+    }
     __syncthreads();
     if (tid == 0) {
       unsigned n;
@@ -389,19 +394,21 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
     }
     __syncthreads();
     if (!c.flag) continue;
-    const float* all = p.logits + static_cast<size_t>(g) * p.slices * p.tok_group * p.E;
-    const int n = p.slices * p.tok_group * p.E;
+    // a thread adds up one pair's slices, or every few of them, straight from L2
+    const float* all = p.logits + static_cast<size_t>(g) * p.slices * pairs;
+    const int adders = kThreads / pairs, pair = tid % pairs;
+    float v = 0.f;
+    if (tid < adders * pairs)
 #pragma unroll 8
-    for (int i = tid; i < n; i += kThreads) wg[i] = __ldcg(all + i);
+      for (int q = tid / pairs; q < p.slices; q += adders)
+        v += __ldcg(all + static_cast<size_t>(q) * pairs + pair);
+    red[tid] = v;
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < kGroupTok; ++t) acc[t] = 0.f;
-    if (part < parts)
-      for (int q = part; q < p.slices; q += parts)
-#pragma unroll
-        for (int t = 0; t < kGroupTok; ++t)
-          if (t < nt) acc[t] += wg[(q * p.tok_group + t) * p.E + e];
-    add_parts(logit, kMaxE, p.b);
+    if (tid < nt * p.E) {
+      const int t = tid / p.E, ee = tid - t * p.E;
+      const float sum = add_up(red + tid, adders, pairs);
+      logit[t * kMaxE + ee] = p.b ? sum + __ldg(p.b + ee) : sum;
+    }
     __syncthreads();
     if (warp < nt)
       select_topk(p, t0 + warp, lane < p.E ? logit[warp * kMaxE + lane] : 0.f,
@@ -409,10 +416,11 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
   }
 }
 
-// x rows to e4m3, a block for each row.
+// x rows to e4m3, a block for each row, from the last block on: with few tokens
+// the router has no unit for it, and it must not hold up the router's.
 __device__ void quant_x(const Params& p, float* red) {
   const int tid = threadIdx.x, n8 = p.h / 8;
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+  for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) {
     const uint4* row = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.h);
     float m = 0.f;
     for (int c = tid; c < n8; c += kThreads) m = fmaxf(m, amax8(row[c]));
@@ -435,16 +443,25 @@ __device__ void quant_x(const Params& p, float* red) {
 __device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int R = p.T * p.k, chunks = (R + 31) / 32;
+  constexpr int kMine = kMaxRows / kThreads;
+  int rank[kMine], mine[kMine];  // my assignments' rank within their chunk of 32, expert
+  float gate[kMine], sx = 0.f;
+#pragma unroll
+  for (int n = 0; n < kMine; ++n) {  // all loads at once
+    const int a = (warp + n * (kThreads / 32)) * 32 + lane;
+    mine[n] = a < R ? __ldcg(p.idx + a) : -1;
+    gate[n] = a < R ? __ldcg(p.gates + a) : 0.f;
+  }
+  if (f8 && tid < p.T) sx = __ldcg(p.sx + tid);
   for (int i = tid; i < chunks * kMaxE; i += kThreads) c.hist[i / kMaxE][i % kMaxE] = 0;
-  if (f8)
-    for (int t = tid; t < p.T; t += kThreads) c.sx[t] = __ldcg(p.sx + t);
+  if (f8 && tid < p.T) c.sx[tid] = sx;
   __syncthreads();
-  int rank[kMaxRows / kThreads];  // of my assignments within their chunk of 32
-  for (int ch = warp, n = 0; ch < chunks; ch += kThreads / 32, ++n) {
-    const int a = ch * 32 + lane;
-    int e = a < R ? __ldcg(p.idx + a) : -1;
+#pragma unroll
+  for (int n = 0; n < kMine; ++n) {
+    const int ch = warp + n * (kThreads / 32), a = ch * 32 + lane, e = mine[n];
+    if (ch >= chunks) break;
     if (a < R) {
-      c.gate[a] = __ldcg(p.gates + a);
+      c.gate[a] = gate[n];
       c.exp[a] = static_cast<uint8_t>(e);
     }
     const unsigned same = __match_any_sync(kFull, e);
@@ -492,10 +509,11 @@ __device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
     }
   }
   __syncthreads();
-  for (int ch = warp, n = 0; ch < chunks; ch += kThreads / 32, ++n) {
-    const int a = ch * 32 + lane;
+#pragma unroll
+  for (int n = 0; n < kMine; ++n) {
+    const int ch = warp + n * (kThreads / 32), a = ch * 32 + lane, e = mine[n];
     if (a >= R) break;
-    const int e = c.exp[a], r = c.hist[ch][e] + rank[n];
+    const int r = c.hist[ch][e] + rank[n];
     const bool placed = r < p.capacity;
     const int row = c.off[e] + r;
     c.pos[a] = static_cast<int16_t>(placed ? row : -1);
@@ -730,11 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   // ------------------------------------------------------------- route
-  if (F8) {
-    quant_x(p, reinterpret_cast<float*>(smem));
+  if (F8)
     for (int i = blockIdx.x * kThreads + tid; i < p.T * p.k; i += G * kThreads) p.amax[i] = 0;
-  }
   route(p, c, smem);
+  if (F8) quant_x(p, reinterpret_cast<float*>(smem));
   fence_proxy_async_all();  // xq for TMA; and the ring's memory, used by route above
   __syncthreads();
   if (tid == 0 && !grid_barrier(words + kBarWord, G, p.status)) c.abort = 1;
@@ -1214,9 +1231,8 @@ struct Layout {
 
 struct Plan {
   int n1, stages, smem;
-  int tok_group, groups, slices, slice_h, red_at;
+  int tok_group, groups, slices, slice_h;
   size_t pieces;
-  bool ok;
 };
 
 // The most k-steps that a phase can have, with every expert that can be hit.
@@ -1251,11 +1267,6 @@ Plan plan_of(const moe_dims& d, int blocks, bool fp8) {
   p.slices = (d.h + p.slice_h - 1) / p.slice_h;
   p.pieces = static_cast<size_t>(blocks) *
              (most_steps(d, fp8) >= static_cast<long long>(kRoundsFrom) * blocks ? kRounds : 1);
-  // so do a group's partial logits of all slices, where h is not enormous
-  const int slice = p.slice_h * (d.E * 4 + kGroupTok * 2);
-  const int back = (p.slices * p.tok_group * d.E * 4 + 15) / 16 * 16;
-  p.red_at = slice > back ? slice : back;
-  p.ok = p.red_at <= room;
   return p;
 }
 
@@ -1293,7 +1304,6 @@ bool supported(const moe_dims& d, bool fp8) {
   // (a k-step is 32 KiB of weights: 14 million of them are 450 GB)
   if (most_steps(d, fp8) >= (1ll << 31) / moe_api::num_sms()) return false;
   if (moe_api::num_sms() * kRounds > kMaxPieces) return false;
-  if (d.T > 0 && !plan_of(d, moe_api::num_sms(), fp8).ok) return false;
   if (d.f > (1 << 22)) return false;  // Ctrl::join's tile numbers
   return static_cast<long long>(d.E) * (d.h > d.f ? d.h : d.f) * 2 < (1ll << 31);
 }
@@ -1348,7 +1358,6 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
   p.groups = plan.groups;
   p.slices = plan.slices;
   p.slice_h = plan.slice_h;
-  p.red_at = plan.red_at;
   p.x = x;
   p.Wg = Wg;
   p.b = d.has_bias ? b : nullptr;
