@@ -29,11 +29,11 @@
 //   * FC2's first stages of weights are loaded before the barriers that make H
 //     whole (bringing more of them into L2 meanwhile gained nothing).
 // Measured on GB300 (1.9 GHz): 128 tokens, top 2 of 8 experts of 4096 x 14336 in
-// 458 us, the weights at 6.2 TB/s over all and 6.6 in FC1 (a kernel of these
+// 457 us, the weights at 6.2 TB/s over all and 6.6 in FC1 (a kernel of these
 // loads and nothing else reads 7.1); 32 tokens, top 6 of 64 experts of 2048 x 1408
-// in 180 us (DRAM reads 1.08 GB, the weights hit; tensor pipe 6% busy); one token
-// of the same layer in 39 us, of which the weights need 15: the rest is the
-// router (7), the first loads (3), four grid barriers (1 each), joins and combine.
+// in 179 us (DRAM reads 1.08 GB, the weights hit; tensor pipe 6% busy); one token
+// of the same layer in 37 us, of which the weights need 15: the rest is the
+// router (5), the first loads (3), four grid barriers (1 each), joins and combine.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -322,7 +322,7 @@ __device__ __forceinline__ float add_up(const float* s, int n, int stride) {
 // that a unit reads is asked for at once (the slice's rows of Wg are one
 // contiguous piece); what this phase costs is latency, and loads in the loop's
 // order took 14 us for one token and 25 us for 32 where this takes 4 to 5.
-// The block that finishes a group's last slice adds the slices in order and
+// The block that finishes a group's last slice adds the slices in a fixed order and
 // chooses the experts of its tokens, one warp for each.
 __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
