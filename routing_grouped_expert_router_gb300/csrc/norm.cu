@@ -417,11 +417,15 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
 // row's pieces hold no branch on one, and the two pieces overlap (2^25 elements,
 // bf16, share of HBM without / with: h 1288 63 / 74%, 4096 80 / 88, 6400 64 / 73).
 // N pieces of the row to a thread: three (12 warps on an SM, 168 registers) where
-// that holds more columns on an SM than two (16 warps).
-constexpr int kPairThreads = 384, kThreeThreads = 192;
+// that holds more columns on an SM than two (16 warps), and in a block of 256
+// threads that is alone on its SM three, with two rows side by side, or four.
+constexpr int kPairThreads = 384, kThreeThreads = 192, kWideThreads = 256;
 template <bool F32, int R, bool ALL, int N>
-__global__ void __launch_bounds__(R == 2 ? kPairThreads : N == 3 ? kThreeThreads : kMaxThreads,
-                                  N == 3 ? 2 : 1)
+__global__ void __launch_bounds__(R * N > 3 && N > 2 ? kWideThreads
+                                  : R == 2             ? kPairThreads
+                                  : N == 3             ? kThreeThreads
+                                                       : kMaxThreads,
+                                  R == 1 && N == 3 ? 2 : 1)
     block_norm_bwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxSlots];
@@ -690,16 +694,25 @@ Plan plan_of(const moe_norm_dims& d, bool bwd) {
   const int most = bwd ? 160 << 10 : kSmem;
   if (per_sm * 2 * p.slot_bytes > most) per_sm = most / (2 * p.slot_bytes);
   if (per_sm < 1) per_sm = 1;
+  // Long bf16 rows, a block to an SM: fewer warps with more pieces each.  Share of
+  // HBM with two pieces / 256 threads: h 5120 68 / 74%, 6144 77 / 81, 7168 76 / 79,
+  // 8192 81 / 84 (one piece and twice the threads, 5120: 62).
+  if (bwd && !d.res_f32 && per_sm == 1) {
+    p.threads = kWideThreads;
+    p.pieces = d.h <= 24 * kWideThreads ? 3 : 4;
+  }
   p.slots = kSmem / (per_sm * p.slot_bytes);
   if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-  // Two rows need four slots (one row / two, fp32: h 3584 62 / 83%, 4096 67 / 89;
-  // bf16: 5120 66 / 68).
-  p.rows = bwd && per_sm == 1 && p.slots == kMaxSlots && p.threads <= kPairThreads ? 2 : 1;
+  // Two rows need four slots (one row / two, fp32: h 3584 62 / 83%, 4096 67 / 89).
+  p.rows = bwd && per_sm == 1 && p.slots == kMaxSlots && p.threads <= kPairThreads && p.pieces < 4
+               ? 2
+               : 1;
   // Backward, one row at a time: the row that is worked on and the next.  More of
   // them under way draw less from HBM (2^25 elements, bf16, share with four / two:
   // h 1024 77 / 81%, 1288 70 / 74, 3328 80 / 82, 4096 85 / 88, 8192 83 / 83;
-  // 16384 x 4096: 138 us with four, 128 with two).
-  if (bwd && p.rows == 1) p.slots = 2;
+  // 16384 x 4096: 138 us with four, 128 with two).  Rows of four
+  // pieces take the three or four that fit: 8192 82 / 84%.
+  if (bwd && p.rows == 1 && p.pieces < 4) p.slots = 2;
   p.smem = p.slots * p.slot_bytes;
   const int n = moe_api::num_sms() * per_sm;
   p.blocks = d.T < n ? d.T : n;
@@ -732,9 +745,13 @@ cudaError_t launch_early(void (*kern)(P...), int blocks, int threads, int smem, 
 
 template <bool F32, bool ALL>
 auto bwd_kernel(const Plan& p) {
-  if (p.rows == 2) return block_norm_bwd_kernel<F32, 2, ALL, 2>;
-  if constexpr (!F32)
+  if constexpr (F32) {
+    if (p.rows == 2) return block_norm_bwd_kernel<F32, 2, ALL, 2>;
+  } else {
+    if (p.rows == 2) return block_norm_bwd_kernel<F32, 2, ALL, 3>;
     if (p.pieces == 3) return block_norm_bwd_kernel<F32, 1, ALL, 3>;
+    if (p.pieces == 4) return block_norm_bwd_kernel<F32, 1, ALL, 4>;
+  }
   return block_norm_bwd_kernel<F32, 1, ALL, 2>;
 }
 template <bool F32>

@@ -123,7 +123,7 @@ def close_sum(got, ref, what):
 
 
 SIZES = [(1, 8), (1, 64), (3, 520), (5, 1024), (7, 6400), (33, 2056), (40, 4096), (2, 8192), (1100, 256), (9, 8184),
-         (2000, 768), (650, 4352), (11, 5120), (310, 4096)]  # other numbers of threads and of rows side by side
+         (2000, 768), (650, 4352), (11, 5120), (310, 4096), (613, 5128), (477, 7176)]  # other numbers of threads and of rows side by side
 
 
 @pytest.mark.parametrize("f32", [False, True])
@@ -160,7 +160,7 @@ def test_optional_parts(parts, gate, f32):
     check_parts(37, 1032, parts, gate, f32)
 
 
-@pytest.mark.parametrize("T,h,f32", [(700, 1536, False), (310, 4096, True), (307, 5120, False), (5, 6400, True)])
+@pytest.mark.parametrize("T,h,f32", [(700, 1536, False), (310, 4096, True), (307, 5120, False), (309, 7168, False), (5, 6400, True)])
 @pytest.mark.parametrize("parts", PARTS, ids=["no_post", "no_pre", "residual_only", "first_norm"])
 def test_optional_parts_of_longer_rows(parts, T, h, f32):
     check_parts(T, h, parts, "channel", f32)
