@@ -10,7 +10,7 @@
 // once.  A row has two sums in a chain, and a block that waits for its loads and
 // then for its sums leaves HBM idle (a block for each row: 4.5 TB/s forward), so
 // the blocks stay, each with a ring of the next rows in shared memory that bulk
-// copies fill, and keep the channel weights in registers: two (or three) 8-element
+// copies fill, and keep the channel weights in registers: two to four 8-element
 // pieces of the row to a thread, the same columns for every row.
 // Measured on GB300, bf16, 16384 x 4096: forward 82 us (6.5 TB/s, 0.96 of a copy's
 // rate), backward 128 us (rows 120, the column sums the rest); 7 x 6400 fp32
@@ -253,9 +253,11 @@ __device__ __forceinline__ void after_stream() {
 
 // KEEP: a thread keeps its pieces of r and y between the two sums and the slot is
 // free after the first; otherwise it reads y again, with registers to spare for
-// twice the threads on an SM.
-template <bool F32, bool KEEP>
-__global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kernel(const Args a) {
+// twice the threads on an SM.  N: pieces of a row to a thread.
+constexpr int kKeepThreads = 256;  // of a block with three pieces to a thread
+template <bool F32, bool KEEP, int N>
+__global__ void __launch_bounds__(N == 3 ? kKeepThreads : kMaxThreads, KEEP && N == 2 ? 1 : 2)
+    block_norm_fwd_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kMaxSlots];
   __shared__ __align__(16) Red1 red;
@@ -276,9 +278,9 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
   if (threadIdx.x == 0)
     for (int n = 0; n < a.slots; ++n) ring_load(a, g, full, smem, n);
   // the scale of each of my columns of y, and of u
-  f2 wz[kPieces][4], wu[kPieces][4];
+  f2 wz[N][4], wu[N][4];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
     if (c >= a.h) continue;
     f2 w[4];
@@ -306,12 +308,12 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
     const uint8_t* slot = smem + (n % a.slots) * a.slot_bytes;
     const uint8_t* sy = slot + g.bytes[0];
     const f2 al = both(a.alpha);
-    f2 v[kPieces][4], acc = 0;
+    f2 v[N][4], acc = 0;
     float ss = 0.f;
     if (KEEP) {
-      f2 z[kPieces][4];
+      f2 z[N][4];
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      for (int i = 0; i < N; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
         load_res<F32>(slot, c, v[i]);
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
         if (a.w_post) s *= inv_rms(ss, a);
         const f2 s2 = both(s);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int i = 0; i < N; ++i) {
           const int c = (threadIdx.x + i * blockDim.x) * 8;
           if (c >= a.h) continue;
 #pragma unroll
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
       if (a.w_pre) {
         acc = 0;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
+        for (int i = 0; i < N; ++i)
           if ((threadIdx.x + i * blockDim.x) * 8 < a.h)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
       f2 z[4];
       if (a.w_post) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
+        for (int i = 0; i < N; ++i) {
           const int c = (threadIdx.x + i * blockDim.x) * 8;
           if (c >= a.h) continue;
           unpack8(*reinterpret_cast<const uint4*>(sy + c * 2), z);
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
       const f2 s2 = both(s);
       acc = 0;
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      for (int i = 0; i < N; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
         load_res<F32>(slot, c, v[i]);
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kMaxThreads, KEEP ? 1 : 2) block_norm_fwd_kern
     if (a.w_pre) {
       const f2 rv = both(inv_rms(ss, a));
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      for (int i = 0; i < N; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
         if (c >= a.h) continue;
 #pragma unroll
@@ -669,12 +671,18 @@ Plan plan_of(const moe_norm_dims& d, bool bwd) {
   p.pieces = kPieces;
   const int res = d.res_f32 ? 4 : 2;
   p.slot_bytes = d.h * (bwd ? 2 * res + 4 : res + 2);
-  // Forward: a row's pieces are kept where 512 threads hold enough columns at
-  // once.  Share of HBM over 2^25 elements, kept / read again, bf16 residual:
-  // h 512 82 / 64%, 2048 83 / 76, 4096 91 / 78, 8192 86 / 78; but 768 67 / 72,
-  // 2816 64 / 80, 4608 59 / 83, 5120 64 / 82, 6400 73 / 82; fp32: 768 80 / 74,
-  // 3328 91 / 82, 4096 90 / 80, 6400 81 / 81; but 2816 70 / 80, 4608 75 / 80.
+  // Forward: two pieces of a row to a thread, which keeps them, where 512 threads
+  // hold enough columns at once that way; else three, up to 6144 columns; else two
+  // that are read again (h 6400 bf16, share of HBM over 2^25 elements: kept 73%,
+  // read again 82).  Two read again / three kept, bf16: h 768 71 / 80%, 1288 78 /
+  // 88, 2056 78 / 87, 3328 84 / 89, 4608 82 / 89, 5120 82 / 89, 6144 80 / 82; fp32:
+  // 4352 81 / 87, 5120 80 / 88, 5632 80 / 86.  Two kept, bf16: 2048 89, 4096 88.
   p.keep = kMaxThreads / p.threads * d.h >= (d.res_f32 ? 5700 : 7000);
+  if (!bwd && !p.keep && threads_for(d.h, 3) <= kKeepThreads) {
+    p.keep = true;
+    p.pieces = 3;
+    p.threads = threads_for(d.h, 3);
+  }
   int per_sm = (bwd || p.keep ? kMaxThreads : kFwdThreads) / p.threads;
   // Backward, bf16 residual: three pieces to a thread where blocks of two hold few
   // columns on an SM and blocks of three more.  Share of HBM over 2^25 elements,
@@ -741,6 +749,14 @@ cudaError_t launch_early(void (*kern)(P...), int blocks, int threads, int smem, 
   if (e == cudaSuccess) return moe::launched();
   cudaGetLastError();  // reported here, not by the next launch
   return e;
+}
+
+template <bool F32>
+auto fwd_kernel(const Plan& p) {
+  if (p.pieces == 3) return block_norm_fwd_kernel<F32, true, 3>;
+  if constexpr (!F32)  // fp32 rows that long are always kept
+    if (!p.keep) return block_norm_fwd_kernel<F32, false, 2>;
+  return block_norm_fwd_kernel<F32, true, 2>;
 }
 
 template <bool F32, bool ALL>
@@ -829,11 +845,7 @@ moe_status moe_block_norm_fwd(const moe_norm_dims* dims, const void* r, const mo
   a.status = moe::nows_status_word();
   if (!a.status) return MOE_ERR_CUDA;
   const Plan p = plan_of(d, false);
-  const cudaError_t e =
-      launch(p.keep ? (d.res_f32 ? block_norm_fwd_kernel<true, true> : block_norm_fwd_kernel<false, true>)
-                    : (d.res_f32 ? block_norm_fwd_kernel<true, false>
-                                 : block_norm_fwd_kernel<false, false>),
-             a, p, s);
+  const cudaError_t e = launch(d.res_f32 ? fwd_kernel<true>(p) : fwd_kernel<false>(p), a, p, s);
   return e == cudaSuccess && moe_api::note(s, "block_norm_fwd") ? MOE_OK : MOE_ERR_CUDA;
 }
 
