@@ -657,7 +657,7 @@ int threads_for(int h, int pieces) {
 }
 
 // Blocks on an SM, and the rows that each keeps on their way: as many threads
-// as the registers allow (of a forward thread 64, of a backward one 128: the
+// as the registers allow (a forward thread takes 64 to 128, a backward one 128 to 240: the
 // weights and column sums), and at least two slots for each block within the
 // shared memory.
 struct Plan {
