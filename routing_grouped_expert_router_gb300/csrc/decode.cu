@@ -78,14 +78,14 @@ constexpr int kGroupWord = 32;  // router units done for each token group (16)
 struct Params {
   int T, h, f, E, k, capacity;
   int n1;                   // T rounded up to 16: FC1's MMA columns
-  int stages;
+  int ring_bytes;           // shared memory of the ring
   int tok_group, groups, slices, slice_h;  // router work units
   const uint16_t* x;
   const float *Wg, *b;
   int32_t* idx;
   float* gates;
   float* logits;            // [groups, slices, tok_group, E]
-  uint16_t* H;              // [T*k, f]
+  uint16_t* H;              // [T*k, f]; bf16 weights: [2, T*k, f], H's high and low parts
   float* O;                 // [T*k, h]
   float* part;              // FC1 [2 * pieces][T, 2, 128]: sums of shared tiles;
                             // FC2 [pieces][T, 256]: of tiles begun in another piece
@@ -527,8 +527,19 @@ __device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// H of a row's column from its two sums, rounded to bf16: FC2's tensor-core
-// operand (e4m3: the value that its codes are made from).
+// H of a row's column from its two sums.  With bf16 weights it enters FC2 as two
+// bf16 operands, its rounded value and what that leaves: 16 bits, where one
+// bf16 made y's error 1.4 times that of y's own rounding (0.0024 against
+// 0.0017).  They are more columns of an idle tensor pipe and no more weights.
+// With e4m3 weights H's bf16 value is what its codes are made from.
+// The low parts of two values with the high parts hi (0 where those are not finite).
+__device__ __forceinline__ uint32_t low_parts(float a, float b, uint32_t hi) {
+  const float ha = bf16_lo(hi), hb = bf16_hi(hi);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(fabsf(ha) < INFINITY ? a - ha : 0.f,
+                                                 fabsf(hb) < INFINITY ? b - hb : 0.f);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 template <bool F8>
 __device__ __forceinline__ void store_h(const Params& p, const Ctrl& c, int row, int col, float a,
                                         float b, float w1, float w3, int lane) {
@@ -539,8 +550,12 @@ __device__ __forceinline__ void store_h(const Params& p, const Ctrl& c, int row,
       a *= s * w1;
       b *= s * w3;
     }
-    const __nv_bfloat16 hv = __float2bfloat16_rn(a / (1.f + expf(-a)) * b);
-    p.H[static_cast<size_t>(row) * p.f + col] = *reinterpret_cast<const uint16_t*>(&hv);
+    const float v = a / (1.f + expf(-a)) * b;
+    const __nv_bfloat16 hv = __float2bfloat16_rn(v);
+    const uint16_t hi = *reinterpret_cast<const uint16_t*>(&hv);
+    uint16_t* at = p.H + static_cast<size_t>(row) * p.f + col;
+    *at = hi;
+    if (!F8) at[static_cast<size_t>(p.T) * p.k * p.f] = static_cast<uint16_t>(low_parts(v, 0.f, hi));
     m = fabsf(__bfloat162float(hv));
   }
   if (F8) {
@@ -561,14 +576,17 @@ __device__ __forceinline__ void store_h4(const Params& p, const Ctrl& c, int row
       a = make_float4(a.x * (s * w1.x), a.y * (s * w1.y), a.z * (s * w1.z), a.w * (s * w1.w));
       b = make_float4(b.x * (s * w3.x), b.y * (s * w3.y), b.z * (s * w3.z), b.w * (s * w3.w));
     }
-    const __nv_bfloat162 lo =
-        __floats2bfloat162_rn(a.x / (1.f + expf(-a.x)) * b.x, a.y / (1.f + expf(-a.y)) * b.y);
-    const __nv_bfloat162 hi =
-        __floats2bfloat162_rn(a.z / (1.f + expf(-a.z)) * b.z, a.w / (1.f + expf(-a.w)) * b.w);
+    const float4 v = make_float4(a.x / (1.f + expf(-a.x)) * b.x, a.y / (1.f + expf(-a.y)) * b.y,
+                                 a.z / (1.f + expf(-a.z)) * b.z, a.w / (1.f + expf(-a.w)) * b.w);
+    const __nv_bfloat162 xy = __floats2bfloat162_rn(v.x, v.y), zw = __floats2bfloat162_rn(v.z, v.w);
     uint2 out;
-    out.x = *reinterpret_cast<const uint32_t*>(&lo);
-    out.y = *reinterpret_cast<const uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(p.H + static_cast<size_t>(row) * p.f + col) = out;
+    out.x = *reinterpret_cast<const uint32_t*>(&xy);
+    out.y = *reinterpret_cast<const uint32_t*>(&zw);
+    uint16_t* at = p.H + static_cast<size_t>(row) * p.f + col;
+    *reinterpret_cast<uint2*>(at) = out;
+    if (!F8)
+      *reinterpret_cast<uint2*>(at + static_cast<size_t>(p.T) * p.k * p.f) =
+          make_uint2(low_parts(v.x, v.y, out.x), low_parts(v.z, v.w, out.y));
     m = fmaxf(fmaxf(fabsf(bf16_lo(out.x)), fabsf(bf16_hi(out.x))),
               fmaxf(fabsf(bf16_lo(out.y)), fabsf(bf16_hi(out.y))));
   }
@@ -709,9 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const int bbytes = p.n1 * 128;
-  const int stage_bytes = kWBytes + bbytes;
-  Ctrl& c = *reinterpret_cast<Ctrl*>(smem + p.stages * stage_bytes);
+  constexpr int kParts = F8 ? 1 : 2;  // FC2's operands of tokens (see store_h)
+  Ctrl& c = *reinterpret_cast<Ctrl*>(smem + p.ring_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned G = gridDim.x;
   unsigned* words = reinterpret_cast<unsigned*>(p.status);
@@ -767,7 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned ks2 = p.f / KB, nt2 = (p.h + 255) / 256;
     const Cut cut1(c.nact * nt1 * ks1, G, ks1), cut2(c.nact * nt2 * ks2, G, ks2);
     const unsigned cta = blockIdx.x;
+    // A stage holds FC1's n1 rows of x, or all parts of the busiest expert's rows of
+    // H: 128 tokens over 8 experts have 4 stages so, where room for both parts of
+    // 128 rows would leave 3 (456 and 465 us).
     const uint32_t ring = smem_u32(smem);
+    const int stage_bytes = kWBytes + max(p.n1, kParts * ((c.most + 15) / 16 * 16)) * 128;
+    const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
 
     if (warp == 0) {
       // ---------------------------------------------------- TMA producer
@@ -785,10 +807,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             return;
           }
           mbar_expect_tx(smem_u32(&c.full[s]), bytes);
-          if (filled < p.stages) ++filled;
+          if (filled < stages) ++filled;
         };
         auto next = [&] {
-          if (++s == p.stages) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1;
           }
@@ -833,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned q = cut1.start(piece);
           seek(q, ks1, nt1);
           for (; ok && q < q1; ++q) {
-            claim(kWBytes + bbytes);
+            claim(kWBytes + p.n1 * 128);
             if (!ok) break;
             const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&c.full[s]);
             const int e = c.act[ai], k0 = ks * KB;
@@ -855,10 +877,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int hs = s;
         auto load_h = [&] {
           const int e = c.act[hai], r0 = c.off[e], n = c.off[e + 1] - r0;
+          const int low = (n + 15) / 16 * 16 * 128;  // the low parts follow
           const uint32_t dst = ring + hs * stage_bytes + kWBytes, bar = smem_u32(&c.full[hs]);
-          for (int r = 0; r < n; r += 16)
+          for (int r = 0; r < n; r += 16) {
             tma_load_2d(dst + r * 128, &maps.h, hks * KB, r0 + r, bar);
-          if (++hs == p.stages) hs = 0;
+            if (!F8) tma_load_2d(dst + low + r * 128, &maps.h, hks * KB, p.T * p.k + r0 + r, bar);
+          }
+          if (++hs == stages) hs = 0;
           if (++hks < ks2) return;
           hks = 0;
           if (++htile < nt2) return;
@@ -871,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; ok && piece >= 0; piece = more(cut2, p.claim + 1)) {
           publish(piece);
           const unsigned q0 = cut2.start(piece), q1 = cut2.end(piece);
-          const unsigned ahead = min(q1 - q0, static_cast<unsigned>(p.stages));
+          const unsigned ahead = min(q1 - q0, static_cast<unsigned>(stages));
           seek(q0, ks2, nt2);
           hks = ks;
           hai = ai;
@@ -879,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (unsigned q = q0; ok && q < q1; ++q) {
             const int e = c.act[ai];
             const int rows16 = (c.off[e + 1] - c.off[e] + 15) / 16 * 16;
-            claim(kWBytes + rows16 * 128);
+            claim(kWBytes + kParts * rows16 * 128);
             if (!ok) break;
             const uint32_t dst = ring + s * stage_bytes, bar = smem_u32(&c.full[s]);
             if (F8)
@@ -906,8 +931,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) {
           for (; waiting > 0; --waiting) load_h();
           for (int i = 0; i < filled; ++i) {
-            s = s == 0 ? p.stages - 1 : s - 1;
-            if (s == p.stages - 1) ph ^= 1;
+            s = s == 0 ? stages - 1 : s - 1;
+            if (s == stages - 1) ph ^= 1;
             mbar_wait(smem_u32(&c.full[s]), ph, p.status, kTimeoutCode);
           }
         }
@@ -976,13 +1001,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_e4m3(acc + m * 128, am, bd + kk * 2, idesc, kk ? 1u : add);
                   else
                     umma_bf16(acc + m * 128, am, bd + kk * 2, idesc, kk ? 1u : add);
+                  if (!F8 && !fc1)
+                    umma_bf16(acc + m * 128, am, bd + n * 8 + kk * 2, idesc, 1u);
                 }
               }
               umma_commit(smem_u32(&c.empty[s]));
               if (q + 1 == end) umma_commit(smem_u32(&c.tfull[buf]));
             }
             add = 1;
-            if (++s == p.stages) {
+            if (++s == stages) {
               s = 0;
               ph ^= 1;
             }
@@ -1230,7 +1257,7 @@ struct Layout {
 };
 
 struct Plan {
-  int n1, stages, smem;
+  int n1, ring, smem;
   int tok_group, groups, slices, slice_h;
   size_t pieces;
 };
@@ -1250,10 +1277,10 @@ long long most_steps(const moe_dims& d, bool fp8) {
 Plan plan_of(const moe_dims& d, int blocks, bool fp8) {
   Plan p = {};
   p.n1 = (d.T + 15) / 16 * 16;
-  const int stage = kWBytes + p.n1 * 128;
-  p.stages = (kSmemMax - 1024 - static_cast<int>(sizeof(Ctrl))) / stage;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.smem = 1024 + p.stages * stage + static_cast<int>(sizeof(Ctrl));
+  p.ring = (kSmemMax - 1024 - static_cast<int>(sizeof(Ctrl))) / 1024 * 1024;
+  const int most_ring = kMaxStages * (kWBytes + (fp8 ? 1 : 2) * p.n1 * 128);
+  if (p.ring > most_ring) p.ring = most_ring;
+  p.smem = 1024 + p.ring + static_cast<int>(sizeof(Ctrl));
   p.tok_group = (d.T + 15) / 16;
   p.groups = (d.T + p.tok_group - 1) / p.tok_group;
   int n = blocks / p.groups;
@@ -1261,7 +1288,7 @@ Plan plan_of(const moe_dims& d, int blocks, bool fp8) {
   p.slice_h = ((d.h + n - 1) / n + 7) / 8 * 8;
   if (p.slice_h < 32) p.slice_h = 32;  // a few long slices add up sooner than many short ones
   // a slice of Wg and x, the threads' sums and the logits fit the ring
-  const int room = p.stages * stage - (kThreads + kMaxE) * kGroupTok * 4;
+  const int room = p.ring - (kThreads + kMaxE) * kGroupTok * 4;
   const int most = room / (d.E * 4 + kGroupTok * 2) / 8 * 8;
   if (p.slice_h > most) p.slice_h = most;
   p.slices = (d.h + p.slice_h - 1) / p.slice_h;
@@ -1284,7 +1311,7 @@ Layout layout(const moe_dims& d, bool fp8) {
   L.logits = take(static_cast<size_t>(plan.groups) * plan.slices * plan.tok_group * d.E * 4);
   L.idx = take(R * 4);
   L.gates = take(R * 4);
-  L.H = take(R * f * 2);
+  L.H = take(R * f * (fp8 ? 2 : 4));
   L.O = take(R * h * 4);
   L.part = take(2 * plan.pieces * 2 * T * 128 * 4);
   L.claim = take(8);
@@ -1353,7 +1380,7 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
   p.k = d.k;
   p.capacity = d.capacity > 0 ? d.capacity : INT_MAX;
   p.n1 = plan.n1;
-  p.stages = plan.stages;
+  p.ring_bytes = plan.ring;
   p.tok_group = plan.tok_group;
   p.groups = plan.groups;
   p.slices = plan.slices;
@@ -1394,7 +1421,7 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
     e = launch<true>(p, m, plan.smem, blocks, stream);
   } else {
     if (!make_map_kmajor(&m.x, x, h, d.T, plan.n1, false) || !make_map_columns(&m.w1, W1, f, E * h, 2) ||
-        !make_map_columns(&m.w3, W3, f, E * h, 2) || !make_map_kmajor(&m.h, p.H, f, R, 16, false) ||
+        !make_map_columns(&m.w3, W3, f, E * h, 2) || !make_map_kmajor(&m.h, p.H, f, 2 * R, 16, false) ||
         !make_map_columns(&m.w2, W2, h, E * f, 4))
       return MOE_ERR_CUDA;
     e = launch<false>(p, m, plan.smem, blocks, stream);
