@@ -396,18 +396,29 @@ moe_status moe_layer_decode(const moe_dims* dims, const moe_bf16* x,
                             size_t ws_bytes, moe_stream_t stream);
 
 /* moe_layer_decode on e4m3 weights: `qw` as moe_quantize_weights_fp8 writes it
- * (256-byte aligned).  The arithmetic of moe_layer_fwd_fp8: x quantised with
- * one scale for each token, H (from its bf16 value) with one for each row, the
- * products of codes summed in fp32 and multiplied by the two scales.  The
- * activations' scales are amax times the fp32 reciprocal of 448 (the layer
- * divides: an ulp apart at most, which shows where a value lies exactly
- * between two codes).  h and f multiples of 128 (MOE_ERR_UNSUPPORTED otherwise).
+ * (256-byte aligned).  x is quantised with one scale for each token, H (from
+ * its bf16 value) with one for each row; the products of codes are summed in
+ * fp32 and multiplied by the two scales.  The activations' scales are amax times
+ * the fp32 reciprocal of 448, where moe_layer_fwd_fp8 divides.  The two are an
+ * ulp apart, but a bf16 row holds values exactly between two codes, which
+ * that ulp decides: y is up to 0.011 apart (relative L2, layers of a few hundred
+ * rows and columns).  h and f multiples of 128 (MOE_ERR_UNSUPPORTED otherwise).
  * Workspace: moe_workspace_bytes(dims, MOE_OP_LAYER_DECODE_FP8). */
 moe_status moe_layer_decode_fp8(const moe_dims* dims, const moe_bf16* x,
                                 const float* Wg, const float* b,
                                 const void* qw, moe_bf16* y,
                                 int32_t* topk_idx, float* gates, void* ws,
                                 size_t ws_bytes, moe_stream_t stream);
+
+/* The same with the scales of moe_layer_fwd_fp8 (amax / 448, a float32
+ * division), for a server whose prompts go through that call: x and H get its
+ * codes, and what is left between the two is that it rounds O to bf16. */
+moe_status moe_layer_decode_fp8_as_fwd(const moe_dims* dims, const moe_bf16* x,
+                                       const float* Wg, const float* b,
+                                       const void* qw, moe_bf16* y,
+                                       int32_t* topk_idx, float* gates,
+                                       void* ws, size_t ws_bytes,
+                                       moe_stream_t stream);
 
 /* ------------------------------------------------- norms around the block
  * What joins the layer to its residual stream r [T,h] (bf16, or fp32 with

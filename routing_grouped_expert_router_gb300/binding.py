@@ -115,6 +115,7 @@ _SIGS = {
     "moe_layer_bwd_fp8": (_I, [_D] + [_P] * 11 + [_P, _SZ, _P]),
     "moe_layer_decode": (_I, [_D] + [_P] * 10 + [_SZ, _P]),
     "moe_layer_decode_fp8": (_I, [_D] + [_P] * 8 + [_SZ, _P]),
+    "moe_layer_decode_fp8_as_fwd": (_I, [_D] + [_P] * 8 + [_SZ, _P]),
     "moe_norm_workspace_bytes": (_SZ, [_ND]),
     "moe_block_norm_fwd": (_I, [_ND] + [_P] * 8),
     "moe_block_norm_bwd": (_I, [_ND] + [_P] * 13 + [_SZ, _P]),
@@ -391,6 +392,13 @@ def moe_layer_decode_fp8(d, x, Wg, b, qw, y, topk_idx, gates, ws, ws_bytes=None,
     _check(load().moe_layer_decode_fp8(ctypes.byref(d), _addr(x), _addr(Wg), _addr(b), _addr(qw),
                                        _addr(y), _addr(topk_idx), _addr(gates), _addr(ws),
                                        ws_bytes, _stream(stream)), "moe_layer_decode_fp8")
+
+
+def moe_layer_decode_fp8_as_fwd(d, x, Wg, b, qw, y, topk_idx, gates, ws, ws_bytes=None, stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check(load().moe_layer_decode_fp8_as_fwd(ctypes.byref(d), _addr(x), _addr(Wg), _addr(b), _addr(qw),
+                                              _addr(y), _addr(topk_idx), _addr(gates), _addr(ws),
+                                              ws_bytes, _stream(stream)), "moe_layer_decode_fp8_as_fwd")
 
 
 def moe_norm_workspace_bytes(nd: moe_norm_dims) -> int:

@@ -1,5 +1,5 @@
 // decode.cu -- the whole MoE layer for a few tokens in one kernel:
-// moe_layer_decode and moe_layer_decode_fp8.
+// moe_layer_decode, moe_layer_decode_fp8 and moe_layer_decode_fp8_as_fwd.
 //
 //   l = x Wg (+ b);  the k largest;  gates = softmax over them
 //   H[p] = silu(x W1[e]) * (x W3[e])     for each placed assignment p = (t, e)
@@ -249,11 +249,14 @@ __device__ __forceinline__ void tmem_wait8(uint32_t (&a)[8], uint32_t (&b)[8]) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// The scale and codes of a quantised row.  The scale is amax times the fp32
-// reciprocal of 448, within an ulp of fp8.cu's quotient; where a value lies
-// exactly between two codes, that ulp can choose the other one.
+// The scale and codes of a quantised row.  moe_layer_decode_fp8's scale is amax
+// times the fp32 reciprocal of 448, moe_layer_decode_fp8_as_fwd's is fp8.cu's
+// quotient.  They are an ulp apart, but 0.8 to 6% of a bf16 row's values lie
+// exactly between two codes, and that ulp chooses.
+template <bool QUOT>
 __device__ __forceinline__ float scale_of(float amax) {
-  return amax > 0.f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
+  if (!(amax > 0.f)) return 1.0f;
+  return QUOT ? __fdiv_rn(amax, 448.0f) : __fmul_rn(amax, 1.0f / 448.0f);
 }
 __device__ __forceinline__ uint32_t quant2(uint32_t w, float s) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
@@ -418,6 +421,7 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
 
 // x rows to e4m3, a block for each row, from the last block on: with few tokens
 // the router has no unit for it, and it must not hold up the router's.
+template <bool QUOT>
 __device__ void quant_x(const Params& p, float* red) {
   const int tid = threadIdx.x, n8 = p.h / 8;
   for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) {
@@ -430,7 +434,7 @@ __device__ void quant_x(const Params& p, float* red) {
     if ((tid & 31) == 0) red[tid >> 5] = m;
     __syncthreads();
     for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, red[w]);
-    const float s = scale_of(m);
+    const float s = scale_of<QUOT>(m);
     if (tid == 0) p.sx[t] = s;
     uint2* out = reinterpret_cast<uint2*>(p.xq + static_cast<size_t>(t) * p.h);
     for (int c = tid; c < n8; c += kThreads) out[c] = quant8(row[c], s);
@@ -721,7 +725,9 @@ __device__ __forceinline__ void join_rows(const Params& p, const Ctrl& c, const 
   if (odd) store_h4<F8>(p, c, row + 1, col, ua, ub, w1, w3, lane);
 }
 
-template <bool F8>
+// QUOT: the e4m3 scales of moe_layer_decode_fp8_as_fwd.  A variant of its own: with a
+// choice at run time one token took 78.5 us in place of 78.0, 24 tokens 106.4 for 105.5.
+template <bool F8, bool QUOT>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t smem_raw[];
@@ -768,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (F8)
     for (int i = blockIdx.x * kThreads + tid; i < p.T * p.k; i += G * kThreads) p.amax[i] = 0;
   route(p, c, smem);
-  if (F8) quant_x(p, reinterpret_cast<float*>(smem));
+  if (F8) quant_x<QUOT>(p, reinterpret_cast<float*>(smem));
   fence_proxy_async_all();  // xq for TMA; and the ring's memory, used by route above
   __syncthreads();
   if (tid == 0 && !grid_barrier(words + kBarWord, G, p.status)) c.abort = 1;
@@ -1163,7 +1169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n8 = p.f / 8, all = c.off[kMaxE] * n8;
         for (int i = cta * kHelpers + tid - 64; i < all; i += G * kHelpers) {
           const int row = i / n8;
-          const float s = scale_of(__uint_as_float(__ldcg(p.amax + row)));
+          const float s = scale_of<QUOT>(__uint_as_float(__ldcg(p.amax + row)));
           const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p.H) + i);
           reinterpret_cast<uint2*>(p.Hq)[i] = quant8(w, s);
         }
@@ -1203,7 +1209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               if (i0 + i >= n || col >= p.h) break;
-              if (F8) v[i] *= scale_of(__uint_as_float(__ldcg(p.amax + row0 + i0 + i))) * w2;
+              if (F8) v[i] *= scale_of<QUOT>(__uint_as_float(__ldcg(p.amax + row0 + i0 + i))) * w2;
               __stcg(dst + (i0 + i) * ld, v[i]);
             }
           }
@@ -1338,9 +1344,9 @@ bool supported(const moe_dims& d, bool fp8) {
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool ptr_ok(const void* p) { return p && aligned(p, 16); }
 
-template <bool F8>
+template <bool F8, bool QUOT>
 cudaError_t launch(const Params& p, const Maps& m, int smem, int blocks, cudaStream_t s) {
-  const void* kern = reinterpret_cast<const void*>(decode_kernel<F8>);
+  const void* kern = reinterpret_cast<const void*>(decode_kernel<F8, QUOT>);
   const cudaError_t e = set_smem_once(kern, kSmemMax);
   if (e != cudaSuccess) return e;
   void* args[2] = {const_cast<Params*>(&p), const_cast<Maps*>(&m)};
@@ -1354,7 +1360,7 @@ cudaError_t launch(const Params& p, const Maps& m, int smem, int blocks, cudaStr
 moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, const float* b,
                   const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2, const void* qw,
                   moe_bf16* y, int32_t* topk_idx, float* gates, void* ws, size_t ws_bytes,
-                  cudaStream_t stream, bool fp8) {
+                  cudaStream_t stream, bool fp8, bool quotient) {
   const moe_status st = moe_api::check_dims(dims, true);
   if (st != MOE_OK) return st;
   const moe_dims& d = *dims;
@@ -1418,13 +1424,14 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
         !make_map_codes(&m.w2, view("W2q"), f, h, E, 256))
       return MOE_ERR_CUDA;
     m.w3 = m.w1;
-    e = launch<true>(p, m, plan.smem, blocks, stream);
+    e = quotient ? launch<true, true>(p, m, plan.smem, blocks, stream)
+                 : launch<true, false>(p, m, plan.smem, blocks, stream);
   } else {
     if (!make_map_kmajor(&m.x, x, h, d.T, plan.n1, false) || !make_map_columns(&m.w1, W1, f, E * h, 2) ||
         !make_map_columns(&m.w3, W3, f, E * h, 2) || !make_map_kmajor(&m.h, p.H, f, 2 * R, 16, false) ||
         !make_map_columns(&m.w2, W2, h, E * f, 4))
       return MOE_ERR_CUDA;
-    e = launch<false>(p, m, plan.smem, blocks, stream);
+    e = launch<false, false>(p, m, plan.smem, blocks, stream);
   }
   if (e != cudaSuccess || !moe_api::note(stream, "layer_decode")) return MOE_ERR_CUDA;
   return MOE_OK;
@@ -1445,14 +1452,22 @@ moe_status moe_layer_decode(const moe_dims* dims, const moe_bf16* x, const float
                             const moe_bf16* W2, moe_bf16* y, int32_t* topk_idx, float* gates,
                             void* ws, size_t ws_bytes, moe_stream_t stream) {
   return moe::decode(dims, x, Wg, b, W1, W3, W2, nullptr, y, topk_idx, gates, ws, ws_bytes,
-                     reinterpret_cast<cudaStream_t>(stream), false);
+                     reinterpret_cast<cudaStream_t>(stream), false, false);
 }
 
 moe_status moe_layer_decode_fp8(const moe_dims* dims, const moe_bf16* x, const float* Wg,
                                 const float* b, const void* qw, moe_bf16* y, int32_t* topk_idx,
                                 float* gates, void* ws, size_t ws_bytes, moe_stream_t stream) {
   return moe::decode(dims, x, Wg, b, nullptr, nullptr, nullptr, qw, y, topk_idx, gates, ws,
-                     ws_bytes, reinterpret_cast<cudaStream_t>(stream), true);
+                     ws_bytes, reinterpret_cast<cudaStream_t>(stream), true, false);
+}
+
+moe_status moe_layer_decode_fp8_as_fwd(const moe_dims* dims, const moe_bf16* x, const float* Wg,
+                                       const float* b, const void* qw, moe_bf16* y,
+                                       int32_t* topk_idx, float* gates, void* ws, size_t ws_bytes,
+                                       moe_stream_t stream) {
+  return moe::decode(dims, x, Wg, b, nullptr, nullptr, nullptr, qw, y, topk_idx, gates, ws,
+                     ws_bytes, reinterpret_cast<cudaStream_t>(stream), true, true);
 }
 
 }  // extern "C"
