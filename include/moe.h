@@ -387,7 +387,13 @@ moe_status moe_layer_bwd_fp8(const moe_dims* dims, const moe_bf16* x,
  * as moe_layer_fwd does.  Results do not depend on how blocks are scheduled:
  * the same inputs give the same bits.
  * MOE_ERR_UNSUPPORTED: T > 128, or dims.sar = 1 (there is no context).
- * Workspace: moe_workspace_bytes(dims, MOE_OP_LAYER_DECODE). */
+ * Workspace: moe_workspace_bytes(dims, MOE_OP_LAYER_DECODE).  The blocks meet
+ * at counters in its first 256 bytes: all of these have to be zero before the
+ * first call (every call leaves them so, but for the status word), and calls
+ * that may run at the same time need a workspace each.  Where that was not
+ * so, results are undefined, within bounds: an expert id or row that cannot be
+ * is recorded as MOE_ERR_DEVICE_INDEX, a meeting that fails as
+ * MOE_ERR_DEVICE_TIMEOUT. */
 moe_status moe_layer_decode(const moe_dims* dims, const moe_bf16* x,
                             const float* Wg, const float* b,
                             const moe_bf16* W1, const moe_bf16* W3,

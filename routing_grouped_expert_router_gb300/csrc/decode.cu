@@ -39,7 +39,6 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
-#include <climits>
 #include <cstdint>
 #include <cstring>
 
@@ -443,7 +442,10 @@ __device__ void quant_x(const Params& p, float* red) {
 
 // --------------------------------------------------------------- dispatch
 // Every block builds the same lists from the chosen experts: the rows of each
-// expert in ascending assignment order, at most `capacity` of them.
+// expert in ascending assignment order, at most `capacity` of them (and T: no
+// token chooses an expert twice).  The ids come from memory: where the
+// workspace's header was not zero they may be what an earlier call left there,
+// so one out of range is recorded and not placed, and so is a row past T.
 __device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int R = p.T * p.k, chunks = (R + 31) / 32;
@@ -456,6 +458,9 @@ __device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
     mine[n] = a < R ? __ldcg(p.idx + a) : -1;
     gate[n] = a < R ? __ldcg(p.gates + a) : 0.f;
   }
+#pragma unroll
+  for (int n = 0; n < kMine; ++n)
+    if (static_cast<unsigned>(mine[n]) >= static_cast<unsigned>(p.E)) mine[n] = -1;
   if (f8 && tid < p.T) sx = __ldcg(p.sx + tid);
   for (int i = tid; i < chunks * kMaxE; i += kThreads) c.hist[i / kMaxE][i % kMaxE] = 0;
   if (f8 && tid < p.T) c.sx[tid] = sx;
@@ -464,7 +469,7 @@ __device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
   for (int n = 0; n < kMine; ++n) {
     const int ch = warp + n * (kThreads / 32), a = ch * 32 + lane, e = mine[n];
     if (ch >= chunks) break;
-    if (a < R) {
+    if (e >= 0) {
       c.gate[a] = gate[n];
       c.exp[a] = static_cast<uint8_t>(e);
     }
@@ -517,10 +522,11 @@ __device__ void dispatch(const Params& p, Ctrl& c, bool f8) {
   for (int n = 0; n < kMine; ++n) {
     const int ch = warp + n * (kThreads / 32), a = ch * 32 + lane, e = mine[n];
     if (a >= R) break;
-    const int r = c.hist[ch][e] + rank[n];
+    const int r = e < 0 ? p.T : c.hist[ch][e] + rank[n];
+    if (r >= p.T) report_bad_index(p.status);
     const bool placed = r < p.capacity;
-    const int row = c.off[e] + r;
-    c.pos[a] = static_cast<int16_t>(placed ? row : -1);
+    const int row = placed ? c.off[e] + r : -1;
+    c.pos[a] = static_cast<int16_t>(row);
     if (placed) c.tok[row] = static_cast<uint8_t>(a / p.k);
   }
   __syncthreads();
@@ -531,11 +537,6 @@ __device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// H of a row's column from its two sums.  With bf16 weights it enters FC2 as two
-// bf16 operands, its rounded value and what that leaves: 16 bits, where one
-// bf16 made y's error 1.4 times that of y's own rounding (0.0024 against
-// 0.0017).  They are more columns of an idle tensor pipe and no more weights.
-// With e4m3 weights H's bf16 value is what its codes are made from.
 // The low parts of two values with the high parts hi (0 where those are not finite).
 __device__ __forceinline__ uint32_t low_parts(float a, float b, uint32_t hi) {
   const float ha = bf16_lo(hi), hb = bf16_hi(hi);
@@ -544,6 +545,11 @@ __device__ __forceinline__ uint32_t low_parts(float a, float b, uint32_t hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// H of a row's column from its two sums.  With bf16 weights it enters FC2 as two
+// bf16 operands, its rounded value and what that leaves: 16 bits, where one
+// bf16 made y's error 1.4 times that of y's own rounding (0.0024 against
+// 0.0017).  They are more columns of an idle tensor pipe and no more weights.
+// With e4m3 weights H's bf16 value is what its codes are made from.
 template <bool F8>
 __device__ __forceinline__ void store_h(const Params& p, const Ctrl& c, int row, int col, float a,
                                         float b, float w1, float w3, int lane) {
@@ -1384,7 +1390,7 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
   p.f = d.f;
   p.E = d.E;
   p.k = d.k;
-  p.capacity = d.capacity > 0 ? d.capacity : INT_MAX;
+  p.capacity = d.capacity > 0 && d.capacity < d.T ? d.capacity : d.T;
   p.n1 = plan.n1;
   p.ring_bytes = plan.ring;
   p.tok_group = plan.tok_group;

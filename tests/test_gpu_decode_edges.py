@@ -1,10 +1,11 @@
-"""The few-token layer where the cases of test_gpu_decode.py do not reach: its precision, element by element."""
+"""The few-token layer where the cases of test_gpu_decode.py do not reach: its precision, element by element, and headers that were
+not left zero."""
 import pytest
 import torch
 
 from routing_grouped_expert_router_gb300 import binding as mb
 from routing_grouped_expert_router_gb300 import build as mbuild
-from tests.test_gpu_decode import Run, inputs, layer64
+from tests.test_gpu_decode import Run, check, inputs, layer64
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,45 @@ def test_values_that_bf16_does_not_hold():
     run.call()
     assert run.ok()
     assert torch.isinf(run.y.float()).all() and (run.y > 0).all()
+
+
+GROUPS = slice(128, 192)    # the header's bytes that count each token group's router units
+
+
+@pytest.mark.parametrize("routing", [True, False])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_expert_ids_that_no_router_wrote(fp8, routing):
+    """A dirty header keeps every group from choosing its experts: the ids are what the buffer held.  Those out of range are
+    recorded and not placed, and the next call is right."""
+    cfg, inp = inputs(T=50, h=256, f=256, E=6, k=3, seed=96)
+    run = Run(cfg, inp, fp8=fp8)
+    run.ws[256:] = 0xFF
+    run.ws[GROUPS] = 0x40
+    stale = torch.tensor([6, -1, 2 ** 31 - 1, -2 ** 31, 1000, 64, 255, 256], dtype=torch.int32, device="cuda")
+    run.idx.copy_(stale.repeat(cfg.T * cfg.k // 8 + 1)[:cfg.T * cfg.k].view(cfg.T, cfg.k))
+    run.idx[7] = torch.tensor([2, 4, 6], dtype=torch.int32)
+    run.call(routing=routing)
+    torch.cuda.synchronize()
+    assert mb.moe_read_device_status(run.ws) == mb.MOE_ERR_DEVICE_INDEX
+    rest = [t for t in range(cfg.T) if t != 7 or not routing]
+    assert (run.y[rest] == 0).all()
+    run.call()
+    assert run.ok()
+    check(cfg, inp, run, fp8=fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_expert_for_every_slot(fp8):
+    """The same with ids in range, all of one expert: T * k rows for it, of which T are placed."""
+    cfg, inp = inputs(T=128, h=128, f=256, E=8, k=8, seed=97)
+    run = Run(cfg, inp, fp8=fp8)
+    run.ws[GROUPS] = 0x40
+    run.idx.fill_(5)
+    run.gates.fill_(0.25)
+    run.call()
+    torch.cuda.synchronize()
+    assert mb.moe_read_device_status(run.ws) == mb.MOE_ERR_DEVICE_INDEX
+    assert torch.isfinite(run.y.float()).all()
+    run.call()
+    assert run.ok()
+    check(cfg, inp, run, fp8=fp8)
