@@ -326,7 +326,8 @@ __device__ __forceinline__ float add_up(const float* s, int n, int stride) {
 // order took 14 us for one token and 25 us for 32 where this takes 4 to 5.
 // The block that finishes a group's last slice adds the slices in a fixed order and
 // chooses the experts of its tokens, one warp for each.
-__device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
+// False, in the whole block, where a wait ran out.
+__device__ bool route(const Params& p, Ctrl& c, uint8_t* smem) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned* words = reinterpret_cast<unsigned*>(p.status);
   const int parts = kThreads / p.E;
@@ -351,10 +352,9 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
         bulk_load(smem_u32(xs) + t * nj * 2, p.x + static_cast<size_t>(t0 + t) * p.h + j0, nj * 2,
                   bar);
     }
-    if (!mbar_wait(bar, ph, p.status, kTimeoutCode)) c.abort = 1;
-    ph ^= 1;
+    const bool got = mbar_wait(bar, ph, p.status, kTimeoutCode);
     float acc[kGroupTok] = {};
-    if (part < parts)
+    if (got && part < parts)
       for (int j = part * 8; j < nj; j += parts * 8) {
         float w[8];
 #pragma unroll
@@ -376,7 +376,11 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
 #pragma unroll
     for (int t = 0; t < kGroupTok; ++t)
       if (t < nt) red[t * kThreads + tid] = acc[t];
-    __syncthreads();
+    if (!__syncthreads_and(got)) {  // the loads must land before the block ends
+      if (tid == 0) mbar_wait(bar, ph, p.status, kTimeoutCode);
+      return false;
+    }
+    ph ^= 1;
     // [group][slice][token][expert]
     const int pairs = p.tok_group * p.E;  // 512 at most
     float* mine = p.logits + static_cast<size_t>(unit) * pairs;
@@ -416,6 +420,7 @@ __device__ void route(const Params& p, Ctrl& c, uint8_t* smem) {
       select_topk(p, t0 + warp, lane < p.E ? logit[warp * kMaxE + lane] : 0.f,
                   lane + 32 < p.E ? logit[warp * kMaxE + lane + 32] : 0.f, lane);
   }
+  return true;
 }
 
 // x rows to e4m3, a block for each row, from the last block on: with few tokens
@@ -779,11 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ------------------------------------------------------------- route
   if (F8)
     for (int i = blockIdx.x * kThreads + tid; i < p.T * p.k; i += G * kThreads) p.amax[i] = 0;
-  route(p, c, smem);
-  if (F8) quant_x<QUOT>(p, reinterpret_cast<float*>(smem));
+  const bool routed = route(p, c, smem);
+  if (F8 && routed) quant_x<QUOT>(p, reinterpret_cast<float*>(smem));
   fence_proxy_async_all();  // xq for TMA; and the ring's memory, used by route above
   __syncthreads();
-  if (tid == 0 && !grid_barrier(words + kBarWord, G, p.status)) c.abort = 1;
+  // (a block that gave up does not arrive: the others give up here too)
+  if (tid == 0 && !(routed && grid_barrier(words + kBarWord, G, p.status))) c.abort = 1;
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem_base;

@@ -88,3 +88,20 @@ def test_one_expert_for_every_slot(fp8):
     run.call()
     assert run.ok()
     check(cfg, inp, run, fp8=fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_wait_that_runs_out(fp8):
+    """A barrier's counter that starts far below zero never gets to its target: every block gives up after its limit of 4
+    seconds, the status says so, and the workspace serves the next call."""
+    cfg, inp = inputs(T=6, h=128, f=128, E=4, k=2, seed=98)
+    run = Run(cfg, inp, fp8=fp8)
+    run.ws[67] = 0xC0    # the top byte of the arrivals' 32-bit counter
+    run.call()
+    torch.cuda.synchronize()
+    assert mb.moe_read_device_status(run.ws) == mb.MOE_ERR_DEVICE_TIMEOUT
+    assert (run.y == 7).all()
+    assert not run.ws[:256].any()
+    run.call()
+    assert run.ok()
+    check(cfg, inp, run, fp8=fp8)
