@@ -236,10 +236,11 @@ __device__ __forceinline__ bool ring_wait(const Args& a, uint64_t* full, int n) 
   return moe::mbar_wait(moe::smem_u32(&full[n % a.slots]), (n / a.slots) & 1, a.status,
                         MOE_ERR_DEVICE_TIMEOUT);
 }
-// After a wait ran out: the rows asked for land before the block ends.
+// After a wait for row n ran out: the rows asked for land before the block ends,
+// that one among them.
 __device__ __forceinline__ void ring_drain(const Args& a, uint64_t* full, int n) {
   if (threadIdx.x == 0)
-    for (int i = 1; i < a.slots; ++i)
+    for (int i = 0; i < a.slots; ++i)
       if (blockIdx.x + static_cast<long long>(n + i) * gridDim.x < a.T) ring_wait(a, full, n + i);
 }
 
