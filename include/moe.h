@@ -452,7 +452,9 @@ typedef struct {
   float beta;       /* scale of the block's output */
 } moe_norm_dims;
 
-/* Scratch bytes of moe_block_norm_bwd (0 on invalid dims). */
+/* Scratch bytes of moe_block_norm_bwd (0 on invalid dims).  They grow with T: a
+ * workspace for the most rows serves every smaller call of the same h and
+ * res_f32. */
 size_t moe_norm_workspace_bytes(const moe_norm_dims* dims);
 
 /* The forward above in one pass over r and y.

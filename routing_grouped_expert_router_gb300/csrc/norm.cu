@@ -663,6 +663,7 @@ int threads_for(int h, int pieces) {
 // shared memory.
 struct Plan {
   int threads, blocks, pieces, rows, slots, slot_bytes, smem;  // rows: side by side in a block
+  int most_blocks;  // of any call with at most as many rows: grows with T
   bool keep;
 };
 Plan plan_of(const moe_norm_dims& d, bool bwd) {
@@ -724,7 +725,7 @@ Plan plan_of(const moe_norm_dims& d, bool bwd) {
   if (bwd && p.rows == 1 && p.pieces < 4) p.slots = 2;
   p.smem = p.slots * p.slot_bytes;
   const int n = moe_api::num_sms() * per_sm;
-  p.blocks = d.T < n ? d.T : n;
+  p.most_blocks = p.blocks = d.T < n ? d.T : n;
   // no more blocks than the same number of rounds needs: each leaves its sums
   if (bwd && d.T > 0) {
     const int rounds = (d.T - 1) / (n * p.rows) + 1;
@@ -823,7 +824,8 @@ extern "C" {
 
 size_t moe_norm_workspace_bytes(const moe_norm_dims* dims) {
   if (check(dims) != MOE_OK) return 0;
-  const size_t n = static_cast<size_t>(plan_of(*dims, true).blocks) * 2 * dims->h * sizeof(float);
+  const size_t n =
+      static_cast<size_t>(plan_of(*dims, true).most_blocks) * 2 * dims->h * sizeof(float);
   return kAlign + (n + kAlign - 1) / kAlign * kAlign;
 }
 
