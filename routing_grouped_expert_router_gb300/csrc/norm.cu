@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(R * N > 3 && N > 2 ? kWideThreads
     for (int r = 0; r < R; ++r) {
       if (R > 1 && !live[r]) break;
       const size_t row = static_cast<size_t>(t[r]) * a.h;
-      const f2 k2 = both(post ? -s1[r] * a.inv_h * rys[r] : 0.f), gy = both(gt[r] * rys[r]);
+      const f2 k2 = both(-s1[r] * a.inv_h * rys[r]), gy = both(gt[r] * rys[r]);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -588,7 +588,8 @@ __global__ void __launch_bounds__(R * N > 3 && N > 2 ? kWideThreads
         f2 v[4];
         unpack8(y[r][i], v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = mul2(gy, fma2(k2, v[j], G[r][i][j]));
+        for (int j = 0; j < 4; ++j)  // (without a norm dy does not depend on y, finite or not)
+          v[j] = mul2(gy, post ? fma2(k2, v[j], G[r][i][j]) : G[r][i][j]);
         a.out_u[(row + c) >> 3] = pack8(v);
       }
       if (a.dgate && threadIdx.x == 0) a.dgate[t[r]] = s1[r];
