@@ -378,9 +378,10 @@ moe_status moe_layer_bwd_fp8(const moe_dims* dims, const moe_bf16* x,
  *   gates = softmax over the chosen k;
  *   y[t] = sum_j gates[t,j] (silu(x W1[e_j]) * (x W3[e_j])) W2[e_j]
  * with fp32 sums throughout; H = silu(A) * B enters FC2 as the sum of two bf16
- * values (16 bits); A, B, the experts' outputs and the gated sum stay in fp32
- * until y is rounded.  Only the chosen experts' weights are read, each
- * once.  Nothing is kept for a backward pass.
+ * values (16 bits; a row that meets an infinite weight of W2 may get NaN for
+ * an infinity); A, B, the experts' outputs and the gated sum stay in fp32 until
+ * y is rounded.  Only the chosen experts' weights are read, each once.  Nothing
+ * is kept for a backward pass.
  *
  * In: as moe_layer_fwd.  Out: y [T,h] bf16 and, where the pointers are not
  * NULL, topk_idx [T,k] and gates [T,k].  dims.capacity > 0 drops assignments

@@ -554,33 +554,54 @@ __device__ __forceinline__ uint32_t low_parts(float a, float b, uint32_t hi) {
 // bf16 operands, its rounded value and what that leaves: 16 bits, where one
 // bf16 made y's error 1.4 times that of y's own rounding (0.0024 against
 // 0.0017).  They are more columns of an idle tensor pipe and no more weights.
-// With e4m3 weights H's bf16 value is what its codes are made from.
-template <bool F8>
+// n of eight rows side by side: one after another, with the second part's
+// stores, 128 skewed tokens over 64 experts of 512 x 8192 took 468 us, so 389.
+__device__ __forceinline__ void store_h8(const Params& p, int row, int n, int col,
+                                         const uint32_t (&a)[8], const uint32_t (&b)[8]) {
+  if (col >= p.f) return;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = __uint_as_float(a[i]);
+    v[i] = x / (1.f + expf(-x)) * __uint_as_float(b[i]);
+  }
+  uint16_t* at = p.H + static_cast<size_t>(row) * p.f + col;
+  uint16_t* low = at + static_cast<size_t>(p.T) * p.k * p.f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[i], v[i + 1]);
+    const uint32_t hi = *reinterpret_cast<const uint32_t*>(&h);
+    const uint32_t lo = low_parts(v[i], v[i + 1], hi);
+    if (i < n) {
+      at[i * p.f] = static_cast<uint16_t>(hi);
+      low[i * p.f] = static_cast<uint16_t>(lo);
+    }
+    if (i + 1 < n) {
+      at[(i + 1) * p.f] = static_cast<uint16_t>(hi >> 16);
+      low[(i + 1) * p.f] = static_cast<uint16_t>(lo >> 16);
+    }
+  }
+}
+
+// The same of one row with e4m3 weights: H's bf16 value is what its codes are
+// made from.
 __device__ __forceinline__ void store_h(const Params& p, const Ctrl& c, int row, int col, float a,
                                         float b, float w1, float w3, int lane) {
   float m = 0.f;
   if (col < p.f) {
-    if (F8) {
-      const float s = c.sx[c.tok[row]];
-      a *= s * w1;
-      b *= s * w3;
-    }
-    const float v = a / (1.f + expf(-a)) * b;
-    const __nv_bfloat16 hv = __float2bfloat16_rn(v);
-    const uint16_t hi = *reinterpret_cast<const uint16_t*>(&hv);
-    uint16_t* at = p.H + static_cast<size_t>(row) * p.f + col;
-    *at = hi;
-    if (!F8) at[static_cast<size_t>(p.T) * p.k * p.f] = static_cast<uint16_t>(low_parts(v, 0.f, hi));
+    const float s = c.sx[c.tok[row]];
+    a *= s * w1;
+    b *= s * w3;
+    const __nv_bfloat16 hv = __float2bfloat16_rn(a / (1.f + expf(-a)) * b);
+    p.H[static_cast<size_t>(row) * p.f + col] = *reinterpret_cast<const uint16_t*>(&hv);
     m = fabsf(__bfloat162float(hv));
   }
-  if (F8) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if (lane == 0) atomicMax(p.amax + row, __float_as_uint(m));
-  }
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  if (lane == 0) atomicMax(p.amax + row, __float_as_uint(m));
 }
 
-// The same of four columns (f is a multiple of 64: all in range or none).
+// H of a row's four columns (f is a multiple of 64: all in range or none).
 template <bool F8>
 __device__ __forceinline__ void store_h4(const Params& p, const Ctrl& c, int row, int col, float4 a,
                                          float4 b, float4 w1, float4 w3, int lane) {
@@ -1107,12 +1128,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld1(acc + 128 + t, rb[i]);
           }
           tmem_wait8(ra, rb);
+          if (!F8 && whole) {
+            store_h8(p, row0 + i0, n - i0, col, ra, rb);
+            continue;
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (i0 + i >= n) break;
             const float va = __uint_as_float(ra[i]), vb = __uint_as_float(rb[i]);
             if (whole) {
-              store_h<F8>(p, c, row0 + i0 + i, col, va, vb, w1, w3, lane);
+              store_h(p, c, row0 + i0 + i, col, va, vb, w1, w3, lane);
             } else {
               __stcg(mine + (i0 + i) * 256 + r, va);
               __stcg(mine + (i0 + i) * 256 + 128 + r, vb);
