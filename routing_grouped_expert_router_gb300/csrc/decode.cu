@@ -29,11 +29,15 @@
 //   * FC2's first stages of weights are loaded before the barriers that make H
 //     whole (bringing more of them into L2 meanwhile gained nothing).
 // Measured on GB300 (1.9 GHz): 128 tokens, top 2 of 8 experts of 4096 x 14336 in
-// 457 us, the weights at 6.2 TB/s over all and 6.6 in FC1 (a kernel of these
+// 456 us, the weights at 6.2 TB/s over all and 6.7 in FC1 (a kernel of these
 // loads and nothing else reads 7.1); 32 tokens, top 6 of 64 experts of 2048 x 1408
-// in 179 us (DRAM reads 1.08 GB, the weights hit; tensor pipe 6% busy); one token
-// of the same layer in 37 us, of which the weights need 15: the rest is the
+// in 179 us (DRAM reads 1.08 GB, the weights hit; tensor pipe 8% busy); one token
+// of the same layer in 38 us, of which the weights need 15: the rest is the
 // router (5), the first loads (3), four grid barriers (1 each), joins and combine.
+// Where an expert has many rows and its tiles few k-steps, FC1's end bounds
+// instead, a tile's rows in four warps: 128 tokens, top 8 of 64 experts of
+// 512 x 8192, 281 us (weights 238), with 114 rows to the busiest expert 389 (230);
+// e4m3, with a row at a time, 400 (119) and 970 or more (115).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
