@@ -1,0 +1,406 @@
+"""Cases for the e4m3 operators with a float32 scale for each block of 128: the quantisers of rows (1 x 128 blocks) and of
+weights (128 x 128 blocks), the grouped matrix product of such operands, and the gated feed-forward block built from it,
+forward and backward, for a set of experts or for one dense block.
+
+`run` computes them in their plain form (elementary torch operations in 32 bits) or, where `own` is true, through the
+framework's entry points. Rows of several experts lie expert by expert: offsets[e] .. offsets[e + 1] - 1 are expert e's."""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+E4M3_MAX = 448.0
+BLOCK = 128
+
+
+# ---------------------------------------------------------------- the cases
+def _rows(name, tokens, k, n):
+    return {"name": name, "op": "quantize_rows", "tokens": tokens, "k": k, "n": n}
+
+
+def _weights(name, E, K, N):
+    return {"name": name, "op": "quantize_weights", "E": E, "K": K, "N": N}
+
+
+def _gemm(name, rows, K, N, E, skew=0.0, trans=False, out="bf16"):
+    return {"name": name, "op": "gemm", "rows": rows, "K": K, "N": N, "E": E, "skew": skew, "trans": trans, "out": out}
+
+
+def _ffn(name, op, rows, h, f, E, skew=0.0, keep=True):
+    return {"name": name, "op": op, "rows": rows, "h": h, "f": f, "E": E, "skew": skew, "keep": keep}
+
+
+def listed():
+    return [
+        # one token's activations before a product, as a decode step does it
+        _rows("quantise one row", 1, 1, 4096),
+        # the rows of 16384 tokens, each gathered for its two experts (Mixtral-8x7B-shaped layer, training)
+        _rows("quantise gathered rows", 16384, 2, 4096),
+        # the weights of 8 wide experts after an optimiser step
+        _weights("quantise 8 wide weights", 8, 4096, 14336),
+        # one token through one wide projection: the latency of a dense block's decode step
+        _gemm("product, one row", 1, 4096, 14336, 1),
+        # 32 tokens, top 6 of 64 experts: a few rows to each expert, some experts without any
+        _gemm("product, 64 experts, few rows", 192, 2048, 1408, 64, skew=0.5),
+        # sizes that fill no tile and no block of 128, the transposed weight, float32 sums handed on
+        _gemm("product, odd sizes", 1037, 1104, 720, 5, skew=1.0, trans=True, out="fp32"),
+        # a training step's first projection over 8 wide experts
+        _gemm("product, training", 16384, 4096, 14336, 8),
+        # a dense (shared) expert on one user's next token
+        _ffn("feed-forward, one row", "ffn_fwd", 1, 4096, 14336, 1, keep=False),
+        # a server's batch through the DeepSeekMoE-shaped experts, skewed
+        _ffn("feed-forward, 64 experts", "ffn_fwd", 192, 2048, 1408, 64, skew=0.5, keep=False),
+        # a training step of the DeepSeekMoE-shaped layer: 8192 tokens, top 6, activations kept for the backward
+        _ffn("feed-forward, training", "ffn_fwd", 49152, 2048, 1408, 64, skew=0.2),
+        # a small training step at odd sizes: half blocks of 128, ragged experts
+        _ffn("backward, odd sizes", "ffn_bwd", 1021, 1088, 704, 5, skew=1.0),
+        # the backward of 8 wide experts in training
+        _ffn("backward, training", "ffn_bwd", 16384, 4096, 14336, 8),
+    ]
+
+
+def _logint(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["quantize_rows", "quantize_weights", "gemm", "gemm", "ffn_fwd", "ffn_fwd", "ffn_bwd"])
+    if op == "quantize_rows":
+        while True:
+            tokens, k, n = _logint(rng, 1, 32768), rng.randint(1, 8), 16 * _logint(rng, 8, 1024)
+            if tokens * k * n <= 32768 * 4096:
+                break
+        c = _rows("", tokens, k, n)
+    elif op == "quantize_weights":
+        while True:
+            E, K, N = _logint(rng, 1, 64), 16 * _logint(rng, 16, 896), 16 * _logint(rng, 16, 896)
+            if E * K * N <= 8 * 4096 * 14336:
+                break
+        c = _weights("", E, K, N)
+    else:
+        unit = 16 if op == "gemm" else 64
+        while True:
+            E, skew = _logint(rng, 1, 64), rng.choice([0.0, 0.3, 1.0])
+            rows = _logint(rng, 1, 49152)
+            K, N = unit * _logint(rng, 256 // unit, 14336 // unit), unit * _logint(rng, 256 // unit, 14336 // unit)
+            even = rows * E / sum((1 + e) ** -skew for e in range(E))  # as if every expert had the first one's share
+            most = 49152 * 2048 * 1408 if op == "ffn_fwd" else 16384 * 4096 * 14336
+            if E * K * N <= 8 * 4096 * 14336 and rows * K * N <= most and even * max(K, N) <= 49152 * 4096:
+                break
+        if op == "gemm":
+            c = _gemm("", rows, K, N, E, skew, rng.random() < 0.4, rng.choice(["bf16", "bf16", "fp32"]))
+        else:
+            c = _ffn("", op, rows, K, N, E, skew, op == "ffn_bwd" or rows > 1024)
+    del c["name"]
+    return c
+
+
+# ---------------------------------------------------------------- inputs
+def _counts(c, seed):
+    """How many rows each expert has: a draw over shares that fall with the expert's rank where the load is skewed."""
+    share = (1.0 + np.arange(c["E"])) ** -c["skew"]
+    r = np.random.RandomState(seed % (1 << 32))
+    return r.multinomial(c["rows"], r.permutation(share / share.sum()))
+
+
+def _code_blocks(v, bk, bn):
+    """e4m3 codes of v [K, N] and one scale for each bk x bn block: amax / 448, 1 for a block of zeros."""
+    K, N = v.shape
+    kb, nb = -(-K // bk), -(-N // bn)
+    w = torch.zeros((kb * bk, nb * bn), dtype=torch.float32, device=v.device)
+    w[:K, :N] = v
+    w = w.view(kb, bk, nb, bn)
+    s = w.abs().amax((1, 3))
+    s = torch.where(s > 0, s / torch.full_like(s, E4M3_MAX), torch.ones_like(s))
+    q = (w / s[:, None, :, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    return q.view(kb * bk, nb * bn)[:K, :N], s
+
+
+def _weight_codes(W):
+    E, K, N = W.shape
+    q = torch.empty((E, K, N), dtype=torch.uint8, device=W.device)
+    s = torch.empty((E, -(-K // BLOCK), -(-N // BLOCK)), dtype=torch.float32, device=W.device)
+    for e in range(E):
+        q[e], s[e] = _code_blocks(W[e], BLOCK, BLOCK)
+    return q.view(torch.float8_e4m3fn), s
+
+
+def prepare(case, seed):
+    c, dev = case, "cuda"
+    g = torch.Generator(dev).manual_seed(seed)
+
+    def normal(shape, std=1.0):
+        return torch.empty(shape, dtype=torch.bfloat16, device=dev).normal_(0.0, std, generator=g)
+
+    s = {"case": c}
+    if c["op"] == "quantize_rows":
+        rows = c["tokens"] * c["k"]
+        s["x"] = normal((c["tokens"], c["n"]))
+        # the row of the source that each row comes from, times k: what a dispatch writes
+        s["idx"] = torch.randperm(rows, device=dev, generator=g).to(torch.int32) if c["k"] > 1 else None
+        return s
+    if c["op"] == "quantize_weights":
+        s["W"] = normal((c["E"], c["K"], c["N"]), c["K"] ** -0.5)
+        return s
+    counts = _counts(c, seed)
+    s["most"] = int(counts.max())
+    s["offsets"] = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=dev)
+    R, E = c["rows"], c["E"]
+    if c["op"] == "gemm":
+        K, N = c["K"], c["N"]
+        q, sa = _code_blocks(normal((R, K)), 1, BLOCK)
+        s["aq"], s["sa"] = q.contiguous().view(torch.float8_e4m3fn), sa.t().contiguous()
+        s["bq"], s["sb"] = _weight_codes(normal((E, N, K) if c["trans"] else (E, K, N), K ** -0.5))
+        return s
+    h, f = c["h"], c["f"]
+    s["x"] = normal((R, h))
+    for name, shape in (("1", (E, h, f)), ("3", (E, h, f)), ("2", (E, f, h))):
+        s["W%sq" % name], s["s%s" % name] = _weight_codes(normal(shape, shape[1] ** -0.5))
+    if c["op"] == "ffn_bwd":
+        s["dy"], s["A"], s["B"] = normal((R, h)), normal((R, f)), normal((R, f))
+        a = s["A"].float()
+        s["H"] = (a / (1 + torch.exp(-a)) * s["B"].float()).to(torch.bfloat16)
+    return s
+
+
+# ---------------------------------------------------------------- the plain forms
+def _quantize(v):
+    """Codes and scales of the 1 x 128 blocks of v's rows: v's blocks, the scales with an axis of length one, the codes."""
+    n = v.shape[-1]
+    w = torch.nn.functional.pad(v, (0, -n % BLOCK)).unflatten(-1, (-1, BLOCK))
+    s = w.abs().amax(-1, keepdim=True)
+    s = torch.where(s > 0, s / torch.full_like(s, E4M3_MAX), torch.ones_like(s))
+    return (w / s).to(torch.float8_e4m3fn), s
+
+
+def _dequantize(v):
+    """v as its codes stand for it."""
+    q, s = _quantize(v)
+    return (q.float() * s).flatten(-2)[..., :v.shape[-1]]
+
+
+def _spread(s, shape):
+    """A scale for each element from one for each 128 x 128 block of the last two axes."""
+    s = s.repeat_interleave(BLOCK, -1).repeat_interleave(BLOCK, -2)
+    return s[..., :shape[-2], :shape[-1]]
+
+
+def _value(q, s):
+    return q.float() * _spread(s, q.shape)
+
+
+def _slots(s):
+    """Row numbers [E, most] with an expert's rows in each line, and which of them exist."""
+    o = s["offsets"].long()
+    at = o[:-1, None] + torch.arange(s["most"], device=o.device)
+    real = at < o[1:, None]
+    return torch.where(real, at, 0), real
+
+
+def _by_expert(s, v):
+    at, real = _slots(s)
+    return v[at] * real[..., None]
+
+
+def _by_row(s, v):
+    """The rows of v [E, most, n] in their order."""
+    o, R = s["offsets"].long(), s["case"]["rows"]
+    p = torch.arange(R, device=o.device)
+    e = (p[:, None] >= o[1:]).sum(1)
+    return v[e, p - o[e]]
+
+
+def _plain_gemm(s):
+    c = s["case"]
+    a = s["aq"].float() * s["sa"].t().repeat_interleave(BLOCK, 1)[:, :c["K"]]
+    b = _value(s["bq"], s["sb"])
+    out = _by_row(s, torch.matmul(_by_expert(s, a), b.transpose(1, 2) if c["trans"] else b))
+    return {"C": out.to(torch.float32 if c["out"] == "fp32" else torch.bfloat16)}
+
+
+def _plain_ffn_fwd(s):
+    x = _by_expert(s, _dequantize(s["x"].float()))
+    a, b = torch.matmul(x, _value(s["W1q"], s["s1"])), torch.matmul(x, _value(s["W3q"], s["s3"]))
+    h = (a / (1 + torch.exp(-a)) * b).to(torch.bfloat16)  # H is kept in bf16 and quantised from there
+    y = torch.matmul(_dequantize(h.float()), _value(s["W2q"], s["s2"]))
+    out = {"y": _by_row(s, y).to(torch.bfloat16)}
+    if s["case"]["keep"]:
+        out |= {"A": _by_row(s, a).to(torch.bfloat16), "B": _by_row(s, b).to(torch.bfloat16), "H": _by_row(s, h)}
+    return out
+
+
+def _plain_ffn_bwd(s):
+    x, dy, a, b, h = (_by_expert(s, s[n].float()) for n in ("x", "dy", "A", "B", "H"))
+    dh = torch.matmul(_dequantize(dy), _value(s["W2q"], s["s2"]).transpose(1, 2))
+    g = 1 / (1 + torch.exp(-a))
+    # dA and dB are kept in bf16: both products that follow take the kept values
+    da = (dh * b * g * (1 + a * (1 - g))).to(torch.bfloat16).float()
+    db = (dh * a * g).to(torch.bfloat16).float()
+    dx = torch.matmul(_dequantize(da), _value(s["W1q"], s["s1"]).transpose(1, 2))
+    dx += torch.matmul(_dequantize(db), _value(s["W3q"], s["s3"]).transpose(1, 2))
+    grads = {"dW1": x.transpose(1, 2) @ da, "dW3": x.transpose(1, 2) @ db, "dW2": h.transpose(1, 2) @ dy}
+    return {"dx": _by_row(s, dx).to(torch.bfloat16)} | {n: v.to(torch.bfloat16) for n, v in grads.items()}
+
+
+def _plain(s):
+    op = s["case"]["op"]
+    if op == "quantize_rows":
+        x = s["x"] if s["idx"] is None else s["x"][s["idx"].long() // s["case"]["k"]]
+        q, sc = _quantize(x.float())
+        return {"q": q.flatten(-2).view(torch.uint8)[:, :s["case"]["n"]].contiguous().view(torch.float8_e4m3fn), "scale": sc[..., 0].t().contiguous()}
+    if op == "quantize_weights":
+        W = s["W"].float()
+        K, N = W.shape[1:]
+        w = torch.nn.functional.pad(W, (0, -N % BLOCK, 0, -K % BLOCK)).unflatten(2, (-1, BLOCK)).unflatten(1, (-1, BLOCK))
+        sc = w.abs().amax((2, 4))
+        sc = torch.where(sc > 0, sc / torch.full_like(sc, E4M3_MAX), torch.ones_like(sc))
+        return {"q": (W / _spread(sc, W.shape)).to(torch.float8_e4m3fn), "scale": sc}
+    return {"gemm": _plain_gemm, "ffn_fwd": _plain_ffn_fwd, "ffn_bwd": _plain_ffn_bwd}[op](s)
+
+
+# ---------------------------------------------------------------- one pass
+def _own(s):
+    from routing_grouped_expert_router_gb300 import binding as mb
+    c, op = s["case"], s["case"]["op"]
+    if "out" not in s:  # a program keeps these from step to step
+        new = lambda shape, t: torch.empty(shape, dtype=t, device="cuda")  # noqa: E731
+        f8, bf, f32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
+        room = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+        if op == "quantize_rows":
+            R = c["tokens"] * c["k"]
+            s["out"] = {"q": new((R, c["n"]), f8), "scale": new((-(-c["n"] // BLOCK), R), f32)}
+        elif op == "quantize_weights":
+            s["out"] = {"q": new((c["E"], c["K"], c["N"]), f8), "scale": new((c["E"], -(-c["K"] // BLOCK), -(-c["N"] // BLOCK)), f32)}
+        elif op == "gemm":
+            s["gd"] = mb.gemm_dims(c["rows"], c["K"], c["N"], c["E"], trans_b=c["trans"], out_f32=c["out"] == "fp32")
+            s["ws"] = room(mb.moe_gemm_workspace_bytes(s["gd"]))
+            s["out"] = {"C": new((c["rows"], c["N"]), f32 if c["out"] == "fp32" else bf)}
+        else:
+            s["fd"] = mb.ffn_dims(c["rows"], c["h"], c["f"], c["E"], dw_bf16=True)
+            s["ws"] = room(mb.moe_ffn_workspace_bytes(s["fd"], op == "ffn_bwd"))
+            if op == "ffn_fwd":
+                s["out"] = {"y": new((c["rows"], c["h"]), bf)} | ({n: new((c["rows"], c["f"]), bf) for n in "ABH"} if c["keep"] else {})
+            else:
+                s["out"] = {"dx": new((c["rows"], c["h"]), bf)} | {"dW" + n: new(s["W%sq" % n].shape, bf) for n in "132"}
+    o = s["out"]
+    if op == "quantize_rows":
+        mb.moe_quantize_rows_fp8_block(s["x"], c["tokens"] * c["k"], c["n"], s["idx"], c["k"], c["tokens"], o["q"], o["scale"])
+    elif op == "quantize_weights":
+        mb.moe_quantize_weights_fp8_block(s["W"], c["E"], c["K"], c["N"], o["q"], o["scale"])
+    elif op == "gemm":
+        mb.moe_gemm_fp8_block(s["gd"], s["aq"], s["sa"], s["bq"], s["sb"], s["offsets"], o["C"], s["ws"])
+    elif op == "ffn_fwd":
+        mb.moe_gated_ffn_fwd(s["fd"], s["x"], s["offsets"], s["W1q"], s["s1"], s["W3q"], s["s3"], s["W2q"], s["s2"],
+                             o.get("A"), o.get("B"), o.get("H"), o["y"], s["ws"])
+    else:
+        mb.moe_gated_ffn_bwd(s["fd"], s["x"], s["dy"], s["offsets"], s["W1q"], s["s1"], s["W3q"], s["s3"], s["W2q"], s["s2"],
+                             s["A"], s["B"], s["H"], o["dx"], o["dW1"], o["dW3"], o["dW2"], s["ws"])
+    return o
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ---------------------------------------------------------------- the work
+def _active(c):
+    """How many experts have rows, on average over draws."""
+    return float(np.mean([np.count_nonzero(_counts(c, 1 + i)) for i in range(16)]))
+
+
+def work(case):
+    c = case
+    if c["op"] == "quantize_rows":
+        R = c["tokens"] * c["k"]
+        return {"bytes": 2.0 * c["tokens"] * c["n"] + R * (c["n"] + 4 * -(-c["n"] // BLOCK) + (4 if c["k"] > 1 else 0)), "flops": 3.0 * R * c["n"]}
+    if c["op"] == "quantize_weights":
+        return {"bytes": 3.0 * c["E"] * c["K"] * c["N"], "flops": 3.0 * c["E"] * c["K"] * c["N"]}
+    R, act = c["rows"], _active(c)
+    if c["op"] == "gemm":
+        return {"bytes": R * c["K"] * (1 + 4 / BLOCK) + act * c["K"] * c["N"] + R * c["N"] * (4 if c["out"] == "fp32" else 2),
+                "flops": 2.0 * R * c["K"] * c["N"]}
+    hf = c["h"] * c["f"]
+    if c["op"] == "ffn_fwd":
+        return {"bytes": 3.0 * act * hf + 4.0 * R * c["h"] + (6.0 * R * c["f"] if c["keep"] else 0), "flops": 6.0 * R * hf}
+    return {"bytes": 3.0 * act * hf + 6.0 * c["E"] * hf + 6.0 * R * c["h"] + 6.0 * R * c["f"], "flops": 12.0 * R * hf}
+
+
+# ---------------------------------------------------------------- in 64 bits
+def _e4m3(v):
+    """The nearest e4m3 value (ties to the even code), by its spacing: 2^-3 of the power of two below, 2^-9 at the least."""
+    e = torch.frexp(v.abs())[1].to(torch.float64) - 1
+    step = torch.exp2(torch.clamp(e, min=-6.0) - 3)
+    return torch.clamp(torch.round(v / step) * step, -E4M3_MAX, E4M3_MAX)
+
+
+def _coded64(v, bk=1):
+    """(codes' values, scales) of v [R, n] in blocks of bk x 128, block by block. By definition the scale is a float32 and a
+    code is that of the float32 quotient: rows of bf16 values hold many that lie between two codes, where this decides."""
+    R, n = v.shape
+    codes, scales = torch.empty_like(v), []
+    rows = torch.arange(R, device=v.device) // bk
+    for j in range(0, n, BLOCK):
+        part = v[:, j:j + BLOCK]
+        top = part.abs().amax(1)
+        top = torch.zeros(-(-R // bk), dtype=v.dtype, device=v.device).scatter_reduce(0, rows, top, "amax")
+        sc = (top / E4M3_MAX).to(torch.float32).double()
+        sc[top == 0] = 1.0
+        codes[:, j:j + BLOCK] = _e4m3((part / sc[rows, None]).to(torch.float32).double())
+        scales.append(sc)
+    return codes, torch.stack(scales, 1)
+
+
+def _wide(codes, scales, bk):
+    """codes [R, n] times the scale of each one's bk x 128 block."""
+    R, n = codes.shape
+    r, k = torch.arange(R, device=codes.device) // bk, torch.arange(n, device=codes.device) // BLOCK
+    return codes.double() * scales.double()[r][:, k]
+
+
+def exact(case, seed):
+    s, c = prepare(case, seed), case
+    dev = "cuda"
+    if c["op"] == "quantize_rows":
+        x = s["x"].double()
+        q, sc = _coded64(x if s["idx"] is None else x[torch.div(s["idx"].long(), c["k"], rounding_mode="floor")])
+        return {"q": q, "scale": sc.t().contiguous()}
+    if c["op"] == "quantize_weights":
+        both = [_coded64(w.double(), BLOCK) for w in s["W"]]
+        return {"q": torch.stack([b[0] for b in both]), "scale": torch.stack([b[1] for b in both])}
+    R, o = c["rows"], s["offsets"].tolist()
+    f64 = lambda *shape: torch.zeros(shape, dtype=torch.float64, device=dev)  # noqa: E731
+    if c["op"] == "gemm":
+        out = f64(R, c["N"])
+        for e in range(c["E"]):
+            a, b = slice(o[e], o[e + 1]), _wide(s["bq"][e], s["sb"][e], BLOCK)
+            if o[e] < o[e + 1]:
+                out[a] = _wide(s["aq"][a], s["sa"][:, a].t(), 1) @ (b.t() if c["trans"] else b)
+        return {"C": out}
+    h, f = c["h"], c["f"]
+    back = c["op"] == "ffn_bwd"
+    out = {"dx": f64(R, h)} | {"dW" + n: f64(*s["W%sq" % n].shape) for n in "132"} if back else {"y": f64(R, h)}
+    if not back and c["keep"]:
+        out |= {n: f64(R, f) for n in "ABH"}
+    kept = lambda v: v.to(torch.bfloat16).double()  # noqa: E731
+    for e in range(c["E"]):
+        r = slice(o[e], o[e + 1])
+        if o[e] == o[e + 1]:
+            continue
+        w1, w3, w2 = (_wide(s["W%sq" % n][e], s["s" + n][e], BLOCK) for n in "132")
+        if not back:
+            x = _wide(*_coded64(s["x"][r].double()), 1)
+            a, b = x @ w1, x @ w3
+            hh = a * torch.sigmoid(a) * b
+            out["y"][r] = _wide(*_coded64(kept(hh)), 1) @ w2
+            if c["keep"]:
+                out["A"][r], out["B"][r], out["H"][r] = a, b, hh
+            continue
+        x, dy, a, b, hh = (s[n][r].double() for n in ("x", "dy", "A", "B", "H"))
+        dh = _wide(*_coded64(dy), 1) @ w2.t()
+        g = torch.sigmoid(a)
+        da, db = kept(dh * b * (g + a * g * (1 - g))), kept(dh * a * g)
+        out["dx"][r] = _wide(*_coded64(da), 1) @ w1.t() + _wide(*_coded64(db), 1) @ w3.t()
+        out["dW1"][e], out["dW3"][e], out["dW2"][e] = x.t() @ da, x.t() @ db, hh.t() @ dy
+    return out
