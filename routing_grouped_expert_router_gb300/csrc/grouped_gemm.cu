@@ -82,8 +82,12 @@ enum Epi {
   EPI_SWIGLU_BWD_SAR = 5,  // SwiGLU backward that rebuilds H from A, B (no saved H or O)
   EPI_SWIGLU_F8 = 6,       // EPI_SWIGLU on e4m3 operands: sums rescaled by row x column scales
   EPI_BF16_F8 = 7,         // EPI_BF16 on e4m3 operands, likewise
-  EPI_F32_F8 = 8           // EPI_F32 on e4m3 operands
+  EPI_F32_F8 = 8,          // EPI_F32 on e4m3 operands
+  EPI_WGRAD_BF16 = 9       // EPI_WGRAD with bf16 gradients
 };
+__host__ __device__ constexpr bool is_wgrad(int epi) {
+  return epi == EPI_WGRAD || epi == EPI_WGRAD_BF16;
+}
 __host__ __device__ constexpr bool is_f8(int epi) {
   return epi == EPI_SWIGLU_F8 || epi == EPI_BF16_F8 || epi == EPI_F32_F8;
 }
@@ -97,7 +101,7 @@ __host__ __device__ constexpr int base_epi(int epi) {
 
 struct Params {
   int E;
-  const int32_t* offsets;
+  const int32_t* offsets;  // NULL: one group of all rows
   int rows;          // permuted rows; offsets are clamped into [0, rows]
   int M;             // K-grouped: output rows per expert
   int N;             // output columns per B operand
@@ -512,7 +516,7 @@ __device__ __forceinline__ void rescale_f8(const Params& p, const Tile& tl, int 
 }
 
 // Weight gradient of an expert without tokens: zeros for this row's columns.
-template <int NUM_B>
+template <int NUM_B, int EPI>
 __device__ __forceinline__ void zero_wgrad_row(const Params& p, const Tile& tl, int orow) {
   constexpr int BNB = BN / NUM_B;
   if (orow >= p.M) return;
@@ -523,21 +527,28 @@ __device__ __forceinline__ void zero_wgrad_row(const Params& p, const Tile& tl, 
     const int col = tl.nb * BNB + ch * 32;
     if (col >= p.N) break;
     const size_t o = (static_cast<size_t>(tl.e) * p.M + orow) * p.N + col;
+    if (EPI == EPI_WGRAD_BF16) {
+      store_bf16x32(static_cast<__nv_bfloat16*>(p.out0) + o, z);
+      if (NUM_B == 2) store_bf16x32(static_cast<__nv_bfloat16*>(p.out1) + o, z);
+      continue;
+    }
     store_f32x32(static_cast<float*>(p.out0) + o, z);
     if (NUM_B == 2) store_f32x32(static_cast<float*>(p.out1) + o, z);
   }
 }
 
-// Zero k-rows kv..63 of an MN-major 128-wide A tile (two 64-column chunks):
-// they hold the next expert's rows (or the zero fill) and must add nothing.
+// Zero k-rows kv..63 of 128 columns of an MN-major tile (two 64-column chunks):
+// they hold the next expert's rows (or rows past the last expert's, or the zero
+// fill) and must add nothing.  Both operands are cleared: a zero times an
+// infinity or a NaN of the next expert would be a NaN of this one.
 // The rows past kv are contiguous in each chunk, so a lane clears 16-byte
 // words i and i + 32 ... of both chunks with no index arithmetic beyond the
 // stride (an earlier form divided by the chunk length per word, which put
 // about a thousand cycles per ragged tile on the path to the MMA).
-__device__ __forceinline__ void zero_a_tail(uint8_t* a_tile, int kv, int lane) {
+__device__ __forceinline__ void zero_k_tail(uint8_t* tile, int kv, int lane) {
   const int n = (BK - kv) * 8;  // 16-byte words per chunk
-  uint4* c0 = reinterpret_cast<uint4*>(a_tile + kv * 128);
-  uint4* c1 = reinterpret_cast<uint4*>(a_tile + CHUNK_BYTES + kv * 128);
+  uint4* c0 = reinterpret_cast<uint4*>(tile + kv * 128);
+  uint4* c1 = reinterpret_cast<uint4*>(tile + CHUNK_BYTES + kv * 128);
   const uint4 z = make_uint4(0, 0, 0, 0);
   for (int i = lane; i < n; i += 32) {
     c0[i] = z;
@@ -547,17 +558,20 @@ __device__ __forceinline__ void zero_a_tail(uint8_t* a_tile, int kv, int lane) {
   __syncwarp();
 }
 
-// The fp32 epilogues (EPI_WGRAD, EPI_F32) on one 32-column chunk of a warp's
-// 32 rows.  grow0 / orow0: the M-grouped / K-grouped output row of lane 0.
+// The epilogues of whole rows (EPI_WGRAD, EPI_WGRAD_BF16, EPI_F32) on one
+// 32-column chunk of a warp's 32 rows.  grow0 / orow0: the M-grouped / K-grouped output row of lane 0.
 // The output maps view dW as [E * M, N] and dX as [rows, ldo].
 template <int NUM_B, int EPI>
-__device__ __forceinline__ void fp32_rows_chunk(const Params& p, const Maps& maps, const Tile& tl,
+__device__ __forceinline__ void rows_chunk(const Params& p, const Maps& maps, const Tile& tl,
                                                 float4* stage, int& nblk, int grow0, int orow0,
                                                 int col, bool row_ok, const float* v0,
                                                 const float* v1, int lane) {
   const unsigned ok = __ballot_sync(0xffffffffu, row_ok);
   if (ok == 0u) return;
-  if (EPI == EPI_WGRAD) {
+  if (EPI == EPI_WGRAD_BF16) {  // ldo = N
+    store_bf16_chunk<NUM_B>(p, maps, reinterpret_cast<uint4*>(stage), nblk, tl.e * p.M + orow0,
+                            col, row_ok, v0, v1, v1, lane);
+  } else if (EPI == EPI_WGRAD) {
     const int y = tl.e * p.M + orow0;
     const size_t o = static_cast<size_t>(y) * p.N + col;
     store_f32_block(stage, nblk, v0, &maps.o0, col, y, static_cast<float*>(p.out0) + o, p.N, ok,
@@ -609,7 +623,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   if (warp >= 2) {
     for (int e = threadIdx.x - 64; e <= p.E; e += 128) {
-      const int o = __ldg(p.offsets + e);
+      const int o = p.offsets ? __ldg(p.offsets + e) : (e ? p.rows : 0);
       c.off[e] = o < 0 ? 0 : (o > p.rows ? p.rows : o);
     }
   }
@@ -717,7 +731,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint8_t* a_tile = smem + s * STAGE_BYTES;
         if (GROUP_K) {
           const int kv = tl.row_end - (tl.row0 + kb * BK);
-          if (kv < BK) zero_a_tail(a_tile, kv, lane);
+          if (kv < BK) {
+            zero_k_tail(a_tile, kv, lane);
+            zero_k_tail(a_tile + A_BYTES, kv, lane);
+            zero_k_tail(a_tile + A_BYTES + 2 * CHUNK_BYTES, kv, lane);
+          }
         }
         if (lane == 0) {
           tc_fence_after();
@@ -779,7 +797,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           prefetch_ab_rows<BNB>(maps, tn, quarter * 32);
       }
       if (GROUP_K && tl.nkb == 0) {  // expert without tokens: zero weight gradient
-        zero_wgrad_row<NUM_B>(p, tl, tl.mb * BM + r);
+        zero_wgrad_row<NUM_B, EPI>(p, tl, tl.mb * BM + r);
         continue;
       }
       const int buf = it & 1;
@@ -825,10 +843,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_ld32(tbase + ch * 32, v0);
           if (NUM_B == 2) tmem_ld32(tbase + BNB + ch * 32, v1);
           const int col = tl.nb * BNB + ch * 32;
-          if constexpr (EPI == EPI_WGRAD || base_epi(EPI) == EPI_F32) {
+          if constexpr (is_wgrad(EPI) || base_epi(EPI) == EPI_F32) {
             if (col >= p.N) continue;  // the same for the whole warp
             if (is_f8(EPI) && row_ok) rescale_f8<NUM_B>(p, tl, grow, col, v0, v1);
-            fp32_rows_chunk<NUM_B, EPI>(p, maps, tl, stage, nblk, grow - lane,
+            rows_chunk<NUM_B, EPI>(p, maps, tl, stage, nblk, grow - lane,
                                         tl.mb * BM + quarter * 32, col, row_ok, v0, v1, lane);
           } else {
             if (col >= p.N) continue;  // the same for the whole warp
@@ -947,7 +965,7 @@ __global__ void __launch_bounds__(NUM_THREADS2, 1)
   }
   if (warp >= 2 && warp < 6) {
     for (int e = threadIdx.x - 64; e <= p.E; e += 128) {
-      const int o = __ldg(p.offsets + e);
+      const int o = p.offsets ? __ldg(p.offsets + e) : (e ? p.rows : 0);
       c.off[e] = o < 0 ? 0 : (o > p.rows ? p.rows : o);
     }
   }
@@ -1125,7 +1143,8 @@ __global__ void __launch_bounds__(NUM_THREADS2, 1)
           give_up();
           break;
         }
-        zero_a_tail(smem + s * STAGE2_BYTES, kv, lane);
+        zero_k_tail(smem + s * STAGE2_BYTES, kv, lane);
+        zero_k_tail(smem + s * STAGE2_BYTES + A2_BYTES, kv, lane);
         if (lane == 0) {
           if (full0 == 0)
             mbar_arrive(smem_u32(&c.full[s]));
@@ -1188,7 +1207,7 @@ __global__ void __launch_bounds__(NUM_THREADS2, 1)
       }
       const int orow = tl.mb * PM + half + r;       // K-grouped output row
       if (GROUP_K && tl.nkb == 0) {
-        zero_wgrad_row<NUM_B>(p, tl, orow);
+        zero_wgrad_row<NUM_B, EPI>(p, tl, orow);
         continue;
       }
       const int buf = it & 1;
@@ -1261,10 +1280,10 @@ __global__ void __launch_bounds__(NUM_THREADS2, 1)
           tmem_ld32(tbase + ch * 32, v0);
           if (NUM_B == 2) tmem_ld32(tbase + BNB + ch * 32, v1);
           const int col = tl.nb * BNB + ch * 32;
-          if constexpr (EPI == EPI_WGRAD || base_epi(EPI) == EPI_F32) {
+          if constexpr (is_wgrad(EPI) || base_epi(EPI) == EPI_F32) {
             if (col >= p.N) continue;  // the same for the whole warp
             if (is_f8(EPI) && row_ok) rescale_f8<NUM_B>(p, tl, grow, col, v0, v1);
-            fp32_rows_chunk<NUM_B, EPI>(p, maps, tl, stage, nblk, grow - lane, orow - lane, col,
+            rows_chunk<NUM_B, EPI>(p, maps, tl, stage, nblk, grow - lane, orow - lane, col,
                                         row_ok, v0, v1, lane);
           } else {
             if (col >= p.N) continue;  // the same for the whole warp
@@ -1792,8 +1811,15 @@ cudaError_t gemm_fc1_dgrad(const GemmProblem& g, const void* dA, const void* dB,
                                                  g.num_sms, s);
 }
 
-cudaError_t gemm_fc2_wgrad(const GemmProblem& g, const void* H, const void* dO, float* dW2,
-                           cudaStream_t s) {
+namespace {
+// The maps of a weight gradient's outputs: dW as [E * M, N].
+bool make_map_dw(CUtensorMap* m, const void* dW, uint64_t N, uint64_t rows, bool bf16) {
+  return bf16 ? make_map_out_bf16(m, dW, N, rows) : make_map_out(m, dW, N, rows);
+}
+}  // namespace
+
+cudaError_t gemm_fc2_wgrad(const GemmProblem& g, const void* H, const void* dO, void* dW2,
+                           cudaStream_t s, bool bf16) {
   Maps m;
   memset(&m, 0, sizeof(m));
   if (!make_map_mn(&m.a0, H, g.f, g.rows, BK, BM / 64) ||
@@ -1804,16 +1830,19 @@ cudaError_t gemm_fc2_wgrad(const GemmProblem& g, const void* H, const void* dO, 
   Params p = base_params(g);
   p.M = g.f;
   p.N = g.h;
+  p.ldo = g.h;
   p.out0 = dW2;
-  if (!make_map_out(&m.o0, dW2, g.h, static_cast<uint64_t>(g.E) * g.f)) return cudaErrorInvalidValue;
+  if (!make_map_dw(&m.o0, dW2, g.h, static_cast<uint64_t>(g.E) * g.f, bf16))
+    return cudaErrorInvalidValue;
   p.ktiles = static_cast<int>(kgrouped_tiles(g, EPI_WGRAD, g.f, g.h, BN));
   const long long R = rows_per_expert(g);
   set_raster(p, R * g.f * 2, R * g.h * 2, tile_rows(EPI_WGRAD) * R * 2, BN * R * 2);
-  return launch<true, true, 1, EPI_WGRAD, true>(p, m, p.ktiles, g.num_sms, s);
+  return bf16 ? launch<true, true, 1, EPI_WGRAD_BF16, true>(p, m, p.ktiles, g.num_sms, s)
+              : launch<true, true, 1, EPI_WGRAD, true>(p, m, p.ktiles, g.num_sms, s);
 }
 
 cudaError_t gemm_fc1_wgrad(const GemmProblem& g, const void* x_perm, const void* dA,
-                           const void* dB, float* dW1, float* dW3, cudaStream_t s) {
+                           const void* dB, void* dW1, void* dW3, cudaStream_t s, bool bf16) {
   Maps m;
   memset(&m, 0, sizeof(m));
   if (!make_map_mn(&m.a0, x_perm, g.h, g.rows, BK, BM / 64) ||
@@ -1824,15 +1853,17 @@ cudaError_t gemm_fc1_wgrad(const GemmProblem& g, const void* x_perm, const void*
   Params p = base_params(g);
   p.M = g.h;
   p.N = g.f;
+  p.ldo = g.f;
   p.out0 = dW1;
   p.out1 = dW3;
-  if (!make_map_out(&m.o0, dW1, g.f, static_cast<uint64_t>(g.E) * g.h) ||
-      !make_map_out(&m.o1, dW3, g.f, static_cast<uint64_t>(g.E) * g.h))
+  if (!make_map_dw(&m.o0, dW1, g.f, static_cast<uint64_t>(g.E) * g.h, bf16) ||
+      !make_map_dw(&m.o1, dW3, g.f, static_cast<uint64_t>(g.E) * g.h, bf16))
     return cudaErrorInvalidValue;
   p.ktiles = static_cast<int>(kgrouped_tiles(g, EPI_WGRAD, g.h, g.f, BN / 2));
   const long long R = rows_per_expert(g);
   set_raster(p, R * g.h * 2, R * 2 * g.f * 2, tile_rows(EPI_WGRAD) * R * 2, BN * R * 2);
-  return launch<true, true, 2, EPI_WGRAD, true>(p, m, p.ktiles, g.num_sms, s);
+  return bf16 ? launch<true, true, 2, EPI_WGRAD_BF16, true>(p, m, p.ktiles, g.num_sms, s)
+              : launch<true, true, 2, EPI_WGRAD, true>(p, m, p.ktiles, g.num_sms, s);
 }
 
 }  // namespace moe

@@ -13,7 +13,8 @@ namespace moe {
 
 struct GemmProblem {
   int E;                    // experts
-  const int32_t* offsets;   // [E+1] expert row ranges in the permuted order (device)
+  const int32_t* offsets;   // [E+1] expert row ranges in the permuted order (device);
+                            // NULL: one expert with all rows
   int rows;                 // T*k permuted rows
   int h, f;                 // hidden size, expert width
   int* status;              // device status word
@@ -67,12 +68,13 @@ int gemm_col_tiles(int n);
 // dX_perm = dA W1^T + dB W3^T (K = 2f), fp32 [rows, h].
 cudaError_t gemm_fc1_dgrad(const GemmProblem& p, const void* dA, const void* dB,
                            const void* W1, const void* W3, float* dX, cudaStream_t s);
-// dW2[e] = H_e^T dO_e, ragged K = rows of e.  fp32 [E, f, h].
-cudaError_t gemm_fc2_wgrad(const GemmProblem& p, const void* H, const void* dO, float* dW2,
-                           cudaStream_t s);
-// dW1[e] = X_e^T dA_e, dW3[e] = X_e^T dB_e.  fp32 [E, h, f].
+// dW2[e] = H_e^T dO_e, ragged K = rows of e.  [E, f, h], fp32 or (bf16) bf16.
+cudaError_t gemm_fc2_wgrad(const GemmProblem& p, const void* H, const void* dO, void* dW2,
+                           cudaStream_t s, bool bf16 = false);
+// dW1[e] = X_e^T dA_e, dW3[e] = X_e^T dB_e.  [E, h, f], fp32 or (bf16) bf16.
 cudaError_t gemm_fc1_wgrad(const GemmProblem& p, const void* x_perm, const void* dA,
-                           const void* dB, float* dW1, float* dW3, cudaStream_t s);
+                           const void* dB, void* dW1, void* dW3, cudaStream_t s,
+                           bool bf16 = false);
 
 // TMA maps of tcgen05 operands, 128-byte swizzle, zero fill out of range.
 //   K-major rows: [rows, inner] bf16 (or bytes), boxes of 128 bytes x box_rows.
