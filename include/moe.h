@@ -58,7 +58,7 @@
  *     skipped (an assignment not placed, a zero row, a slot that adds
  *     nothing), so nothing is read or written out of bounds.  The calls that
  *     take no workspace (moe_combine, moe_unpermute, moe_quantize_rows_fp8,
- *     moe_permute_noalloc, moe_block_norm_fwd) record into one status word per device that the
+ *     moe_quantize_rows_fp8_block, moe_permute_noalloc, moe_block_norm_fwd) record into one status word per device that the
  *     library keeps (its address is looked up on the first such call on a
  *     device and kept until the process exits); moe_read_device_status(NULL,
  *     stream) reports that one.
@@ -113,7 +113,9 @@ typedef enum {
   MOE_OP_LAYER_FWD_FP8 = 7,
   MOE_OP_LAYER_BWD_FP8 = 8,
   MOE_OP_LAYER_DECODE = 9,
-  MOE_OP_LAYER_DECODE_FP8 = 10
+  MOE_OP_LAYER_DECODE_FP8 = 10,
+  MOE_OP_LAYER_FWD_FP8_BLOCK = 11,
+  MOE_OP_LAYER_BWD_FP8_BLOCK = 12
 } moe_op;
 
 /* Per-expert capacity for a capacity factor: ceil(factor * T * k / E), the
@@ -370,6 +372,138 @@ moe_status moe_layer_bwd_fp8(const moe_dims* dims, const moe_bf16* x,
                              float* dW1, float* dW3, float* dW2, void* ws,
                              size_t ws_bytes, moe_stream_t stream);
 
+/* ---------------------------------------- e4m3 with a scale for each block
+ * The fine-grained form of e4m3 training and serving: a float32 scale for each
+ * 1 x 128 block of an activation's row and for each 128 x 128 block of a
+ * weight.  Because a weight's block is square, one copy of its codes, in the
+ * weight's own layout, serves the forward and the data gradients, and weights
+ * that come with such scales are used as they are.
+ *   s = amax(|block|) / 448 (IEEE float32 division; 1 for a block of zeros)
+ *   q = e4m3(v / s)         (the float32 quotient, to nearest even, +-448 at most)
+ * A block that holds an infinity or a NaN gets a scale that is not finite, and
+ * so do the results that it enters.  A block at the end of an axis that is no
+ * multiple of 128 is shorter.
+ *   activations [R, n]: codes uint8 [R, n], scales float [ceil(n/128), R]:
+ *                       the scales of block column b of all rows together
+ *   weights [E, K, N]:  codes uint8 [E, K, N], scales
+ *                       float [E, ceil(K/128), ceil(N/128)]
+ * Products are summed block by block: the 128 products of a block in fp32 in
+ * tensor memory, then times both scales and added in fp32 registers. */
+
+/* Rows: as moe_quantize_rows_fp8 (source row idx[p] / div, or p when idx is
+ * NULL), with one scale for each block: scale[b * rows + p] is that of
+ * q[p, 128 b ...].  n a multiple of 16.  A source index out of range gives
+ * codes 0 with scales 1 and MOE_ERR_DEVICE_INDEX in the per-device status
+ * word. */
+moe_status moe_quantize_rows_fp8_block(const moe_bf16* in, int64_t rows,
+                                       int32_t n, const int32_t* idx,
+                                       int32_t div, int64_t src_rows,
+                                       uint8_t* q, float* scale,
+                                       moe_stream_t stream);
+
+/* Weights W [E, K, N] (also a single matrix, E = 1): K and N multiples of
+ * 16. */
+moe_status moe_quantize_weights_fp8_block(const moe_bf16* W, int32_t E,
+                                          int32_t K, int32_t N, uint8_t* q,
+                                          float* scale, moe_stream_t stream);
+
+typedef struct {
+  int32_t rows;     /* rows of the activations */
+  int32_t K;        /* contraction, a multiple of 16, at most 2^20 */
+  int32_t N;        /* output columns, a multiple of 16, at most 2^20 */
+  int32_t E;        /* groups of rows (experts), at most 64 */
+  int32_t trans_b;  /* 0: weights [E, K, N]; 1: [E, N, K], used transposed */
+  int32_t out_f32;  /* 0: C bf16; 1: C fp32 */
+} moe_gemm_dims;
+
+/* Scratch bytes of moe_gemm_fp8_block (0 on invalid dims). */
+size_t moe_gemm_workspace_bytes(const moe_gemm_dims* dims);
+
+/* C[p] = A[p] B[e] for the rows p of each group e, offsets[e] <= p <
+ * offsets[e+1] (offsets [E+1] int32 on the device, from 0; NULL with E = 1: all
+ * rows).  A: aq [rows, K] with sa [ceil(K/128), rows]; B: bq with sb as above;
+ * C [rows, N].  Rows p >= offsets[E] are neither read nor written.  Offsets
+ * out of order or range are clamped and recorded as MOE_ERR_DEVICE_INDEX in
+ * the status word of ws.
+ * The same inputs give the same bits.  Calls that may run at the same time need
+ * a workspace each; the first 256 bytes of ws have to be zero before its first
+ * use. */
+moe_status moe_gemm_fp8_block(const moe_gemm_dims* dims, const uint8_t* aq,
+                              const float* sa, const uint8_t* bq,
+                              const float* sb, const int32_t* offsets, void* C,
+                              void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* A gated feed-forward block on such weights: the experts of a layer on their
+ * rows, or with E = 1 and offsets NULL one dense block (a shared expert) on
+ * all rows.
+ *   A = x W1, B = x W3, H = silu(A) * B, y = H W2
+ * with W1, W3 [E, h, f] and W2 [E, f, h] as codes and scales.  x is quantised
+ * in the call; both projections, the activation, the product and H's codes
+ * (from its bf16 value) come from one kernel. */
+typedef struct {
+  int32_t rows;
+  int32_t h;        /* a multiple of 64, at most 2^20 */
+  int32_t f;        /* a multiple of 64, at most 2^20 */
+  int32_t E;        /* groups of rows (experts), at most 64 */
+  int32_t dw_bf16;  /* type of the weight gradients: 0: fp32, 1: bf16 */
+} moe_ffn_dims;
+
+/* Scratch bytes of moe_gated_ffn_fwd (backward = 0) or moe_gated_ffn_bwd
+ * (backward = 1); 0 on invalid dims. */
+size_t moe_ffn_workspace_bytes(const moe_ffn_dims* dims, int backward);
+
+/* x [rows, h] bf16 (rows of expert e at offsets[e] .. offsets[e+1]-1), y
+ * [rows, h] bf16.  A, B, H [rows, f] bf16 are what the backward takes; all three
+ * NULL where none follows.  Rows p >= offsets[E] are neither read nor
+ * written.  Offsets and ws as in moe_gemm_fp8_block. */
+moe_status moe_gated_ffn_fwd(const moe_ffn_dims* dims, const moe_bf16* x,
+                             const int32_t* offsets, const uint8_t* W1q,
+                             const float* s1, const uint8_t* W3q,
+                             const float* s3, const uint8_t* W2q,
+                             const float* s2, moe_bf16* A, moe_bf16* B,
+                             moe_bf16* H, moe_bf16* y, void* ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
+/* Its backward for dy [rows, h], from the forward's x, A, B, H:
+ *   dH = dy W2^T;  dA = dH * B * s (1 + A (1 - s)), dB = dH * silu(A),
+ *   s = sigmoid(A);  dx = dA W1^T + dB W3^T
+ *   dW1[e] = x_e^T dA_e, dW3[e] = x_e^T dB_e, dW2[e] = H_e^T dy_e
+ * The data gradients run on e4m3 codes (of dy, and of dA and dB from their
+ * bf16 values), the weight gradients on the bf16 x, H, dy, dA, dB.  dx
+ * [rows, h] bf16 (rows p >= offsets[E] untouched); dW1, dW3 [E, h, f], dW2
+ * [E, f, h] fp32 or bf16 (dims.dw_bf16), written, not accumulated, zero for
+ * an expert without rows; all three NULL for weights that are not trained. */
+moe_status moe_gated_ffn_bwd(const moe_ffn_dims* dims, const moe_bf16* x,
+                             const moe_bf16* dy, const int32_t* offsets,
+                             const uint8_t* W1q, const float* s1,
+                             const uint8_t* W3q, const float* s3,
+                             const uint8_t* W2q, const float* s2,
+                             const moe_bf16* A, const moe_bf16* B,
+                             const moe_bf16* H, moe_bf16* dx, void* dW1,
+                             void* dW3, void* dW2, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+
+/* moe_layer_fwd and moe_layer_bwd with the experts above.  The forward writes
+ * the same `saved` context as moe_layer_fwd; the backward takes one from
+ * either of the two.  h and f multiples of 64; dims.sar = 1 is
+ * MOE_ERR_UNSUPPORTED.  Workspaces: moe_workspace_bytes with
+ * MOE_OP_LAYER_FWD_FP8_BLOCK and MOE_OP_LAYER_BWD_FP8_BLOCK. */
+moe_status moe_layer_fwd_fp8_block(const moe_dims* dims, const moe_bf16* x,
+                                   const float* Wg, const float* b,
+                                   const uint8_t* W1q, const float* s1,
+                                   const uint8_t* W3q, const float* s3,
+                                   const uint8_t* W2q, const float* s2,
+                                   moe_bf16* y, void* saved, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream);
+moe_status moe_layer_bwd_fp8_block(const moe_dims* dims, const moe_bf16* x,
+                                   const moe_bf16* dy, const float* Wg,
+                                   const uint8_t* W1q, const float* s1,
+                                   const uint8_t* W3q, const float* s3,
+                                   const uint8_t* W2q, const float* s2,
+                                   const void* saved, moe_bf16* dx, float* dWg,
+                                   float* dW1, float* dW3, float* dW2, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream);
+
 /* ------------------------------------------------------- a few tokens
  * The whole layer for 1 <= T <= 128 tokens, as a serving loop calls it for the
  * next token of each of its sequences.  The same mathematics as
@@ -509,7 +643,7 @@ const char* moe_status_string(moe_status status);
 /* Synchronises `stream`, returns the status word at the start of `ws` and
  * clears it.  ws = NULL: the status word of the calls that take no workspace
  * (moe_combine, moe_unpermute, moe_quantize_rows_fp8, moe_permute_noalloc,
- * moe_block_norm_fwd) on the current device.
+ * moe_quantize_rows_fp8_block, moe_block_norm_fwd) on the current device.
  * MOE_ERR_CUDA if the synchronisation itself failed. */
 moe_status moe_read_device_status(void* ws, moe_stream_t stream);
 

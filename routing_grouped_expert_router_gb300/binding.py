@@ -24,7 +24,7 @@ MOE_ERR_DEVICE_INDEX = 6
 
 OP_ROUTE, OP_PERMUTE, OP_EXPERT_FFN_FWD, OP_EXPERT_FFN_BWD, OP_ROUTER_BWD, \
     OP_LAYER_FWD, OP_LAYER_BWD, OP_LAYER_FWD_FP8, OP_LAYER_BWD_FP8, OP_LAYER_DECODE, \
-    OP_LAYER_DECODE_FP8 = range(11)
+    OP_LAYER_DECODE_FP8, OP_LAYER_FWD_FP8_BLOCK, OP_LAYER_BWD_FP8_BLOCK = range(13)
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = range(3)
 
 HEADER = os.path.join(_build.ROOT, "include", "moe.h")
@@ -64,6 +64,24 @@ def norm_dims(T, h, res_f32=False, gate=GATE_NONE, eps=1e-5, alpha=1.0,
                          float(beta))
 
 
+class moe_gemm_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("trans_b", ctypes.c_int32), ("out_f32", ctypes.c_int32)]
+
+
+def gemm_dims(rows, K, N, E=1, trans_b=False, out_f32=False) -> moe_gemm_dims:
+    return moe_gemm_dims(int(rows), int(K), int(N), int(E), int(bool(trans_b)), int(bool(out_f32)))
+
+
+class moe_ffn_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("h", ctypes.c_int32), ("f", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("dw_bf16", ctypes.c_int32)]
+
+
+def ffn_dims(rows, h, f, E=1, dw_bf16=False) -> moe_ffn_dims:
+    return moe_ffn_dims(int(rows), int(h), int(f), int(E), int(bool(dw_bf16)))
+
+
 def capacity_for(T, k, E, factor: float) -> int:
     """moe_capacity_for: the per-expert capacity for a capacity factor."""
     c = load().moe_capacity_for(int(T), int(k), int(E), float(factor))
@@ -78,6 +96,8 @@ _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _D = ctypes.POINTER(moe_dims)
 _ND = ctypes.POINTER(moe_norm_dims)
+_GD = ctypes.POINTER(moe_gemm_dims)
+_FD = ctypes.POINTER(moe_ffn_dims)
 
 _SIGS = {
     "moe_workspace_bytes": (_SZ, [_D, _I]),
@@ -116,6 +136,16 @@ _SIGS = {
     "moe_layer_decode": (_I, [_D] + [_P] * 10 + [_SZ, _P]),
     "moe_layer_decode_fp8": (_I, [_D] + [_P] * 8 + [_SZ, _P]),
     "moe_layer_decode_fp8_as_fwd": (_I, [_D] + [_P] * 8 + [_SZ, _P]),
+    "moe_quantize_rows_fp8_block": (_I, [_P, ctypes.c_int64, ctypes.c_int32, _P, ctypes.c_int32,
+                                         ctypes.c_int64, _P, _P, _P]),
+    "moe_quantize_weights_fp8_block": (_I, [_P] + [ctypes.c_int32] * 3 + [_P, _P, _P]),
+    "moe_gemm_workspace_bytes": (_SZ, [_GD]),
+    "moe_gemm_fp8_block": (_I, [_GD] + [_P] * 7 + [_SZ, _P]),
+    "moe_ffn_workspace_bytes": (_SZ, [_FD, _I]),
+    "moe_gated_ffn_fwd": (_I, [_FD] + [_P] * 13 + [_SZ, _P]),
+    "moe_gated_ffn_bwd": (_I, [_FD] + [_P] * 17 + [_SZ, _P]),
+    "moe_layer_fwd_fp8_block": (_I, [_D] + [_P] * 12 + [_SZ, _P]),
+    "moe_layer_bwd_fp8_block": (_I, [_D] + [_P] * 16 + [_SZ, _P]),
     "moe_norm_workspace_bytes": (_SZ, [_ND]),
     "moe_block_norm_fwd": (_I, [_ND] + [_P] * 8),
     "moe_block_norm_bwd": (_I, [_ND] + [_P] * 13 + [_SZ, _P]),
@@ -417,3 +447,62 @@ def moe_block_norm_bwd(nd, r_out, y, w_post, gate, w_pre, du, dr_out, dr, dy, dw
     args = [r_out, y, w_post, gate, w_pre, du, dr_out, dr, dy, dw_post, dgate, dw_pre]
     _check(load().moe_block_norm_bwd(ctypes.byref(nd), *[_addr(a) for a in args], _addr(ws),
                                      ws_bytes, _stream(stream)), "moe_block_norm_bwd")
+
+
+def moe_quantize_rows_fp8_block(inp, rows, n, idx, div, src_rows, q, scale, stream=None):
+    _check(load().moe_quantize_rows_fp8_block(_addr(inp), int(rows), int(n), _addr(idx), int(div),
+                                              int(src_rows), _addr(q), _addr(scale),
+                                              _stream(stream)), "moe_quantize_rows_fp8_block")
+
+
+def moe_quantize_weights_fp8_block(W, E, K, N, q, scale, stream=None):
+    _check(load().moe_quantize_weights_fp8_block(_addr(W), int(E), int(K), int(N), _addr(q),
+                                                 _addr(scale), _stream(stream)),
+           "moe_quantize_weights_fp8_block")
+
+
+def moe_gemm_workspace_bytes(gd: moe_gemm_dims) -> int:
+    return int(load().moe_gemm_workspace_bytes(ctypes.byref(gd)))
+
+
+def moe_gemm_fp8_block(gd, aq, sa, bq, sb, offsets, C, ws, ws_bytes=None, stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check(load().moe_gemm_fp8_block(ctypes.byref(gd), _addr(aq), _addr(sa), _addr(bq), _addr(sb),
+                                     _addr(offsets), _addr(C), _addr(ws), ws_bytes,
+                                     _stream(stream)), "moe_gemm_fp8_block")
+
+
+def moe_ffn_workspace_bytes(fd: moe_ffn_dims, backward) -> int:
+    return int(load().moe_ffn_workspace_bytes(ctypes.byref(fd), int(bool(backward))))
+
+
+def moe_gated_ffn_fwd(fd, x, offsets, W1q, s1, W3q, s3, W2q, s2, A, B, H, y, ws, ws_bytes=None,
+                      stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    args = [x, offsets, W1q, s1, W3q, s3, W2q, s2, A, B, H, y]
+    _check(load().moe_gated_ffn_fwd(ctypes.byref(fd), *[_addr(a) for a in args], _addr(ws),
+                                    ws_bytes, _stream(stream)), "moe_gated_ffn_fwd")
+
+
+def moe_gated_ffn_bwd(fd, x, dy, offsets, W1q, s1, W3q, s3, W2q, s2, A, B, H, dx, dW1, dW3, dW2,
+                      ws, ws_bytes=None, stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    args = [x, dy, offsets, W1q, s1, W3q, s3, W2q, s2, A, B, H, dx, dW1, dW3, dW2]
+    _check(load().moe_gated_ffn_bwd(ctypes.byref(fd), *[_addr(a) for a in args], _addr(ws),
+                                    ws_bytes, _stream(stream)), "moe_gated_ffn_bwd")
+
+
+def moe_layer_fwd_fp8_block(d, x, Wg, b, W1q, s1, W3q, s3, W2q, s2, y, saved, ws, ws_bytes=None,
+                            stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    args = [x, Wg, b, W1q, s1, W3q, s3, W2q, s2, y, saved]
+    _check(load().moe_layer_fwd_fp8_block(ctypes.byref(d), *[_addr(a) for a in args], _addr(ws),
+                                          ws_bytes, _stream(stream)), "moe_layer_fwd_fp8_block")
+
+
+def moe_layer_bwd_fp8_block(d, x, dy, Wg, W1q, s1, W3q, s3, W2q, s2, saved, dx, dWg, dW1, dW3,
+                            dW2, ws, ws_bytes=None, stream=None):
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    args = [x, dy, Wg, W1q, s1, W3q, s3, W2q, s2, saved, dx, dWg, dW1, dW3, dW2]
+    _check(load().moe_layer_bwd_fp8_block(ctypes.byref(d), *[_addr(a) for a in args], _addr(ws),
+                                          ws_bytes, _stream(stream)), "moe_layer_bwd_fp8_block")

@@ -14,6 +14,7 @@
 
 #include "../../include/moe.h"
 #include "api_internal.h"
+#include "block.cuh"
 #include "decode.cuh"
 #include "grouped_gemm.cuh"
 #include "kernels.cuh"
@@ -66,7 +67,8 @@ moe_status check_dims(const moe_dims* d, bool routed) {
 bool routed_op(int op) {
   return op == MOE_OP_ROUTE || op == MOE_OP_LAYER_FWD || op == MOE_OP_LAYER_BWD ||
          op == MOE_OP_LAYER_FWD_FP8 || op == MOE_OP_LAYER_BWD_FP8 ||
-         op == MOE_OP_LAYER_DECODE || op == MOE_OP_LAYER_DECODE_FP8;
+         op == MOE_OP_LAYER_DECODE || op == MOE_OP_LAYER_DECODE_FP8 ||
+         op == MOE_OP_LAYER_FWD_FP8_BLOCK || op == MOE_OP_LAYER_BWD_FP8_BLOCK;
 }
 
 
@@ -172,6 +174,7 @@ struct WsLayout {
   size_t Xq = 0, sx = 0, Hq = 0, sh = 0;     // fp8 forward
   size_t h_amax = 0;                         // fp8 forward: per-tile amax of H
   size_t dAq = 0, dBq = 0, sab = 0, ab_amax = 0;  // fp8 backward
+  size_t dOq = 0, sdo = 0, sda = 0, sdb = 0;  // block-scaled fp8 backward (with dAq, dBq)
   size_t total = 0;
 };
 WsLayout ws_layout(const moe_dims& d, int op) {
@@ -196,7 +199,30 @@ WsLayout ws_layout(const moe_dims& d, int op) {
     L.dA = c.take(R * d.f * 2);
     L.dB = c.take(R * d.f * 2);
   };
+  const size_t hb = moe::blocks_of(d.h), fb = moe::blocks_of(d.f);
   switch (op) {
+    case MOE_OP_LAYER_FWD_FP8_BLOCK:
+      if (d.sar) return WsLayout{};
+      route();
+      dispatch();
+      L.Xq = c.take(R * d.h);
+      L.sx = c.take(R * hb * 4);
+      L.Hq = c.take(R * d.f);
+      L.sh = c.take(R * fb * 4);
+      break;
+    case MOE_OP_LAYER_BWD_FP8_BLOCK:
+      if (d.sar) return WsLayout{};
+      expert_bwd(false);
+      L.dOq = c.take(R * d.h);
+      L.sdo = c.take(R * hb * 4);
+      L.dAq = c.take(R * d.f);
+      L.sda = c.take(R * fb * 4);
+      L.dBq = c.take(R * d.f);
+      L.sdb = c.take(R * fb * 4);
+      L.dX = c.take(R * d.h * 4);
+      L.dg = c.take(R * 4);
+      router_bwd();
+      break;
     case MOE_OP_ROUTE: route(); break;
     case MOE_OP_PERMUTE: dispatch(); break;
     case MOE_OP_EXPERT_FFN_FWD: L.x_perm = c.take(R * d.h * 2); break;
@@ -945,6 +971,118 @@ moe_status moe_layer_bwd_fp8(const moe_dims* dims, const moe_bf16* x, const moe_
                                     at<float>(ws, L.sab), at<uint8_t>(qwb, Q.W1r),
                                     at<uint8_t>(qwb, Q.W3r), at<float>(qwb, Q.s13r), dX, stream),
             "gg_fc1_dgrad_fp8");
+    MOE_RUN(moe::gemm_fc1_wgrad(g, at<uint16_t>(saved, S.x_perm), dA, dB, dW1, dW3, stream),
+            moe::kGemmNames[5]);
+  }
+  return do_router_bwd(d, x, Wg, idx, gates, dg, dX, pdst, dx, dWg, ws, L, stream);
+}
+
+moe_status moe_layer_fwd_fp8_block(const moe_dims* dims, const moe_bf16* x, const float* Wg,
+                                   const float* b, const uint8_t* W1q, const float* s1,
+                                   const uint8_t* W3q, const float* s3, const uint8_t* W2q,
+                                   const float* s2, moe_bf16* y, void* saved, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream_) {
+  moe_status st = check_dims(dims, true);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (d.sar) return MOE_ERR_UNSUPPORTED;  // as in moe_layer_fwd_fp8
+  const size_t T = d.T;
+  if (!buf_ok(x, T) || !ptr_ok(Wg) || !ptr_ok(W1q) || !ptr_ok(s1) || !ptr_ok(W3q) || !ptr_ok(s3) ||
+      !ptr_ok(W2q) || !ptr_ok(s2) || !buf_ok(y, T) || (d.has_bias && !ptr_ok(b)) || !saved ||
+      !aligned(saved, kAlign))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = ws_check(d, MOE_OP_LAYER_FWD_FP8_BLOCK, ws, ws_bytes)) != MOE_OK) return st;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const WsLayout L = ws_layout(d, MOE_OP_LAYER_FWD_FP8_BLOCK);
+  const SavedLayout S = saved_layout(d);
+  int32_t* idx = at<int32_t>(saved, S.topk_idx);
+  float* gates = at<float>(saved, S.gates);
+  int32_t* offsets = at<int32_t>(saved, S.offsets);
+  int32_t* psrc = at<int32_t>(saved, S.perm_src);
+  int32_t* pdst = at<int32_t>(saved, S.perm_dst);
+  uint16_t* O = at<uint16_t>(saved, S.O);
+  uint8_t *Xq = at<uint8_t>(ws, L.Xq), *Hq = at<uint8_t>(ws, L.Hq);
+  float *sx = at<float>(ws, L.sx), *sh = at<float>(ws, L.sh);
+  const long long R = static_cast<long long>(rows_of(d));
+  if ((st = do_route(d, x, Wg, b, idx, gates, ws, L, stream)) != MOE_OK) return st;
+  if ((st = do_dispatch(d, selection(d, 0, d.E), idx, at<int32_t>(saved, S.counts), offsets, psrc,
+                        pdst, ws, L, stream)) != MOE_OK)
+    return st;
+  // the rows' codes for FC1 and, in the same pass, the bf16 rows of the weight gradients
+  MOE_RUN(moe::launch_quant_rows_block(x, psrc, d.k, R, d.T, d.h, Xq, sx, num_sms(), stream,
+                                       offsets + d.E, at<uint16_t>(saved, S.x_perm),
+                                       at<int>(ws, 0)),
+          "permute_quant_x_block");
+  if (R > 0) {
+    const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms()};
+    MOE_RUN(moe::block_fc1_fwd(r, {Xq, sx}, {W1q, s1}, {W3q, s3}, d.h, d.f,
+                               at<uint16_t>(saved, S.A), at<uint16_t>(saved, S.B),
+                               at<uint16_t>(saved, S.H), Hq, sh, stream),
+            "block_fc1_fwd");
+    MOE_RUN(moe::block_product(r, {Hq, sh}, {W2q, s2}, d.f, d.h, false, false, O, stream),
+            "block_fc2_fwd");
+  }
+  MOE_RUN(moe::launch_combine(O, gates, pdst, d.T, d.k, d.h, y, num_sms(), stream,
+                              at<int>(ws, 0)),
+          "combine");
+  return MOE_OK;
+}
+
+moe_status moe_layer_bwd_fp8_block(const moe_dims* dims, const moe_bf16* x, const moe_bf16* dy,
+                                   const float* Wg, const uint8_t* W1q, const float* s1,
+                                   const uint8_t* W3q, const float* s3, const uint8_t* W2q,
+                                   const float* s2, const void* saved, moe_bf16* dx, float* dWg,
+                                   float* dW1, float* dW3, float* dW2, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream_) {
+  moe_status st = check_dims(dims, true);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (d.sar) return MOE_ERR_UNSUPPORTED;
+  const size_t T = d.T;
+  if (!buf_ok(x, T) || !buf_ok(dy, T) || !ptr_ok(Wg) || !ptr_ok(W1q) || !ptr_ok(s1) ||
+      !ptr_ok(W3q) || !ptr_ok(s3) || !ptr_ok(W2q) || !ptr_ok(s2) || !saved ||
+      !aligned(saved, kAlign) || !buf_ok(dx, T) || !ptr_ok(dWg) || !ptr_ok(dW1) || !ptr_ok(dW3) ||
+      !ptr_ok(dW2))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = ws_check(d, MOE_OP_LAYER_BWD_FP8_BLOCK, ws, ws_bytes)) != MOE_OK) return st;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const WsLayout L = ws_layout(d, MOE_OP_LAYER_BWD_FP8_BLOCK);
+  const SavedLayout S = saved_layout(d);
+  const int32_t* idx = at<int32_t>(saved, S.topk_idx);
+  const float* gates = at<float>(saved, S.gates);
+  const int32_t* offsets = at<int32_t>(saved, S.offsets);
+  const int32_t* psrc = at<int32_t>(saved, S.perm_src);
+  const int32_t* pdst = at<int32_t>(saved, S.perm_dst);
+  uint16_t *dO = at<uint16_t>(ws, L.dO), *dA = at<uint16_t>(ws, L.dA), *dB = at<uint16_t>(ws, L.dB);
+  uint8_t *dOq = at<uint8_t>(ws, L.dOq), *dAq = at<uint8_t>(ws, L.dAq),
+          *dBq = at<uint8_t>(ws, L.dBq);
+  float *sdo = at<float>(ws, L.sdo), *sda = at<float>(ws, L.sda), *sdb = at<float>(ws, L.sdb);
+  float* dX = at<float>(ws, L.dX);
+  float* dg = at<float>(ws, L.dg);
+  const long long R = static_cast<long long>(rows_of(d));
+  const int32_t* nvalid = offsets + d.E;
+  MOE_RUN(moe::launch_bwd_prep(dy, at<uint16_t>(saved, S.O), gates, psrc, R, d.k, d.h, dO, dg,
+                               num_sms(), stream, nvalid, at<int>(ws, 0)),
+          "bwd_prep");
+  if (R == 0) {
+    const size_t wbytes = static_cast<size_t>(d.E) * d.h * d.f * 4;
+    MOE_RUN(cudaMemsetAsync(dW1, 0, wbytes, stream), "zero_dW1");
+    MOE_RUN(cudaMemsetAsync(dW3, 0, wbytes, stream), "zero_dW3");
+    MOE_RUN(cudaMemsetAsync(dW2, 0, wbytes, stream), "zero_dW2");
+  } else {
+    const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms()};
+    MOE_RUN(moe::launch_quant_rows_block(dO, nullptr, 1, R, R, d.h, dOq, sdo, num_sms(), stream,
+                                         nvalid, nullptr, at<int>(ws, 0)),
+            "quant_dO_block");
+    MOE_RUN(moe::block_fc2_dgrad(r, {dOq, sdo}, {W2q, s2}, d.h, d.f, at<uint16_t>(saved, S.A),
+                                 at<uint16_t>(saved, S.B), dA, dB, dAq, sda, dBq, sdb, stream),
+            "block_fc2_dgrad");
+    MOE_RUN(moe::block_fc1_dgrad(r, {dAq, sda}, {dBq, sdb}, {W1q, s1}, {W3q, s3}, d.h, d.f, true,
+                                 dX, stream),
+            "block_fc1_dgrad");
+    const GemmProblem g = problem(d, offsets, ws);
+    MOE_RUN(moe::gemm_fc2_wgrad(g, at<uint16_t>(saved, S.H), dO, dW2, stream),
+            moe::kGemmNames[4]);
     MOE_RUN(moe::gemm_fc1_wgrad(g, at<uint16_t>(saved, S.x_perm), dA, dB, dW1, dW3, stream),
             moe::kGemmNames[5]);
   }

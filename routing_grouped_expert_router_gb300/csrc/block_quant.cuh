@@ -1,0 +1,59 @@
+// block_quant.cuh -- how a value becomes an e4m3 code under its block's scale,
+// shared by the quantisers and by the epilogues of the grouped products.
+#pragma once
+#include <cstdint>
+#include <cuda_fp8.h>
+
+namespace moe {
+
+constexpr float kCodeMax = 448.0f;  // the largest e4m3 value
+
+// A block's scale and what dividing by it takes.  `top` is the bit pattern of
+// the largest |v|: patterns of non-negative floats order as their values do,
+// with infinity and NaN above all of them, so an integer maximum keeps a NaN.
+struct BlockScale {
+  float s;     // amax / 448, 1 for a block of zeros
+  float r;     // its reciprocal, correctly rounded
+  bool plain;  // s lies where the quick quotient below is exact
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t top) {
+  BlockScale b;
+  b.s = top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top), kCodeMax);
+  b.r = __frcp_rn(b.s);
+  b.plain = b.s > 7.9e-31f && b.s < 1.2e30f;  // 2^-100 .. 2^100
+  return b;
+}
+
+// The float32 quotient v / s, rounded as IEEE division rounds it.  With r the
+// correctly rounded reciprocal of s, q0 = v r is within an ulp of the quotient,
+// the residual v - q0 s is exact in one fused multiply-add, and one more gives
+// the correctly rounded quotient (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990).
+// That holds while nothing leaves the normal range: for scales of 2^-100 to
+// 2^100 a residual that does belongs to a quotient far below the least code,
+// 2^-9.  Other scales (and those that are not finite) take the division.
+__device__ __forceinline__ float block_quotient(float v, const BlockScale& b) {
+  const float q0 = v * b.r;
+  return fmaf(fmaf(-q0, b.s, v), b.r, q0);
+}
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+  return static_cast<uint32_t>(
+      __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
+}
+// Four values -> four codes, the first in the low byte.
+__device__ __forceinline__ uint32_t codes4(const float (&v)[4], const BlockScale& b) {
+  if (b.plain)
+    return codes2(block_quotient(v[0], b), block_quotient(v[1], b)) |
+           (codes2(block_quotient(v[2], b), block_quotient(v[3], b)) << 16);
+  return codes2(__fdiv_rn(v[0], b.s), __fdiv_rn(v[1], b.s)) |
+         (codes2(__fdiv_rn(v[2], b.s), __fdiv_rn(v[3], b.s)) << 16);
+}
+
+// The larger magnitude's bit pattern of the two bf16 in w and of top.
+__device__ __forceinline__ uint32_t top_of_pair(uint32_t top, uint32_t w) {
+  const uint32_t hi = w & 0x7FFF0000u;
+  const uint32_t lo = (w << 16) & 0x7FFF0000u;
+  return max(top, max(hi, lo));
+}
+
+}  // namespace moe

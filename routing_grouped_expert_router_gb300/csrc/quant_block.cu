@@ -1,0 +1,201 @@
+// quant_block.cu -- e4m3 codes with a float32 scale for each block of 128: rows
+// in 1 x 128 blocks, weights in 128 x 128 blocks.  s = amax / 448 (1 for zeros),
+// q = e4m3(v / s); the quotient is the IEEE one (block_quant.cuh).
+//
+// Both read their input once: a block's values wait in registers for its
+// maximum.  HBM bounds them: 3 bytes an element and the scales.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/moe.h"
+#include "api_internal.h"
+#include "block.cuh"
+#include "block_quant.cuh"
+#include "kernels.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kRowThreads = 256;
+constexpr int kRowAhead = 4;  // 16-byte loads a lane has under way
+
+__device__ __forceinline__ void codes8(const uint4& w, const BlockScale& b, uint2& out) {
+  const float lo[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+  const float hi[4] = {__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xFFFF0000u),
+                       __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xFFFF0000u)};
+  out = make_uint2(codes4(lo, b), codes4(hi, b));
+}
+__device__ __forceinline__ uint32_t top8(const uint4& w) {
+  return top_of_pair(top_of_pair(top_of_pair(top_of_pair(0, w.x), w.y), w.z), w.w);
+}
+
+// A warp takes a row's blocks two at a time, 16 lanes of 8 values to a block,
+// with kRowAhead such pairs under way.  blockIdx.y splits a row's pairs where
+// there are too few rows to fill the GPU.
+__global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
+    const uint4* __restrict__ in, const int32_t* __restrict__ idx, int div, long long rows,
+    long long src_rows, const int32_t* __restrict__ nvalid, int n8, int pairs, int pairs_each,
+    uint2* __restrict__ q, float* __restrict__ scale, uint4* __restrict__ copy,
+    int* __restrict__ status) {
+  const int lane = threadIdx.x & 31;
+  const long long warp0 = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
+  const long long warps = (static_cast<long long>(gridDim.x) * kRowThreads) >> 5;
+  const long long ld = rows;  // of the scales
+  long long last = rows;
+  if (nvalid) {
+    const long long nv = __ldg(nvalid);
+    last = nv < rows ? nv : rows;
+  }
+  const int first_pair = blockIdx.y * pairs_each;
+  const int end_pair = min(first_pair + pairs_each, pairs);
+  for (long long p = warp0; p < last; p += warps) {
+    long long src = p;
+    if (idx) {
+      const int32_t a = __ldg(idx + p);
+      src = a < 0 ? -1 : a / div;
+    }
+    const bool bad = src < 0 || src >= src_rows;
+    if (bad && lane == 0 && blockIdx.y == 0) report_bad_index(status);
+    const uint4* from = in + (bad ? 0 : src) * n8;
+    for (int j0 = first_pair; j0 < end_pair; j0 += kRowAhead) {
+      uint4 w[kRowAhead];
+#pragma unroll
+      for (int i = 0; i < kRowAhead; ++i) {
+        const int c = (j0 + i) * 32 + lane;
+        w[i] = (!bad && j0 + i < end_pair && c < n8) ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kRowAhead; ++i) {
+        if (j0 + i >= end_pair) break;  // the same for the whole warp
+        const int c = (j0 + i) * 32 + lane;
+        uint32_t top = top8(w[i]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+        const BlockScale b = block_scale(top);
+        if (c >= n8) continue;
+        uint2 codes;
+        codes8(w[i], b, codes);
+        q[p * n8 + c] = codes;
+        if (copy) copy[p * n8 + c] = w[i];
+        if ((lane & 15) == 0) scale[static_cast<long long>(c >> 4) * ld + p] = b.s;
+      }
+    }
+  }
+}
+
+// One 128 x 128 block of one weight to a block of 256 threads: 16 lanes along a
+// row's 128 values, 16 rows at a time, eight 16-byte loads a lane under way.
+constexpr int kWeightThreads = 256;
+__global__ void __launch_bounds__(kWeightThreads) quant_weights_block_kernel(
+    const uint4* __restrict__ W, int K, int n8, int kb, int nb, uint2* __restrict__ q,
+    float* __restrict__ scale) {
+  __shared__ uint32_t tops[kWeightThreads / 32];
+  const long long tile = blockIdx.x;
+  const int jn = static_cast<int>(tile % nb);
+  const long long ek = tile / nb;
+  const int jk = static_cast<int>(ek % kb);
+  const long long e = ek / kb;
+  const int c = jn * 16 + (threadIdx.x & 15);
+  const int r0 = jk * kBlock + (threadIdx.x >> 4);
+  const long long base = (e * K + r0) * n8 + c;
+  uint4 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] = (c < n8 && r0 + 16 * i < K) ? __ldg(W + base + 16ll * i * n8) : make_uint4(0, 0, 0, 0);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, top8(w[i]));
+  top = __reduce_max_sync(kFull, top);
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWeightThreads / 32; ++i) top = max(top, tops[i]);
+  const BlockScale b = block_scale(top);
+  if (threadIdx.x == 0) scale[tile] = b.s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c < n8 && r0 + 16 * i < K) {
+      uint2 codes;
+      codes8(w[i], b, codes);
+      q[base + 16ll * i * n8] = codes;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_quant_rows_block(const uint16_t* in, const int32_t* idx, int div,
+                                    long long rows, long long src_rows, int n, uint8_t* q,
+                                    float* scale, int num_sms, cudaStream_t s,
+                                    const int32_t* nvalid, uint16_t* copy, int* status) {
+  if (rows == 0) return cudaSuccess;
+  const int pairs = (n + 2 * kBlock - 1) / (2 * kBlock);
+  const long long row_blocks = (rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
+  const long long cap = 8ll * num_sms;
+  const int gx = static_cast<int>(row_blocks < cap ? row_blocks : cap);
+  // a row's pairs over several blocks while the rows alone do not fill the SMs
+  int split = static_cast<int>((cap + gx - 1) / gx);
+  const int most = (pairs + kRowAhead - 1) / kRowAhead;
+  if (split > most) split = most;
+  const int each = (pairs + split - 1) / split;
+  const dim3 grid(gx, (pairs + each - 1) / each, 1);
+  quant_rows_block_kernel<<<grid, kRowThreads, 0, s>>>(
+      reinterpret_cast<const uint4*>(in), idx, idx ? div : 1, rows, src_rows, nvalid, n / 8, pairs,
+      each, reinterpret_cast<uint2*>(q), scale, reinterpret_cast<uint4*>(copy), status);
+  return launched();
+}
+
+cudaError_t launch_quant_weights_block(const uint16_t* W, int E, int K, int N, uint8_t* q,
+                                       float* scale, cudaStream_t s) {
+  const int kb = blocks_of(K), nb = blocks_of(N);
+  const long long tiles = static_cast<long long>(E) * kb * nb;
+  quant_weights_block_kernel<<<static_cast<unsigned>(tiles), kWeightThreads, 0, s>>>(
+      reinterpret_cast<const uint4*>(W), K, N / 8, kb, nb, reinterpret_cast<uint2*>(q), scale);
+  return launched();
+}
+
+}  // namespace moe
+
+// =================================================================== C ABI
+namespace {
+bool ptr_ok(const void* p) { return p && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+}  // namespace
+
+extern "C" {
+
+moe_status moe_quantize_rows_fp8_block(const moe_bf16* in, int64_t rows, int32_t n,
+                                       const int32_t* idx, int32_t div, int64_t src_rows,
+                                       uint8_t* q, float* scale, moe_stream_t stream) {
+  if (rows < 0 || src_rows < 0 || n <= 0 || n % 16 != 0 || (idx && div <= 0))
+    return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!ptr_ok(in) || !ptr_ok(q) || !ptr_ok(scale) || (idx && !ptr_ok(idx))))
+    return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && !idx && src_rows < rows) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  int* status = moe::nows_status_word();
+  if (!status) return MOE_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (moe::launch_quant_rows_block(in, idx, div, rows, src_rows, n, q, scale, moe_api::num_sms(),
+                                   s, nullptr, nullptr, status) != cudaSuccess ||
+      !moe_api::note(s, "quant_rows_block"))
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+moe_status moe_quantize_weights_fp8_block(const moe_bf16* W, int32_t E, int32_t K, int32_t N,
+                                          uint8_t* q, float* scale, moe_stream_t stream) {
+  if (E <= 0 || K <= 0 || N <= 0 || K % 16 != 0 || N % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (static_cast<double>(E) * moe::blocks_of(K) * moe::blocks_of(N) > 2147483647.0)
+    return MOE_ERR_UNSUPPORTED;
+  if (!ptr_ok(W) || !ptr_ok(q) || !ptr_ok(scale)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (moe::launch_quant_weights_block(W, E, K, N, q, scale, s) != cudaSuccess ||
+      !moe_api::note(s, "quant_weights_block"))
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+}  // extern "C"
