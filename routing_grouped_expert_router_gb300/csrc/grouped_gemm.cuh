@@ -88,6 +88,13 @@ bool make_map_columns(CUtensorMap* m, const void* base, uint64_t inner, uint64_t
 //   128 bytes x box_rows that do not run into the next expert.
 bool make_map_codes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t experts, uint32_t box_rows);
+//   Rows for an epilogue's copies: [rows, inner] bf16 (or fp32), boxes of 128
+//   bytes x 32 rows, 128-byte swizzle.
+bool make_map_box(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t rows);
+
+// Clusters of two CTAs of `kern` (launch settings cfg) that the current device
+// holds at once: a persistent grid's size.
+int pairs_that_fit(const void* kern, const cudaLaunchConfig_t& cfg, int num_sms);
 
 // Kernel names, in launch order of a layer, for the measurement hook.
 extern const char* const kGemmNames[6];
