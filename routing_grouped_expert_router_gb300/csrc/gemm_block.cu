@@ -11,9 +11,13 @@
 // times the row's and the column block's scale, and add them to sums in
 // registers, 64 x 2 for each of 256 threads, while the tensor cores work on the
 // next block in another accumulator.  Roles of a CTA's 384 threads:
-//   warp 0      TMA producer: 128 rows of A and 128 columns of B a stage
+//   warps 0, 2  TMA producers of A (128 rows a stage) and B (128 columns a stage)
 //   warp 1      tensor memory; in the even CTA the MMA issuer of the pair
-//   warps 2-3   none: registers are dealt out by groups of four warps
+//   warp 3      scales: places the tiles and copies each block's 128 row scales and
+//               its columns' into a ring of slots, up to SLOTS blocks ahead (the way
+//               through a busy L2 takes some 2000 cycles, four blocks; loaded two
+//               blocks ahead into the sum warps' registers they held those up for
+//               700 cycles every two blocks: 285 us for 16384 x 4096 x 4864)
 //   warps 4-11  the sums (warp w: TMEM lanes 32 (w mod 4), columns 64 ((w-4)/4)
 //               of each half) and, at a tile's end, its epilogue
 // The weight's square blocks let both uses of a weight, as it is (MN-major B)
@@ -41,12 +45,14 @@ constexpr int kTimeoutCode = 5;   // MOE_ERR_DEVICE_TIMEOUT
 constexpr int MAX_E = 64;
 constexpr int PM = 256;           // rows of a pair's tile
 constexpr int NUM_THREADS = 384;
-// Registers of a thread: 168 at launch (3 x 168 x 128 = 64512), then 72 for warps 0-3 and
-// 216 for the others, 504 x 128 again.
-constexpr int FEW_REGS = 72, MANY_REGS = 216;
+// Registers of a thread: 168 at launch (3 x 168 x 128 = 64512), then 56 for warps 0-3 and
+// 224 for the others, 504 x 128 again.
+constexpr int FEW_REGS = 56, MANY_REGS = 224;
 constexpr int FIRST_SUM_WARP = 4;
 constexpr int SUM_WARPS = 8;
-constexpr int SET_BYTES = 4096;   // 32 rows x 128 bytes: one copy of an epilogue
+constexpr int LOAD_A = 0, ISSUE = 1, LOAD_B = 2, SCALES = 3;  // warps
+constexpr int SET_BYTES = 2048;   // 32 rows x 64 bytes: one copy of an epilogue
+constexpr int SLOTS = 8;          // blocks whose scales wait for the sums
 
 struct Params {
   int E;
@@ -69,40 +75,52 @@ struct Params {
 
 struct Maps {
   CUtensorMap a[2], b[2];
-  CUtensorMap o[3];   // outputs, 128-byte boxes of 32 rows
+  CUtensorMap o[3];   // outputs, boxes of 64 bytes x 32 rows
+  CUtensorMap c[1];   // GATED: H's codes
   CUtensorMap i[2];   // GATED_BWD: A and B
 };
 
+// A pair's tile: NH halves of 128 columns, the even CTA loading the first, the odd the
+// second (NH = 1: 64 columns each).
 template <int FORM>
 struct Shape {
-  static constexpr int NH = FORM == GATED_BWD ? 1 : 2;  // halves of 128 columns
-  static constexpr int COLS = 128 * NH;                 // accumulator columns
+  static constexpr int NH = FORM == GATED_BWD ? 1 : 2;
+  static constexpr int COLS = 128 * NH;
   static constexpr int OUT_COLS = FORM == GATED ? 128 : COLS;  // output columns of a tile
   static constexpr int B_COLS = COLS / 2;               // B columns a CTA loads
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_COLS * 128;
   static constexpr int STAGES = NH == 2 ? 5 : 6;
   static constexpr int BUFS = 512 / COLS;               // accumulators in tensor memory
+  static constexpr int SETS = FORM == GATED_BWD ? 4 : 3;  // of a warp
   static constexpr int TOPS = FORM == GATED ? 1 : FORM == GATED_BWD ? 2 : 0;
 };
 
+// One block's scales, with the place of its tile.
+struct Slot {
+  float a[128];
+  float b[2];
+  int nb, row0, row_end;   // nb < 0: no more tiles
+};
 template <int FORM>
 struct alignas(8) Ctrl {
   using S = Shape<FORM>;
   uint64_t full[S::STAGES], empty[S::STAGES];
   uint64_t tfull[S::BUFS], tempty[S::BUFS];
-  uint64_t ab[SUM_WARPS];   // GATED_BWD: A and B in a warp's two sets
+  uint64_t sfull[SLOTS], sempty[SLOTS];
+  uint64_t ab[SUM_WARPS];   // GATED_BWD: A and B in a warp's sets
+  uint64_t met;             // the sum warps, once for each tile (TOPS)
   uint64_t drain;
   uint32_t tmem_base;
-  int abort;
   int off[MAX_E + 1];
   int cum[MAX_E + 1];       // row tiles before each group
-  uint16_t tops[S::TOPS ? 2 * S::TOPS * 256 : 1];  // bf16 patterns [tile parity][value][warps' half][row]
+  Slot slots[SLOTS];
+  uint16_t tops[S::TOPS ? 2 * S::TOPS * 256 : 1];  // bf16 patterns [tile parity][value][side][row]
 };
 template <int FORM>
 constexpr int smem_bytes() {
-  return 1024 + Shape<FORM>::STAGES * Shape<FORM>::STAGE_BYTES + SUM_WARPS * 2 * SET_BYTES +
-         static_cast<int>(sizeof(Ctrl<FORM>));
+  return 1024 + Shape<FORM>::STAGES * Shape<FORM>::STAGE_BYTES +
+         SUM_WARPS * Shape<FORM>::SETS * SET_BYTES + static_cast<int>(sizeof(Ctrl<FORM>));
 }
 static_assert(smem_bytes<PLAIN_BF16>() <= 232448 && smem_bytes<GATED>() <= 232448 &&
                   smem_bytes<GATED_BWD>() <= 232448,
@@ -143,84 +161,44 @@ __device__ __forceinline__ bool place(const Params& p, const int* off, const int
   return true;
 }
 
-// This thread's scales of one block: its row's, and those of the halves' columns.
-struct Scales {
-  float a, b[2];
-};
-// Walks the blocks of a CTA's tiles ahead of the sums.
-template <int FORM>
-struct ScaleWalk {
-  const float* a;
-  const float* b[2];
-  int kb, t;
-  bool real, row_ok;
-  __device__ __forceinline__ void enter(const Params& p, const int* off, const int* cum,
-                                        int row_in_tile) {
-    Tile tl;
-    real = place<FORM>(p, off, cum, t, tl);
-    kb = 0;
-    if (!real) return;
-    const int row = tl.row0 + row_in_tile;
-    row_ok = row < tl.row_end;
-    point(p, tl.e, tl.nb, row, 0);
-    e_ = tl.e;
-    nb_ = tl.nb;
-    row_ = row;
-  }
-  __device__ __forceinline__ void point(const Params& p, int e, int nb, int row, int product) {
-    a = p.sa[product] + (row_ok ? row : 0);
-    if (FORM == GATED) {
-      for (int i = 0; i < 2; ++i)
-        b[i] = p.sb[i] + static_cast<size_t>(e) * p.sb_group + static_cast<size_t>(nb) * p.sb_n;
-    } else {
-#pragma unroll
-      for (int i = 0; i < Shape<FORM>::NH; ++i) {
-        const int n = min(Shape<FORM>::NH * nb + i, p.nblocks - 1);  // past the last: zeros anyway
-        b[i] = p.sb[product] + static_cast<size_t>(e) * p.sb_group + static_cast<size_t>(n) * p.sb_n;
-      }
-    }
-  }
-  __device__ __forceinline__ Scales next(const Params& p, const int* off, const int* cum,
-                                         int row_in_tile, int step) {
-    Scales s = {0.f, {0.f, 0.f}};
-    if (!real) return s;
-    if (row_ok) s.a = __ldg(a);
-#pragma unroll
-    for (int i = 0; i < Shape<FORM>::NH; ++i) s.b[i] = __ldg(b[i]);
-    ++kb;
-    a += p.rows;
-#pragma unroll
-    for (int i = 0; i < Shape<FORM>::NH; ++i) b[i] += p.sb_k;
-    if (kb == p.kblocks && p.products == 2) point(p, e_, nb_, row_, 1);
-    if (kb == p.kblocks * p.products) {
-      t += step;
-      enter(p, off, cum, row_in_tile);
-    }
-    return s;
-  }
-  int e_, nb_, row_;
-};
-
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
+// 32 columns of this thread's TMEM lane: asked for here, there after tmem_wait().
+__device__ __forceinline__ void tmem_ask32(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
 }
-__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+// The wait names the registers that the loads fill, so that nothing reads them before.
+__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+        "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+        "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]),
+        "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
+        "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+      :);
+  asm volatile("" : "+f"(v[30]), "+f"(v[31]) : : "memory");
 }
-// sums += scale * (32 columns of this thread's TMEM lane)
-__device__ __forceinline__ void add_block(uint32_t taddr, float scale, uint64_t* sums) {
-  float v[32];
-  tmem_ld32(taddr, v);
-  const uint64_t s2 = pair_of(scale, scale);
+__device__ __forceinline__ void add_32(const float (&v)[32], float scale, float* sums) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    asm("fma.rn.f32x2 %0, %1, %2, %0;"
-        : "+l"(sums[i])
-        : "l"(pair_of(v[2 * i], v[2 * i + 1])), "l"(s2));
+  for (int i = 0; i < 32; ++i) sums[i] = fmaf(v[i], scale, sums[i]);
 }
-
+__device__ __forceinline__ void add_64(uint32_t taddr, float scale, float* sums) {
+#pragma unroll
+  for (int i = 0; i < 64; i += 32) {
+    float v[32];
+    tmem_ask32(taddr + i, v);
+    tmem_wait(v);
+    add_32(v, scale, sums + i);
+  }
+}
 // sigmoid and silu with the fast exponential and quotient: their few ulps are
 // far below the bf16 rounding of all that is stored.
 __device__ __forceinline__ float sigmoid_f(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
@@ -233,19 +211,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// A warp's two 4 KiB sets between its registers and the TMA unit: 32 rows of 128
-// bytes, 16-byte piece j of row i in slot j ^ (i mod 8) (128-byte swizzle).
+// A warp's sets between its registers and the TMA unit: 32 rows of 64 bytes, 16-byte
+// piece j of row i in slot j ^ ((i / 2) mod 4) (64-byte swizzle; no bank conflicts).
+template <int SETS>
 struct Staging {
   uint4* sets;
-  int used = 0;
+  int next = 0;
   // A set whose last copy has been read.
   __device__ __forceinline__ uint4* take(int lane) {
-    uint4* s = sets + (used++ & 1) * (SET_BYTES / 16);
-    if (lane == 0) bulk_wait_read_1();
+    uint4* s = sets + next * (SET_BYTES / 16);
+    if (++next == SETS) next = 0;
+    static_assert(SETS == 3, "the wait goes by the number of sets");
+    if (lane == 0) bulk_wait_read_2();
     __syncwarp();
     return s;
   }
 };
+__device__ __forceinline__ int slot_of(int lane, int j) { return lane * 4 + (j ^ ((lane >> 1) & 3)); }
 __device__ __forceinline__ void send(const CUtensorMap* map, uint4* set, int x, int y, int lane) {
   fence_proxy_async_smem();
   __syncwarp();
@@ -254,41 +236,53 @@ __device__ __forceinline__ void send(const CUtensorMap* map, uint4* set, int x, 
     bulk_commit();
   }
 }
-// 64 columns of bf16 (w: 32 pairs) of a warp's 32 rows to out [., N] at (row, col): whole
-// rows by TMA, or, where a row is not this group's, each lane its own.
-__device__ __forceinline__ void put_bf16(Staging& st, const CUtensorMap* map, void* out, int N,
-                                         const uint32_t* w, int row, int col, bool row_ok,
-                                         bool all_ok, int lane) {
+// 64 bytes (w) of each of a warp's 32 rows to out [., N] (elements of SIZE bytes) at (row,
+// col): whole rows by TMA, or, where a row is not this group's, each lane its own.
+template <int SIZE, int SETS>
+__device__ __forceinline__ void put(Staging<SETS>& st, const CUtensorMap* map, void* out, int N,
+                                    const uint4 (&w)[4], int row, int col, bool row_ok,
+                                    bool all_ok, int lane) {
+  if (col >= N) return;
   if (all_ok) {
     uint4* set = st.take(lane);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      set[lane * 8 + (j ^ (lane & 7))] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    for (int j = 0; j < 4; ++j) set[slot_of(lane, j)] = w[j];
     send(map, set, col, row - lane, lane);
   } else if (row_ok) {
-    uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + static_cast<size_t>(row) * N + col);
+    uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
+                                        (static_cast<size_t>(row) * N + col) * SIZE);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + 8 * j < N) d[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    for (int j = 0; j < 4; ++j)
+      if (col + 16 / SIZE * j < N) d[j] = w[j];
   }
 }
-__device__ __forceinline__ void put_f32(Staging& st, const CUtensorMap* map, void* out, int N,
-                                        const uint64_t* v, int row, int col, bool row_ok,
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                    pack_bf16(f[6], f[7]));
+}
+// 64 columns of fp32 as bf16.
+template <int SETS>
+__device__ __forceinline__ void put_bf16(Staging<SETS>& st, const CUtensorMap* map, void* out,
+                                         int N, const float* f, int row, int col, bool row_ok,
+                                         bool all_ok, int lane) {
+#pragma unroll
+  for (int i = 0; i < 64; i += 32) {
+    const uint4 w[4] = {pack8(f + i), pack8(f + i + 8), pack8(f + i + 16), pack8(f + i + 24)};
+    put<2>(st, map, out, N, w, row, col + i, row_ok, all_ok, lane);
+  }
+}
+template <int SETS>
+__device__ __forceinline__ void put_f32(Staging<SETS>& st, const CUtensorMap* map, void* out,
+                                        int N, const float* f, int row, int col, bool row_ok,
                                         bool all_ok, int lane) {
-  float f[32];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) split(v[i], f[2 * i], f[2 * i + 1]);
-  if (all_ok) {
-    float4* set = reinterpret_cast<float4*>(st.take(lane));
+  for (int i = 0; i < 64; i += 16) {
+    uint4 w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      set[lane * 8 + (j ^ (lane & 7))] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-    send(map, reinterpret_cast<uint4*>(set), col, row - lane, lane);
-  } else if (row_ok) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + static_cast<size_t>(row) * N + col);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + 4 * j < N) d[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+    for (int j = 0; j < 4; ++j)
+      w[j] = make_uint4(__float_as_uint(f[i + 4 * j]), __float_as_uint(f[i + 4 * j + 1]),
+                        __float_as_uint(f[i + 4 * j + 2]), __float_as_uint(f[i + 4 * j + 3]));
+    put<4>(st, map, out, N, w, row, col + i, row_ok, all_ok, lane);
   }
 }
 // 16 codes of eight bf16 pairs.
@@ -302,8 +296,38 @@ __device__ __forceinline__ uint4 codes16(const uint32_t* w, const BlockScale& b)
   return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-__device__ __forceinline__ void sum_warps_sync() {
-  asm volatile("bar.sync 1, 256;" ::: "memory");
+// An asynchronous copy of four bytes (of zero, where `real` is not set).
+__device__ __forceinline__ void copy_4(float* dst, const float* src, bool real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(real ? 4 : 0)
+               : "memory");
+}
+// Arrives on `bar` once this thread's copies so far are there.
+__device__ __forceinline__ void arrive_copied(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The pair's MMA on descriptors given by their low words; the high word (1024 bytes between
+// groups of eight rows, version, 128-byte swizzle) is the same for all.
+__device__ __forceinline__ void umma2_e4m3_at(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                              uint32_t idesc, uint32_t accumulate) {
+  constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI)
+      : "memory");
+}
+
+// A whole warp's wait: true for all lanes or for none.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, int* status) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  ok = mbar_wait(bar, parity, status, kTimeoutCode);
+  return __all_sync(0xffffffffu, ok);
 }
 
 template <int FORM, bool B_MN>
@@ -314,7 +338,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* staging = smem + S::STAGES * S::STAGE_BYTES;
-  Ctrl<FORM>& c = *reinterpret_cast<Ctrl<FORM>*>(staging + SUM_WARPS * 2 * SET_BYTES);
+  Ctrl<FORM>& c = *reinterpret_cast<Ctrl<FORM>*>(staging + SUM_WARPS * S::SETS * SET_BYTES);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -325,21 +349,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // ------------------------------------------------------------ set-up
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < S::STAGES; ++s) {
-      mbar_init(smem_u32(&c.full[s]), 1);
+      mbar_init(smem_u32(&c.full[s]), 2);  // the producers of A and of B
       mbar_init(smem_u32(&c.empty[s]), 1);
     }
     for (int b = 0; b < S::BUFS; ++b) {
       mbar_init(smem_u32(&c.tfull[b]), 1);
       mbar_init(smem_u32(&c.tempty[b]), 2 * SUM_WARPS);
     }
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(smem_u32(&c.sfull[i]), 33);  // 32 lanes' copies, and the tile's place
+      mbar_init(smem_u32(&c.sempty[i]), SUM_WARPS);
+    }
     for (int w = 0; w < SUM_WARPS; ++w) mbar_init(smem_u32(&c.ab[w]), 1);
+    mbar_init(smem_u32(&c.met), SUM_WARPS);
     mbar_init(smem_u32(&c.drain), 1);
-    c.abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.a[0]);
     tma_prefetch_desc(&maps.b[0]);
   }
-  if (warp == 1) {
+  if (warp == ISSUE) {
     tmem_alloc2(smem_u32(&c.tmem_base), 512);
     tmem_relinquish2();
     tc_fence_before();
@@ -364,261 +392,294 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   cluster_sync_all();  // both CTAs' barriers exist before any arrival from the other
   tc_fence_after();
-  const uint32_t tmem_base = c.tmem_base;
-  volatile int* abort_flag = &c.abort;
-  const uint32_t peer_abort = mapa_shared(smem_u32(&c.abort), rank ^ 1u);
-  auto give_up = [&]() {
-    *abort_flag = 1;
-    st_cluster_u32(peer_abort, 1);
-  };
-
+  constexpr uint32_t tmem_base = 0;  // all 512 columns are this block's
+  // Every wait below is bounded: a role whose wait runs out records it and ends, and those
+  // that wait for it do the same.
   if (warp < FIRST_SUM_WARP) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW_REGS));
-  if (warp == 0) {
-    // ------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int q = 0;
-      bool ok = true;
-      Tile tl;
-      for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
-        for (int kb = 0; kb < nkb; ++kb, ++q) {
-          const int s = q % S::STAGES;
-          const uint32_t ph = (q / S::STAGES) & 1;
-          if (*abort_flag || !mbar_wait(smem_u32(&c.empty[s]), ph ^ 1, p.status, kTimeoutCode)) {
-            give_up();
-            ok = false;
-            break;
-          }
+  if (warp == LOAD_A || warp == LOAD_B) {
+    // ------------------------------------------------------ TMA producers
+    const bool is_a = warp == LOAD_A;
+    const bool one = elect_one();
+    int s = 0, asked = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    Tile tl;
+    for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
+      const int e = __shfl_sync(0xffffffffu, tl.e, 0);
+      const int at = __shfl_sync(0xffffffffu,
+                                 is_a ? tl.row0 + rank * 128
+                                      : (FORM == GATED ? tl.nb * 128
+                                                       : tl.nb * S::COLS + rank * S::B_COLS),
+                                 0);
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = wait_all(smem_u32(&c.empty[s]), ph, p.status);
+        if (!ok) break;
+        const int which = kb >= p.kblocks ? 1 : 0;
+        const int k = (which ? kb - p.kblocks : kb) * kBlock;
+        if (one) {
           // the even CTA's barrier counts both CTAs' bytes
           const uint32_t own = smem_u32(&c.full[s]);
-          const uint32_t bar = rank == 0 ? own : mapa_shared(own, 0);
-          if (rank == 0) mbar_expect_tx(own, 2 * S::STAGE_BYTES);
-          const int which = kb >= p.kblocks ? 1 : 0;
-          const int k = (which ? kb - p.kblocks : kb) * kBlock;
-          const uint32_t a_dst = smem_u32(smem + s * S::STAGE_BYTES);
-          const uint32_t b_dst = a_dst + S::A_BYTES;
-          const CUtensorMap* bm = FORM == GATED ? &maps.b[rank] : &maps.b[which];
-          const int n = FORM == GATED ? tl.nb * 128 : tl.nb * S::COLS + rank * S::B_COLS;
+          const uint32_t dst = smem_u32(smem + s * S::STAGE_BYTES) + (is_a ? 0 : S::A_BYTES);
           if (rank == 0) {
-            tma_load_2d(a_dst, &maps.a[which], k, tl.row0, bar);
-            tma_load_3d(b_dst, bm, B_MN ? n : k, B_MN ? k : n, tl.e, bar);
+            mbar_expect_tx(own, 2 * (is_a ? S::A_BYTES : S::STAGE_BYTES - S::A_BYTES));
+            if (is_a)
+              tma_load_2d(dst, &maps.a[which], k, at, own);
+            else
+              tma_load_3d(dst, FORM == GATED ? &maps.b[0] : &maps.b[which], B_MN ? at : k,
+                          B_MN ? k : at, e, own);
           } else {
-            tma_load_2d_pair(a_dst, &maps.a[which], k, tl.row0 + 128, bar);
-            tma_load_3d_pair(b_dst, bm, B_MN ? n : k, B_MN ? k : n, tl.e, bar);
+            const uint32_t bar = mapa_shared(own, 0);
+            if (is_a)
+              tma_load_2d_pair(dst, &maps.a[which], k, at, bar);
+            else
+              tma_load_3d_pair(dst, FORM == GATED ? &maps.b[1] : &maps.b[which], B_MN ? at : k,
+                               B_MN ? k : at, e, bar);
           }
         }
-      }
-      if (!ok && rank == 0) {
-        // the loads already asked for land before the CTA can end
-        const int first = q > S::STAGES ? q - S::STAGES : 0;
-        for (int r = first; r < q; ++r)
-          mbar_wait_cluster(smem_u32(&c.full[r % S::STAGES]), (r / S::STAGES) & 1, p.status,
-                            kTimeoutCode);
+        __syncwarp();
+        ++asked;
+        if (++s == S::STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
       }
     }
-  } else if (warp == 1) {
+    if (!ok && rank == 0) {
+      // the loads already asked for land before the CTA can end
+      const int first = asked > S::STAGES ? asked - S::STAGES : 0;
+      for (int r = first; r < asked; ++r)
+        mbar_wait_cluster(smem_u32(&c.full[r % S::STAGES]), (r / S::STAGES) & 1, p.status,
+                          kTimeoutCode);
+    }
+  } else if (warp == ISSUE) {
     if (rank == 0) {
       // ----------------------------------------------- MMA issuer (even CTA)
       constexpr uint32_t IDESC = idesc_e4m3(PM, S::COLS) | (B_MN ? 1u << 16 : 0u);
       // 32 deep: 32 bytes of a K-major row; 32 rows of 128 bytes of an MN-major tile
       constexpr uint32_t B_STEP = B_MN ? 32 * 128 : 32;
-      int q = 0;
+      const uint32_t a_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem), 16, 1024));
+      const bool one = elect_one();
+      const int tiles = ((p.N + S::OUT_COLS - 1) / S::OUT_COLS) * c.cum[p.E];
+      const int all = cid < tiles ? ((tiles - cid + ncl - 1) / ncl) * nkb : 0;
+      int left = __shfl_sync(0xffffffffu, all, 0);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, bph = 1;
       bool ok = true;
-      Tile tl;
-      for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
-        for (int kb = 0; kb < nkb; ++kb, ++q) {
-          const int s = q % S::STAGES;
-          const int buf = q % S::BUFS;
-          if (*abort_flag ||
-              !mbar_wait(smem_u32(&c.tempty[buf]), ((q / S::BUFS) & 1) ^ 1, p.status,
-                         kTimeoutCode) ||
-              !mbar_wait(smem_u32(&c.full[s]), (q / S::STAGES) & 1, p.status, kTimeoutCode)) {
-            give_up();
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            tc_fence_after();
-            const uint32_t a_base = smem_u32(smem + s * S::STAGE_BYTES);
-            const uint32_t b_base = a_base + S::A_BYTES;
+      for (; left > 0; --left) {
+        ok = wait_all(smem_u32(&c.full[s]), ph, p.status) &&
+             wait_all(smem_u32(&c.tempty[buf]), bph, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = a_lo + s * (S::STAGE_BYTES >> 4);
+        const uint32_t b = a + (S::A_BYTES >> 4);
+        if (one) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma2_e4m3(tmem_base + buf * S::COLS, smem_desc(a_base + kk * 32, 16, 1024),
-                         smem_desc(b_base + kk * B_STEP, 16, 1024), IDESC, kk != 0);
-            umma2_commit_mc(smem_u32(&c.empty[s]), 0x3);
-            umma2_commit_mc(smem_u32(&c.tfull[buf]), 0x3);
-          }
-          __syncwarp();
+          for (int kk = 0; kk < 4; ++kk)
+            umma2_e4m3_at(tmem_base + buf * S::COLS, a + (kk * 32 >> 4), b + (kk * B_STEP >> 4),
+                          IDESC, kk != 0);
+          umma2_commit_mc(smem_u32(&c.tfull[buf]), 0x3);
+          umma2_commit_mc(smem_u32(&c.empty[s]), 0x3);
+        }
+        __syncwarp();
+        if (++s == S::STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+        if (++buf == S::BUFS) {
+          buf = 0;
+          bph ^= 1;
         }
       }
-      if (lane == 0) {
+      if (one) {
         umma2_commit(smem_u32(&c.drain));
         mbar_wait(smem_u32(&c.drain), 0, p.status, kTimeoutCode);
       }
       __syncwarp();
     }
+  } else if (warp == SCALES) {
+    // ------------------------------------------------------------- scales
+    int i = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    Tile tl = {};
+    auto give = [&](int nb) {  // what a slot says of its tile, and that it is filled
+      if (lane == 0) {
+        c.slots[i].nb = nb;
+        c.slots[i].row0 = tl.row0;
+        c.slots[i].row_end = tl.row_end;
+      }
+      arrive_copied(smem_u32(&c.sfull[i]));
+      if (lane == 0) mbar_arrive(smem_u32(&c.sfull[i]));
+      __syncwarp();
+      if (++i == SLOTS) {
+        i = 0;
+        ph ^= 1;
+      }
+    };
+    for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
+      // indexes fit 32 bits: a scale stands for 128 bytes of codes or more
+      const int row = tl.row0 + rank * 128 + lane;
+      uint32_t base = 0;
+      if (lane < S::NH) {
+        // past the last column block: its products are zeros
+        const int n = FORM == GATED ? tl.nb : min(S::NH * tl.nb + lane, p.nblocks - 1);
+        base = static_cast<uint32_t>(tl.e) * p.sb_group + static_cast<uint32_t>(n) * p.sb_n;
+      }
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = wait_all(smem_u32(&c.sempty[i]), ph, p.status);
+        if (!ok) break;
+        const int product = kb >= p.kblocks ? 1 : 0;
+        const uint32_t k = kb - (product ? p.kblocks : 0);
+        const float* sa = p.sa[product] + k * static_cast<uint32_t>(p.rows);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool real = row + 32 * j < tl.row_end;
+          copy_4(&c.slots[i].a[lane + 32 * j], sa + (real ? row + 32 * j : 0), real);
+        }
+        if (lane < S::NH)
+          copy_4(&c.slots[i].b[lane], p.sb[FORM == GATED ? lane : product] + (base + k * p.sb_k),
+                 true);
+        give(tl.nb);
+      }
+    }
+    if (ok && wait_all(smem_u32(&c.sempty[i]), ph, p.status)) give(-1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MANY_REGS));
     // ------------------------------------------- sums and epilogue (8 warps)
-    const int quarter = warp & 3;                 // TMEM lanes this warp may read
-    const int side = (warp - FIRST_SUM_WARP) >> 2;             // which 64 columns of each half
-    const int trow = quarter * 32 + lane;         // TMEM lane: row of this CTA's 128
-    const int row_in_tile = rank * 128 + trow;
+    const int quarter = warp & 3;                    // TMEM lanes this warp may read
+    const int side = (warp - FIRST_SUM_WARP) >> 2;   // which 64 columns of each half
+    const int trow = quarter * 32 + lane;            // TMEM lane: row of this CTA's 128
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    Staging st;
-    st.sets = reinterpret_cast<uint4*>(staging + (warp - FIRST_SUM_WARP) * 2 * SET_BYTES);
-    int q = 0, it = 0;
-    Tile tl;
-    ScaleWalk<FORM> walk;
-    walk.t = cid;
-    walk.enter(p, c.off, c.cum, row_in_tile);
-    // two blocks ahead: a load's way to L2 and back
-    Scales s0 = walk.next(p, c.off, c.cum, row_in_tile, ncl);
-    Scales s1 = walk.next(p, c.off, c.cum, row_in_tile, ncl);
+    Staging<S::SETS> st;
+    st.sets = reinterpret_cast<uint4*>(staging + (warp - FIRST_SUM_WARP) * S::SETS * SET_BYTES);
+    int it = 0, i = 0, buf = 0;
+    uint32_t iph = 0, bph = 0;
     int asked = 0, had = 0;  // GATED_BWD: loads of A and B into the sets, and those that landed
     bool ok = true;
-    // After an abort the forms that meet at a barrier for each tile go on meeting there.
-    for (int t = cid; (ok || S::TOPS) && place<FORM>(p, c.off, c.cum, t, tl); t += ncl, ++it) {
-      const int row = tl.row0 + row_in_tile;
-      const bool row_ok = row < tl.row_end;
+    for (;; ++it) {
+      ok = wait_all(smem_u32(&c.sfull[i]), iph, p.status);
+      if (!ok) break;
+      const int nb = c.slots[i].nb;
+      if (nb < 0) break;
+      const int row = c.slots[i].row0 + rank * 128 + trow;
+      const bool row_ok = row < c.slots[i].row_end;
       const bool all_ok = __all_sync(0xffffffffu, row_ok);
-      const int col0 = tl.nb * S::OUT_COLS + side * 64;
+      const int col0 = nb * S::OUT_COLS + side * 64;
       if constexpr (FORM == GATED_BWD) {
         // this warp's rows and columns of A and B come while the sums run
-        if (ok && col0 < p.N) {
+        if (col0 < p.N) {
           fence_proxy_async_smem();  // the reads of the sets come before the refill
           __syncwarp();
           ++asked;
           if (lane == 0) {
             bulk_wait_read_0();
-            mbar_expect_tx(smem_u32(&c.ab[warp - FIRST_SUM_WARP]), 2 * SET_BYTES);
-            tma_load_2d(smem_u32(st.sets), &maps.i[0], col0, row - lane, smem_u32(&c.ab[warp - FIRST_SUM_WARP]));
-            tma_load_2d(smem_u32(st.sets + SET_BYTES / 16), &maps.i[1], col0, row - lane,
-                        smem_u32(&c.ab[warp - FIRST_SUM_WARP]));
+            const uint32_t bar = smem_u32(&c.ab[warp - FIRST_SUM_WARP]);
+            mbar_expect_tx(bar, 4 * SET_BYTES);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // A's 64 columns in sets 0 and 1, B's in 2 and 3
+              tma_load_2d(smem_u32(st.sets + j * (SET_BYTES / 16)), &maps.i[j >> 1],
+                          col0 + 32 * (j & 1), row - lane, bar);
           }
         }
       }
-      uint64_t sums[S::NH][32];
+      float sums[S::NH][64];
 #pragma unroll
       for (int h = 0; h < S::NH; ++h)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sums[h][i] = 0;
+        for (int j = 0; j < 64; ++j) sums[h][j] = 0.f;
 #pragma unroll 1
-      for (int kb = 0; ok && kb < nkb; ++kb, ++q) {
-        const Scales s = s0;
-        s0 = s1;
-        s1 = walk.next(p, c.off, c.cum, row_in_tile, ncl);
-        const int buf = q % S::BUFS;
-        const bool got = !*abort_flag &&
-                         mbar_wait(smem_u32(&c.tfull[buf]), (q / S::BUFS) & 1, p.status, kTimeoutCode);
-        if (!__all_sync(0xffffffffu, got)) {
-          give_up();
-          ok = false;
-          continue;
-        }
-        tc_fence_after();
-        const uint32_t at = tmem_base + buf * S::COLS + lanes + side * 64;
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (kb && !(ok = wait_all(smem_u32(&c.sfull[i]), iph, p.status))) break;
+        const float a = c.slots[i].a[trow];
+        float scale[S::NH];
 #pragma unroll
-        for (int h = 0; h < S::NH; ++h) {
-          add_block(at + h * 128, s.a * s.b[h], sums[h]);
-          add_block(at + h * 128 + 32, s.a * s.b[h], sums[h] + 16);
+        for (int h = 0; h < S::NH; ++h) scale[h] = a * c.slots[i].b[h];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.sempty[i]));
+        if (++i == SLOTS) {
+          i = 0;
+          iph ^= 1;
         }
+        if (!(ok = wait_all(smem_u32(&c.tfull[buf]), bph, p.status))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < S::NH; ++h)
+          add_64(tmem_base + buf * S::COLS + lanes + side * 64 + h * 128, scale[h], sums[h]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&c.tempty[buf]), 0));
+        if (++buf == S::BUFS) {
+          buf = 0;
+          bph ^= 1;
+        }
       }
-      if (!ok) {
-        if (S::TOPS) sum_warps_sync();
-        continue;
-      }
+      if (!ok) break;
       if constexpr (FORM == PLAIN_BF16) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int col = col0 + h * 128;
-          if (col >= p.N) continue;
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float lo, hi;
-            split(sums[h][i], lo, hi);
-            w[i] = pack_bf16(lo, hi);
-          }
-          put_bf16(st, &maps.o[0], p.out[0], p.N, w, row, col, row_ok, all_ok, lane);
-        }
+        for (int h = 0; h < 2; ++h)
+          put_bf16(st, &maps.o[0], p.out[0], p.N, sums[h], row, col0 + h * 128, row_ok, all_ok, lane);
       } else if constexpr (FORM == PLAIN_F32) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int col = col0 + h * 128 + i * 32;
-            if (col < p.N)
-              put_f32(st, &maps.o[0], p.out[0], p.N, sums[h] + 16 * i, row, col, row_ok, all_ok, lane);
-          }
+          put_f32(st, &maps.o[0], p.out[0], p.N, sums[h], row, col0 + h * 128, row_ok, all_ok, lane);
       } else if constexpr (FORM == GATED) {
-        uint32_t w[32];
+        if (p.out[0]) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            put_bf16(st, &maps.o[h], p.out[h], p.N, sums[h], row, col0, row_ok, all_ok, lane);
+        }
+        uint32_t w[32];  // H
         uint32_t top = 0;
         if (col0 < p.N) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float a0, a1, b0, b1;
-            split(sums[0][i], a0, a1);
-            split(sums[1][i], b0, b1);
-            w[i] = pack_bf16(silu_f(a0) * b0, silu_f(a1) * b1);
-            top = top_of_pair(top, w[i]);
+          for (int j = 0; j < 32; ++j) {
+            w[j] = pack_bf16(silu_f(sums[0][2 * j]) * sums[1][2 * j],
+                             silu_f(sums[0][2 * j + 1]) * sums[1][2 * j + 1]);
+            top = top_of_pair(top, w[j]);
           }
         }
         uint16_t* tops = c.tops + (it & 1) * 256;
         tops[side * 128 + trow] = static_cast<uint16_t>(top >> 16);
-        sum_warps_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.met));
+        if (p.out[0]) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 h4[4] = {make_uint4(w[16 * j], w[16 * j + 1], w[16 * j + 2], w[16 * j + 3]),
+                                 make_uint4(w[16 * j + 4], w[16 * j + 5], w[16 * j + 6], w[16 * j + 7]),
+                                 make_uint4(w[16 * j + 8], w[16 * j + 9], w[16 * j + 10], w[16 * j + 11]),
+                                 make_uint4(w[16 * j + 12], w[16 * j + 13], w[16 * j + 14], w[16 * j + 15])};
+            put<2>(st, &maps.o[2], p.out[2], p.N, h4, row, col0 + 32 * j, row_ok, all_ok, lane);
+          }
+        }
+        if (!(ok = wait_all(smem_u32(&c.met), it & 1, p.status))) break;
         top = max(top, static_cast<uint32_t>(tops[(side ^ 1) * 128 + trow]) << 16);
         if (col0 < p.N) {
           const BlockScale bs = block_scale(top);
-          if (row_ok) {
-            if (side == 0) p.scales[0][static_cast<size_t>(tl.nb) * p.rows + row] = bs.s;
-            uint4* d = reinterpret_cast<uint4*>(p.codes[0] + static_cast<size_t>(row) * p.N + col0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = codes16(w + 8 * j, bs);
-          }
-          if (p.out[0]) {
-            put_bf16(st, &maps.o[2], p.out[2], p.N, w, row, col0, row_ok, all_ok, lane);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float lo, hi;
-                split(sums[h][i], lo, hi);
-                w[i] = pack_bf16(lo, hi);
-              }
-              put_bf16(st, &maps.o[h], p.out[h], p.N, w, row, col0, row_ok, all_ok, lane);
-            }
-          }
+          if (row_ok && side == 0) p.scales[0][static_cast<size_t>(nb) * p.rows + row] = bs.s;
+          const uint4 q4[4] = {codes16(w, bs), codes16(w + 8, bs), codes16(w + 16, bs), codes16(w + 24, bs)};
+          put<1>(st, &maps.c[0], p.codes[0], p.N, q4, row, col0, row_ok, all_ok, lane);
         }
       } else {
         uint32_t top_a = 0, top_b = 0;
         uint4* sa = st.sets;
-        uint4* sb = st.sets + SET_BYTES / 16;
+        uint4* sb = st.sets + 2 * (SET_BYTES / 16);
         if (col0 < p.N) {
-          const bool got = mbar_wait(smem_u32(&c.ab[warp - FIRST_SUM_WARP]), had & 1, p.status,
-                                     kTimeoutCode);
+          if (!(ok = wait_all(smem_u32(&c.ab[warp - FIRST_SUM_WARP]), had & 1, p.status))) break;
           ++had;
-          if (!__all_sync(0xffffffffu, got)) {
-            give_up();
-            ok = false;
-          }
-        }
-        if (ok && col0 < p.N) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int at = lane * 8 + (j ^ (lane & 7));
+            const int at = (j >> 2) * (SET_BYTES / 16) + slot_of(lane, j & 3);
             const uint4 ra = sa[at], rb = sb[at];
             const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
             uint32_t da[4], db[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float dh[2];
-              split(sums[0][4 * j + i], dh[0], dh[1]);
-              const float av[2] = {lo_of(wa[i]), hi_of(wa[i])}, bv[2] = {lo_of(wb[i]), hi_of(wb[i])};
+            for (int m = 0; m < 4; ++m) {
+              const float* dh = sums[0] + 8 * j + 2 * m;
+              const float av[2] = {lo_of(wa[m]), hi_of(wa[m])}, bv[2] = {lo_of(wb[m]), hi_of(wb[m])};
               float xa[2], xb[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
@@ -626,50 +687,50 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 xa[k] = dh[k] * bv[k] * sg * (1.0f + av[k] * (1.0f - sg));
                 xb[k] = dh[k] * av[k] * sg;
               }
-              da[i] = pack_bf16(xa[0], xa[1]);
-              db[i] = pack_bf16(xb[0], xb[1]);
-              top_a = top_of_pair(top_a, da[i]);
-              top_b = top_of_pair(top_b, db[i]);
+              da[m] = pack_bf16(xa[0], xa[1]);
+              db[m] = pack_bf16(xb[0], xb[1]);
+              top_a = top_of_pair(top_a, da[m]);
+              top_b = top_of_pair(top_b, db[m]);
             }
             sa[at] = make_uint4(da[0], da[1], da[2], da[3]);
             sb[at] = make_uint4(db[0], db[1], db[2], db[3]);
+          }
+          if (all_ok) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              send(&maps.o[j >> 1], st.sets + j * (SET_BYTES / 16), col0 + 32 * (j & 1), row - lane, lane);
           }
         }
         uint16_t* tops = c.tops + (it & 1) * 512;
         tops[side * 128 + trow] = static_cast<uint16_t>(top_a >> 16);
         tops[256 + side * 128 + trow] = static_cast<uint16_t>(top_b >> 16);
-        sum_warps_sync();
-        if (!ok) continue;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.met));
+        if (!(ok = wait_all(smem_u32(&c.met), it & 1, p.status))) break;
         top_a = max(top_a, static_cast<uint32_t>(tops[(side ^ 1) * 128 + trow]) << 16);
         top_b = max(top_b, static_cast<uint32_t>(tops[256 + (side ^ 1) * 128 + trow]) << 16);
-        if (col0 < p.N) {
-          if (all_ok) {
-            send(&maps.o[0], sa, col0, row - lane, lane);
-            send(&maps.o[1], sb, col0, row - lane, lane);
+        if (col0 < p.N && row_ok) {
+          const BlockScale ba = block_scale(top_a), bb = block_scale(top_b);
+          if (side == 0) {
+            p.scales[0][static_cast<size_t>(nb) * p.rows + row] = ba.s;
+            p.scales[1][static_cast<size_t>(nb) * p.rows + row] = bb.s;
           }
-          if (row_ok) {
-            const BlockScale ba = block_scale(top_a), bb = block_scale(top_b);
-            if (side == 0) {
-              p.scales[0][static_cast<size_t>(tl.nb) * p.rows + row] = ba.s;
-              p.scales[1][static_cast<size_t>(tl.nb) * p.rows + row] = bb.s;
-            }
-            const size_t o = static_cast<size_t>(row) * p.N + col0;
+          const size_t o = static_cast<size_t>(row) * p.N + col0;
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const uint4* set = v ? sb : sa;
-              const BlockScale& b = v ? bb : ba;
-              uint4* d = reinterpret_cast<uint4*>(p.codes[v] + o);
-              uint4* keep = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[v]) + o);
+          for (int v = 0; v < 2; ++v) {
+            const uint4* set = v ? sb : sa;
+            const BlockScale& b = v ? bb : ba;
+            uint4* d = reinterpret_cast<uint4*>(p.codes[v] + o);
+            uint4* keep = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[v]) + o);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint4 x = set[lane * 8 + ((2 * j) ^ (lane & 7))];
-                const uint4 y = set[lane * 8 + ((2 * j + 1) ^ (lane & 7))];
-                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                d[j] = codes16(w, b);
-                if (!all_ok) {
-                  keep[2 * j] = x;
-                  keep[2 * j + 1] = y;
-                }
+            for (int j = 0; j < 4; ++j) {
+              const uint4* half = set + (j >> 1) * (SET_BYTES / 16);
+              const uint4 x = half[slot_of(lane, (2 * j) & 3)], y = half[slot_of(lane, (2 * j + 1) & 3)];
+              const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+              d[j] = codes16(w, b);
+              if (!all_ok) {
+                keep[2 * j] = x;
+                keep[2 * j + 1] = y;
               }
             }
           }
@@ -684,7 +745,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // ------------------------------------------------------------ teardown
   __syncthreads();
   cluster_sync_all();  // the pair's MMAs and TMEM reads are finished
-  if (warp == 1) {
+  if (warp == ISSUE) {
     tc_fence_after();
     tmem_dealloc2(tmem_base, 512);
   }
@@ -771,7 +832,7 @@ cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, in
   Maps m;
   memset(&m, 0, sizeof(m));
   if (!map_rows(&m.a[0], a.q, K, r.rows) || !map_weight(&m.b[0], b.q, r.E, K, N, trans, 128) ||
-      !make_map_box(&m.o[0], C, out_f32, N, r.rows))
+      !make_map_box(&m.o[0], C, out_f32 ? 4 : 2, N, r.rows))
     return cudaErrorInvalidValue;
   set_raster(p, rows_each(r) * K, 1ll * K * N, 1ll * PM * K, 256ll * K);
   if (out_f32)
@@ -799,9 +860,10 @@ cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, c
   if (!map_rows(&m.a[0], x.q, h, r.rows) || !map_weight(&m.b[0], w1.q, r.E, h, f, false, 128) ||
       !map_weight(&m.b[1], w3.q, r.E, h, f, false, 128))
     return cudaErrorInvalidValue;
-  if (A && (!make_map_box(&m.o[0], A, false, f, r.rows) ||
-            !make_map_box(&m.o[1], B, false, f, r.rows) ||
-            !make_map_box(&m.o[2], H, false, f, r.rows)))
+  if (!make_map_box(&m.c[0], Hq, 1, f, r.rows)) return cudaErrorInvalidValue;
+  if (A && (!make_map_box(&m.o[0], A, 2, f, r.rows) ||
+            !make_map_box(&m.o[1], B, 2, f, r.rows) ||
+            !make_map_box(&m.o[2], H, 2, f, r.rows)))
     return cudaErrorInvalidValue;
   set_raster(p, rows_each(r) * h, 2ll * h * f, 1ll * PM * h, 256ll * h);
   return launch_pairs<GATED, true>(p, m, r.num_sms, s);
@@ -823,8 +885,8 @@ cudaError_t block_fc2_dgrad(const BlockRows& r, const Coded& dy, const Coded& w2
   Maps m;
   memset(&m, 0, sizeof(m));
   if (!map_rows(&m.a[0], dy.q, h, r.rows) || !map_weight(&m.b[0], w2.q, r.E, h, f, true, 64) ||
-      !make_map_box(&m.o[0], dA, false, f, r.rows) || !make_map_box(&m.o[1], dB, false, f, r.rows) ||
-      !make_map_box(&m.i[0], A, false, f, r.rows) || !make_map_box(&m.i[1], B, false, f, r.rows))
+      !make_map_box(&m.o[0], dA, 2, f, r.rows) || !make_map_box(&m.o[1], dB, 2, f, r.rows) ||
+      !make_map_box(&m.i[0], A, 2, f, r.rows) || !make_map_box(&m.i[1], B, 2, f, r.rows))
     return cudaErrorInvalidValue;
   set_raster(p, rows_each(r) * h, 1ll * h * f, 1ll * PM * h, 128ll * h);
   return launch_pairs<GATED_BWD, false>(p, m, r.num_sms, s);
@@ -846,7 +908,7 @@ cudaError_t block_fc1_dgrad(const BlockRows& r, const Coded& da, const Coded& db
   if (!map_rows(&m.a[0], da.q, f, r.rows) || !map_rows(&m.a[1], db.q, f, r.rows) ||
       !map_weight(&m.b[0], w1.q, r.E, f, h, true, 128) ||
       !map_weight(&m.b[1], w3.q, r.E, f, h, true, 128) ||
-      !make_map_box(&m.o[0], dX, out_f32, h, r.rows))
+      !make_map_box(&m.o[0], dX, out_f32 ? 4 : 2, h, r.rows))
     return cudaErrorInvalidValue;
   set_raster(p, rows_each(r) * 2 * f, 2ll * f * h, 1ll * PM * 2 * f, 256ll * 2 * f);
   return out_f32 ? launch_pairs<PLAIN_F32, false>(p, m, r.num_sms, s)

@@ -1582,17 +1582,19 @@ bool make_map_codes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t r
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_map_box(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t rows) {
+bool make_map_box(CUtensorMap* m, const void* base, int size, uint64_t inner, uint64_t rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const uint32_t size = f32 ? 4 : 2;
   cuuint64_t dims[2] = {inner, rows};
   cuuint64_t strides[1] = {inner * size};
-  cuuint32_t box[2] = {128 / size, 32};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / size), 32};
   cuuint32_t es[2] = {1, 1};
-  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+  return fn(m,
+            size == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+            : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                        : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+            2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

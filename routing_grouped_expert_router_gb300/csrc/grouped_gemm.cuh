@@ -88,9 +88,9 @@ bool make_map_columns(CUtensorMap* m, const void* base, uint64_t inner, uint64_t
 //   128 bytes x box_rows that do not run into the next expert.
 bool make_map_codes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
                     uint64_t experts, uint32_t box_rows);
-//   Rows for an epilogue's copies: [rows, inner] bf16 (or fp32), boxes of 128
-//   bytes x 32 rows, 128-byte swizzle.
-bool make_map_box(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t rows);
+//   Rows for an epilogue's copies: [rows, inner] of 1-, 2- (bf16) or 4-byte (fp32)
+//   elements, boxes of 64 bytes x 32 rows, 64-byte swizzle.
+bool make_map_box(CUtensorMap* m, const void* base, int size, uint64_t inner, uint64_t rows);
 
 // Clusters of two CTAs of `kern` (launch settings cfg) that the current device
 // holds at once: a persistent grid's size.

@@ -138,6 +138,9 @@ __device__ __forceinline__ void bulk_commit() {
 __device__ __forceinline__ void bulk_wait_read_1() {
   asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
+__device__ __forceinline__ void bulk_wait_read_2() {
+  asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory");
+}
 // Until none of this thread's bulk groups still reads shared memory.
 __device__ __forceinline__ void bulk_wait_read_0() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
