@@ -52,7 +52,8 @@ constexpr int FIRST_SUM_WARP = 4;
 constexpr int SUM_WARPS = 8;
 constexpr int LOAD_A = 0, ISSUE = 1, LOAD_B = 2, SCALES = 3;  // warps
 constexpr int SET_BYTES = 2048;   // 32 rows x 64 bytes: one copy of an epilogue
-constexpr int SLOTS = 8;          // blocks whose scales wait for the sums
+constexpr int SLOTS = 4;          // groups of blocks whose scales wait for the sums
+constexpr int GROUP = 4;          // blocks of a slot
 
 struct Params {
   int E;
@@ -90,20 +91,20 @@ struct Shape {
   static constexpr int B_COLS = COLS / 2;               // B columns a CTA loads
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_COLS * 128;
-  static constexpr int STAGES = NH == 2 ? 5 : 6;
+  static constexpr int STAGES = NH == 2 ? 4 : 6;
   static constexpr int BUFS = 512 / COLS;               // accumulators in tensor memory
-  static constexpr int SETS = FORM == GATED_BWD ? 4 : 3;  // of a warp
+  static constexpr int SETS = 4;                        // of a warp
   static constexpr int TOPS = FORM == GATED ? 1 : FORM == GATED_BWD ? 2 : 0;
 };
 
-// One block's scales, with the place of its tile.
-struct Slot {
-  float a[128];
-  float b[2];
+// The scales of up to GROUP blocks, with the place of their tile.
+struct alignas(16) Slot {
+  float a[128][GROUP];
+  float b[2][GROUP];
   int nb, row0, row_end;   // nb < 0: no more tiles
 };
 template <int FORM>
-struct alignas(8) Ctrl {
+struct alignas(16) Ctrl {
   using S = Shape<FORM>;
   uint64_t full[S::STAGES], empty[S::STAGES];
   uint64_t tfull[S::BUFS], tempty[S::BUFS];
@@ -190,15 +191,6 @@ __device__ __forceinline__ void add_32(const float (&v)[32], float scale, float*
 #pragma unroll
   for (int i = 0; i < 32; ++i) sums[i] = fmaf(v[i], scale, sums[i]);
 }
-__device__ __forceinline__ void add_64(uint32_t taddr, float scale, float* sums) {
-#pragma unroll
-  for (int i = 0; i < 64; i += 32) {
-    float v[32];
-    tmem_ask32(taddr + i, v);
-    tmem_wait(v);
-    add_32(v, scale, sums + i);
-  }
-}
 // sigmoid and silu with the fast exponential and quotient: their few ulps are
 // far below the bf16 rounding of all that is stored.
 __device__ __forceinline__ float sigmoid_f(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
@@ -212,47 +204,49 @@ __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w <<
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // A warp's sets between its registers and the TMA unit: 32 rows of 64 bytes, 16-byte
-// piece j of row i in slot j ^ ((i / 2) mod 4) (64-byte swizzle; no bank conflicts).
-template <int SETS>
+// piece j of row i in slot j ^ ((i / 2) mod 4) (64-byte swizzle; no bank conflicts).  Two
+// sets go out together.
 struct Staging {
   uint4* sets;
   int next = 0;
-  // A set whose last copy has been read.
+  // Two sets whose last copies have been read.
   __device__ __forceinline__ uint4* take(int lane) {
-    uint4* s = sets + next * (SET_BYTES / 16);
-    if (++next == SETS) next = 0;
-    static_assert(SETS == 3, "the wait goes by the number of sets");
-    if (lane == 0) bulk_wait_read_2();
+    uint4* s = sets + next * (2 * SET_BYTES / 16);
+    next ^= 1;
+    if (lane == 0) bulk_wait_read_1();
     __syncwarp();
     return s;
   }
 };
 __device__ __forceinline__ int slot_of(int lane, int j) { return lane * 4 + (j ^ ((lane >> 1) & 3)); }
-__device__ __forceinline__ void send(const CUtensorMap* map, uint4* set, int x, int y, int lane) {
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_2d(map, smem_u32(set), x, y);
-    bulk_commit();
-  }
-}
-// 64 bytes (w) of each of a warp's 32 rows to out [., N] (elements of SIZE bytes) at (row,
-// col): whole rows by TMA, or, where a row is not this group's, each lane its own.
-template <int SIZE, int SETS>
-__device__ __forceinline__ void put(Staging<SETS>& st, const CUtensorMap* map, void* out, int N,
-                                    const uint4 (&w)[4], int row, int col, bool row_ok,
+// Two pieces of 64 bytes (w) of each of a warp's 32 rows to out [., N] (elements of SIZE
+// bytes) at (row, col) and right of it: whole rows by TMA, or, where a row is not this
+// group's, each lane its own.  PIECES = 1: one piece.
+template <int SIZE, int PIECES = 2>
+__device__ __forceinline__ void put(Staging& st, const CUtensorMap* map, void* out, int N,
+                                    const uint4 (&w)[4 * PIECES], int row, int col, bool row_ok,
                                     bool all_ok, int lane) {
+  constexpr int WIDE = 64 / SIZE;
   if (col >= N) return;
   if (all_ok) {
     uint4* set = st.take(lane);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) set[slot_of(lane, j)] = w[j];
-    send(map, set, col, row - lane, lane);
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) set[i * (SET_BYTES / 16) + slot_of(lane, j)] = w[4 * i + j];
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, smem_u32(set), col, row - lane);
+      if (PIECES == 2 && col + WIDE < N)
+        tma_store_2d(map, smem_u32(set + SET_BYTES / 16), col + WIDE, row - lane);
+      bulk_commit();
+    }
   } else if (row_ok) {
     uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
                                         (static_cast<size_t>(row) * N + col) * SIZE);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4 * PIECES; ++j)
       if (col + 16 / SIZE * j < N) d[j] = w[j];
   }
 }
@@ -261,25 +255,22 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                     pack_bf16(f[6], f[7]));
 }
 // 64 columns of fp32 as bf16.
-template <int SETS>
-__device__ __forceinline__ void put_bf16(Staging<SETS>& st, const CUtensorMap* map, void* out,
-                                         int N, const float* f, int row, int col, bool row_ok,
+__device__ __forceinline__ void put_bf16(Staging& st, const CUtensorMap* map, void* out, int N,
+                                         const float* f, int row, int col, bool row_ok,
                                          bool all_ok, int lane) {
+  uint4 w[8];
 #pragma unroll
-  for (int i = 0; i < 64; i += 32) {
-    const uint4 w[4] = {pack8(f + i), pack8(f + i + 8), pack8(f + i + 16), pack8(f + i + 24)};
-    put<2>(st, map, out, N, w, row, col + i, row_ok, all_ok, lane);
-  }
+  for (int i = 0; i < 8; ++i) w[i] = pack8(f + 8 * i);
+  put<2>(st, map, out, N, w, row, col, row_ok, all_ok, lane);
 }
-template <int SETS>
-__device__ __forceinline__ void put_f32(Staging<SETS>& st, const CUtensorMap* map, void* out,
-                                        int N, const float* f, int row, int col, bool row_ok,
+__device__ __forceinline__ void put_f32(Staging& st, const CUtensorMap* map, void* out, int N,
+                                        const float* f, int row, int col, bool row_ok,
                                         bool all_ok, int lane) {
 #pragma unroll
-  for (int i = 0; i < 64; i += 16) {
-    uint4 w[4];
+  for (int i = 0; i < 64; i += 32) {
+    uint4 w[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
       w[j] = make_uint4(__float_as_uint(f[i + 4 * j]), __float_as_uint(f[i + 4 * j + 1]),
                         __float_as_uint(f[i + 4 * j + 2]), __float_as_uint(f[i + 4 * j + 3]));
     put<4>(st, map, out, N, w, row, col + i, row_ok, all_ok, lane);
@@ -526,20 +517,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int n = FORM == GATED ? tl.nb : min(S::NH * tl.nb + lane, p.nblocks - 1);
         base = static_cast<uint32_t>(tl.e) * p.sb_group + static_cast<uint32_t>(n) * p.sb_n;
       }
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb0 = 0; kb0 < nkb; kb0 += GROUP) {
         ok = wait_all(smem_u32(&c.sempty[i]), ph, p.status);
         if (!ok) break;
-        const int product = kb >= p.kblocks ? 1 : 0;
-        const uint32_t k = kb - (product ? p.kblocks : 0);
-        const float* sa = p.sa[product] + k * static_cast<uint32_t>(p.rows);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool real = row + 32 * j < tl.row_end;
-          copy_4(&c.slots[i].a[lane + 32 * j], sa + (real ? row + 32 * j : 0), real);
+        for (int g = 0; g < GROUP; ++g) {
+          if (kb0 + g >= nkb) break;
+          const int product = kb0 + g >= p.kblocks ? 1 : 0;
+          const uint32_t k = kb0 + g - (product ? p.kblocks : 0);
+          const float* sa = p.sa[product] + k * static_cast<uint32_t>(p.rows);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool real = row + 32 * j < tl.row_end;
+            copy_4(&c.slots[i].a[lane + 32 * j][g], sa + (real ? row + 32 * j : 0), real);
+          }
+          if (lane < S::NH)
+            copy_4(&c.slots[i].b[lane][g],
+                   p.sb[FORM == GATED ? lane : product] + (base + k * p.sb_k), true);
         }
-        if (lane < S::NH)
-          copy_4(&c.slots[i].b[lane], p.sb[FORM == GATED ? lane : product] + (base + k * p.sb_k),
-                 true);
         give(tl.nb);
       }
     }
@@ -553,7 +548,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int side = (warp - FIRST_SUM_WARP) >> 2;   // which 64 columns of each half
     const int trow = quarter * 32 + lane;            // TMEM lane: row of this CTA's 128
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    Staging<S::SETS> st;
+    Staging st;
     st.sets = reinterpret_cast<uint4*>(staging + (warp - FIRST_SUM_WARP) * S::SETS * SET_BYTES);
     int it = 0, i = 0, buf = 0;
     uint32_t iph = 0, bph = 0;
@@ -590,31 +585,62 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int h = 0; h < S::NH; ++h)
 #pragma unroll
         for (int j = 0; j < 64; ++j) sums[h][j] = 0.f;
+      bool ready = false;   // the next accumulator, looked at while the last one was added
 #pragma unroll 1
-      for (int kb = 0; kb < nkb; ++kb) {
-        if (kb && !(ok = wait_all(smem_u32(&c.sfull[i]), iph, p.status))) break;
-        const float a = c.slots[i].a[trow];
-        float scale[S::NH];
+      for (int kb0 = 0; kb0 < nkb; kb0 += GROUP) {
+        if (kb0 && !(ok = wait_all(smem_u32(&c.sfull[i]), iph, p.status))) break;
+        float scale[S::NH][GROUP];
+        {
+          const float4 a = *reinterpret_cast<const float4*>(c.slots[i].a[trow]);
 #pragma unroll
-        for (int h = 0; h < S::NH; ++h) scale[h] = a * c.slots[i].b[h];
+          for (int h = 0; h < S::NH; ++h) {
+            const float4 b = *reinterpret_cast<const float4*>(c.slots[i].b[h]);
+            scale[h][0] = a.x * b.x;
+            scale[h][1] = a.y * b.y;
+            scale[h][2] = a.z * b.z;
+            scale[h][3] = a.w * b.w;
+          }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.sempty[i]));
         if (++i == SLOTS) {
           i = 0;
           iph ^= 1;
         }
-        if (!(ok = wait_all(smem_u32(&c.tfull[buf]), bph, p.status))) break;
-        tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < S::NH; ++h)
-          add_64(tmem_base + buf * S::COLS + lanes + side * 64 + h * 128, scale[h], sums[h]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&c.tempty[buf]), 0));
-        if (++buf == S::BUFS) {
-          buf = 0;
-          bph ^= 1;
+        for (int g = 0; g < GROUP; ++g) {
+          if (kb0 + g >= nkb) break;
+          if (!ready && !(ok = wait_all(smem_u32(&c.tfull[buf]), bph, p.status))) break;
+          tc_fence_after();
+          const uint32_t at = tmem_base + buf * S::COLS + lanes + side * 64;
+          const uint32_t done = smem_u32(&c.tempty[buf]);
+          if (++buf == S::BUFS) {
+            buf = 0;
+            bph ^= 1;
+          }
+          // 32 columns come while those before are added; the accumulator is free as soon as
+          // the last have come
+          float v[32], w[32];
+          tmem_ask32(at, v);
+          ready = __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&c.tfull[buf]), bph));
+          tmem_wait(v);
+          tmem_ask32(at + 32, w);
+          add_32(v, scale[0][g], sums[0]);
+          tmem_wait(w);
+          if constexpr (S::NH == 2) {
+            tmem_ask32(at + 128, v);
+            add_32(w, scale[0][g], sums[0] + 32);
+            tmem_wait(v);
+            tmem_ask32(at + 160, w);
+            add_32(v, scale[S::NH - 1][g], sums[S::NH - 1]);
+            tmem_wait(w);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(mapa_shared(done, 0));
+          add_32(w, scale[S::NH - 1][g], sums[S::NH - 1] + 32);
         }
+        if (!ok) break;
       }
       if (!ok) break;
       if constexpr (FORM == PLAIN_BF16) {
@@ -646,14 +672,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.met));
         if (p.out[0]) {
+          uint4 h8[8];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint4 h4[4] = {make_uint4(w[16 * j], w[16 * j + 1], w[16 * j + 2], w[16 * j + 3]),
-                                 make_uint4(w[16 * j + 4], w[16 * j + 5], w[16 * j + 6], w[16 * j + 7]),
-                                 make_uint4(w[16 * j + 8], w[16 * j + 9], w[16 * j + 10], w[16 * j + 11]),
-                                 make_uint4(w[16 * j + 12], w[16 * j + 13], w[16 * j + 14], w[16 * j + 15])};
-            put<2>(st, &maps.o[2], p.out[2], p.N, h4, row, col0 + 32 * j, row_ok, all_ok, lane);
-          }
+          for (int j = 0; j < 8; ++j)
+            h8[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          put<2>(st, &maps.o[2], p.out[2], p.N, h8, row, col0, row_ok, all_ok, lane);
         }
         if (!(ok = wait_all(smem_u32(&c.met), it & 1, p.status))) break;
         top = max(top, static_cast<uint32_t>(tops[(side ^ 1) * 128 + trow]) << 16);
@@ -661,7 +684,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const BlockScale bs = block_scale(top);
           if (row_ok && side == 0) p.scales[0][static_cast<size_t>(nb) * p.rows + row] = bs.s;
           const uint4 q4[4] = {codes16(w, bs), codes16(w + 8, bs), codes16(w + 16, bs), codes16(w + 24, bs)};
-          put<1>(st, &maps.c[0], p.codes[0], p.N, q4, row, col0, row_ok, all_ok, lane);
+          put<1, 1>(st, &maps.c[0], p.codes[0], p.N, q4, row, col0, row_ok, all_ok, lane);
         }
       } else {
         uint32_t top_a = 0, top_b = 0;
@@ -696,9 +719,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             sb[at] = make_uint4(db[0], db[1], db[2], db[3]);
           }
           if (all_ok) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              send(&maps.o[j >> 1], st.sets + j * (SET_BYTES / 16), col0 + 32 * (j & 1), row - lane, lane);
+              for (int j = 0; j < 4; ++j)
+                tma_store_2d(&maps.o[j >> 1], smem_u32(st.sets + j * (SET_BYTES / 16)),
+                             col0 + 32 * (j & 1), row - lane);
+              bulk_commit();
+            }
           }
         }
         uint16_t* tops = c.tops + (it & 1) * 512;

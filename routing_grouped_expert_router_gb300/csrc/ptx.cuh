@@ -55,6 +55,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether the phase is over, without waiting for it.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Longest time one wait may take before the kernel gives up (ns).  A wait in
 // a working pipeline lasts microseconds.
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
@@ -137,9 +150,6 @@ __device__ __forceinline__ void bulk_commit() {
 // Until at most one of this thread's bulk groups still reads shared memory.
 __device__ __forceinline__ void bulk_wait_read_1() {
   asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_read_2() {
-  asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory");
 }
 // Until none of this thread's bulk groups still reads shared memory.
 __device__ __forceinline__ void bulk_wait_read_0() {
