@@ -416,7 +416,8 @@ typedef struct {
   int32_t out_f32;  /* 0: C bf16; 1: C fp32 */
 } moe_gemm_dims;
 
-/* Scratch bytes of moe_gemm_fp8_block (0 on invalid dims). */
+/* Scratch bytes of moe_gemm_fp8_block (0 on invalid dims).  They grow with
+ * rows: a workspace for the most rows serves every smaller call of the same E. */
 size_t moe_gemm_workspace_bytes(const moe_gemm_dims* dims);
 
 /* C[p] = A[p] B[e] for the rows p of each group e, offsets[e] <= p <
@@ -449,7 +450,8 @@ typedef struct {
 } moe_ffn_dims;
 
 /* Scratch bytes of moe_gated_ffn_fwd (backward = 0) or moe_gated_ffn_bwd
- * (backward = 1); 0 on invalid dims. */
+ * (backward = 1); 0 on invalid dims.  They grow with rows: a workspace for the
+ * most rows serves every smaller call of the same h, f and E. */
 size_t moe_ffn_workspace_bytes(const moe_ffn_dims* dims, int backward);
 
 /* x [rows, h] bf16 (rows of expert e at offsets[e] .. offsets[e+1]-1), y

@@ -174,6 +174,7 @@ struct WsLayout {
   size_t Xq = 0, sx = 0, Hq = 0, sh = 0;     // fp8 forward
   size_t h_amax = 0;                         // fp8 forward: per-tile amax of H
   size_t dAq = 0, dBq = 0, sab = 0, ab_amax = 0;  // fp8 backward
+  size_t part = 0;                           // block-scaled fp8 forward
   size_t dOq = 0, sdo = 0, sda = 0, sdb = 0;  // block-scaled fp8 backward (with dAq, dBq)
   size_t total = 0;
 };
@@ -209,6 +210,7 @@ WsLayout ws_layout(const moe_dims& d, int op) {
       L.sx = c.take(R * hb * 4);
       L.Hq = c.take(R * d.f);
       L.sh = c.take(R * fb * 4);
+      L.part = c.take(moe::few_part_bytes(static_cast<int>(R), d.E, 2));
       break;
     case MOE_OP_LAYER_BWD_FP8_BLOCK:
       if (d.sar) return WsLayout{};
@@ -1014,7 +1016,8 @@ moe_status moe_layer_fwd_fp8_block(const moe_dims* dims, const moe_bf16* x, cons
                                        at<int>(ws, 0)),
           "permute_quant_x_block");
   if (R > 0) {
-    const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms()};
+    const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms(),
+                              at<float>(ws, L.part)};
     MOE_RUN(moe::block_fc1_fwd(r, {Xq, sx}, {W1q, s1}, {W3q, s3}, d.h, d.f,
                                at<uint16_t>(saved, S.A), at<uint16_t>(saved, S.B),
                                at<uint16_t>(saved, S.H), Hq, sh, stream),
@@ -1070,7 +1073,8 @@ moe_status moe_layer_bwd_fp8_block(const moe_dims* dims, const moe_bf16* x, cons
     MOE_RUN(cudaMemsetAsync(dW3, 0, wbytes, stream), "zero_dW3");
     MOE_RUN(cudaMemsetAsync(dW2, 0, wbytes, stream), "zero_dW2");
   } else {
-    const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms()};
+    const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms(),
+                              nullptr};
     MOE_RUN(moe::launch_quant_rows_block(dO, nullptr, 1, R, R, d.h, dOq, sdo, num_sms(), stream,
                                          nvalid, nullptr, at<int>(ws, 0)),
             "quant_dO_block");

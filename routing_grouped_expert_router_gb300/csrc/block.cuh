@@ -31,9 +31,16 @@ struct BlockRows {
   int E;
   const int32_t* offsets;
   int rows;
-  int* status;    // device status word
+  int* status;    // device status word, at the start of the workspace's 256-byte header
   int num_sms;
+  float* part;    // few_part_bytes(rows, E, weights) bytes
 };
+// Whether a group's rows are so few that reading the weights bounds the product
+// (gemm_block_few.cu).  Up to 64 rows to a group on average; what that costs and saves
+// stands at block_product.
+inline bool few_rows(int rows, int E) { return rows <= 64ll * E; }
+// Grows with rows, so that a workspace for the most rows serves fewer.
+size_t few_part_bytes(int rows, int E, int weights);
 // Codes and scales of an activation or a weight.
 struct Coded {
   const uint8_t* q;
@@ -46,6 +53,12 @@ cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, in
 cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
                           int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                           float* sh, cudaStream_t s);
+// The same for few rows.
+cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
+                        bool trans, bool out_f32, void* C, cudaStream_t s);
+cudaError_t few_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
+                        int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
+                        float* sh, cudaStream_t s);
 // dH = dY W2^T, fused with the SwiGLU backward: dA, dB in bf16 and their codes.
 cudaError_t block_fc2_dgrad(const BlockRows& r, const Coded& dy, const Coded& w2, int h, int f,
                             const uint16_t* A, const uint16_t* B, uint16_t* dA, uint16_t* dB,

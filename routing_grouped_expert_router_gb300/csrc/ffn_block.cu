@@ -61,7 +61,7 @@ moe_status check_ffn(const moe_ffn_dims* d) {
 struct FfnLayout {
   size_t status = 0;
   size_t Xq = 0, sx = 0;                 // the rows' codes (of x, or of dy in the backward)
-  size_t Hq = 0, sh = 0;                 // forward
+  size_t Hq = 0, sh = 0, part = 0;       // forward
   size_t dA = 0, dB = 0;                 // backward
   size_t dAq = 0, sda = 0, dBq = 0, sdb = 0;
   size_t total = 0;
@@ -76,6 +76,7 @@ FfnLayout ffn_layout(const moe_ffn_dims& d, bool backward) {
   if (!backward) {
     L.Hq = c.take(R * d.f);
     L.sh = c.take(R * fb * 4);
+    L.part = c.take(moe::few_part_bytes(d.rows, d.E, 2));
   } else {
     L.dA = c.take(R * d.f * 2);
     L.dB = c.take(R * d.f * 2);
@@ -100,7 +101,7 @@ extern "C" {
 
 size_t moe_gemm_workspace_bytes(const moe_gemm_dims* dims) {
   if (check_gemm(dims) != MOE_OK) return 0;
-  return kAlign;
+  return kAlign + moe::few_part_bytes(dims->rows, dims->E, 1);
 }
 
 moe_status moe_gemm_fp8_block(const moe_gemm_dims* dims, const uint8_t* aq, const float* sa,
@@ -115,7 +116,8 @@ moe_status moe_gemm_fp8_block(const moe_gemm_dims* dims, const uint8_t* aq, cons
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_gemm_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const moe::BlockRows r = {d.E, offsets, d.rows, at<int>(ws, 0), moe_api::num_sms()};
+  const moe::BlockRows r = {d.E, offsets, d.rows, at<int>(ws, 0), moe_api::num_sms(),
+                            at<float>(ws, kAlign)};
   BLOCK_RUN(moe::block_product(r, {aq, sa}, {bq, sb}, d.K, d.N, d.trans_b != 0, d.out_f32 != 0, C,
                                stream),
             "block_product");
@@ -145,7 +147,8 @@ moe_status moe_gated_ffn_fwd(const moe_ffn_dims* dims, const moe_bf16* x, const 
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (R == 0) return MOE_OK;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const moe::BlockRows r = {d.E, offsets, d.rows, at<int>(ws, 0), moe_api::num_sms()};
+  const moe::BlockRows r = {d.E, offsets, d.rows, at<int>(ws, 0), moe_api::num_sms(),
+                            at<float>(ws, L.part)};
   uint8_t *xq = at<uint8_t>(ws, L.Xq), *hq = at<uint8_t>(ws, L.Hq);
   float *sx = at<float>(ws, L.sx), *sh = at<float>(ws, L.sh);
   BLOCK_RUN(moe::launch_quant_rows_block(x, nullptr, 1, d.rows, d.rows, d.h, xq, sx, r.num_sms,
@@ -186,7 +189,7 @@ moe_status moe_gated_ffn_bwd(const moe_ffn_dims* dims, const moe_bf16* x, const 
         BLOCK_RUN(cudaMemsetAsync(w, 0, bytes, stream), "zero_dW");
     return MOE_OK;
   }
-  const moe::BlockRows r = {d.E, offsets, d.rows, at<int>(ws, 0), moe_api::num_sms()};
+  const moe::BlockRows r = {d.E, offsets, d.rows, at<int>(ws, 0), moe_api::num_sms(), nullptr};
   uint8_t *dyq = at<uint8_t>(ws, L.Xq), *daq = at<uint8_t>(ws, L.dAq), *dbq = at<uint8_t>(ws, L.dBq);
   float *sdy = at<float>(ws, L.sx), *sda = at<float>(ws, L.sda), *sdb = at<float>(ws, L.sdb);
   uint16_t *da = at<uint16_t>(ws, L.dA), *db = at<uint16_t>(ws, L.dB);

@@ -173,6 +173,7 @@ SHAPES = [
     ([127], 400, 272), ([128], 256, 256), ([129], 384, 528), ([300], 1104, 720), ([1000], 640, 1040),
     ([0, 5, 0, 130, 1, 0], 400, 272), ([33, 0, 64, 1, 200], 1088, 704), ([0, 0, 7], 128, 1408), ([600, 3, 500], 272, 1552),
     ([4] * 64, 2048, 144), ([0] * 63 + [9], 256, 384), ([257, 255, 0, 1], 896, 640),
+    ([1, 400, 0, 3], 400, 272), ([2, 0, 290, 1, 70], 1040, 592), ([65], 1408, 2048), ([30] * 9, 640, 272), ([200, 1, 0, 3, 40], 1936, 400),
 ]
 
 
