@@ -50,14 +50,15 @@ struct Coded {
 cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
                           bool trans, bool out_f32, void* C, cudaStream_t s);
 // A = X W1, B = X W3, H = silu(A) * B with the codes of bf16(H); A, B, H may be NULL.
+// w2: the weight of the product that follows, brought to L2 towards the end (few rows).
 cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
-                          int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
+                          const Coded& w2, int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                           float* sh, cudaStream_t s);
 // The same for few rows.
 cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
                         bool trans, bool out_f32, void* C, cudaStream_t s);
 cudaError_t few_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
-                        int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
+                        const Coded& w2, int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                         float* sh, cudaStream_t s);
 // dH = dY W2^T, fused with the SwiGLU backward: dA, dB in bf16 and their codes.
 cudaError_t block_fc2_dgrad(const BlockRows& r, const Coded& dy, const Coded& w2, int h, int f,

@@ -18,7 +18,15 @@ struct BlockScale {
 };
 __device__ __forceinline__ BlockScale block_scale(uint32_t top) {
   BlockScale b;
-  b.s = top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top), kCodeMax);
+  const float amax = __uint_as_float(top);
+  if (amax > 7.9e-31f && amax < 1.2e30f) {
+    // as in block_quotient below, with the constant's reciprocal
+    constexpr float r = 1.0f / kCodeMax;
+    const float q0 = amax * r;
+    b.s = fmaf(fmaf(-q0, kCodeMax, amax), r, q0);
+  } else {
+    b.s = top == 0 ? 1.0f : __fdiv_rn(amax, kCodeMax);
+  }
   b.r = __frcp_rn(b.s);
   b.plain = b.s > 7.9e-31f && b.s < 1.2e30f;  // 2^-100 .. 2^100
   return b;

@@ -155,7 +155,7 @@ moe_status moe_gated_ffn_fwd(const moe_ffn_dims* dims, const moe_bf16* x, const 
                                          stream, offsets ? offsets + d.E : nullptr, nullptr,
                                          r.status),
             "quant_rows_block");
-  BLOCK_RUN(moe::block_fc1_fwd(r, {xq, sx}, {W1q, s1}, {W3q, s3}, d.h, d.f, A, B, H, hq, sh,
+  BLOCK_RUN(moe::block_fc1_fwd(r, {xq, sx}, {W1q, s1}, {W3q, s3}, {W2q, s2}, d.h, d.f, A, B, H, hq, sh,
                                stream),
             "block_fc1_fwd");
   BLOCK_RUN(moe::block_product(r, {hq, sh}, {W2q, s2}, d.f, d.h, false, false, y, stream),

@@ -873,10 +873,10 @@ cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, in
 }
 
 cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
-                          int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
+                          const Coded& w2, int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                           float* sh, cudaStream_t s) {
   if (r.rows == 0) return cudaSuccess;
-  if (few_rows(r.rows, r.E)) return few_fc1_fwd(r, x, w1, w3, h, f, A, B, H, Hq, sh, s);
+  if (few_rows(r.rows, r.E)) return few_fc1_fwd(r, x, w1, w3, w2, h, f, A, B, H, Hq, sh, s);
   Params p = params_of(r, h, f, false);
   p.sa[0] = x.s;
   p.sb[0] = w1.s;

@@ -19,7 +19,6 @@
 
 #include <cstdint>
 #include <cstring>
-#include <type_traits>
 
 #include "block.cuh"
 #include "block_quant.cuh"
@@ -27,6 +26,12 @@
 #include "kernels.cuh"
 #include "ptx.cuh"
 
+#ifndef V_HALF
+#define V_HALF 1
+#endif
+#ifndef V_EARLY
+#define V_EARLY 8
+#endif
 namespace moe {
 
 namespace {
@@ -38,7 +43,6 @@ constexpr int MAX_E = 64;
 constexpr int MAX_BLOCKS = 160;  // of the grid
 constexpr int NUM_THREADS = 256;
 constexpr int W_BYTES = 128 * 128;
-constexpr int BUFS = 4;          // steps whose sums wait in tensor memory
 constexpr int SLOTS = 8;         // steps whose scales wait
 constexpr int LOAD_W = 0, ISSUE = 1, SCALES = 2, LOAD_X = 3, FIRST_SUM_WARP = 4;
 
@@ -54,10 +58,12 @@ struct Params {
   float* scales;
   float* part;              // [grid, 2] slots of a shared tile's sums
   uint32_t* arrived;        // a byte for each block of the grid: pieces of its last tile
+  int next_n, next_nkb;     // that product's columns and blocks; not transposed
   int* status;
 };
 struct Maps {
   CUtensorMap x, w[2];
+  CUtensorMap next;         // the weight of the product that follows (next_n > 0)
 };
 
 template <int FORM, int NT>
@@ -66,10 +72,15 @@ struct Shape {
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = NB * W_BYTES + X_BYTES;
   static constexpr int UNIT = NB * NT;               // accumulator columns of a step
-  static constexpr int PITCH = 128 * 4 + 16;         // staging: bytes of a row
-  static constexpr int FIT = (232448 - 1024 - NT * PITCH - 6144) / STAGE_BYTES;
+  static constexpr int PITCH = (FORM == PLAIN_F32 ? 512 : 256) + 16;  // staging: bytes of a row
+  // Two blocks fit an SM where two or more stages do in half of it: the next kernel of the
+  // stream then sets itself up beside the last blocks of this one.
+  static constexpr bool HALF = V_HALF && (NT == 16 || (NT == 32 && NB == 1));
+  static constexpr int FIT = ((HALF ? 114688 : 232448) - 1024 - NT * PITCH - 3072) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 12 ? 12 : FIT;
-  static_assert(X_BYTES % 1024 == 0 && BUFS * UNIT <= 512, "stage or tensor memory");
+  static constexpr int BUFS = 4 * UNIT > 256 ? 2 : 4;  // steps whose sums wait in tensor memory
+  static constexpr int TMEM = BUFS * UNIT;           // columns (a power of two, 64 to 256)
+  static_assert(X_BYTES % 1024 == 0 && TMEM <= 256 && TMEM >= 32 && STAGES >= 2, "does not fit");
 };
 template <int NT>
 struct alignas(16) Slot {
@@ -80,14 +91,13 @@ template <int FORM, int NT>
 struct alignas(16) Ctrl {
   using S = Shape<FORM, NT>;
   uint64_t full[S::STAGES], empty[S::STAGES];
-  uint64_t tfull[BUFS], tempty[BUFS];
+  uint64_t tfull[S::BUFS], tempty[S::BUFS];
   uint64_t sfull[SLOTS], sempty[SLOTS];
   uint64_t met, drain;
   uint32_t tmem_base;
   uint32_t last;            // whether this block joins the tile
   int off[MAX_E + 1];
   int cum[MAX_E + 1];       // row tiles before each group
-  uint32_t tops[4][NT];     // bf16 patterns, one of each sum warp
   Slot<NT> slots[SLOTS];
 };
 template <int FORM, int NT>
@@ -99,11 +109,17 @@ constexpr int smem_bytes() {
 struct Tile {
   int e, n, row0, row_end;  // group, column tile, rows
 };
+// Steps of the next product that each block brings to L2 after its own loads: 384 KiB of
+// codes, 57 MB over all SMs, what HBM moves while a tile is joined and the next kernel
+// starts up.
+constexpr int kNextSteps = 24;
+constexpr int kEarlySteps = V_EARLY;  // 16 KiB blocks of weights asked for before the kernel before has ended
+
 // Tile t: groups in order; in one, column tiles in order; row tiles of a column tile
 // side by side, so that they find the weight in L2.
 template <int NT>
-__device__ __forceinline__ Tile place(const Params& p, const int* off, const int* cum, int t) {
-  const int tiles_n = (p.N + 127) / 128;
+__device__ __forceinline__ Tile place(const Params& p, int N, const int* off, const int* cum, int t) {
+  const int tiles_n = (N + 127) / 128;
   int e = 0, hi = p.E - 1;
   while (e < hi) {
     const int mid = (e + hi + 1) >> 1;
@@ -189,7 +205,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(smem_u32(&c.full[s]), 2);  // the producers of weights and of activations
       mbar_init(smem_u32(&c.empty[s]), 1);
     }
-    for (int b = 0; b < BUFS; ++b) {
+    for (int b = 0; b < S::BUFS; ++b) {
       mbar_init(smem_u32(&c.tfull[b]), 1);
       mbar_init(smem_u32(&c.tempty[b]), 4);
     }
@@ -204,9 +220,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&maps.w[0]);
   }
   if (warp == ISSUE) {
-    tmem_alloc(smem_u32(&c.tmem_base), 512);
+    tmem_alloc(smem_u32(&c.tmem_base), S::TMEM);
     tmem_relinquish();
     tc_fence_before();
+  }
+  // One group: the steps are known before its rows are, and the weights can come to L2 while
+  // the kernel before ends (should it write them, L2 has what it wrote).
+  if (warp == LOAD_W && p.E == 1) {
+    Share guess;
+    guess.steps = static_cast<long long>((p.N + 127) / 128) * ((p.rows + NT - 1) / NT) * p.nkb;
+    guess.blocks = static_cast<int>(guess.steps < gridDim.x ? guess.steps : gridDim.x);
+    if (static_cast<int>(blockIdx.x) < guess.blocks) {
+      const long long from = guess.lo(blockIdx.x);
+      const long long to = min(guess.lo(blockIdx.x + 1), from + kEarlySteps / S::NB);
+      if (elect_one())
+        for (long long i = from; i < to; ++i) {
+          const int n = static_cast<int>(i / p.nkb) / ((p.rows + NT - 1) / NT) * 128;
+          const int k = static_cast<int>(i % p.nkb) * kBlock;
+          for (int o = 0; o < S::NB; ++o)
+            tma_prefetch_l2_3d(&maps.w[o], TRANS ? k : n, TRANS ? n : k, 0);
+        }
+    }
+    __syncwarp();
   }
   // the kernel before may have written all that is read from here on; the next one may begin
   // its own set-up
@@ -231,7 +266,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   __syncthreads();
   tc_fence_after();
-  constexpr uint32_t tmem_base = 0;  // all 512 columns are this block's
+  const uint32_t tmem_base = c.tmem_base;
   const int nkb = p.nkb;
   Share share;
   share.steps = static_cast<long long>((p.N + 127) / 128) * c.cum[p.E] * nkb;
@@ -251,7 +286,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     Tile tl = {};
     for (int i = 0; i < count; ++i) {
-      if (i == 0 || kb == 0) tl = place<NT>(p, c.off, c.cum, t);
+      if (i == 0 || kb == 0) tl = place<NT>(p, p.N, c.off, c.cum, t);
       ok = wait_all(&c.empty[s], ph, p.status);
       if (!ok) break;
       if (one) {
@@ -278,6 +313,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (++kb == nkb) {
         kb = 0;
         ++t;
+      }
+    }
+    if (ok && warp == LOAD_W && p.next_n > 0) {
+      Share after;
+      after.steps = static_cast<long long>((p.next_n + 127) / 128) * c.cum[p.E] * p.next_nkb;
+      after.blocks = static_cast<int>(after.steps < gridDim.x ? after.steps : gridDim.x);
+      if (me < after.blocks) {
+        const long long from = after.lo(me), to = min(after.lo(me + 1), from + kNextSteps);
+        int at = static_cast<int>(from / p.next_nkb);
+        int k = static_cast<int>(from - static_cast<long long>(at) * p.next_nkb);
+        for (long long i = from; i < to; ++i) {
+          if (i == from || k == 0) tl = place<NT>(p, p.next_n, c.off, c.cum, at);
+          if (one) tma_prefetch_l2_3d(&maps.next, tl.n * 128, k * kBlock, tl.e);
+          if (++k == p.next_nkb) {
+            k = 0;
+            ++at;
+          }
+        }
       }
     }
     if (!ok) {
@@ -314,7 +367,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         s = 0;
         ph ^= 1;
       }
-      if (++buf == BUFS) {
+      if (++buf == S::BUFS) {
         buf = 0;
         bph ^= 1;
       }
@@ -330,7 +383,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t ph = 1;
     Tile tl = {};
     for (int n = 0; n < count; ++n) {
-      if (n == 0 || kb == 0) tl = place<NT>(p, c.off, c.cum, t);
+      if (n == 0 || kb == 0) tl = place<NT>(p, p.N, c.off, c.cum, t);
       if (!wait_all(&c.sempty[i], ph, p.status)) break;
       // indexes fit 32 bits: a scale stands for 128 bytes of codes or more
 #pragma unroll
@@ -372,7 +425,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     int left = count;
     while (ok && left > 0) {
-      const Tile tl = place<NT>(p, c.off, c.cum, t);
+      const Tile tl = place<NT>(p, p.N, c.off, c.cum, t);
       const int n = min(nkb - kb, left);  // this block's steps of the tile
       float sums[S::NB][NT];
 #pragma unroll
@@ -407,7 +460,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           i = 0;
           iph ^= 1;
         }
-        if (++buf == BUFS) {
+        if (++buf == S::BUFS) {
           buf = 0;
           bph ^= 1;
         }
@@ -425,9 +478,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < NT; ++j)
             if (tl.row0 + j < tl.row_end) slot[(o * NT + j) * 128] = sums[o][j];
-        __threadfence();
         if (!(ok = meet())) break;
         if (tid == 0) {
+          __threadfence();  // what the four warps wrote before they met
           const uint32_t shift = 8 * (first & 3);
           const uint32_t old = (atomicAdd(p.arrived + (first >> 2), 1u << shift) >> shift) & 0xFFu;
           c.last = old == static_cast<uint32_t>(last - first);
@@ -442,6 +495,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int o = 0; o < S::NB; ++o)
 #pragma unroll
             for (int j = 0; j < NT; ++j) sums[o][j] = 0.f;
+#pragma unroll 2
           for (int b = first; b <= last; ++b) {
             const float* from = p.part + (2ll * b + (s0 <= share.lo(b) ? 0 : 1)) * SLOT + tid;
 #pragma unroll
@@ -451,74 +505,52 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (tl.row0 + j < tl.row_end) sums[o][j] += __ldcg(from + (o * NT + j) * 128);
           }
         }
-        if (!(ok = meet())) break;  // c.last is read before it is written again
       }
       if (mine) {
+        // A thread's column goes to a staging area, and a warp takes whole rows from there: the
+        // loop over rows is one short piece of code (unrolled with the sums in registers it was
+        // fetched anew for each tile, 7000 cycles).
         const int rows = min(NT, tl.row_end - tl.row0);
-        const int cols = min(128, p.N - tl.n * 128);
-        // a thread's column of `v`, as bf16 or fp32, to rows of `out` through shared memory
-        auto store = [&](auto* out, const float* v) {
-          using T = std::remove_pointer_t<decltype(out)>;
-          if (!meet()) return false;  // the staging area's last use is over
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            if (j < rows) {
-              T* d = reinterpret_cast<T*>(staging + j * S::PITCH) + tid;
-              if constexpr (sizeof(T) == 4)
-                *d = v[j];
-              else if constexpr (sizeof(T) == 2)
-                *d = __float2bfloat16_rn(v[j]);
-            }
-          if (!meet()) return false;
-          constexpr int EACH = 16 / sizeof(T), LINE = 128 / EACH;  // elements and pieces of a row
-          for (int x = tid; x < rows * LINE; x += 128) {
-            const int j = x / LINE, q = x % LINE;
-            if (q * EACH < cols)
-              *reinterpret_cast<uint4*>(out + static_cast<size_t>(tl.row0 + j) * p.N + tl.n * 128 + q * EACH) =
-                  *reinterpret_cast<const uint4*>(staging + j * S::PITCH + q * 16);
-          }
-          return true;
-        };
-        if constexpr (FORM == PLAIN_F32) {
-          ok = store(static_cast<float*>(p.out[0]), sums[0]);
-        } else if constexpr (FORM == PLAIN_BF16) {
-          ok = store(static_cast<__nv_bfloat16*>(p.out[0]), sums[0]);
-        } else {
-          if (p.out[0])
-            ok = store(static_cast<__nv_bfloat16*>(p.out[0]), sums[0]) &&
-                 store(static_cast<__nv_bfloat16*>(p.out[1]), sums[S::NB - 1]);
-          if (!ok) break;
-          // H in bf16 (in sums[0]) and its largest value over the tile's columns, a row at a time
+        const int col = tl.n * 128 + 4 * lane;  // of a row, four to a lane
+        const bool col_ok = col < p.N;
+        constexpr int PASSES = FORM == GATED ? 3 : 1;
+        for (int pass = FORM == GATED && !p.out[0] ? 2 : 0; ok && pass < PASSES; ++pass) {
+          if (!(ok = meet())) break;  // the area's last rows have been read
+          float* f = reinterpret_cast<float*>(staging) + tid;
+          __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(staging) + tid;
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            float h = 0.f;
-            if (tid < cols && j < rows)
-              h = __bfloat162float(__float2bfloat16_rn(silu_f(sums[0][j]) * sums[S::NB - 1][j]));
-            sums[0][j] = h;
-            if (j < rows) {
-              const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu);
-              if (lane == 0) c.tops[warp - FIRST_SUM_WARP][j] = top;
-            }
-          }
-          if (p.out[2] && !(ok = store(static_cast<__nv_bfloat16*>(p.out[2]), sums[0]))) break;
-          if (!(ok = meet())) break;
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            if (j < rows) {
-              const uint32_t top = max(max(c.tops[0][j], c.tops[1][j]), max(c.tops[2][j], c.tops[3][j]));
-              const BlockScale b = block_scale(top);
-              if (tid == 0) p.scales[static_cast<size_t>(tl.n) * p.rows + tl.row0 + j] = b.s;
-              const float one_code[4] = {sums[0][j], 0.f, 0.f, 0.f};
-              staging[j * S::PITCH + tid] = static_cast<uint8_t>(codes4(one_code, b));
-            }
-          if (!(ok = meet())) break;
-          for (int x = tid; x < rows * 8; x += 128) {
-            const int j = x / 8, q = x % 8;
-            if (q * 16 < cols)
-              *reinterpret_cast<uint4*>(p.codes + static_cast<size_t>(tl.row0 + j) * p.N + tl.n * 128 + q * 16) =
-                  *reinterpret_cast<const uint4*>(staging + j * S::PITCH + q * 16);
+            if (FORM == PLAIN_F32)
+              f[j * (S::PITCH / 4)] = sums[0][j];
+            else
+              h[j * (S::PITCH / 2)] = __float2bfloat16_rn(
+                  FORM == PLAIN_BF16 || pass == 0 ? sums[0][j]
+                  : pass == 1                     ? sums[S::NB - 1][j]
+                                                  : silu_f(sums[0][j]) * sums[S::NB - 1][j]);
           }
           if (!(ok = meet())) break;
+#pragma unroll 1
+          for (int j = warp - FIRST_SUM_WARP; j < rows; j += 4) {
+            const size_t at = static_cast<size_t>(tl.row0 + j) * p.N + col;
+            if constexpr (FORM == PLAIN_F32) {
+              if (col_ok)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out[0]) + at) =
+                    *reinterpret_cast<const float4*>(staging + j * S::PITCH + 16 * lane);
+            } else {
+              uint2 w = *reinterpret_cast<const uint2*>(staging + j * S::PITCH + 8 * lane);
+              if (!col_ok) w = make_uint2(0, 0);
+              if (p.out[pass] && col_ok)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out[pass]) + at) = w;
+              if (FORM == GATED && pass == 2) {
+                const BlockScale b = block_scale(
+                    __reduce_max_sync(0xffffffffu, top_of_pair(top_of_pair(0, w.x), w.y)));
+                const float v[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                    __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)};
+                if (col_ok) *reinterpret_cast<uint32_t*>(p.codes + at) = codes4(v, b);
+                if (lane == 0) p.scales[static_cast<size_t>(tl.n) * p.rows + tl.row0 + j] = b.s;
+              }
+            }
+          }
         }
       }
       left -= n;
@@ -533,7 +565,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   if (warp == ISSUE) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    tmem_dealloc(tmem_base, S::TMEM);
   }
 }
 
@@ -614,15 +646,18 @@ cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int 
                : launch<PLAIN_BF16, false>(nt, p, m, r.num_sms, s);
 }
 
-cudaError_t few_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3, int h,
-                        int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq, float* sh,
-                        cudaStream_t s) {
+cudaError_t few_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
+                        const Coded& w2, int h, int f, uint16_t* A, uint16_t* B, uint16_t* H,
+                        uint8_t* Hq, float* sh, cudaStream_t s) {
   Params p;
   Maps m;
   const int nt = tile_rows(r.rows, r.E);
   if (!fill(p, m, r, x, h, f, false, nt) || !map_weight(&m.w[0], w1.q, r.E, h, f, false) ||
-      !map_weight(&m.w[1], w3.q, r.E, h, f, false))
+      !map_weight(&m.w[1], w3.q, r.E, h, f, false) ||
+      !map_weight(&m.next, w2.q, r.E, f, h, false))
     return cudaErrorInvalidValue;
+  p.next_n = h;
+  p.next_nkb = blocks_of(f);
   p.sb[0] = w1.s;
   p.sb[1] = w3.s;
   p.out[0] = A;

@@ -20,7 +20,7 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kRowThreads = 256;
-constexpr int kRowAhead = 4;  // 16-byte loads a lane has under way
+constexpr int kRowAhead = 2;  // blocks of a lane under way, 32 bytes of each
 
 __device__ __forceinline__ void codes8(const uint4& w, const BlockScale& b, uint2& out) {
   const float lo[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
@@ -33,14 +33,19 @@ __device__ __forceinline__ uint32_t top8(const uint4& w) {
   return top_of_pair(top_of_pair(top_of_pair(top_of_pair(0, w.x), w.y), w.z), w.w);
 }
 
-// A warp takes a row's blocks two at a time, 16 lanes of 8 values to a block,
-// with kRowAhead such pairs under way.  blockIdx.y splits a row's pairs where
-// there are too few rows to fill the GPU.
+// A warp takes a row's blocks four at a time, eight lanes of two 16-byte pieces to a
+// block, with kRowAhead such quads under way: sixteen values share the arithmetic of a
+// block's scale, which with eight took as many instructions as all else (16384 x 4096
+// rows gathered twice: 90 us).  blockIdx.y splits a row's quads where there are too few
+// rows to fill the GPU.
 __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
     const uint4* __restrict__ in, const int32_t* __restrict__ idx, int div, long long rows,
-    long long src_rows, const int32_t* __restrict__ nvalid, int n8, int pairs, int pairs_each,
+    long long src_rows, const int32_t* __restrict__ nvalid, int n8, int quads, int quads_each,
     uint2* __restrict__ q, float* __restrict__ scale, uint4* __restrict__ copy,
     int* __restrict__ status) {
+  // the kernel before may have written what is read here; the next one may set itself up
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   const int lane = threadIdx.x & 31;
   const long long warp0 = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   const long long warps = (static_cast<long long>(gridDim.x) * kRowThreads) >> 5;
@@ -50,8 +55,9 @@ __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
     const long long nv = __ldg(nvalid);
     last = nv < rows ? nv : rows;
   }
-  const int first_pair = blockIdx.y * pairs_each;
-  const int end_pair = min(first_pair + pairs_each, pairs);
+  const int first_quad = blockIdx.y * quads_each;
+  const int end_quad = min(first_quad + quads_each, quads);
+  const int c0 = (lane >> 3) * 16 + (lane & 7);  // this lane's first piece of a quad; then + 8
   for (long long p = warp0; p < last; p += warps) {
     long long src = p;
     if (idx) {
@@ -61,27 +67,32 @@ __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
     const bool bad = src < 0 || src >= src_rows;
     if (bad && lane == 0 && blockIdx.y == 0) report_bad_index(status);
     const uint4* from = in + (bad ? 0 : src) * n8;
-    for (int j0 = first_pair; j0 < end_pair; j0 += kRowAhead) {
-      uint4 w[kRowAhead];
+    for (int j0 = first_quad; j0 < end_quad; j0 += kRowAhead) {
+      uint4 w[kRowAhead][2];
+#pragma unroll
+      for (int i = 0; i < kRowAhead; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = (j0 + i) * 64 + c0 + 8 * h;
+          w[i][h] = (!bad && j0 + i < end_quad && c < n8) ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
       for (int i = 0; i < kRowAhead; ++i) {
-        const int c = (j0 + i) * 32 + lane;
-        w[i] = (!bad && j0 + i < end_pair && c < n8) ? __ldg(from + c) : make_uint4(0, 0, 0, 0);
-      }
+        if (j0 + i >= end_quad) break;  // the same for the whole warp
+        uint32_t top = max(top8(w[i][0]), top8(w[i][1]));
 #pragma unroll
-      for (int i = 0; i < kRowAhead; ++i) {
-        if (j0 + i >= end_pair) break;  // the same for the whole warp
-        const int c = (j0 + i) * 32 + lane;
-        uint32_t top = top8(w[i]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+        for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
         const BlockScale b = block_scale(top);
-        if (c >= n8) continue;
-        uint2 codes;
-        codes8(w[i], b, codes);
-        q[p * n8 + c] = codes;
-        if (copy) copy[p * n8 + c] = w[i];
-        if ((lane & 15) == 0) scale[static_cast<long long>(c >> 4) * ld + p] = b.s;
+        const int c = (j0 + i) * 64 + c0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (c + 8 * h < n8) {
+            uint2 codes;
+            codes8(w[i][h], b, codes);
+            q[p * n8 + c + 8 * h] = codes;
+            if (copy) copy[p * n8 + c + 8 * h] = w[i][h];
+          }
+        if ((lane & 7) == 0 && c < n8) scale[static_cast<long long>(c >> 4) * ld + p] = b.s;
       }
     }
   }
@@ -132,20 +143,28 @@ cudaError_t launch_quant_rows_block(const uint16_t* in, const int32_t* idx, int 
                                     float* scale, int num_sms, cudaStream_t s,
                                     const int32_t* nvalid, uint16_t* copy, int* status) {
   if (rows == 0) return cudaSuccess;
-  const int pairs = (n + 2 * kBlock - 1) / (2 * kBlock);
+  const int quads = (n + 4 * kBlock - 1) / (4 * kBlock);
   const long long row_blocks = (rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
   const long long cap = 8ll * num_sms;
   const int gx = static_cast<int>(row_blocks < cap ? row_blocks : cap);
-  // a row's pairs over several blocks while the rows alone do not fill the SMs
+  // a row's quads over several blocks while the rows alone do not fill the SMs
   int split = static_cast<int>((cap + gx - 1) / gx);
-  const int most = (pairs + kRowAhead - 1) / kRowAhead;
-  if (split > most) split = most;
-  const int each = (pairs + split - 1) / split;
-  const dim3 grid(gx, (pairs + each - 1) / each, 1);
-  quant_rows_block_kernel<<<grid, kRowThreads, 0, s>>>(
-      reinterpret_cast<const uint4*>(in), idx, idx ? div : 1, rows, src_rows, nvalid, n / 8, pairs,
-      each, reinterpret_cast<uint2*>(q), scale, reinterpret_cast<uint4*>(copy), status);
-  return launched();
+  if (split > quads) split = quads;
+  const int each = (quads + split - 1) / split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(gx, (quads + each - 1) / each, 1);
+  cfg.blockDim = dim3(kRowThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, quant_rows_block_kernel, reinterpret_cast<const uint4*>(in), idx, idx ? div : 1, rows,
+      src_rows, nvalid, n / 8, quads, each, reinterpret_cast<uint2*>(q), scale,
+      reinterpret_cast<uint4*>(copy), status);
+  return e == cudaSuccess ? launched() : e;
 }
 
 cudaError_t launch_quant_weights_block(const uint16_t* W, int E, int K, int N, uint8_t* q,
