@@ -1018,11 +1018,11 @@ moe_status moe_layer_fwd_fp8_block(const moe_dims* dims, const moe_bf16* x, cons
   if (R > 0) {
     const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms(),
                               at<float>(ws, L.part)};
-    MOE_RUN(moe::block_fc1_fwd(r, {Xq, sx}, {W1q, s1}, {W3q, s3}, {W2q, s2}, d.h, d.f,
+    MOE_RUN(moe::block_fc1_fwd(r, {Xq, sx}, {W1q, s1}, {W3q, s3}, d.h, d.f,
                                at<uint16_t>(saved, S.A), at<uint16_t>(saved, S.B),
                                at<uint16_t>(saved, S.H), Hq, sh, stream),
             "block_fc1_fwd");
-    MOE_RUN(moe::block_product(r, {Hq, sh}, {W2q, s2}, d.f, d.h, false, false, O, stream),
+    MOE_RUN(moe::block_product(r, {Hq, sh}, {W2q, s2}, d.f, d.h, false, false, O, stream, true),
             "block_fc2_fwd");
   }
   MOE_RUN(moe::launch_combine(O, gates, pdst, d.T, d.k, d.h, y, num_sms(), stream,

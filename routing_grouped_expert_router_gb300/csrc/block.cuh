@@ -47,18 +47,20 @@ struct Coded {
   const float* s;
 };
 // C = A B[e] (trans: A B[e]^T, B [E, N, K]); C [rows, N] bf16 or fp32.
+// ahead: the launch just before on the stream is one of block_fc1_fwd, so that weights and
+// offsets may be read before it ends (few rows).
 cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
-                          bool trans, bool out_f32, void* C, cudaStream_t s);
+                          bool trans, bool out_f32, void* C, cudaStream_t s, bool ahead = false);
 // A = X W1, B = X W3, H = silu(A) * B with the codes of bf16(H); A, B, H may be NULL.
-// w2: the weight of the product that follows, brought to L2 towards the end (few rows).
+// The launch just before on the stream is launch_quant_rows_block's of x.
 cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
-                          const Coded& w2, int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
+                          int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                           float* sh, cudaStream_t s);
 // The same for few rows.
 cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
-                        bool trans, bool out_f32, void* C, cudaStream_t s);
+                        bool trans, bool out_f32, void* C, cudaStream_t s, bool ahead);
 cudaError_t few_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
-                        const Coded& w2, int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
+                        int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                         float* sh, cudaStream_t s);
 // dH = dY W2^T, fused with the SwiGLU backward: dA, dB in bf16 and their codes.
 cudaError_t block_fc2_dgrad(const BlockRows& r, const Coded& dy, const Coded& w2, int h, int f,

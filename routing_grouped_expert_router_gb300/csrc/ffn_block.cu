@@ -15,7 +15,6 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int32_t kMaxSide = 1 << 20;
-constexpr int kMaxGroups = 64;
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool ptr_ok(const void* p) { return p && aligned(p, 16); }
@@ -43,7 +42,7 @@ bool tiles_fit(int rows, int E, int n) {
 moe_status check_gemm(const moe_gemm_dims* d) {
   if (!d || d->rows < 0 || d->K <= 0 || d->N <= 0 || d->E <= 0) return MOE_ERR_INVALID_ARG;
   if ((d->trans_b | 1) != 1 || (d->out_f32 | 1) != 1) return MOE_ERR_INVALID_ARG;
-  if (d->E > kMaxGroups || d->K % 16 != 0 || d->N % 16 != 0 || d->K > kMaxSide ||
+  if (d->E > 64 || d->K % 16 != 0 || d->N % 16 != 0 || d->K > kMaxSide ||
       d->N > kMaxSide || !tiles_fit(d->rows, d->E, d->N))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -52,7 +51,7 @@ moe_status check_gemm(const moe_gemm_dims* d) {
 moe_status check_ffn(const moe_ffn_dims* d) {
   if (!d || d->rows < 0 || d->h <= 0 || d->f <= 0 || d->E <= 0 || (d->dw_bf16 | 1) != 1)
     return MOE_ERR_INVALID_ARG;
-  if (d->E > kMaxGroups || d->h % 64 != 0 || d->f % 64 != 0 || d->h > kMaxSide ||
+  if (d->E > 64 || d->h % 64 != 0 || d->f % 64 != 0 || d->h > kMaxSide ||
       d->f > kMaxSide || !tiles_fit(d->rows, d->E, d->h) || !tiles_fit(d->rows, d->E, d->f))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -155,10 +154,10 @@ moe_status moe_gated_ffn_fwd(const moe_ffn_dims* dims, const moe_bf16* x, const 
                                          stream, offsets ? offsets + d.E : nullptr, nullptr,
                                          r.status),
             "quant_rows_block");
-  BLOCK_RUN(moe::block_fc1_fwd(r, {xq, sx}, {W1q, s1}, {W3q, s3}, {W2q, s2}, d.h, d.f, A, B, H, hq, sh,
+  BLOCK_RUN(moe::block_fc1_fwd(r, {xq, sx}, {W1q, s1}, {W3q, s3}, d.h, d.f, A, B, H, hq, sh,
                                stream),
             "block_fc1_fwd");
-  BLOCK_RUN(moe::block_product(r, {hq, sh}, {W2q, s2}, d.f, d.h, false, false, y, stream),
+  BLOCK_RUN(moe::block_product(r, {hq, sh}, {W2q, s2}, d.f, d.h, false, false, y, stream, true),
             "block_fc2_fwd");
   return MOE_OK;
 }

@@ -30,6 +30,7 @@
 #include <cstring>
 
 #include "block.cuh"
+#include "block_groups.cuh"
 #include "block_quant.cuh"
 #include "grouped_gemm.cuh"
 #include "kernels.cuh"
@@ -42,7 +43,6 @@ namespace {
 enum Form { PLAIN_BF16 = 0, PLAIN_F32 = 1, GATED = 2, GATED_BWD = 3 };
 
 constexpr int kTimeoutCode = 5;   // MOE_ERR_DEVICE_TIMEOUT
-constexpr int MAX_E = 64;
 constexpr int PM = 256;           // rows of a pair's tile
 constexpr int NUM_THREADS = 384;
 // Registers of a thread: 168 at launch (3 x 168 x 128 = 64512), then 56 for warps 0-3 and
@@ -113,8 +113,8 @@ struct alignas(16) Ctrl {
   uint64_t met;             // the sum warps, once for each tile (TOPS)
   uint64_t drain;
   uint32_t tmem_base;
-  int off[MAX_E + 1];
-  int cum[MAX_E + 1];       // row tiles before each group
+  int off[kMaxGroups + 1];
+  int cum[kMaxGroups + 1];       // row tiles before each group
   Slot slots[SLOTS];
   uint16_t tops[S::TOPS ? 2 * S::TOPS * 256 : 1];  // bf16 patterns [tile parity][value][side][row]
 };
@@ -363,24 +363,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_relinquish2();
     tc_fence_before();
   }
-  if (warp >= FIRST_SUM_WARP) {
-    for (int e = threadIdx.x - 32 * FIRST_SUM_WARP; e <= p.E; e += 256)
-      c.off[e] = p.offsets ? __ldg(p.offsets + e) : (e ? p.rows : 0);
-  }
-  __syncthreads();
-  if (threadIdx.x == 32 * FIRST_SUM_WARP) {
-    // clamped into order, so that every access stays inside its buffer
-    bool bad = c.off[0] != 0;
-    for (int e = 0; e <= p.E; ++e) {
-      const int o = c.off[e], low = e ? c.off[e - 1] : 0;
-      const int in = min(max(o, low), p.rows);
-      bad = bad || in != o;
-      c.off[e] = in;
-    }
-    if (bad) report_bad_index(p.status);
-    c.cum[0] = 0;
-    for (int e = 0; e < p.E; ++e) c.cum[e + 1] = c.cum[e] + (c.off[e + 1] - c.off[e] + PM - 1) / PM;
-  }
+  if (warp == FIRST_SUM_WARP)
+    group_tables(p.offsets, p.E, p.rows, PM, c.off, c.cum, p.status, lane);
   cluster_sync_all();  // both CTAs' barriers exist before any arrival from the other
   tc_fence_after();
   constexpr uint32_t tmem_base = 0;  // all 512 columns are this block's
@@ -852,9 +836,9 @@ bool map_weight(CUtensorMap* m, const void* q, int E, int K, int N, bool trans, 
 }  // namespace
 
 cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
-                          bool trans, bool out_f32, void* C, cudaStream_t s) {
+                          bool trans, bool out_f32, void* C, cudaStream_t s, bool ahead) {
   if (r.rows == 0) return cudaSuccess;
-  if (few_rows(r.rows, r.E)) return few_product(r, a, b, K, N, trans, out_f32, C, s);
+  if (few_rows(r.rows, r.E)) return few_product(r, a, b, K, N, trans, out_f32, C, s, ahead);
   Params p = params_of(r, K, N, trans);
   p.sa[0] = a.s;
   p.sb[0] = b.s;
@@ -873,10 +857,10 @@ cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, in
 }
 
 cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
-                          const Coded& w2, int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
+                          int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                           float* sh, cudaStream_t s) {
   if (r.rows == 0) return cudaSuccess;
-  if (few_rows(r.rows, r.E)) return few_fc1_fwd(r, x, w1, w3, w2, h, f, A, B, H, Hq, sh, s);
+  if (few_rows(r.rows, r.E)) return few_fc1_fwd(r, x, w1, w3, h, f, A, B, H, Hq, sh, s);
   Params p = params_of(r, h, f, false);
   p.sa[0] = x.s;
   p.sb[0] = w1.s;

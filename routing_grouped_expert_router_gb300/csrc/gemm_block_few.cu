@@ -21,17 +21,12 @@
 #include <cstring>
 
 #include "block.cuh"
+#include "block_groups.cuh"
 #include "block_quant.cuh"
 #include "grouped_gemm.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 
-#ifndef V_HALF
-#define V_HALF 1
-#endif
-#ifndef V_EARLY
-#define V_EARLY 8
-#endif
 namespace moe {
 
 namespace {
@@ -39,7 +34,6 @@ namespace {
 enum Form { PLAIN_BF16 = 0, PLAIN_F32 = 1, GATED = 2 };
 
 constexpr int kTimeoutCode = 5;  // MOE_ERR_DEVICE_TIMEOUT
-constexpr int MAX_E = 64;
 constexpr int MAX_BLOCKS = 160;  // of the grid
 constexpr int NUM_THREADS = 256;
 constexpr int W_BYTES = 128 * 128;
@@ -58,12 +52,12 @@ struct Params {
   float* scales;
   float* part;              // [grid, 2] slots of a shared tile's sums
   uint32_t* arrived;        // a byte for each block of the grid: pieces of its last tile
-  int next_n, next_nkb;     // that product's columns and blocks; not transposed
+  int ahead;                // the kernel before (which has waited for all before it) writes
+                            // neither the weights nor the offsets
   int* status;
 };
 struct Maps {
   CUtensorMap x, w[2];
-  CUtensorMap next;         // the weight of the product that follows (next_n > 0)
 };
 
 template <int FORM, int NT>
@@ -73,10 +67,7 @@ struct Shape {
   static constexpr int STAGE_BYTES = NB * W_BYTES + X_BYTES;
   static constexpr int UNIT = NB * NT;               // accumulator columns of a step
   static constexpr int PITCH = (FORM == PLAIN_F32 ? 512 : 256) + 16;  // staging: bytes of a row
-  // Two blocks fit an SM where two or more stages do in half of it: the next kernel of the
-  // stream then sets itself up beside the last blocks of this one.
-  static constexpr bool HALF = V_HALF && (NT == 16 || (NT == 32 && NB == 1));
-  static constexpr int FIT = ((HALF ? 114688 : 232448) - 1024 - NT * PITCH - 3072) / STAGE_BYTES;
+  static constexpr int FIT = (232448 - 1024 - NT * PITCH - 3072) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 12 ? 12 : FIT;
   static constexpr int BUFS = 4 * UNIT > 256 ? 2 : 4;  // steps whose sums wait in tensor memory
   static constexpr int TMEM = BUFS * UNIT;           // columns (a power of two, 64 to 256)
@@ -96,8 +87,8 @@ struct alignas(16) Ctrl {
   uint64_t met, drain;
   uint32_t tmem_base;
   uint32_t last;            // whether this block joins the tile
-  int off[MAX_E + 1];
-  int cum[MAX_E + 1];       // row tiles before each group
+  int off[kMaxGroups + 1];
+  int cum[kMaxGroups + 1];       // row tiles before each group
   Slot<NT> slots[SLOTS];
 };
 template <int FORM, int NT>
@@ -109,17 +100,14 @@ constexpr int smem_bytes() {
 struct Tile {
   int e, n, row0, row_end;  // group, column tile, rows
 };
-// Steps of the next product that each block brings to L2 after its own loads: 384 KiB of
-// codes, 57 MB over all SMs, what HBM moves while a tile is joined and the next kernel
-// starts up.
-constexpr int kNextSteps = 24;
-constexpr int kEarlySteps = V_EARLY;  // 16 KiB blocks of weights asked for before the kernel before has ended
+// Steps of weights that a block asks L2 for before the kernel before has ended.
+constexpr int kEarlySteps = 8;
 
 // Tile t: groups in order; in one, column tiles in order; row tiles of a column tile
 // side by side, so that they find the weight in L2.
 template <int NT>
-__device__ __forceinline__ Tile place(const Params& p, int N, const int* off, const int* cum, int t) {
-  const int tiles_n = (N + 127) / 128;
+__device__ __forceinline__ Tile place(const Params& p, const int* off, const int* cum, int t) {
+  const int tiles_n = (p.N + 127) / 128;
   int e = 0, hi = p.E - 1;
   while (e < hi) {
     const int mid = (e + hi + 1) >> 1;
@@ -224,46 +212,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_relinquish();
     tc_fence_before();
   }
-  // One group: the steps are known before its rows are, and the weights can come to L2 while
-  // the kernel before ends (should it write them, L2 has what it wrote).
-  if (warp == LOAD_W && p.E == 1) {
-    Share guess;
-    guess.steps = static_cast<long long>((p.N + 127) / 128) * ((p.rows + NT - 1) / NT) * p.nkb;
-    guess.blocks = static_cast<int>(guess.steps < gridDim.x ? guess.steps : gridDim.x);
-    if (static_cast<int>(blockIdx.x) < guess.blocks) {
-      const long long from = guess.lo(blockIdx.x);
-      const long long to = min(guess.lo(blockIdx.x + 1), from + kEarlySteps / S::NB);
-      if (elect_one())
-        for (long long i = from; i < to; ++i) {
-          const int n = static_cast<int>(i / p.nkb) / ((p.rows + NT - 1) / NT) * 128;
-          const int k = static_cast<int>(i % p.nkb) * kBlock;
-          for (int o = 0; o < S::NB; ++o)
-            tma_prefetch_l2_3d(&maps.w[o], TRANS ? k : n, TRANS ? n : k, 0);
-        }
+  if (!p.ahead) {
+    // One group: the steps are known before its rows are, and the weights can come to L2 while
+    // the kernel before ends (should it write them, L2 has what it wrote).
+    if (warp == LOAD_W && p.E == 1) {
+      Share guess;
+      guess.steps = static_cast<long long>((p.N + 127) / 128) * ((p.rows + NT - 1) / NT) * p.nkb;
+      guess.blocks = static_cast<int>(guess.steps < gridDim.x ? guess.steps : gridDim.x);
+      if (static_cast<int>(blockIdx.x) < guess.blocks) {
+        const long long from = guess.lo(blockIdx.x);
+        const long long to = min(guess.lo(blockIdx.x + 1), from + kEarlySteps);
+        if (elect_one())
+          for (long long i = from; i < to; ++i) {
+            const int n = static_cast<int>(i / p.nkb) / ((p.rows + NT - 1) / NT) * 128;
+            const int k = static_cast<int>(i % p.nkb) * kBlock;
+            tma_prefetch_l2_3d(&maps.w[0], TRANS ? k : n, TRANS ? n : k, 0);
+          }
+      }
+      __syncwarp();
     }
-    __syncwarp();
+    // the kernel before may have written all that is read from here on
+    cudaGridDependencySynchronize();
   }
-  // the kernel before may have written all that is read from here on; the next one may begin
-  // its own set-up
-  cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();
-  if (warp >= FIRST_SUM_WARP) {
-    for (int e = threadIdx.x - 32 * FIRST_SUM_WARP; e <= p.E; e += 128)
-      c.off[e] = p.offsets ? __ldg(p.offsets + e) : (e ? p.rows : 0);
-  }
-  __syncthreads();
-  if (threadIdx.x == 32 * FIRST_SUM_WARP) {
-    bool bad = c.off[0] != 0;  // clamped into order, so that every access stays inside its buffer
-    for (int e = 0; e <= p.E; ++e) {
-      const int o = c.off[e], low = e ? c.off[e - 1] : 0;
-      const int in = min(max(o, low), p.rows);
-      bad = bad || in != o;
-      c.off[e] = in;
-    }
-    if (bad) report_bad_index(p.status);
-    c.cum[0] = 0;
-    for (int e = 0; e < p.E; ++e) c.cum[e + 1] = c.cum[e] + (c.off[e + 1] - c.off[e] + NT - 1) / NT;
-  }
+  if (warp == FIRST_SUM_WARP)
+    group_tables(p.offsets, p.E, p.rows, NT, c.off, c.cum, p.status, lane);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = c.tmem_base;
@@ -278,6 +250,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   int t = count ? static_cast<int>(lo / nkb) : 0;
   int kb = count ? static_cast<int>(lo - static_cast<long long>(t) * nkb) : 0;
 
+  // Ahead of the end of the kernel before, the weights stream in; what it writes (the
+  // activations, their scales, the slots of shared tiles) waits for it.  The kernel after
+  // this one may start once all before this one are done.
+  if (p.ahead && warp != LOAD_W && warp != ISSUE) cudaGridDependencySynchronize();
+  if (warp == FIRST_SUM_WARP) cudaTriggerProgrammaticLaunchCompletion();
+
   if (warp == LOAD_W || warp == LOAD_X) {
     // -------------------------------------------------------- TMA producers
     const bool one = elect_one();
@@ -286,7 +264,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     Tile tl = {};
     for (int i = 0; i < count; ++i) {
-      if (i == 0 || kb == 0) tl = place<NT>(p, p.N, c.off, c.cum, t);
+      if (i == 0 || kb == 0) tl = place<NT>(p, c.off, c.cum, t);
       ok = wait_all(&c.empty[s], ph, p.status);
       if (!ok) break;
       if (one) {
@@ -313,24 +291,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (++kb == nkb) {
         kb = 0;
         ++t;
-      }
-    }
-    if (ok && warp == LOAD_W && p.next_n > 0) {
-      Share after;
-      after.steps = static_cast<long long>((p.next_n + 127) / 128) * c.cum[p.E] * p.next_nkb;
-      after.blocks = static_cast<int>(after.steps < gridDim.x ? after.steps : gridDim.x);
-      if (me < after.blocks) {
-        const long long from = after.lo(me), to = min(after.lo(me + 1), from + kNextSteps);
-        int at = static_cast<int>(from / p.next_nkb);
-        int k = static_cast<int>(from - static_cast<long long>(at) * p.next_nkb);
-        for (long long i = from; i < to; ++i) {
-          if (i == from || k == 0) tl = place<NT>(p, p.next_n, c.off, c.cum, at);
-          if (one) tma_prefetch_l2_3d(&maps.next, tl.n * 128, k * kBlock, tl.e);
-          if (++k == p.next_nkb) {
-            k = 0;
-            ++at;
-          }
-        }
       }
     }
     if (!ok) {
@@ -383,7 +343,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t ph = 1;
     Tile tl = {};
     for (int n = 0; n < count; ++n) {
-      if (n == 0 || kb == 0) tl = place<NT>(p, p.N, c.off, c.cum, t);
+      if (n == 0 || kb == 0) tl = place<NT>(p, c.off, c.cum, t);
       if (!wait_all(&c.sempty[i], ph, p.status)) break;
       // indexes fit 32 bits: a scale stands for 128 bytes of codes or more
 #pragma unroll
@@ -425,7 +385,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     int left = count;
     while (ok && left > 0) {
-      const Tile tl = place<NT>(p, p.N, c.off, c.cum, t);
+      const Tile tl = place<NT>(p, c.off, c.cum, t);
       const int n = min(nkb - kb, left);  // this block's steps of the tile
       float sums[S::NB][NT];
 #pragma unroll
@@ -602,7 +562,8 @@ cudaError_t launch(int nt, const Params& p, const Maps& m, int num_sms, cudaStre
                     : launch<FORM, 64, TRANS>(p, m, num_sms, s);
 }
 
-bool fill(Params& p, Maps& m, const BlockRows& r, const Coded& x, int K, int N, bool trans, int nt) {
+bool fill(Params& p, Maps& m, const BlockRows& r, const Coded& x, int K, int N, bool trans, int nt,
+          bool ahead) {
   memset(&p, 0, sizeof(p));
   memset(&m, 0, sizeof(m));
   p.E = r.E;
@@ -617,6 +578,7 @@ bool fill(Params& p, Maps& m, const BlockRows& r, const Coded& x, int K, int N, 
   p.part = r.part;
   p.arrived = reinterpret_cast<uint32_t*>(r.status) + 16;  // bytes 64 .. 223 of the header
   p.status = r.status;
+  p.ahead = ahead;
   return make_map_kmajor(&m.x, x.q, K, r.rows, nt, true);
 }
 bool map_weight(CUtensorMap* m, const void* q, int E, int K, int N, bool trans) {
@@ -631,11 +593,11 @@ size_t few_part_bytes(int rows, int E, int weights) {
 }
 
 cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N, bool trans,
-                        bool out_f32, void* C, cudaStream_t s) {
+                        bool out_f32, void* C, cudaStream_t s, bool ahead) {
   Params p;
   Maps m;
   const int nt = tile_rows(r.rows, r.E);
-  if (!fill(p, m, r, a, K, N, trans, nt) || !map_weight(&m.w[0], b.q, r.E, K, N, trans))
+  if (!fill(p, m, r, a, K, N, trans, nt, ahead) || !map_weight(&m.w[0], b.q, r.E, K, N, trans))
     return cudaErrorInvalidValue;
   p.sb[0] = p.sb[1] = b.s;
   p.out[0] = C;
@@ -647,17 +609,14 @@ cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int 
 }
 
 cudaError_t few_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, const Coded& w3,
-                        const Coded& w2, int h, int f, uint16_t* A, uint16_t* B, uint16_t* H,
+                        int h, int f, uint16_t* A, uint16_t* B, uint16_t* H,
                         uint8_t* Hq, float* sh, cudaStream_t s) {
   Params p;
   Maps m;
   const int nt = tile_rows(r.rows, r.E);
-  if (!fill(p, m, r, x, h, f, false, nt) || !map_weight(&m.w[0], w1.q, r.E, h, f, false) ||
-      !map_weight(&m.w[1], w3.q, r.E, h, f, false) ||
-      !map_weight(&m.next, w2.q, r.E, f, h, false))
+  if (!fill(p, m, r, x, h, f, false, nt, true) || !map_weight(&m.w[0], w1.q, r.E, h, f, false) ||
+      !map_weight(&m.w[1], w3.q, r.E, h, f, false))
     return cudaErrorInvalidValue;
-  p.next_n = h;
-  p.next_nkb = blocks_of(f);
   p.sb[0] = w1.s;
   p.sb[1] = w3.s;
   p.out[0] = A;

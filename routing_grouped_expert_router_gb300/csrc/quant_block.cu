@@ -43,9 +43,10 @@ __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
     long long src_rows, const int32_t* __restrict__ nvalid, int n8, int quads, int quads_each,
     uint2* __restrict__ q, float* __restrict__ scale, uint4* __restrict__ copy,
     int* __restrict__ status) {
-  // the kernel before may have written what is read here; the next one may set itself up
-  cudaTriggerProgrammaticLaunchCompletion();
+  // The kernel before may have written what is read here.  The next one may start once all
+  // before this one are done: it can read what neither this one nor itself writes.
   cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
   const int lane = threadIdx.x & 31;
   const long long warp0 = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   const long long warps = (static_cast<long long>(gridDim.x) * kRowThreads) >> 5;
