@@ -64,4 +64,15 @@ __device__ __forceinline__ uint32_t top_of_pair(uint32_t top, uint32_t w) {
   return max(top, max(hi, lo));
 }
 
+// The same for two columns of pairs at once: the larger magnitudes of w's two bf16 and of
+// top's, each in its half (a NaN stays one), and the larger of the two halves as a pattern.
+__device__ __forceinline__ uint32_t top_2(uint32_t top, uint32_t w) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(w & 0x7FFF7FFFu));
+  return r;
+}
+__device__ __forceinline__ uint32_t top_of_2(uint32_t top) {
+  return max(top << 16, top & 0xFFFF0000u);
+}
+
 }  // namespace moe

@@ -45,9 +45,6 @@ enum Form { PLAIN_BF16 = 0, PLAIN_F32 = 1, GATED = 2, GATED_BWD = 3 };
 constexpr int kTimeoutCode = 5;   // MOE_ERR_DEVICE_TIMEOUT
 constexpr int PM = 256;           // rows of a pair's tile
 constexpr int NUM_THREADS = 384;
-// Registers of a thread: 168 at launch (3 x 168 x 128 = 64512), then 56 for warps 0-3 and
-// 224 for the others, 504 x 128 again.
-constexpr int FEW_REGS = 56, MANY_REGS = 224;
 constexpr int FIRST_SUM_WARP = 4;
 constexpr int SUM_WARPS = 8;
 constexpr int LOAD_A = 0, ISSUE = 1, LOAD_B = 2, SCALES = 3;  // warps
@@ -93,6 +90,10 @@ struct Shape {
   static constexpr int STAGE_BYTES = A_BYTES + B_COLS * 128;
   static constexpr int STAGES = NH == 2 ? 4 : 6;
   static constexpr int BUFS = 512 / COLS;               // accumulators in tensor memory
+  // Registers of a thread: 168 at launch (3 x 168 x 128 = 64512), then FEW for warps 0-3 and
+  // MANY for the others, 504 x 128 again.  What the sums spill costs more than what the
+  // others do: 789 against 725 us for the product of 16384 x 4096 x 14336.
+  static constexpr int FEW = FORM == GATED_BWD ? 56 : 40, MANY = (504 - FEW) / 2;
   static constexpr int SETS = 4;                        // of a warp
   static constexpr int TOPS = FORM == GATED ? 1 : FORM == GATED_BWD ? 2 : 0;
 };
@@ -191,8 +192,8 @@ __device__ __forceinline__ void add_32(const float (&v)[32], float scale, float*
 #pragma unroll
   for (int i = 0; i < 32; ++i) sums[i] = fmaf(v[i], scale, sums[i]);
 }
-// sigmoid and silu with the fast exponential and quotient: their few ulps are
-// far below the bf16 rounding of all that is stored.
+// sigmoid and silu with the fast exponential and quotient: their few ulps are far below the
+// bf16 rounding of all that is stored.  (Two sigmoids with one reciprocal were slower.)
 __device__ __forceinline__ float sigmoid_f(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
 __device__ __forceinline__ float silu_f(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // Every wait below is bounded: a role whose wait runs out records it and ends, and those
   // that wait for it do the same.
   if (warp < FIRST_SUM_WARP) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW_REGS));
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::FEW));
   if (warp == LOAD_A || warp == LOAD_B) {
     // ------------------------------------------------------ TMA producers
     const bool is_a = warp == LOAD_A;
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MANY_REGS));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::MANY));
     // ------------------------------------------- sums and epilogue (8 warps)
     const int quarter = warp & 3;                    // TMEM lanes this warp may read
     const int side = (warp - FIRST_SUM_WARP) >> 2;   // which 64 columns of each half
@@ -648,9 +649,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int j = 0; j < 32; ++j) {
             w[j] = pack_bf16(silu_f(sums[0][2 * j]) * sums[1][2 * j],
                              silu_f(sums[0][2 * j + 1]) * sums[1][2 * j + 1]);
-            top = top_of_pair(top, w[j]);
+            top = top_2(top, w[j]);
           }
         }
+        top = top_of_2(top);
         uint16_t* tops = c.tops + (it & 1) * 256;
         tops[side * 128 + trow] = static_cast<uint16_t>(top >> 16);
         __syncwarp();
@@ -677,30 +679,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (col0 < p.N) {
           if (!(ok = wait_all(smem_u32(&c.ab[warp - FIRST_SUM_WARP]), had & 1, p.status))) break;
           ++had;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 4; ++i0) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int at = (j >> 2) * (SET_BYTES / 16) + slot_of(lane, j & 3);
-            const uint4 ra = sa[at], rb = sb[at];
-            const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-            uint32_t da[4], db[4];
+            for (int i1 = 0; i1 < 2; ++i1) {
+              const int j = 2 * i0 + i1;
+              const int at = (j >> 2) * (SET_BYTES / 16) + slot_of(lane, j & 3);
+              const uint4 ra = sa[at], rb = sb[at];
+              const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+              uint32_t da[4], db[4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const float* dh = sums[0] + 8 * j + 2 * m;
-              const float av[2] = {lo_of(wa[m]), hi_of(wa[m])}, bv[2] = {lo_of(wb[m]), hi_of(wb[m])};
-              float xa[2], xb[2];
+              for (int m = 0; m < 4; ++m) {
+                const float* dh = sums[0] + 8 * i1 + 2 * m;
+                const float av[2] = {lo_of(wa[m]), hi_of(wa[m])}, bv[2] = {lo_of(wb[m]), hi_of(wb[m])};
+                float xa[2], xb[2];
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float sg = sigmoid_f(av[k]);
-                xa[k] = dh[k] * bv[k] * sg * (1.0f + av[k] * (1.0f - sg));
-                xb[k] = dh[k] * av[k] * sg;
+                for (int k = 0; k < 2; ++k) {
+                  const float sg = sigmoid_f(av[k]);
+                  const float dhs = dh[k] * sg;
+                  xa[k] = dhs * bv[k] * (1.0f + av[k] * (1.0f - sg));
+                  xb[k] = dhs * av[k];
+                }
+                da[m] = pack_bf16(xa[0], xa[1]);
+                db[m] = pack_bf16(xb[0], xb[1]);
+                top_a = top_2(top_a, da[m]);
+                top_b = top_2(top_b, db[m]);
               }
-              da[m] = pack_bf16(xa[0], xa[1]);
-              db[m] = pack_bf16(xb[0], xb[1]);
-              top_a = top_of_pair(top_a, da[m]);
-              top_b = top_of_pair(top_b, db[m]);
+              sa[at] = make_uint4(da[0], da[1], da[2], da[3]);
+              sb[at] = make_uint4(db[0], db[1], db[2], db[3]);
             }
-            sa[at] = make_uint4(da[0], da[1], da[2], da[3]);
-            sb[at] = make_uint4(db[0], db[1], db[2], db[3]);
+            // the next 16 sums move down (unrolled over all 64 columns this loop was slower)
+#pragma unroll
+            for (int m = 0; m < 48; ++m) sums[0][m] = sums[0][m + 16];
           }
           if (all_ok) {
             fence_proxy_async_smem();
@@ -714,6 +724,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
         }
+        top_a = top_of_2(top_a);
+        top_b = top_of_2(top_b);
         uint16_t* tops = c.tops + (it & 1) * 512;
         tops[side * 128 + trow] = static_cast<uint16_t>(top_a >> 16);
         tops[256 + side * 128 + trow] = static_cast<uint16_t>(top_b >> 16);
@@ -729,10 +741,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             p.scales[1][static_cast<size_t>(nb) * p.rows + row] = bb.s;
           }
           const size_t o = static_cast<size_t>(row) * p.N + col0;
-#pragma unroll
+#pragma unroll 1
           for (int v = 0; v < 2; ++v) {
             const uint4* set = v ? sb : sa;
-            const BlockScale& b = v ? bb : ba;
+            const BlockScale b = v ? bb : ba;
             uint4* d = reinterpret_cast<uint4*>(p.codes[v] + o);
             uint4* keep = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[v]) + o);
 #pragma unroll
