@@ -210,7 +210,7 @@ WsLayout ws_layout(const moe_dims& d, int op) {
       L.sx = c.take(R * hb * 4);
       L.Hq = c.take(R * d.f);
       L.sh = c.take(R * fb * 4);
-      L.part = c.take(moe::few_part_bytes(static_cast<int>(R), d.E, 2));
+      L.part = c.take(moe::few_part_bytes(static_cast<int>(R), d.E));
       break;
     case MOE_OP_LAYER_BWD_FP8_BLOCK:
       if (d.sar) return WsLayout{};

@@ -33,14 +33,22 @@ struct BlockRows {
   int rows;
   int* status;    // device status word, at the start of the workspace's 256-byte header
   int num_sms;
-  float* part;    // few_part_bytes(rows, E, weights) bytes
+  float* part;    // few_part_bytes(rows, E) bytes
 };
-// Whether a group's rows are so few that reading the weights bounds the product
-// (gemm_block_few.cu).  Up to 64 rows to a group on average; what that costs and saves
-// stands at block_product.
-inline bool few_rows(int rows, int E) { return rows <= 64ll * E; }
+// Whether a group's rows are so few that gemm_block_few.cu's kernel is the faster one.  Times
+// in us, few rows' kernel against the pairs' (each in a graph, weights not in L2):
+//   rows to a group           1          16         32         64
+//   4096 x 14336, 1 group     18 : 26    21 : 20    24 : 19    35 : 20
+//   2048 x 1408, 1 group      9 : 11     10 : 11    13 : 11    20 : 12
+//   4096 x 14336, 8 groups    78 : 117   84 : 94    91 : 96    99 : 98
+//   2048 x 1408, 64 groups    43 : 50    49 : 52    58 : 53    66 : 54
+//   14336 x 4096, 1 group     19 : 47    25 : 47    33 : 48    54 : 48
+// A long contraction with few columns leaves most pairs idle: there it stays ahead longer.
+inline bool few_rows(int rows, int E, int K, int N) {
+  return rows <= 16ll * E || (rows <= 48ll * E && K >= 8192 && E * blocks_of(N) <= 64);
+}
 // Grows with rows, so that a workspace for the most rows serves fewer.
-size_t few_part_bytes(int rows, int E, int weights);
+size_t few_part_bytes(int rows, int E);
 // Codes and scales of an activation or a weight.
 struct Coded {
   const uint8_t* q;

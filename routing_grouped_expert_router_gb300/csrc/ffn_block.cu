@@ -75,7 +75,7 @@ FfnLayout ffn_layout(const moe_ffn_dims& d, bool backward) {
   if (!backward) {
     L.Hq = c.take(R * d.f);
     L.sh = c.take(R * fb * 4);
-    L.part = c.take(moe::few_part_bytes(d.rows, d.E, 2));
+    L.part = c.take(moe::few_part_bytes(d.rows, d.E));
   } else {
     L.dA = c.take(R * d.f * 2);
     L.dB = c.take(R * d.f * 2);
@@ -100,7 +100,7 @@ extern "C" {
 
 size_t moe_gemm_workspace_bytes(const moe_gemm_dims* dims) {
   if (check_gemm(dims) != MOE_OK) return 0;
-  return kAlign + moe::few_part_bytes(dims->rows, dims->E, 1);
+  return kAlign + moe::few_part_bytes(dims->rows, dims->E);
 }
 
 moe_status moe_gemm_fp8_block(const moe_gemm_dims* dims, const uint8_t* aq, const float* sa,

@@ -3,8 +3,10 @@
 //
 //   * The product is taken transposed: 128 columns of the weight are the tensor
 //     cores' rows (from the weight's own layout, MN-major or K-major), 16 to 64 rows
-//     of activations their columns, so that a stage of 128 x 128 codes costs one
-//     block's MMAs whatever the number of rows.
+//     of activations their columns, so that a block of 128 x 128 codes costs one
+//     block's MMAs whatever the number of rows.  A step has two such blocks: side by
+//     side in one weight (256 bytes in a row of it: with 128 HBM moved 10% less), or the
+//     same columns of W1 and W3.
 //   * All k-steps of all tiles are cut into equal contiguous pieces, one for each
 //     block of the grid, so that every SM streams the same bytes whatever the tiles'
 //     number.  A tile that several blocks share is joined by the last to arrive, in the
@@ -62,7 +64,8 @@ struct Maps {
 
 template <int FORM, int NT>
 struct Shape {
-  static constexpr int NB = FORM == GATED ? 2 : 1;   // weights
+  static constexpr int NB = 2;                       // blocks of weights in a step
+  static constexpr int COLS = FORM == GATED ? 128 : 256;  // output columns of a tile
   static constexpr int X_BYTES = NT * 128;
   static constexpr int STAGE_BYTES = NB * W_BYTES + X_BYTES;
   static constexpr int UNIT = NB * NT;               // accumulator columns of a step
@@ -101,13 +104,13 @@ struct Tile {
   int e, n, row0, row_end;  // group, column tile, rows
 };
 // Steps of weights that a block asks L2 for before the kernel before has ended.
-constexpr int kEarlySteps = 8;
+constexpr int kEarlySteps = 4;
 
 // Tile t: groups in order; in one, column tiles in order; row tiles of a column tile
 // side by side, so that they find the weight in L2.
-template <int NT>
+template <int FORM, int NT>
 __device__ __forceinline__ Tile place(const Params& p, const int* off, const int* cum, int t) {
-  const int tiles_n = (p.N + 127) / 128;
+  const int tiles_n = (p.N + Shape<FORM, NT>::COLS - 1) / Shape<FORM, NT>::COLS;
   int e = 0, hi = p.E - 1;
   while (e < hi) {
     const int mid = (e + hi + 1) >> 1;
@@ -135,6 +138,14 @@ struct Share {
     return static_cast<int>(((s + 1) * blocks + steps - 1) / steps) - 1;
   }
 };
+
+// Blocks that share so many steps: pieces of fewer than MIN_STEPS cost more to join than they
+// save.
+constexpr int MIN_STEPS = 4;
+__device__ __forceinline__ int blocks_for(long long steps) {
+  const long long n = steps / MIN_STEPS;
+  return static_cast<int>(n < 1 ? (steps ? 1 : 0) : n < gridDim.x ? n : gridDim.x);
+}
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* status) {
   bool ok = mbar_try_wait(smem_u32(bar), parity);
@@ -217,16 +228,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // the kernel before ends (should it write them, L2 has what it wrote).
     if (warp == LOAD_W && p.E == 1) {
       Share guess;
-      guess.steps = static_cast<long long>((p.N + 127) / 128) * ((p.rows + NT - 1) / NT) * p.nkb;
-      guess.blocks = static_cast<int>(guess.steps < gridDim.x ? guess.steps : gridDim.x);
+      guess.steps = static_cast<long long>((p.N + S::COLS - 1) / S::COLS) * ((p.rows + NT - 1) / NT) * p.nkb;
+      guess.blocks = blocks_for(guess.steps);
       if (static_cast<int>(blockIdx.x) < guess.blocks) {
         const long long from = guess.lo(blockIdx.x);
         const long long to = min(guess.lo(blockIdx.x + 1), from + kEarlySteps);
         if (elect_one())
           for (long long i = from; i < to; ++i) {
-            const int n = static_cast<int>(i / p.nkb) / ((p.rows + NT - 1) / NT) * 128;
+            const int n = static_cast<int>(i / p.nkb) / ((p.rows + NT - 1) / NT) * S::COLS;
             const int k = static_cast<int>(i % p.nkb) * kBlock;
-            tma_prefetch_l2_3d(&maps.w[0], TRANS ? k : n, TRANS ? n : k, 0);
+#pragma unroll
+            for (int o = 0; o < S::NB; ++o) {
+              const int at = n + (FORM == GATED ? 0 : o * 128);
+              tma_prefetch_l2_3d(&maps.w[FORM == GATED ? o : 0], TRANS ? k : at, TRANS ? at : k, 0);
+            }
           }
       }
       __syncwarp();
@@ -241,8 +256,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = c.tmem_base;
   const int nkb = p.nkb;
   Share share;
-  share.steps = static_cast<long long>((p.N + 127) / 128) * c.cum[p.E] * nkb;
-  share.blocks = static_cast<int>(share.steps < gridDim.x ? share.steps : gridDim.x);
+  share.steps = static_cast<long long>((p.N + S::COLS - 1) / S::COLS) * c.cum[p.E] * nkb;
+  share.blocks = blocks_for(share.steps);
   const int me = static_cast<int>(blockIdx.x);
   const long long lo = me < share.blocks ? share.lo(me) : 0;
   const long long hi = me < share.blocks ? share.lo(me + 1) : 0;
@@ -264,7 +279,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     Tile tl = {};
     for (int i = 0; i < count; ++i) {
-      if (i == 0 || kb == 0) tl = place<NT>(p, c.off, c.cum, t);
+      if (i == 0 || kb == 0) tl = place<FORM, NT>(p, c.off, c.cum, t);
       ok = wait_all(&c.empty[s], ph, p.status);
       if (!ok) break;
       if (one) {
@@ -274,9 +289,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (warp == LOAD_W) {
           mbar_expect_tx(bar, S::NB * W_BYTES);
 #pragma unroll
-          for (int o = 0; o < S::NB; ++o)
-            tma_load_3d(dst + o * W_BYTES, &maps.w[o], TRANS ? k : tl.n * 128,
-                        TRANS ? tl.n * 128 : k, tl.e, bar);
+          for (int o = 0; o < S::NB; ++o) {
+            const int n = tl.n * S::COLS + (FORM == GATED ? 0 : o * 128);
+            tma_load_3d(dst + o * W_BYTES, &maps.w[FORM == GATED ? o : 0], TRANS ? k : n,
+                        TRANS ? n : k, tl.e, bar);
+          }
         } else {
           mbar_expect_tx(bar, S::X_BYTES);
           tma_load_2d(dst + S::NB * W_BYTES, &maps.x, k, tl.row0, bar);
@@ -343,7 +360,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t ph = 1;
     Tile tl = {};
     for (int n = 0; n < count; ++n) {
-      if (n == 0 || kb == 0) tl = place<NT>(p, c.off, c.cum, t);
+      if (n == 0 || kb == 0) tl = place<FORM, NT>(p, c.off, c.cum, t);
       if (!wait_all(&c.sempty[i], ph, p.status)) break;
       // indexes fit 32 bits: a scale stands for 128 bytes of codes or more
 #pragma unroll
@@ -352,11 +369,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool real = row < tl.row_end;
         copy_4(&c.slots[i].a[j], p.sa + (static_cast<uint32_t>(kb) * p.rows + (real ? row : 0)), real);
       }
-      if (lane < S::NB)
+      if (lane < S::NB) {
+        // past the last column block: its products are zeros
+        const int n = FORM == GATED ? tl.n : min(2 * tl.n + lane, (p.N + 127) / 128 - 1);
         copy_4(&c.slots[i].b[lane],
-               p.sb[lane] + (static_cast<uint32_t>(tl.e) * p.sb_group +
-                             static_cast<uint32_t>(kb) * p.sb_k + static_cast<uint32_t>(tl.n) * p.sb_n),
+               p.sb[FORM == GATED ? lane : 0] +
+                   (static_cast<uint32_t>(tl.e) * p.sb_group + static_cast<uint32_t>(kb) * p.sb_k +
+                    static_cast<uint32_t>(n) * p.sb_n),
                true);
+      }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&c.sfull[i]))
                    : "memory");
       if (++i == SLOTS) {
@@ -385,7 +406,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     int left = count;
     while (ok && left > 0) {
-      const Tile tl = place<NT>(p, c.off, c.cum, t);
+      const Tile tl = place<FORM, NT>(p, c.off, c.cum, t);
       const int n = min(nkb - kb, left);  // this block's steps of the tile
       float sums[S::NB][NT];
 #pragma unroll
@@ -471,22 +492,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // loop over rows is one short piece of code (unrolled with the sums in registers it was
         // fetched anew for each tile, 7000 cycles).
         const int rows = min(NT, tl.row_end - tl.row0);
-        const int col = tl.n * 128 + 4 * lane;  // of a row, four to a lane
-        const bool col_ok = col < p.N;
-        constexpr int PASSES = FORM == GATED ? 3 : 1;
+        constexpr int PASSES = FORM == GATED ? 3 : 2;
         for (int pass = FORM == GATED && !p.out[0] ? 2 : 0; ok && pass < PASSES; ++pass) {
+          // of a row, four columns to a lane
+          const int col = tl.n * S::COLS + (FORM == GATED ? 0 : pass * 128) + 4 * lane;
+          const bool col_ok = col < p.N;
+          if (FORM != GATED && tl.n * S::COLS + pass * 128 >= p.N) break;
           if (!(ok = meet())) break;  // the area's last rows have been read
           float* f = reinterpret_cast<float*>(staging) + tid;
           __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(staging) + tid;
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
+            const float a = FORM == GATED || pass == 0 ? sums[0][j] : sums[1][j];
             if (FORM == PLAIN_F32)
-              f[j * (S::PITCH / 4)] = sums[0][j];
+              f[j * (S::PITCH / 4)] = a;
             else
-              h[j * (S::PITCH / 2)] = __float2bfloat16_rn(
-                  FORM == PLAIN_BF16 || pass == 0 ? sums[0][j]
-                  : pass == 1                     ? sums[S::NB - 1][j]
-                                                  : silu_f(sums[0][j]) * sums[S::NB - 1][j]);
+              h[j * (S::PITCH / 2)] = __float2bfloat16_rn(FORM != GATED || pass == 0 ? a
+                                                          : pass == 1 ? sums[1][j]
+                                                                      : silu_f(a) * sums[1][j]);
           }
           if (!(ok = meet())) break;
 #pragma unroll 1
@@ -499,8 +522,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             } else {
               uint2 w = *reinterpret_cast<const uint2*>(staging + j * S::PITCH + 8 * lane);
               if (!col_ok) w = make_uint2(0, 0);
-              if (p.out[pass] && col_ok)
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out[pass]) + at) = w;
+              void* out = p.out[FORM == GATED ? pass : 0];
+              if (out && col_ok) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = w;
               if (FORM == GATED && pass == 2) {
                 const BlockScale b = block_scale(
                     __reduce_max_sync(0xffffffffu, top_of_pair(top_of_pair(0, w.x), w.y)));
@@ -587,9 +610,9 @@ bool map_weight(CUtensorMap* m, const void* q, int E, int K, int N, bool trans) 
 
 }  // namespace
 
-size_t few_part_bytes(int rows, int E, int weights) {
+size_t few_part_bytes(int rows, int E) {
   if (rows == 0) return 0;
-  return static_cast<size_t>(2) * MAX_BLOCKS * weights * tile_rows(rows, E) * 128 * 4;
+  return static_cast<size_t>(2) * MAX_BLOCKS * 2 * tile_rows(rows, E) * 128 * 4;
 }
 
 cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N, bool trans,
@@ -599,7 +622,7 @@ cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int 
   const int nt = tile_rows(r.rows, r.E);
   if (!fill(p, m, r, a, K, N, trans, nt, ahead) || !map_weight(&m.w[0], b.q, r.E, K, N, trans))
     return cudaErrorInvalidValue;
-  p.sb[0] = p.sb[1] = b.s;
+  p.sb[0] = b.s;
   p.out[0] = C;
   if (out_f32)
     return trans ? launch<PLAIN_F32, true>(nt, p, m, r.num_sms, s)

@@ -174,6 +174,8 @@ SHAPES = [
     ([0, 5, 0, 130, 1, 0], 400, 272), ([33, 0, 64, 1, 200], 1088, 704), ([0, 0, 7], 128, 1408), ([600, 3, 500], 272, 1552),
     ([4] * 64, 2048, 144), ([0] * 63 + [9], 256, 384), ([257, 255, 0, 1], 896, 640),
     ([1, 400, 0, 3], 400, 272), ([2, 0, 290, 1, 70], 1040, 592), ([65], 1408, 2048), ([30] * 9, 640, 272), ([200, 1, 0, 3, 40], 1936, 400),
+    ([16], 8320, 400), ([17], 8320, 272), ([48], 8192, 144), ([49], 8192, 144), ([10, 40, 0, 30], 8192, 272), ([12] * 3, 2048, 2064),
+    ([16], 272, 128), ([17], 272, 640), ([5, 43, 0], 640, 1040), ([33, 64, 31], 400, 272), ([32] * 4, 640, 528), ([96, 160], 272, 384),
 ]
 
 
@@ -194,7 +196,7 @@ def test_product_leaves_rows_behind_the_last_group(lib, counts, K, N, behind, tr
     assert (C[n:] == 77).all()
 
 
-@pytest.mark.parametrize("rows", [1, 40, 200, 700])
+@pytest.mark.parametrize("rows", [1, 16, 40, 200, 700])
 def test_product_without_offsets(lib, rows):
     C, ref, bound = _product([rows], 528, 400, False, True, seed=rows, dense=True)
     assert ((C.double() - ref).abs() <= bound).all()
@@ -260,7 +262,8 @@ def _ffn_fwd(x, offsets, w, f, E, keep=True, y=None):
 
 
 FFN = [([1], 64, 64), ([1], 4096, 448), ([5], 192, 320), ([64], 256, 128), ([130], 704, 1088), ([700], 320, 640),
-       ([0, 9, 0, 33, 1], 448, 704), ([140, 0, 256, 3], 1088, 320), ([3] * 64, 128, 192), ([513, 129], 256, 2112)]
+       ([0, 9, 0, 33, 1], 448, 704), ([140, 0, 256, 3], 1088, 320), ([3] * 64, 128, 192), ([513, 129], 256, 2112),
+       ([16], 128, 8256), ([17], 320, 448), ([48], 192, 8256), ([20, 0, 40], 704, 320), ([40, 7, 0, 17], 256, 8192)]
 
 
 def _check_fwd(x, A, B, H, y, w, counts):
