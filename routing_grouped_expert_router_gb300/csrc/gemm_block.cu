@@ -14,14 +14,21 @@
 //   warps 0, 2  TMA producers of A (128 rows a stage) and B (128 columns a stage)
 //   warp 1      tensor memory; in the even CTA the MMA issuer of the pair
 //   warp 3      scales: places the tiles and copies each block's 128 row scales and
-//               its columns' into a ring of slots, up to SLOTS blocks ahead (the way
-//               through a busy L2 takes some 2000 cycles, four blocks; loaded two
-//               blocks ahead into the sum warps' registers they held those up for
-//               700 cycles every two blocks: 285 us for 16384 x 4096 x 4864)
+//               its columns' into a ring of slots, up to SLOTS * GROUP blocks ahead
+//               (the way through a busy L2 takes some 2000 cycles, more than two
+//               blocks' sums; read by the sum warps themselves, two blocks ahead, the
+//               scales held those up for 700 cycles every two blocks)
 //   warps 4-11  the sums (warp w: TMEM lanes 32 (w mod 4), columns 64 ((w-4)/4)
 //               of each half) and, at a tile's end, its epilogue
 // The weight's square blocks let both uses of a weight, as it is (MN-major B)
 // and transposed (K-major B), take the same codes.
+//
+// Measured: 16384 x 4096 x 14336 in eight groups, bf16 out, 716 us, 2.69 PFLOP/s, 0.67 of
+// twice the measured bf16 rate.  The sum warps bound it: a block's 128 x 2 columns are
+// loads from tensor memory and 256 fused multiply-adds for each of a scheduler's two warps,
+// some 900 cycles with the waits, against the tensor cores' 512.  One CTA instead of a
+// pair, four accumulators of 128 columns (818 us), packed multiply-adds (no gain) and two
+// issuing warps were all slower.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -372,160 +379,160 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // Every wait below is bounded: a role whose wait runs out records it and ends, and those
   // that wait for it do the same.
   if (warp < FIRST_SUM_WARP) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::FEW));
-  if (warp == LOAD_A || warp == LOAD_B) {
-    // ------------------------------------------------------ TMA producers
-    const bool is_a = warp == LOAD_A;
-    const bool one = elect_one();
-    int s = 0, asked = 0;
-    uint32_t ph = 1;
-    bool ok = true;
-    Tile tl;
-    for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
-      const int e = __shfl_sync(0xffffffffu, tl.e, 0);
-      const int at = __shfl_sync(0xffffffffu,
-                                 is_a ? tl.row0 + rank * 128
-                                      : (FORM == GATED ? tl.nb * 128
-                                                       : tl.nb * S::COLS + rank * S::B_COLS),
-                                 0);
-      for (int kb = 0; kb < nkb; ++kb) {
-        ok = wait_all(smem_u32(&c.empty[s]), ph, p.status);
-        if (!ok) break;
-        const int which = kb >= p.kblocks ? 1 : 0;
-        const int k = (which ? kb - p.kblocks : kb) * kBlock;
-        if (one) {
-          // the even CTA's barrier counts both CTAs' bytes
-          const uint32_t own = smem_u32(&c.full[s]);
-          const uint32_t dst = smem_u32(smem + s * S::STAGE_BYTES) + (is_a ? 0 : S::A_BYTES);
-          if (rank == 0) {
-            mbar_expect_tx(own, 2 * (is_a ? S::A_BYTES : S::STAGE_BYTES - S::A_BYTES));
-            if (is_a)
-              tma_load_2d(dst, &maps.a[which], k, at, own);
-            else
-              tma_load_3d(dst, FORM == GATED ? &maps.b[0] : &maps.b[which], B_MN ? at : k,
-                          B_MN ? k : at, e, own);
-          } else {
-            const uint32_t bar = mapa_shared(own, 0);
-            if (is_a)
-              tma_load_2d_pair(dst, &maps.a[which], k, at, bar);
-            else
-              tma_load_3d_pair(dst, FORM == GATED ? &maps.b[1] : &maps.b[which], B_MN ? at : k,
-                               B_MN ? k : at, e, bar);
-          }
-        }
-        __syncwarp();
-        ++asked;
-        if (++s == S::STAGES) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    if (!ok && rank == 0) {
-      // the loads already asked for land before the CTA can end
-      const int first = asked > S::STAGES ? asked - S::STAGES : 0;
-      for (int r = first; r < asked; ++r)
-        mbar_wait_cluster(smem_u32(&c.full[r % S::STAGES]), (r / S::STAGES) & 1, p.status,
-                          kTimeoutCode);
-    }
-  } else if (warp == ISSUE) {
-    if (rank == 0) {
-      // ----------------------------------------------- MMA issuer (even CTA)
-      constexpr uint32_t IDESC = idesc_e4m3(PM, S::COLS) | (B_MN ? 1u << 16 : 0u);
-      // 32 deep: 32 bytes of a K-major row; 32 rows of 128 bytes of an MN-major tile
-      constexpr uint32_t B_STEP = B_MN ? 32 * 128 : 32;
-      const uint32_t a_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem), 16, 1024));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::FEW));
+    if (warp == LOAD_A || warp == LOAD_B) {
+      // ------------------------------------------------------ TMA producers
+      const bool is_a = warp == LOAD_A;
       const bool one = elect_one();
-      const int tiles = ((p.N + S::OUT_COLS - 1) / S::OUT_COLS) * c.cum[p.E];
-      const int all = cid < tiles ? ((tiles - cid + ncl - 1) / ncl) * nkb : 0;
-      int left = __shfl_sync(0xffffffffu, all, 0);
-      int s = 0, buf = 0;
-      uint32_t ph = 0, bph = 1;
+      int s = 0, asked = 0;
+      uint32_t ph = 1;
       bool ok = true;
-      for (; left > 0; --left) {
-        ok = wait_all(smem_u32(&c.full[s]), ph, p.status) &&
-             wait_all(smem_u32(&c.tempty[buf]), bph, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t a = a_lo + s * (S::STAGE_BYTES >> 4);
-        const uint32_t b = a + (S::A_BYTES >> 4);
-        if (one) {
+      Tile tl;
+      for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
+        const int e = __shfl_sync(0xffffffffu, tl.e, 0);
+        const int at = __shfl_sync(0xffffffffu,
+                                   is_a ? tl.row0 + rank * 128
+                                        : (FORM == GATED ? tl.nb * 128
+                                                         : tl.nb * S::COLS + rank * S::B_COLS),
+                                   0);
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = wait_all(smem_u32(&c.empty[s]), ph, p.status);
+          if (!ok) break;
+          const int which = kb >= p.kblocks ? 1 : 0;
+          const int k = (which ? kb - p.kblocks : kb) * kBlock;
+          if (one) {
+            // the even CTA's barrier counts both CTAs' bytes
+            const uint32_t own = smem_u32(&c.full[s]);
+            const uint32_t dst = smem_u32(smem + s * S::STAGE_BYTES) + (is_a ? 0 : S::A_BYTES);
+            if (rank == 0) {
+              mbar_expect_tx(own, 2 * (is_a ? S::A_BYTES : S::STAGE_BYTES - S::A_BYTES));
+              if (is_a)
+                tma_load_2d(dst, &maps.a[which], k, at, own);
+              else
+                tma_load_3d(dst, FORM == GATED ? &maps.b[0] : &maps.b[which], B_MN ? at : k,
+                            B_MN ? k : at, e, own);
+            } else {
+              const uint32_t bar = mapa_shared(own, 0);
+              if (is_a)
+                tma_load_2d_pair(dst, &maps.a[which], k, at, bar);
+              else
+                tma_load_3d_pair(dst, FORM == GATED ? &maps.b[1] : &maps.b[which], B_MN ? at : k,
+                                 B_MN ? k : at, e, bar);
+            }
+          }
+          __syncwarp();
+          ++asked;
+          if (++s == S::STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        // the loads already asked for land before the CTA can end
+        const int first = asked > S::STAGES ? asked - S::STAGES : 0;
+        for (int r = first; r < asked; ++r)
+          mbar_wait_cluster(smem_u32(&c.full[r % S::STAGES]), (r / S::STAGES) & 1, p.status,
+                            kTimeoutCode);
+      }
+    } else if (warp == ISSUE) {
+      if (rank == 0) {
+        // ----------------------------------------------- MMA issuer (even CTA)
+        constexpr uint32_t IDESC = idesc_e4m3(PM, S::COLS) | (B_MN ? 1u << 16 : 0u);
+        // 32 deep: 32 bytes of a K-major row; 32 rows of 128 bytes of an MN-major tile
+        constexpr uint32_t B_STEP = B_MN ? 32 * 128 : 32;
+        const uint32_t a_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem), 16, 1024));
+        const bool one = elect_one();
+        const int tiles = ((p.N + S::OUT_COLS - 1) / S::OUT_COLS) * c.cum[p.E];
+        const int all = cid < tiles ? ((tiles - cid + ncl - 1) / ncl) * nkb : 0;
+        int left = __shfl_sync(0xffffffffu, all, 0);
+        int s = 0, buf = 0;
+        uint32_t ph = 0, bph = 1;
+        bool ok = true;
+        for (; left > 0; --left) {
+          ok = wait_all(smem_u32(&c.full[s]), ph, p.status) &&
+               wait_all(smem_u32(&c.tempty[buf]), bph, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = a_lo + s * (S::STAGE_BYTES >> 4);
+          const uint32_t b = a + (S::A_BYTES >> 4);
+          if (one) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma2_e4m3_at(tmem_base + buf * S::COLS, a + (kk * 32 >> 4), b + (kk * B_STEP >> 4),
-                          IDESC, kk != 0);
-          umma2_commit_mc(smem_u32(&c.tfull[buf]), 0x3);
-          umma2_commit_mc(smem_u32(&c.empty[s]), 0x3);
+            for (int kk = 0; kk < 4; ++kk)
+              umma2_e4m3_at(tmem_base + buf * S::COLS, a + (kk * 32 >> 4), b + (kk * B_STEP >> 4),
+                            IDESC, kk != 0);
+            umma2_commit_mc(smem_u32(&c.tfull[buf]), 0x3);
+            umma2_commit_mc(smem_u32(&c.empty[s]), 0x3);
+          }
+          __syncwarp();
+          if (++s == S::STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+          if (++buf == S::BUFS) {
+            buf = 0;
+            bph ^= 1;
+          }
+        }
+        if (one) {
+          umma2_commit(smem_u32(&c.drain));
+          mbar_wait(smem_u32(&c.drain), 0, p.status, kTimeoutCode);
         }
         __syncwarp();
-        if (++s == S::STAGES) {
-          s = 0;
+      }
+    } else if (warp == SCALES) {
+      // ------------------------------------------------------------- scales
+      int i = 0;
+      uint32_t ph = 1;
+      bool ok = true;
+      Tile tl = {};
+      auto give = [&](int nb) {  // what a slot says of its tile, and that it is filled
+        if (lane == 0) {
+          c.slots[i].nb = nb;
+          c.slots[i].row0 = tl.row0;
+          c.slots[i].row_end = tl.row_end;
+        }
+        arrive_copied(smem_u32(&c.sfull[i]));
+        if (lane == 0) mbar_arrive(smem_u32(&c.sfull[i]));
+        __syncwarp();
+        if (++i == SLOTS) {
+          i = 0;
           ph ^= 1;
         }
-        if (++buf == S::BUFS) {
-          buf = 0;
-          bph ^= 1;
+      };
+      for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
+        // indexes fit 32 bits: a scale stands for 128 bytes of codes or more
+        const int row = tl.row0 + rank * 128 + lane;
+        uint32_t base = 0;
+        if (lane < S::NH) {
+          // past the last column block: its products are zeros
+          const int n = FORM == GATED ? tl.nb : min(S::NH * tl.nb + lane, p.nblocks - 1);
+          base = static_cast<uint32_t>(tl.e) * p.sb_group + static_cast<uint32_t>(n) * p.sb_n;
         }
-      }
-      if (one) {
-        umma2_commit(smem_u32(&c.drain));
-        mbar_wait(smem_u32(&c.drain), 0, p.status, kTimeoutCode);
-      }
-      __syncwarp();
-    }
-  } else if (warp == SCALES) {
-    // ------------------------------------------------------------- scales
-    int i = 0;
-    uint32_t ph = 1;
-    bool ok = true;
-    Tile tl = {};
-    auto give = [&](int nb) {  // what a slot says of its tile, and that it is filled
-      if (lane == 0) {
-        c.slots[i].nb = nb;
-        c.slots[i].row0 = tl.row0;
-        c.slots[i].row_end = tl.row_end;
-      }
-      arrive_copied(smem_u32(&c.sfull[i]));
-      if (lane == 0) mbar_arrive(smem_u32(&c.sfull[i]));
-      __syncwarp();
-      if (++i == SLOTS) {
-        i = 0;
-        ph ^= 1;
-      }
-    };
-    for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
-      // indexes fit 32 bits: a scale stands for 128 bytes of codes or more
-      const int row = tl.row0 + rank * 128 + lane;
-      uint32_t base = 0;
-      if (lane < S::NH) {
-        // past the last column block: its products are zeros
-        const int n = FORM == GATED ? tl.nb : min(S::NH * tl.nb + lane, p.nblocks - 1);
-        base = static_cast<uint32_t>(tl.e) * p.sb_group + static_cast<uint32_t>(n) * p.sb_n;
-      }
-      for (int kb0 = 0; kb0 < nkb; kb0 += GROUP) {
-        ok = wait_all(smem_u32(&c.sempty[i]), ph, p.status);
-        if (!ok) break;
+        for (int kb0 = 0; kb0 < nkb; kb0 += GROUP) {
+          ok = wait_all(smem_u32(&c.sempty[i]), ph, p.status);
+          if (!ok) break;
 #pragma unroll
-        for (int g = 0; g < GROUP; ++g) {
-          if (kb0 + g >= nkb) break;
-          const int product = kb0 + g >= p.kblocks ? 1 : 0;
-          const uint32_t k = kb0 + g - (product ? p.kblocks : 0);
-          const float* sa = p.sa[product] + k * static_cast<uint32_t>(p.rows);
+          for (int g = 0; g < GROUP; ++g) {
+            if (kb0 + g >= nkb) break;
+            const int product = kb0 + g >= p.kblocks ? 1 : 0;
+            const uint32_t k = kb0 + g - (product ? p.kblocks : 0);
+            const float* sa = p.sa[product] + k * static_cast<uint32_t>(p.rows);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool real = row + 32 * j < tl.row_end;
-            copy_4(&c.slots[i].a[lane + 32 * j][g], sa + (real ? row + 32 * j : 0), real);
+            for (int j = 0; j < 4; ++j) {
+              const bool real = row + 32 * j < tl.row_end;
+              copy_4(&c.slots[i].a[lane + 32 * j][g], sa + (real ? row + 32 * j : 0), real);
+            }
+            if (lane < S::NH)
+              copy_4(&c.slots[i].b[lane][g],
+                     p.sb[FORM == GATED ? lane : product] + (base + k * p.sb_k), true);
           }
-          if (lane < S::NH)
-            copy_4(&c.slots[i].b[lane][g],
-                   p.sb[FORM == GATED ? lane : product] + (base + k * p.sb_k), true);
+          give(tl.nb);
         }
-        give(tl.nb);
       }
+      if (ok && wait_all(smem_u32(&c.sempty[i]), ph, p.status)) give(-1);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    if (ok && wait_all(smem_u32(&c.sempty[i]), ph, p.status)) give(-1);
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::MANY));
     // ------------------------------------------- sums and epilogue (8 warps)
@@ -777,7 +784,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 // The smaller operand of a group stays in L2 where it fits, in one band; otherwise
-// bands of eight pair tiles.
+// bands of sixteen pair tiles.
 constexpr long long kL2ResidentBytes = 48ll << 20;
 void set_raster(Params& p, long long a_bytes, long long b_bytes, long long slab_a, long long slab_b) {
   auto bands = [](long long slab) {
