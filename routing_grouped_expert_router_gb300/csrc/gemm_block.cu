@@ -27,8 +27,8 @@
 // twice the measured bf16 rate.  The sum warps bound it: a block's 128 x 2 columns are
 // loads from tensor memory and 256 fused multiply-adds for each of a scheduler's two warps,
 // some 900 cycles with the waits, against the tensor cores' 512.  One CTA instead of a
-// pair, four accumulators of 128 columns (818 us), packed multiply-adds (no gain) and two
-// issuing warps were all slower.
+// pair, four accumulators of 128 columns (818 us), sixteen sum warps of half the columns
+// (799), and two issuing warps were all slower; packed multiply-adds made no difference.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
