@@ -20,7 +20,7 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t top) {
   BlockScale b;
   const float amax = __uint_as_float(top);
   if (amax > 7.9e-31f && amax < 1.2e30f) {
-    // as in block_quotient below, with the constant's reciprocal
+    // as the quotients below, with the constant's reciprocal
     constexpr float r = 1.0f / kCodeMax;
     const float q0 = amax * r;
     b.s = fmaf(fmaf(-q0, kCodeMax, amax), r, q0);
@@ -40,19 +40,41 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t top) {
 // That holds while nothing leaves the normal range: for scales of 2^-100 to
 // 2^100 a residual that does belongs to a quotient far below the least code,
 // 2^-9.  Other scales (and those that are not finite) take the division.
-__device__ __forceinline__ float block_quotient(float v, const BlockScale& b) {
-  const float q0 = v * b.r;
-  return fmaf(fmaf(-q0, b.s, v), b.r, q0);
+// Two values at a time: these instructions are issued for two, and issue slots are what
+// codes cost.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ void halves_of(uint64_t p, float (&v)[2]) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
   return static_cast<uint32_t>(
       __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
 }
+__device__ __forceinline__ uint32_t quick_codes2(float lo, float hi, const BlockScale& b) {
+  const uint64_t v = pair_of(lo, hi), r = pair_of(b.r, b.r), minus_s = pair_of(-b.s, -b.s);
+  const uint64_t q0 = mul_2(v, r);
+  const uint64_t q = fma_2(fma_2(q0, minus_s, v), r, q0);
+  float c[2];
+  halves_of(q, c);
+  return codes2(c[0], c[1]);
+}
 // Four values -> four codes, the first in the low byte.
 __device__ __forceinline__ uint32_t codes4(const float (&v)[4], const BlockScale& b) {
-  if (b.plain)
-    return codes2(block_quotient(v[0], b), block_quotient(v[1], b)) |
-           (codes2(block_quotient(v[2], b), block_quotient(v[3], b)) << 16);
+  if (b.plain) return quick_codes2(v[0], v[1], b) | (quick_codes2(v[2], v[3], b) << 16);
   return codes2(__fdiv_rn(v[0], b.s), __fdiv_rn(v[1], b.s)) |
          (codes2(__fdiv_rn(v[2], b.s), __fdiv_rn(v[3], b.s)) << 16);
 }

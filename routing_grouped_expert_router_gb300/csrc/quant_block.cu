@@ -5,7 +5,7 @@
 // Both read their input once: a block's values wait in registers for its
 // maximum.  HBM bounds them: 3 bytes an element and the scales.  Measured: eight weights of
 // 4096 x 14336, 219 us, 0.96 of the copy bandwidth; 16384 x 4096 rows, each gathered twice,
-// 70 us, 41 at the copy bandwidth with each source row read once (60 with it read twice).
+// 62 us, 41 at the copy bandwidth with each source row read once (60 with it read twice).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -21,7 +21,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 constexpr int kRowAhead = 2;  // blocks of a lane under way, 32 bytes of each
 
 __device__ __forceinline__ void codes8(const uint4& w, const BlockScale& b, uint2& out) {
@@ -31,14 +31,15 @@ __device__ __forceinline__ void codes8(const uint4& w, const BlockScale& b, uint
                        __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xFFFF0000u)};
   out = make_uint2(codes4(lo, b), codes4(hi, b));
 }
+// The larger magnitudes of the low and of the high values, each in its half.
 __device__ __forceinline__ uint32_t top8(const uint4& w) {
-  return top_of_pair(top_of_pair(top_of_pair(top_of_pair(0, w.x), w.y), w.z), w.w);
+  return top_2(top_2(top_2(w.x & 0x7FFF7FFFu, w.y), w.z), w.w);
 }
 
 // A warp takes a row's blocks four at a time, eight lanes of two 16-byte pieces to a
 // block, with kRowAhead such quads under way: sixteen values share the arithmetic of a
 // block's scale, which with eight took as many instructions as all else (16384 x 4096
-// rows gathered twice: 90 us).  blockIdx.y splits a row's quads where there are too few
+// rows gathered twice: 90 us); with quotients and maxima of one value at a time it was 70.  blockIdx.y splits a row's quads where there are too few
 // rows to fill the GPU.
 __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
     const uint4* __restrict__ in, const int32_t* __restrict__ idx, int div, long long rows,
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
 #pragma unroll
       for (int i = 0; i < kRowAhead; ++i) {
         if (j0 + i >= end_quad) break;  // the same for the whole warp
-        uint32_t top = max(top8(w[i][0]), top8(w[i][1]));
+        uint32_t top = top_of_2(top_2(top8(w[i][0]), top8(w[i][1])));
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
         const BlockScale b = block_scale(top);
@@ -92,7 +93,8 @@ __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
           if (c + 8 * h < n8) {
             uint2 codes;
             codes8(w[i][h], b, codes);
-            q[p * n8 + c + 8 * h] = codes;
+            // written to be evicted first: the source's rows, read again, stay in L2 longer (64 to 62 us)
+            __stcs(q + p * n8 + c + 8 * h, codes);
             if (copy) copy[p * n8 + c + 8 * h] = w[i][h];
           }
         if ((lane & 7) == 0 && c < n8) scale[static_cast<long long>(c >> 4) * ld + p] = b.s;
@@ -122,7 +124,8 @@ __global__ void __launch_bounds__(kWeightThreads) quant_weights_block_kernel(
     w[i] = (c < n8 && r0 + 16 * i < K) ? __ldg(W + base + 16ll * i * n8) : make_uint4(0, 0, 0, 0);
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, top8(w[i]));
+  for (int i = 0; i < 8; ++i) top = top_2(top, top8(w[i]));
+  top = top_of_2(top);
   top = __reduce_max_sync(kFull, top);
   if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
   __syncthreads();
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kWeightThreads) quant_weights_block_kernel(
     if (c < n8 && r0 + 16 * i < K) {
       uint2 codes;
       codes8(w[i], b, codes);
-      q[base + 16ll * i * n8] = codes;
+      __stcs(q + base + 16ll * i * n8, codes);
     }
 }
 
@@ -148,7 +151,7 @@ cudaError_t launch_quant_rows_block(const uint16_t* in, const int32_t* idx, int 
   if (rows == 0) return cudaSuccess;
   const int quads = (n + 4 * kBlock - 1) / (4 * kBlock);
   const long long row_blocks = (rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
-  const long long cap = 8ll * num_sms;
+  const long long cap = 16ll * num_sms;
   const int gx = static_cast<int>(row_blocks < cap ? row_blocks : cap);
   // a row's quads over several blocks while the rows alone do not fill the SMs
   int split = static_cast<int>((cap + gx - 1) / gx);
