@@ -174,7 +174,7 @@ struct WsLayout {
   size_t Xq = 0, sx = 0, Hq = 0, sh = 0;     // fp8 forward
   size_t h_amax = 0;                         // fp8 forward: per-tile amax of H
   size_t dAq = 0, dBq = 0, sab = 0, ab_amax = 0;  // fp8 backward
-  size_t part = 0;                           // block-scaled fp8 forward
+  size_t part = 0;                           // block-scaled fp8: shared tiles' sums
   size_t dOq = 0, sdo = 0, sda = 0, sdb = 0;  // block-scaled fp8 backward (with dAq, dBq)
   size_t total = 0;
 };
@@ -210,7 +210,7 @@ WsLayout ws_layout(const moe_dims& d, int op) {
       L.sx = c.take(R * hb * 4);
       L.Hq = c.take(R * d.f);
       L.sh = c.take(R * fb * 4);
-      L.part = c.take(moe::few_part_bytes(static_cast<int>(R), d.E));
+      L.part = c.take(moe::part_bytes(static_cast<int>(R)));
       break;
     case MOE_OP_LAYER_BWD_FP8_BLOCK:
       if (d.sar) return WsLayout{};
@@ -221,6 +221,7 @@ WsLayout ws_layout(const moe_dims& d, int op) {
       L.sda = c.take(R * fb * 4);
       L.dBq = c.take(R * d.f);
       L.sdb = c.take(R * fb * 4);
+      L.part = c.take(moe::part_bytes(static_cast<int>(R)));
       L.dX = c.take(R * d.h * 4);
       L.dg = c.take(R * 4);
       router_bwd();
@@ -1074,7 +1075,7 @@ moe_status moe_layer_bwd_fp8_block(const moe_dims* dims, const moe_bf16* x, cons
     MOE_RUN(cudaMemsetAsync(dW2, 0, wbytes, stream), "zero_dW2");
   } else {
     const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms(),
-                              nullptr};
+                              at<float>(ws, L.part)};
     MOE_RUN(moe::launch_quant_rows_block(dO, nullptr, 1, R, R, d.h, dOq, sdo, num_sms(), stream,
                                          nvalid, nullptr, at<int>(ws, 0)),
             "quant_dO_block");

@@ -33,22 +33,42 @@ struct BlockRows {
   int rows;
   int* status;    // device status word, at the start of the workspace's 256-byte header
   int num_sms;
-  float* part;    // few_part_bytes(rows, E) bytes
+  float* part;    // part_bytes(rows) bytes for the sums of tiles that several blocks share
 };
-// Whether a group's rows are so few that gemm_block_few.cu's kernel is the faster one.  Times
-// in us, few rows' kernel against the pairs' (each in a graph, weights not in L2):
-//   rows to a group           1          16         32         64
-//   4096 x 14336, 1 group     18 : 26    21 : 20    24 : 19    35 : 20
-//   2048 x 1408, 1 group      9 : 11     10 : 11    13 : 11    20 : 12
-//   4096 x 14336, 8 groups    78 : 117   84 : 94    91 : 96    99 : 98
-//   2048 x 1408, 64 groups    43 : 50    49 : 52    58 : 53    66 : 54
-//   14336 x 4096, 1 group     19 : 47    25 : 47    33 : 48    54 : 48
-// A long contraction with few columns leaves most pairs idle: there it stays ahead longer.
-inline bool few_rows(int rows, int E, int K, int N) {
-  return rows <= 16ll * E || (rows <= 48ll * E && K >= 8192 && E * blocks_of(N) <= 64);
+// Whether a group's rows are so few that gemm_block_few.cu's kernel is the faster one where
+// another of these launches comes before it (whose end its first weights need not wait for).
+// The feed-forward block in a graph, us, that kernel against the pairs':
+//   rows to a group           1          8          16         24         48
+//   4096, 14336, 1 group      49 : 82    53 : 77    57 : 74    68 : 75    108 : 76
+//   2048, 1408, 1 group       19 : 27    21 : 27    23 : 28    29 : 28    46 : 28
+//   2048, 1408, 8 groups      30 : 44    33 : 44    39 : 43    56 : 44    65 : 44
+//   4096, 14336, 8 groups     289 : 381  295 : 324  303 : 328  334 : 334  345 : 338
+//   2048, 1408, 64 groups     122 : 179  127 : 167  139 : 170  167 : 172  190 : 175
+inline bool few_rows(int rows, int E) { return rows <= 16ll * E; }
+// The same for a product by itself, whose weights may be what the launch before writes: the
+// joins' time, rows times the pieces of a tile, is then not hidden, and has to be little beside
+// the weights' stream.  Products in a graph, us, as above:
+//   rows to a group           1          4          8          16         32
+//   4096 x 14336, 1 group     18 : 28    19 : 20    19 : 20    21 : 20    24 : 20
+//   2048 x 4096, 1 group      9 : 12     10 : 12    10 : 12    11 : 12    15 : 12
+//   8192 x 2048, 1 group      16 : 18    20 : 17    22 : 17    27 : 17    38 : 18
+//   14336 x 4096, 1 group     20 : 28    21 : 26    23 : 23    26 : 23    34 : 24
+//   2048 x 1408, 8 groups     14 : 13    15 : 13    15 : 13    18 : 13    25 : 13
+//   512 x 2048, 64 groups     25 : 24    26 : 24    26 : 25    29 : 25
+//   2048 x 640, 64 groups     25 : 29    26 : 29    27 : 30    28 : 30
+//   2048 x 1408, 64 groups    41 : 50    43 : 51    45 : 53    47 : 53    57 : 53
+//   4096 x 14336, 8 groups    78 : 122   80 : 94    81 : 95    84 : 97    91 : 98
+inline bool few_rows_alone(int rows, int E, int K, int N, int num_sms) {
+  if (!few_rows(rows, E)) return false;
+  if (1ll * E * K * N > 64ll << 20) return true;
+  const long long tiles = 1ll * E * ((N + 255) / 256);
+  const long long shared = tiles < num_sms ? num_sms / tiles : 1, most = (blocks_of(K) + 3) / 4;
+  return 1ll * rows * (shared < most ? shared : most) <= 64;
 }
-// Grows with rows, so that a workspace for the most rows serves fewer.
-size_t few_part_bytes(int rows, int E);
+constexpr int kPartBlocks = 160;  // blocks of a grid that have room for a shared tile's sums
+inline size_t part_bytes(int rows) {  // 128 x 256 sums for each: the most of either kernel
+  return rows ? static_cast<size_t>(kPartBlocks) * 128 * 256 * 4 : 0;
+}
 // Codes and scales of an activation or a weight.
 struct Coded {
   const uint8_t* q;

@@ -60,9 +60,10 @@ moe_status check_ffn(const moe_ffn_dims* d) {
 struct FfnLayout {
   size_t status = 0;
   size_t Xq = 0, sx = 0;                 // the rows' codes (of x, or of dy in the backward)
-  size_t Hq = 0, sh = 0, part = 0;       // forward
+  size_t Hq = 0, sh = 0;                 // forward
   size_t dA = 0, dB = 0;                 // backward
   size_t dAq = 0, sda = 0, dBq = 0, sdb = 0;
+  size_t part = 0;                       // shared tiles' sums
   size_t total = 0;
 };
 FfnLayout ffn_layout(const moe_ffn_dims& d, bool backward) {
@@ -75,7 +76,7 @@ FfnLayout ffn_layout(const moe_ffn_dims& d, bool backward) {
   if (!backward) {
     L.Hq = c.take(R * d.f);
     L.sh = c.take(R * fb * 4);
-    L.part = c.take(moe::few_part_bytes(d.rows, d.E));
+    L.part = c.take(moe::part_bytes(d.rows));
   } else {
     L.dA = c.take(R * d.f * 2);
     L.dB = c.take(R * d.f * 2);
@@ -83,6 +84,7 @@ FfnLayout ffn_layout(const moe_ffn_dims& d, bool backward) {
     L.sda = c.take(R * fb * 4);
     L.dBq = c.take(R * d.f);
     L.sdb = c.take(R * fb * 4);
+    L.part = c.take(moe::part_bytes(d.rows));
   }
   L.total = c.off;
   return L;
@@ -100,7 +102,7 @@ extern "C" {
 
 size_t moe_gemm_workspace_bytes(const moe_gemm_dims* dims) {
   if (check_gemm(dims) != MOE_OK) return 0;
-  return kAlign + moe::few_part_bytes(dims->rows, dims->E);
+  return kAlign + moe::part_bytes(dims->rows);
 }
 
 moe_status moe_gemm_fp8_block(const moe_gemm_dims* dims, const uint8_t* aq, const float* sa,
@@ -188,7 +190,8 @@ moe_status moe_gated_ffn_bwd(const moe_ffn_dims* dims, const moe_bf16* x, const 
         BLOCK_RUN(cudaMemsetAsync(w, 0, bytes, stream), "zero_dW");
     return MOE_OK;
   }
-  const moe::BlockRows r = {d.E, offsets, d.rows, at<int>(ws, 0), moe_api::num_sms(), nullptr};
+  const moe::BlockRows r = {d.E, offsets, d.rows, at<int>(ws, 0), moe_api::num_sms(),
+                            at<float>(ws, L.part)};
   uint8_t *dyq = at<uint8_t>(ws, L.Xq), *daq = at<uint8_t>(ws, L.dAq), *dbq = at<uint8_t>(ws, L.dBq);
   float *sdy = at<float>(ws, L.sx), *sda = at<float>(ws, L.sda), *sdb = at<float>(ws, L.sdb);
   uint16_t *da = at<uint16_t>(ws, L.dA), *db = at<uint16_t>(ws, L.dB);

@@ -23,6 +23,10 @@
 // The weight's square blocks let both uses of a weight, as it is (MN-major B)
 // and transposed (K-major B), take the same codes.
 //
+// Where tiles are so few that two pairs or more would go to one, and the contraction is long,
+// each pair takes a piece of a tile's contraction; the last to arrive adds the pieces' sums in
+// their order (20 to 128 rows by 14336 x 4096: 23 to 29 us, 50 in one piece; see pieces_of).
+//
 // Measured: 16384 x 4096 x 14336 in eight groups, bf16 out, 716 us, 2.69 PFLOP/s, 0.67 of
 // twice the measured bf16 rate.  The sum warps bound it: a block's 128 x 2 columns are
 // loads from tensor memory and 256 fused multiply-adds for each of a scheduler's two warps,
@@ -58,6 +62,7 @@ constexpr int LOAD_A = 0, ISSUE = 1, LOAD_B = 2, SCALES = 3;  // warps
 constexpr int SET_BYTES = 2048;   // 32 rows x 64 bytes: one copy of an epilogue
 constexpr int SLOTS = 4;          // groups of blocks whose scales wait for the sums
 constexpr int GROUP = 4;          // blocks of a slot
+constexpr int kMostPairs = kPartBlocks / 2;  // of the grid: each has room for shared sums
 
 struct Params {
   int E;
@@ -76,6 +81,9 @@ struct Params {
   float* scales[2];
   int* status;
   int raster_n, group;      // tile order (see place)
+  float* part;              // shared tiles' sums
+  uint32_t* arrived;        // a byte for each CTA's rows of a shared tile
+  int most_pieces;          // of a tile
 };
 
 struct Maps {
@@ -119,8 +127,10 @@ struct alignas(16) Ctrl {
   uint64_t sfull[SLOTS], sempty[SLOTS];
   uint64_t ab[SUM_WARPS];   // GATED_BWD: A and B in a warp's sets
   uint64_t met;             // the sum warps, once for each tile (TOPS)
+  uint64_t join;            // the sum warps, twice for a shared tile
   uint64_t drain;
   uint32_t tmem_base;
+  uint32_t last;            // whether this CTA joins the tile
   int off[kMaxGroups + 1];
   int cum[kMaxGroups + 1];       // row tiles before each group
   Slot slots[SLOTS];
@@ -329,7 +339,9 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, int* sta
   return __all_sync(0xffffffffu, ok);
 }
 
-template <int FORM, bool B_MN>
+// PIECES: tiles may be so few that several pairs share one's contraction (a kernel of its own:
+// what it keeps in registers costs the others 4%).
+template <int FORM, bool B_MN, bool PIECES>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     block_pair_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using S = Shape<FORM>;
@@ -343,7 +355,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int rank = static_cast<int>(cluster_ctarank());
   const int cid = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(cluster_count_x());
-  const int nkb = p.kblocks * p.products;
 
   // ------------------------------------------------------------ set-up
   if (warp == 0 && lane == 0) {
@@ -361,6 +372,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int w = 0; w < SUM_WARPS; ++w) mbar_init(smem_u32(&c.ab[w]), 1);
     mbar_init(smem_u32(&c.met), SUM_WARPS);
+    mbar_init(smem_u32(&c.join), SUM_WARPS);
     mbar_init(smem_u32(&c.drain), 1);
     fence_mbar_init();
     tma_prefetch_desc(&maps.a[0]);
@@ -376,6 +388,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   cluster_sync_all();  // both CTAs' barriers exist before any arrival from the other
   tc_fence_after();
   constexpr uint32_t tmem_base = 0;  // all 512 columns are this block's
+  // With two pairs or more to a tile, each takes a piece of the contraction: this one's tiles
+  // are tile0, tile0 + ncl, .. (with pieces only the first exists), its blocks kb_lo ..
+  // kb_lo + nkb - 1.
+  const int tiles = ((p.N + S::OUT_COLS - 1) / S::OUT_COLS) * c.cum[p.E];
+  int pieces = 1, tile0 = cid, kb_lo = 0, nkb = p.kblocks * p.products;
+  if (PIECES && tiles > 0 && 2 * tiles <= ncl) {
+    pieces = min(ncl / tiles, p.most_pieces);
+    tile0 = cid < tiles * pieces ? cid / pieces : tiles;
+    const int piece = cid % pieces;
+    kb_lo = nkb * piece / pieces;
+    nkb = nkb * (piece + 1) / pieces - kb_lo;
+  }
   // Every wait below is bounded: a role whose wait runs out records it and ends, and those
   // that wait for it do the same.
   if (warp < FIRST_SUM_WARP) {
@@ -388,14 +412,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t ph = 1;
       bool ok = true;
       Tile tl;
-      for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
+      for (int t = tile0; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
         const int e = __shfl_sync(0xffffffffu, tl.e, 0);
         const int at = __shfl_sync(0xffffffffu,
                                    is_a ? tl.row0 + rank * 128
                                         : (FORM == GATED ? tl.nb * 128
                                                          : tl.nb * S::COLS + rank * S::B_COLS),
                                    0);
-        for (int kb = 0; kb < nkb; ++kb) {
+        for (int kb = kb_lo; kb < kb_lo + nkb; ++kb) {
           ok = wait_all(smem_u32(&c.empty[s]), ph, p.status);
           if (!ok) break;
           const int which = kb >= p.kblocks ? 1 : 0;
@@ -443,8 +467,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         constexpr uint32_t B_STEP = B_MN ? 32 * 128 : 32;
         const uint32_t a_lo = static_cast<uint32_t>(smem_desc(smem_u32(smem), 16, 1024));
         const bool one = elect_one();
-        const int tiles = ((p.N + S::OUT_COLS - 1) / S::OUT_COLS) * c.cum[p.E];
-        const int all = cid < tiles ? ((tiles - cid + ncl - 1) / ncl) * nkb : 0;
+        const int all = tile0 < tiles ? ((tiles - tile0 + ncl - 1) / ncl) * nkb : 0;
         int left = __shfl_sync(0xffffffffu, all, 0);
         int s = 0, buf = 0;
         uint32_t ph = 0, bph = 1;
@@ -500,7 +523,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ph ^= 1;
         }
       };
-      for (int t = cid; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
+      for (int t = tile0; ok && place<FORM>(p, c.off, c.cum, t, tl); t += ncl) {
         // indexes fit 32 bits: a scale stands for 128 bytes of codes or more
         const int row = tl.row0 + rank * 128 + lane;
         uint32_t base = 0;
@@ -515,8 +538,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int g = 0; g < GROUP; ++g) {
             if (kb0 + g >= nkb) break;
-            const int product = kb0 + g >= p.kblocks ? 1 : 0;
-            const uint32_t k = kb0 + g - (product ? p.kblocks : 0);
+            const int product = kb_lo + kb0 + g >= p.kblocks ? 1 : 0;
+            const uint32_t k = kb_lo + kb0 + g - (product ? p.kblocks : 0);
             const float* sa = p.sa[product] + k * static_cast<uint32_t>(p.rows);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -635,6 +658,66 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
       }
       if (!ok) break;
+      if (PIECES && pieces > 1) {
+        // This piece's sums to its slot; the last of the tile's to arrive adds all in order and
+        // goes on to the epilogue.
+        constexpr int SLOT = 128 * S::COLS / 4;  // four columns of a row side by side
+        float4* slot = reinterpret_cast<float4*>(p.part) + static_cast<size_t>(2 * cid + rank) * SLOT +
+                       side * 16 * 128 + trow;
+        if (row_ok) {
+#pragma unroll
+          for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              __stcg(slot + (h * 32 + j) * 128, make_float4(sums[h][4 * j], sums[h][4 * j + 1],
+                                                            sums[h][4 * j + 2], sums[h][4 * j + 3]));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.join));
+        if (!(ok = wait_all(smem_u32(&c.join), 0, p.status))) break;
+        if (warp == FIRST_SUM_WARP && lane == 0) {
+          __threadfence();  // what the eight warps wrote before they met
+          const int index = 2 * tile0 + rank;
+          const uint32_t shift = 8 * (index & 3);
+          uint32_t* word = p.arrived + (index >> 2);
+          const uint32_t old = (atomicAdd(word, 1u << shift) >> shift) & 0xFFu;
+          c.last = old == static_cast<uint32_t>(pieces - 1);
+          // every piece is there: the byte is zero again for the next call
+          if (c.last) atomicSub(word, static_cast<uint32_t>(pieces) << shift);
+          __threadfence();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.join));
+        if (!(ok = wait_all(smem_u32(&c.join), 1, p.status))) break;
+        if (!c.last) continue;
+        if (row_ok) {
+          const float4* from = slot - static_cast<size_t>(2 * (cid % pieces)) * SLOT;
+#pragma unroll
+          for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float4 v = __ldcg(from + (h * 32 + j) * 128);
+              sums[h][4 * j] = v.x;
+              sums[h][4 * j + 1] = v.y;
+              sums[h][4 * j + 2] = v.z;
+              sums[h][4 * j + 3] = v.w;
+            }
+#pragma unroll 1
+          for (int b = 1; b < pieces; ++b) {
+            from += 2 * SLOT;
+#pragma unroll
+            for (int h = 0; h < S::NH; ++h)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float4 v = __ldcg(from + (h * 32 + j) * 128);
+                sums[h][4 * j] += v.x;
+                sums[h][4 * j + 1] += v.y;
+                sums[h][4 * j + 2] += v.z;
+                sums[h][4 * j + 3] += v.w;
+              }
+          }
+        }
+      }
       if constexpr (FORM == PLAIN_BF16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -801,9 +884,9 @@ void set_raster(Params& p, long long a_bytes, long long b_bytes, long long slab_
   }
 }
 
-template <int FORM, bool B_MN>
-cudaError_t launch_pairs(const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
-  auto kern = block_pair_kernel<FORM, B_MN>;
+template <int FORM, bool B_MN, bool PIECES>
+cudaError_t launch_with(const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
+  auto kern = block_pair_kernel<FORM, B_MN, PIECES>;
   constexpr int smem = smem_bytes<FORM>();
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -819,14 +902,37 @@ cudaError_t launch_pairs(const Params& p, const Maps& m, int num_sms, cudaStream
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const long long nt = (p.N + Shape<FORM>::OUT_COLS - 1) / Shape<FORM>::OUT_COLS;
-  const long long most = nt * ((p.rows + PM - 1) / PM + p.E);
-  const int fit = pairs_that_fit(reinterpret_cast<const void*>(kern), cfg, num_sms);
+  const long long most = nt * ((p.rows + PM - 1) / PM + p.E) * (PIECES ? p.most_pieces : 1);
+  int fit = pairs_that_fit(reinterpret_cast<const void*>(kern), cfg, num_sms);
+  if (PIECES && fit > kMostPairs) fit = kMostPairs;
   cfg.gridDim = dim3(2 * static_cast<unsigned>(most < fit ? most : fit), 1, 1);
   const cudaError_t le = cudaLaunchKernelEx(&cfg, kern, p, m);
   return le == cudaSuccess ? launched() : le;
 }
+template <int FORM, bool B_MN>
+cudaError_t launch_pairs(const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
+  // the fewest tiles that these rows can make; the kernel counts those there are
+  const long long nt = (p.N + Shape<FORM>::OUT_COLS - 1) / Shape<FORM>::OUT_COLS;
+  const long long least = nt * ((p.rows + PM - 1) / PM);
+  return p.most_pieces > 1 && 4 * least <= num_sms ? launch_with<FORM, B_MN, true>(p, m, num_sms, s)
+                                                   : launch_with<FORM, B_MN, false>(p, m, num_sms, s);
+}
 
-Params params_of(const BlockRows& r, int K, int N, bool trans) {
+// Pieces of a tile's contraction of `blocks` blocks, where pairs would idle otherwise.  Blocks
+// take 0.45 us each in their turn; a join takes some 4.5 us, and 0.5 to 1.5 for each piece (few
+// rows to 128).  Times in us, one group, 20 and 128 rows, in a graph, of 1, 2, 3, 4 pieces:
+//   2048 x 4096    11.7 12.5 12.9 13.4    12.6 15.8 16.6 17.7
+//   4096 x 4096    18.5 16.0 14.7 15.0    19.2 19.5 18.7 19.8
+//   8192 x 2048    30.5 22.0 18.5 17.2    31.4 25.3 22.8 21.7
+//   14336 x 4096   50.2 31.9 25.8 23.4    51.3 35.5 30.2 28.7
+int pieces_of(int blocks) {
+  if (blocks < 32) return 1;
+  int n = 3;
+  while (10 * (n + 1) * (n + 1) <= 3 * blocks) ++n;
+  return n;
+}
+
+Params params_of(const BlockRows& r, int K, int N, bool trans, int products = 1) {
   Params p;
   memset(&p, 0, sizeof(p));
   p.E = r.E;
@@ -835,7 +941,10 @@ Params params_of(const BlockRows& r, int K, int N, bool trans) {
   p.status = r.status;
   p.N = N;
   p.kblocks = blocks_of(K);
-  p.products = 1;
+  p.products = products;
+  p.part = r.part;
+  p.arrived = reinterpret_cast<uint32_t*>(r.status) + 16;  // bytes 64 .. 223 of the header
+  p.most_pieces = pieces_of(p.kblocks * products);
   p.nblocks = blocks_of(N);
   p.sb_group = p.kblocks * p.nblocks;
   p.sb_k = trans ? 1 : p.nblocks;
@@ -857,7 +966,8 @@ bool map_weight(CUtensorMap* m, const void* q, int E, int K, int N, bool trans, 
 cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
                           bool trans, bool out_f32, void* C, cudaStream_t s, bool ahead) {
   if (r.rows == 0) return cudaSuccess;
-  if (few_rows(r.rows, r.E, K, N)) return few_product(r, a, b, K, N, trans, out_f32, C, s, ahead);
+  if (ahead ? few_rows(r.rows, r.E) : few_rows_alone(r.rows, r.E, K, N, r.num_sms))
+    return few_product(r, a, b, K, N, trans, out_f32, C, s, ahead);
   Params p = params_of(r, K, N, trans);
   p.sa[0] = a.s;
   p.sb[0] = b.s;
@@ -879,7 +989,7 @@ cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, c
                           int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                           float* sh, cudaStream_t s) {
   if (r.rows == 0) return cudaSuccess;
-  if (few_rows(r.rows, r.E, h, f)) return few_fc1_fwd(r, x, w1, w3, h, f, A, B, H, Hq, sh, s);
+  if (few_rows(r.rows, r.E)) return few_fc1_fwd(r, x, w1, w3, h, f, A, B, H, Hq, sh, s);
   Params p = params_of(r, h, f, false);
   p.sa[0] = x.s;
   p.sb[0] = w1.s;
@@ -930,8 +1040,7 @@ cudaError_t block_fc1_dgrad(const BlockRows& r, const Coded& da, const Coded& db
                             const Coded& w3, int h, int f, bool out_f32, void* dX,
                             cudaStream_t s) {
   if (r.rows == 0) return cudaSuccess;
-  Params p = params_of(r, f, h, true);
-  p.products = 2;
+  Params p = params_of(r, f, h, true, 2);
   p.sa[0] = da.s;
   p.sa[1] = db.s;
   p.sb[0] = w1.s;

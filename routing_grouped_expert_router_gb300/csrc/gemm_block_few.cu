@@ -12,7 +12,7 @@
 //     number.  A tile that several blocks share is joined by the last to arrive, in the
 //     pieces' order: the same inputs give the same bits.
 //   * A ring of some 190 KiB of stages is under way on each SM.
-// Measured, in a graph, weights not in L2: one row by 4096 x 14336, 14.6 us (8.8 at the copy
+// Measured, in a graph, weights not in L2: one row by 4096 x 14336, 18 us (8.8 at the copy
 // bandwidth); 192 rows in 64 groups of 2048 x 1408, 42 us (25.6).  What is left is the start
 // (some 3 us to the first weights), the join of shared tiles (3 to 4 us) and SMs that HBM
 // serves unevenly; tiles in place of equal pieces left a third of the SMs idle.
@@ -40,7 +40,7 @@ namespace {
 enum Form { PLAIN_BF16 = 0, PLAIN_F32 = 1, GATED = 2 };
 
 constexpr int kTimeoutCode = 5;  // MOE_ERR_DEVICE_TIMEOUT
-constexpr int MAX_BLOCKS = 160;  // of the grid
+constexpr int MAX_BLOCKS = kPartBlocks;  // of the grid
 constexpr int NUM_THREADS = 256;
 constexpr int W_BYTES = 128 * 128;
 constexpr int SLOTS = 8;         // steps whose scales wait
@@ -98,6 +98,7 @@ struct alignas(16) Ctrl {
   int cum[kMaxGroups + 1];       // row tiles before each group
   Slot<NT> slots[SLOTS];
 };
+static_assert(2 * 2 * 64 * 128 <= 128 * 256, "a block's two slots fit its part");
 template <int FORM, int NT>
 constexpr int smem_bytes() {
   using S = Shape<FORM, NT>;
@@ -613,11 +614,6 @@ bool map_weight(CUtensorMap* m, const void* q, int E, int K, int N, bool trans) 
 }
 
 }  // namespace
-
-size_t few_part_bytes(int rows, int E) {
-  if (rows == 0) return 0;
-  return static_cast<size_t>(2) * MAX_BLOCKS * 2 * tile_rows(rows, E) * 128 * 4;
-}
 
 cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N, bool trans,
                         bool out_f32, void* C, cudaStream_t s, bool ahead) {

@@ -8,7 +8,7 @@ import torch
 
 from routing_grouped_expert_router_gb300 import binding as mb
 from tests import block_ref as br
-from tests.test_gpu_block_fp8 import BF, F32, _check_fwd, _ffn_bwd, _ffn_fwd, _ffn_weights, _normal, _offsets, _quantize_rows, _rel, _ws, lib  # noqa: F401
+from tests.test_gpu_block_fp8 import BF, F32, _check_fwd, _ffn_bwd, _ffn_fwd, _ffn_weights, _groups, _normal, _offsets, _quantize_rows, _rel, _ws, lib  # noqa: F401
 
 pytestmark = [pytest.mark.gpu]
 
@@ -140,3 +140,28 @@ def test_two_graphs_on_one_workspace(lib):  # noqa: F811
         assert all(torch.equal(a, b) for a, b in zip(want, ys)) and torch.equal(C, C0)
     assert mb.moe_read_device_status(ws) == mb.MOE_OK
     assert not ws[:256].any()
+
+
+@pytest.mark.parametrize("counts,h,f", [([50], 4096, 1152), ([130, 0, 300], 2048, 256), ([20, 0, 40], 192, 8192)])
+def test_shared_tiles_give_the_same_bits_each_time(lib, counts, h, f):  # noqa: F811
+    """Few tiles with a long contraction: pieces of a tile are joined in their order, whichever arrives last."""
+    E, R = len(counts), sum(counts)
+    w, x, dy, o = _ffn_weights(E, h, f, 21), _normal((R, h), 22), _normal((R, h), 23), _offsets(counts)
+    (q1, s1, _), (q3, s3, _), (q2, s2, _) = w
+    fd = mb.ffn_dims(R, h, f, E)
+    ws = _ws(max(mb.moe_ffn_workspace_bytes(fd, b) for b in (0, 1)))
+    A, B, H = (torch.empty(R, f, dtype=BF, device="cuda") for _ in range(3))
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    first = None
+    for _ in range(40):
+        for t in (A, B, H, y, dx):
+            t.fill_(3)
+        mb.moe_gated_ffn_fwd(fd, x, o, q1, s1, q3, s3, q2, s2, A, B, H, y, ws)
+        mb.moe_gated_ffn_bwd(fd, x, dy, o, q1, s1, q3, s3, q2, s2, A, B, H, dx, None, None, None, ws)
+        got = [t.clone() for t in (A, B, H, y, dx)]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    _check_fwd(x, A, B, H, y, w, counts)
+    want = br.ffn_bwd(*[t.double() for t in (x, dy, A, B, H)], *[v[2] for v in w], _groups(counts))
+    assert _rel(dx, want[0]) <= 5e-3
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK and not ws[:256].any()
