@@ -8,6 +8,10 @@ namespace moe {
 
 constexpr int kMaxGroups = 64;
 
+// Orders what this thread wrote, and what it has seen written, before what follows for the
+// whole GPU (__threadfence() orders more, and takes longer).
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 // off[0 .. E]: the offsets (all `rows` in one group where `offsets` is NULL), clamped into
 // order so that every access that follows stays inside its buffer; one that had to be is
 // recorded.  cum[0 .. E]: tiles of `tile` rows before each group.

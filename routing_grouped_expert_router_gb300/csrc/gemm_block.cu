@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0) mbar_arrive(smem_u32(&c.join));
         if (!(ok = wait_all(smem_u32(&c.join), 0, p.status))) break;
         if (warp == FIRST_SUM_WARP && lane == 0) {
-          __threadfence();  // what the eight warps wrote before they met
+          fence_gpu();  // what the eight warps wrote before they met
           const int index = 2 * tile0 + rank;
           const uint32_t shift = 8 * (index & 3);
           uint32_t* word = p.arrived + (index >> 2);
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           c.last = old == static_cast<uint32_t>(pieces - 1);
           // every piece is there: the byte is zero again for the next call
           if (c.last) atomicSub(word, static_cast<uint32_t>(pieces) << shift);
-          __threadfence();
+          fence_gpu();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.join));

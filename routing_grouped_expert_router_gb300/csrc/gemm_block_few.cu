@@ -413,6 +413,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     while (ok && left > 0) {
       const Tile tl = place<FORM, NT>(p, c.off, c.cum, t);
       const int n = min(nkb - kb, left);  // this block's steps of the tile
+      // Where the tile is shared: the pieces' blocks, and the first one's slot (the others
+      // begin with the tile: slot 0).  Divisions, done while the first weights are on the way.
+      const long long s0 = static_cast<long long>(t) * nkb;
+      int first = 0, last = 0, first_slot = 0;
+      if (n < nkb) {
+        first = share.owner(s0);
+        last = share.owner(s0 + nkb - 1);
+        first_slot = share.lo(first) == s0 ? 0 : 1;
+      }
       float sums[S::NB][NT];
 #pragma unroll
       for (int o = 0; o < S::NB; ++o)
@@ -455,10 +464,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool mine = true;  // whether the tile is finished here
       if (n < nkb) {
         // shared: this block's sums to its slot; the last to arrive adds all in order
-        const long long s0 = static_cast<long long>(t) * nkb;
-        const int first = share.owner(s0), last = share.owner(s0 + nkb - 1);
         constexpr int SLOT = S::NB * NT * 128;
-        float* slot = p.part + (2ll * me + (s0 <= lo ? 0 : 1)) * SLOT + tid;
+        float* slot = p.part + (2ll * me + (me == first ? first_slot : 0)) * SLOT + tid;
 #pragma unroll
         for (int o = 0; o < S::NB; ++o)
 #pragma unroll
@@ -466,13 +473,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (tl.row0 + j < tl.row_end) slot[(o * NT + j) * 128] = sums[o][j];
         if (!(ok = meet())) break;
         if (tid == 0) {
-          __threadfence();  // what the four warps wrote before they met
+          fence_gpu();  // what the four warps wrote before they met
           const uint32_t shift = 8 * (first & 3);
           const uint32_t old = (atomicAdd(p.arrived + (first >> 2), 1u << shift) >> shift) & 0xFFu;
           c.last = old == static_cast<uint32_t>(last - first);
           // every piece is there: the byte is zero again for the next call
           if (c.last) atomicSub(p.arrived + (first >> 2), static_cast<uint32_t>(last - first + 1) << shift);
-          __threadfence();
+          fence_gpu();
         }
         if (!(ok = meet())) break;
         mine = c.last != 0;
@@ -483,7 +490,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int j = 0; j < NT; ++j) sums[o][j] = 0.f;
 #pragma unroll 2
           for (int b = first; b <= last; ++b) {
-            const float* from = p.part + (2ll * b + (s0 <= share.lo(b) ? 0 : 1)) * SLOT + tid;
+            const float* from = p.part + (2ll * b + (b == first ? first_slot : 0)) * SLOT + tid;
 #pragma unroll
             for (int o = 0; o < S::NB; ++o)
 #pragma unroll
