@@ -44,7 +44,10 @@ struct BlockRows {
 //   2048, 1408, 8 groups      30 : 44    33 : 44    39 : 43    56 : 44    65 : 44
 //   4096, 14336, 8 groups     289 : 381  295 : 324  303 : 328  334 : 334  345 : 338
 //   2048, 1408, 64 groups     122 : 179  127 : 167  139 : 170  167 : 172  190 : 175
-inline bool few_rows(int rows, int E) { return rows <= 16ll * E; }
+// The steps of such a launch are counted in 32 bits.
+inline bool few_rows(int rows, int E, int K, int N) {
+  return rows <= 16ll * E && (rows / 16 + E) * (N / 128 + 1ll) * blocks_of(K) < 2147483647ll;
+}
 // The same for a product by itself, whose weights may be what the launch before writes: the
 // joins' time, rows times the pieces of a tile, is then not hidden, and has to be little beside
 // the weights' stream.  Products in a graph, us, as above:
@@ -59,7 +62,7 @@ inline bool few_rows(int rows, int E) { return rows <= 16ll * E; }
 //   2048 x 1408, 64 groups    41 : 50    43 : 51    45 : 53    47 : 53    57 : 53
 //   4096 x 14336, 8 groups    78 : 122   80 : 94    81 : 95    84 : 97    91 : 98
 inline bool few_rows_alone(int rows, int E, int K, int N, int num_sms) {
-  if (!few_rows(rows, E)) return false;
+  if (!few_rows(rows, E, K, N)) return false;
   if (1ll * E * K * N > 64ll << 20) return true;
   const long long tiles = 1ll * E * ((N + 255) / 256);
   const long long shared = tiles < num_sms ? num_sms / tiles : 1, most = (blocks_of(K) + 3) / 4;

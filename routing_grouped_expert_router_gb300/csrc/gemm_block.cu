@@ -966,7 +966,7 @@ bool map_weight(CUtensorMap* m, const void* q, int E, int K, int N, bool trans, 
 cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
                           bool trans, bool out_f32, void* C, cudaStream_t s, bool ahead) {
   if (r.rows == 0) return cudaSuccess;
-  if (ahead ? few_rows(r.rows, r.E) : few_rows_alone(r.rows, r.E, K, N, r.num_sms))
+  if (ahead ? few_rows(r.rows, r.E, K, N) : few_rows_alone(r.rows, r.E, K, N, r.num_sms))
     return few_product(r, a, b, K, N, trans, out_f32, C, s, ahead);
   Params p = params_of(r, K, N, trans);
   p.sa[0] = a.s;
@@ -989,7 +989,7 @@ cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, c
                           int h, int f, uint16_t* A, uint16_t* B, uint16_t* H, uint8_t* Hq,
                           float* sh, cudaStream_t s) {
   if (r.rows == 0) return cudaSuccess;
-  if (few_rows(r.rows, r.E)) return few_fc1_fwd(r, x, w1, w3, h, f, A, B, H, Hq, sh, s);
+  if (few_rows(r.rows, r.E, h, f)) return few_fc1_fwd(r, x, w1, w3, h, f, A, B, H, Hq, sh, s);
   Params p = params_of(r, h, f, false);
   p.sa[0] = x.s;
   p.sb[0] = w1.s;

@@ -119,7 +119,7 @@ __device__ __forceinline__ Tile place(const Params& p, const int* off, const int
   int e = 0, hi = p.E - 1;
   while (e < hi) {
     const int mid = (e + hi + 1) >> 1;
-    if (static_cast<long long>(tiles_n) * cum[mid] <= t)
+    if (tiles_n * cum[mid] <= t)
       e = mid;
     else
       hi = mid - 1;
@@ -134,22 +134,23 @@ __device__ __forceinline__ Tile place(const Params& p, const int* off, const int
   return tl;
 }
 
-// This block's steps [lo, hi) of all `steps`; step s belongs to block owner(s).
+// How `steps` are cut into `blocks` contiguous pieces, the first of them one step longer where
+// they do not divide evenly; step s belongs to block owner(s).  In 32 bits (see few_rows): the
+// divisions stand before a block's first load.
 struct Share {
-  long long steps;
-  int blocks;
-  __device__ __forceinline__ long long lo(int c) const { return steps * c / blocks; }
-  __device__ __forceinline__ int owner(long long s) const {
-    return static_cast<int>(((s + 1) * blocks + steps - 1) / steps) - 1;
+  int each, longer;  // steps of a piece; pieces of one step more
+  __device__ __forceinline__ int lo(int c) const { return each * c + min(c, longer); }
+  __device__ __forceinline__ int owner(int s) const {
+    const int edge = (each + 1) * longer;
+    return s < edge ? s / (each + 1) : longer + (s - edge) / each;
   }
 };
-
-// Blocks that share so many steps: pieces of fewer than MIN_STEPS cost more to join than they
-// save.
-constexpr int MIN_STEPS = 4;
-__device__ __forceinline__ int blocks_for(long long steps) {
-  const long long n = steps / MIN_STEPS;
-  return static_cast<int>(n < 1 ? (steps ? 1 : 0) : n < gridDim.x ? n : gridDim.x);
+constexpr int MIN_STEPS = 4;  // pieces of fewer cost more to join than they save
+__device__ __forceinline__ Share share_of(int steps) {
+  const int most = steps / MIN_STEPS;
+  const int blocks = most < 1 ? 1 : min(most, static_cast<int>(gridDim.x));
+  const int each = steps / blocks;
+  return {each, steps - each * blocks};
 }
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* status) {
@@ -232,23 +233,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // One group: the steps are known before its rows are, and the weights can come to L2 while
     // the kernel before ends (should it write them, L2 has what it wrote).
     if (warp == LOAD_W && p.E == 1) {
-      Share guess;
-      guess.steps = static_cast<long long>((p.N + S::COLS - 1) / S::COLS) * ((p.rows + NT - 1) / NT) * p.nkb;
-      guess.blocks = blocks_for(guess.steps);
-      if (static_cast<int>(blockIdx.x) < guess.blocks) {
-        const long long from = guess.lo(blockIdx.x);
-        const long long to = min(guess.lo(blockIdx.x + 1), from + kEarlySteps);
-        if (elect_one())
-          for (long long i = from; i < to; ++i) {
-            const int n = static_cast<int>(i / p.nkb) / ((p.rows + NT - 1) / NT) * S::COLS;
-            const int k = static_cast<int>(i % p.nkb) * kBlock;
+      const int row_tiles = (p.rows + NT - 1) / NT;
+      const int steps = (p.N + S::COLS - 1) / S::COLS * row_tiles * p.nkb;
+      const Share guess = share_of(steps);
+      const int from = guess.lo(blockIdx.x);
+      const int to = min(min(guess.lo(blockIdx.x + 1), steps), from + kEarlySteps);
+      if (elect_one())
+        for (int i = from; i < to; ++i) {
+          const int n = i / p.nkb / row_tiles * S::COLS;
+          const int k = i % p.nkb * kBlock;
 #pragma unroll
-            for (int o = 0; o < S::NB; ++o) {
-              const int at = n + (FORM == GATED ? 0 : o * 128);
-              tma_prefetch_l2_3d(&maps.w[FORM == GATED ? o : 0], TRANS ? k : at, TRANS ? at : k, 0);
-            }
+          for (int o = 0; o < S::NB; ++o) {
+            const int at = n + (FORM == GATED ? 0 : o * 128);
+            tma_prefetch_l2_3d(&maps.w[FORM == GATED ? o : 0], TRANS ? k : at, TRANS ? at : k, 0);
           }
-      }
+        }
       __syncwarp();
     }
     // the kernel before may have written all that is read from here on
@@ -260,15 +259,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = c.tmem_base;
   const int nkb = p.nkb;
-  Share share;
-  share.steps = static_cast<long long>((p.N + S::COLS - 1) / S::COLS) * c.cum[p.E] * nkb;
-  share.blocks = blocks_for(share.steps);
+  const int steps = (p.N + S::COLS - 1) / S::COLS * c.cum[p.E] * nkb;
+  const Share share = share_of(steps);
   const int me = static_cast<int>(blockIdx.x);
-  const long long lo = me < share.blocks ? share.lo(me) : 0;
-  const long long hi = me < share.blocks ? share.lo(me + 1) : 0;
-  const int count = static_cast<int>(hi - lo);
-  int t = count ? static_cast<int>(lo / nkb) : 0;
-  int kb = count ? static_cast<int>(lo - static_cast<long long>(t) * nkb) : 0;
+  const int lo = min(share.lo(me), steps);  // blocks past the pieces: none
+  const int count = min(share.lo(me + 1), steps) - lo;
+  int t = lo / nkb;
+  int kb = lo - t * nkb;
 
   // Ahead of the end of the kernel before, the weights stream in; what it writes (the
   // activations, their scales, the slots of shared tiles) waits for it.  The kernel after
@@ -415,7 +412,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int n = min(nkb - kb, left);  // this block's steps of the tile
       // Where the tile is shared: the pieces' blocks, and the first one's slot (the others
       // begin with the tile: slot 0).  Divisions, done while the first weights are on the way.
-      const long long s0 = static_cast<long long>(t) * nkb;
+      const int s0 = t * nkb;
       int first = 0, last = 0, first_slot = 0;
       if (n < nkb) {
         first = share.owner(s0);
