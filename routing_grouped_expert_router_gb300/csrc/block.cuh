@@ -38,35 +38,35 @@ struct BlockRows {
 // Whether a group's rows are so few that gemm_block_few.cu's kernel is the faster one where
 // another of these launches comes before it (whose end its first weights need not wait for).
 // The feed-forward block in a graph, us, that kernel against the pairs':
-//   rows to a group           1          8          16         24         48
-//   4096, 14336, 1 group      49 : 82    53 : 77    57 : 74    68 : 75    108 : 76
-//   2048, 1408, 1 group       19 : 27    21 : 27    23 : 28    29 : 28    46 : 28
-//   2048, 1408, 8 groups      30 : 44    33 : 44    39 : 43    56 : 44    65 : 44
-//   4096, 14336, 8 groups     289 : 381  295 : 324  303 : 328  334 : 334  345 : 338
-//   2048, 1408, 64 groups     122 : 179  127 : 167  139 : 170  167 : 172  190 : 175
+//   rows to a group           1          8          16         24         32
+//   4096, 14336, 1 group      46 : 78    49 : 73    52 : 71    62 : 71    65 : 71
+//   4096, 4096, 1 group       26 : 41    29 : 38    32 : 38    39 : 38    42 : 39
+//   2048, 1408, 1 group       17 : 26    19 : 26    21 : 26    26 : 26    28 : 26
+//   2048, 1408, 8 groups      28 : 41    30 : 42    37 : 42    50 : 42    54 : 42
+//   4096, 2048, 4 groups      33 : 50    35 : 47    41 : 47    63 : 47    65 : 47
+//   4096, 14336, 8 groups     276 : 371  283 : 316  292 : 318  315 : 320  320 : 320
+//   2048, 1408, 64 groups     118 : 172  123 : 159  132 : 161  163 : 163  169 : 164
 // The steps of such a launch are counted in 32 bits.
 inline bool few_rows(int rows, int E, int K, int N) {
-  return rows <= 16ll * E && (rows / 16 + E) * (N / 128 + 1ll) * blocks_of(K) < 2147483647ll;
+  return rows <= (E == 1 ? 24 : 16ll * E) && (rows / 16 + E) * (N / 128 + 1ll) * blocks_of(K) < 2147483647ll;
 }
 // The same for a product by itself, whose weights may be what the launch before writes: the
-// joins' time, rows times the pieces of a tile, is then not hidden, and has to be little beside
-// the weights' stream.  Products in a graph, us, as above:
+// rows have to fit its smallest tile (16, twice a group's mean), or the weights' stream to be
+// long beside the join.  Products in a graph, us, as above:
 //   rows to a group           1          4          8          16         32
-//   4096 x 14336, 1 group     18 : 28    19 : 20    19 : 20    21 : 20    24 : 20
-//   2048 x 4096, 1 group      9 : 12     10 : 12    10 : 12    11 : 12    15 : 12
-//   8192 x 2048, 1 group      16 : 18    20 : 17    22 : 17    27 : 17    38 : 18
-//   14336 x 4096, 1 group     20 : 28    21 : 26    23 : 23    26 : 23    34 : 24
-//   2048 x 1408, 8 groups     14 : 13    15 : 13    15 : 13    18 : 13    25 : 13
-//   512 x 2048, 64 groups     25 : 24    26 : 24    26 : 25    29 : 25
-//   2048 x 640, 64 groups     25 : 29    26 : 29    27 : 30    28 : 30
-//   2048 x 1408, 64 groups    41 : 50    43 : 51    45 : 53    47 : 53    57 : 53
-//   4096 x 14336, 8 groups    78 : 122   80 : 94    81 : 95    84 : 97    91 : 98
-inline bool few_rows_alone(int rows, int E, int K, int N, int num_sms) {
-  if (!few_rows(rows, E, K, N)) return false;
-  if (1ll * E * K * N > 64ll << 20) return true;
-  const long long tiles = 1ll * E * ((N + 255) / 256);
-  const long long shared = tiles < num_sms ? num_sms / tiles : 1, most = (blocks_of(K) + 3) / 4;
-  return 1ll * rows * (shared < most ? shared : most) <= 64;
+//   4096 x 14336, 1 group     17 : 26    17 : 20    18 : 20    19 : 20    23 : 19
+//   4096 x 4096, 1 group      10 : 17    10 : 15    11 : 15    13 : 15    19 : 15
+//   8192 x 2048, 1 group      12 : 17    12 : 17    15 : 17    18 : 17    29 : 18
+//   14336 x 4096, 1 group     18 : 28    18 : 26    20 : 23    21 : 23    29 : 24
+//   2048 x 1408, 8 groups     13 : 13    13 : 13    14 : 13    17 : 13    23 : 13
+//   4096 x 1024, 8 groups     15 : 17    15 : 17    16 : 17    20 : 17    27 : 18
+//   512 x 2048, 64 groups     23 : 24    23 : 24    24 : 24    26 : 25    33 : 26
+//   2048 x 640, 64 groups     24 : 29    24 : 29    25 : 30    27 : 30    36 : 30
+//   2048 x 1408, 64 groups    40 : 49    41 : 50    42 : 51    46 : 52    56 : 52
+//   4096 x 14336, 8 groups    77 : 120   79 : 92    80 : 93    82 : 94    89 : 97
+inline bool few_rows_alone(int rows, int E, int K, int N) {
+  return few_rows(rows, E, K, N) &&
+         (rows <= (E == 1 ? 16 : 8ll * E) || 1ll * E * K * N > 64ll << 20);
 }
 constexpr int kPartBlocks = 160;  // blocks of a grid that have room for a shared tile's sums
 inline size_t part_bytes(int rows) {  // 128 x 256 sums for each: the most of either kernel

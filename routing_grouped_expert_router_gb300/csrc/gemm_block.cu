@@ -28,11 +28,12 @@
 // their order (20 to 128 rows by 14336 x 4096: 23 to 29 us, 50 in one piece; see pieces_of).
 //
 // Measured: 16384 x 4096 x 14336 in eight groups, bf16 out, 716 us, 2.69 PFLOP/s, 0.67 of
-// twice the measured bf16 rate.  The sum warps bound it: a block's 128 x 2 columns are
-// loads from tensor memory and 256 fused multiply-adds for each of a scheduler's two warps,
-// some 900 cycles with the waits, against the tensor cores' 512.  One CTA instead of a
-// pair, four accumulators of 128 columns (818 us), sixteen sum warps of half the columns
-// (799), and two issuing warps were all slower; packed multiply-adds made no difference.
+// twice the measured bf16 rate.  No one part bounds it: 666 us without the multiply-adds, 603
+// without the loads from tensor memory too, 516 without operand loads as well; a block takes
+// some 900 cycles, 512 of them the tensor cores'.  One CTA instead of a pair, four accumulators
+// of 128 columns (818 us), sixteen sum warps of half the columns (799), a block's first columns
+// asked for during the block before (740) and two issuing warps were all slower; packed
+// multiply-adds made no difference.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -966,7 +967,7 @@ bool map_weight(CUtensorMap* m, const void* q, int E, int K, int N, bool trans, 
 cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, int K, int N,
                           bool trans, bool out_f32, void* C, cudaStream_t s, bool ahead) {
   if (r.rows == 0) return cudaSuccess;
-  if (ahead ? few_rows(r.rows, r.E, K, N) : few_rows_alone(r.rows, r.E, K, N, r.num_sms))
+  if (ahead ? few_rows(r.rows, r.E, K, N) : few_rows_alone(r.rows, r.E, K, N))
     return few_product(r, a, b, K, N, trans, out_f32, C, s, ahead);
   Params p = params_of(r, K, N, trans);
   p.sa[0] = a.s;
