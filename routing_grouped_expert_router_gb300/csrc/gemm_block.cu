@@ -340,9 +340,10 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, int* sta
   return __all_sync(0xffffffffu, ok);
 }
 
-// PIECES: tiles may be so few that several pairs share one's contraction (a kernel of its own:
-// what it keeps in registers costs the others 4%).
-template <int FORM, bool B_MN, bool PIECES>
+// SMALL: a launch of few tiles, which may begin before the kernel before has ended and whose
+// pairs may share a tile's contraction (a kernel of its own: what that keeps in registers costs
+// large launches 4%).
+template <int FORM, bool B_MN, bool SMALL>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     block_pair_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using S = Shape<FORM>;
@@ -384,6 +385,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_relinquish2();
     tc_fence_before();
   }
+  // launched early (launch_with), the set-up so far ran beside the end of the kernel before,
+  // which may have written all that is read from here on
+  if (SMALL) cudaGridDependencySynchronize();
   if (warp == FIRST_SUM_WARP)
     group_tables(p.offsets, p.E, p.rows, PM, c.off, c.cum, p.status, lane);
   cluster_sync_all();  // both CTAs' barriers exist before any arrival from the other
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // kb_lo + nkb - 1.
   const int tiles = ((p.N + S::OUT_COLS - 1) / S::OUT_COLS) * c.cum[p.E];
   int pieces = 1, tile0 = cid, kb_lo = 0, nkb = p.kblocks * p.products;
-  if (PIECES && tiles > 0 && 2 * tiles <= ncl) {
+  if (SMALL && tiles > 0 && 2 * tiles <= ncl) {
     pieces = min(ncl / tiles, p.most_pieces);
     tile0 = cid < tiles * pieces ? cid / pieces : tiles;
     const int piece = cid % pieces;
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
       }
       if (!ok) break;
-      if (PIECES && pieces > 1) {
+      if (SMALL && pieces > 1) {
         // This piece's sums to its slot; the last of the tile's to arrive adds all in order and
         // goes on to the epilogue.
         constexpr int SLOT = 128 * S::COLS / 4;  // four columns of a row side by side
@@ -885,9 +889,17 @@ void set_raster(Params& p, long long a_bytes, long long b_bytes, long long slab_
   }
 }
 
-template <int FORM, bool B_MN, bool PIECES>
-cudaError_t launch_with(const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
-  auto kern = block_pair_kernel<FORM, B_MN, PIECES>;
+template <int FORM>
+long long column_tiles(const Params& p) {
+  return (p.N + Shape<FORM>::OUT_COLS - 1) / Shape<FORM>::OUT_COLS;
+}
+template <int FORM>
+long long most_tiles(const Params& p) {
+  return column_tiles<FORM>(p) * ((p.rows + PM - 1) / PM + p.E);
+}
+template <int FORM, bool B_MN, bool SMALL>
+cudaError_t launch_with(const Params& p, const Maps& m, int num_sms, bool early, cudaStream_t s) {
+  auto kern = block_pair_kernel<FORM, B_MN, SMALL>;
   constexpr int smem = smem_bytes<FORM>();
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
@@ -895,28 +907,42 @@ cudaError_t launch_with(const Params& p, const Maps& m, int num_sms, cudaStream_
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const long long nt = (p.N + Shape<FORM>::OUT_COLS - 1) / Shape<FORM>::OUT_COLS;
-  const long long most = nt * ((p.rows + PM - 1) / PM + p.E) * (PIECES ? p.most_pieces : 1);
   int fit = pairs_that_fit(reinterpret_cast<const void*>(kern), cfg, num_sms);
-  if (PIECES && fit > kMostPairs) fit = kMostPairs;
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(most < fit ? most : fit), 1, 1);
+  if (SMALL && fit > kMostPairs) fit = kMostPairs;
+  const long long items = most_tiles<FORM>(p) * (SMALL ? p.most_pieces : 1);
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(items < fit ? items : fit), 1, 1);
+  if (early) cfg.numAttrs = 2;
   const cudaError_t le = cudaLaunchKernelEx(&cfg, kern, p, m);
   return le == cudaSuccess ? launched() : le;
 }
+// Which of the two: the small one where pairs may share tiles, and for launches of some 15 us
+// (32 blocks in turn) or less in a stream, which then begin before the kernel before has ended.
+// Calls in a stream, us, without and with: 1037 x 1104 x 720 12.3 10.9, 100 x 4096 x 4096
+// 20.4 17.7, its feed-forward block 44.9 41.6; with 64 blocks in turn 70.7 73.8.  In a graph an
+// early launch gains nothing.
 template <int FORM, bool B_MN>
 cudaError_t launch_pairs(const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &capture);
+  if (e != cudaSuccess) return e;
+  const bool stream = capture == cudaStreamCaptureStatusNone;
+  const long long pairs = num_sms > 1 ? num_sms / 2 : 1;
+  const long long turns = (most_tiles<FORM>(p) + pairs - 1) / pairs;
   // the fewest tiles that these rows can make; the kernel counts those there are
-  const long long nt = (p.N + Shape<FORM>::OUT_COLS - 1) / Shape<FORM>::OUT_COLS;
-  const long long least = nt * ((p.rows + PM - 1) / PM);
-  return p.most_pieces > 1 && 4 * least <= num_sms ? launch_with<FORM, B_MN, true>(p, m, num_sms, s)
-                                                   : launch_with<FORM, B_MN, false>(p, m, num_sms, s);
+  const long long least = column_tiles<FORM>(p) * ((p.rows + PM - 1) / PM);
+  const bool shared = p.most_pieces > 1 && 2 * least <= pairs;
+  return shared || (stream && turns * p.kblocks * p.products <= 32)
+             ? launch_with<FORM, B_MN, true>(p, m, num_sms, stream, s)
+             : launch_with<FORM, B_MN, false>(p, m, num_sms, false, s);
 }
 
 // Pieces of a tile's contraction of `blocks` blocks, where pairs would idle otherwise.  Blocks
