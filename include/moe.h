@@ -428,7 +428,8 @@ size_t moe_gemm_workspace_bytes(const moe_gemm_dims* dims);
  * the status word of ws.
  * The same inputs give the same bits.  Calls that may run at the same time need
  * a workspace each; the first 256 bytes of ws have to be zero before its first
- * use. */
+ * use (every call leaves them so, but for the status word; after
+ * MOE_ERR_DEVICE_TIMEOUT call moe_clear_device_status). */
 moe_status moe_gemm_fp8_block(const moe_gemm_dims* dims, const uint8_t* aq,
                               const float* sa, const uint8_t* bq,
                               const float* sb, const int32_t* offsets, void* C,
@@ -474,7 +475,8 @@ moe_status moe_gated_ffn_fwd(const moe_ffn_dims* dims, const moe_bf16* x,
  * bf16 values), the weight gradients on the bf16 x, H, dy, dA, dB.  dx
  * [rows, h] bf16 (rows p >= offsets[E] untouched); dW1, dW3 [E, h, f], dW2
  * [E, f, h] fp32 or bf16 (dims.dw_bf16), written, not accumulated, zero for
- * an expert without rows; all three NULL for weights that are not trained. */
+ * an expert without rows; all three NULL for weights that are not trained.
+ * Offsets and ws as in moe_gemm_fp8_block. */
 moe_status moe_gated_ffn_bwd(const moe_ffn_dims* dims, const moe_bf16* x,
                              const moe_bf16* dy, const int32_t* offsets,
                              const uint8_t* W1q, const float* s1,

@@ -74,7 +74,7 @@ struct Shape {
   static constexpr int STAGE_BYTES = NB * W_BYTES + X_BYTES;
   static constexpr int UNIT = NB * NT;               // accumulator columns of a step
   static constexpr int PITCH = (FORM == PLAIN_F32 ? 512 : 256) + 16;  // staging: bytes of a row
-  static constexpr int FIT = (232448 - 1024 - NT * PITCH - 3072) / STAGE_BYTES;
+  static constexpr int FIT = (232448 - 1024 - NT * PITCH - 3 * 1024) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 12 ? 12 : FIT;
   static constexpr int BUFS = 4 * UNIT > 256 ? 2 : 4;  // steps whose sums wait in tensor memory
   static constexpr int TMEM = BUFS * UNIT;           // columns (a power of two, 64 to 256)

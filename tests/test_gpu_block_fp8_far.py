@@ -165,3 +165,51 @@ def test_shared_tiles_give_the_same_bits_each_time(lib, counts, h, f):  # noqa: 
     want = br.ffn_bwd(*[t.double() for t in (x, dy, A, B, H)], *[v[2] for v in w], _groups(counts))
     assert _rel(dx, want[0]) <= 5e-3
     assert mb.moe_read_device_status(ws) == mb.MOE_OK and not ws[:256].any()
+
+
+@pytest.mark.parametrize("rows", [2, 60, 300])
+def test_weights_written_just_before(lib, rows):  # noqa: F811
+    """Launches that begin early read the weights, offsets and rows that the launches just before them wrote."""
+    E, h, f, n = 2, 512, 384, 24
+    g = torch.Generator("cuda").manual_seed(31)
+    Ws = [torch.empty((n, E, a, b), dtype=BF, device="cuda").normal_(0.0, a ** -0.5, generator=g) for a, b in ((h, f), (h, f), (f, h))]
+    xs = torch.empty((n, rows, h), dtype=BF, device="cuda").normal_(0.0, 1.0, generator=g)
+    cuts = [(7 * i) % (rows + 1) for i in range(n)]
+    offs = torch.tensor([[0, c, rows] for c in cuts], dtype=torch.int32, device="cuda")
+    q = [torch.empty(W.shape[1:], dtype=torch.uint8, device="cuda") for W in Ws]
+    s = [torch.empty((E, -(-W.shape[2] // 128), -(-W.shape[3] // 128)), dtype=F32, device="cuda") for W in Ws]
+    x, o = torch.empty_like(xs[0]), torch.empty_like(offs[0])
+    aq, sa = torch.empty((rows, h), dtype=torch.uint8, device="cuda"), torch.empty((h // 128, rows), dtype=F32, device="cuda")
+    fd, gd = mb.ffn_dims(rows, h, f, E), mb.gemm_dims(rows, h, f, E)
+    ws = _ws(max(mb.moe_ffn_workspace_bytes(fd, 0), mb.moe_gemm_workspace_bytes(gd)))
+    y = torch.empty_like(xs)
+    C = torch.empty((n, rows, f), dtype=BF, device="cuda")
+
+    def step(i, wait):
+        def then():
+            if wait:
+                torch.cuda.synchronize()
+        x.copy_(xs[i])
+        o.copy_(offs[i])
+        mb.moe_quantize_rows_fp8_block(x, rows, h, None, 1, rows, aq, sa)
+        then()
+        mb.moe_quantize_weights_fp8_block(Ws[0][i], E, h, f, q[0], s[0])
+        then()
+        mb.moe_gemm_fp8_block(gd, aq, sa, q[0], s[0], o, C[i], ws)
+        then()
+        for j in (1, 2):
+            mb.moe_quantize_weights_fp8_block(Ws[j][i], *Ws[j].shape[1:], q[j], s[j])
+        then()
+        mb.moe_gated_ffn_fwd(fd, x, o, q[0], s[0], q[1], s[1], q[2], s[2], None, None, None, y[i], ws)
+        then()
+
+    for i in range(n):
+        step(i, True)
+    want = y.clone(), C.clone()
+    for _ in range(5):
+        y.fill_(3)
+        C.fill_(3)
+        for i in range(n):
+            step(i, False)
+        assert torch.equal(y, want[0]) and torch.equal(C, want[1])
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK
