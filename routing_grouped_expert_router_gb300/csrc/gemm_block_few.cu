@@ -7,15 +7,15 @@
 //     block's MMAs whatever the number of rows.  A step has two such blocks: side by
 //     side in one weight (256 bytes in a row of it: with 128 HBM moved 10% less), or the
 //     same columns of W1 and W3.
-//   * All k-steps of all tiles are cut into equal contiguous pieces, one for each
-//     block of the grid, so that every SM streams the same bytes whatever the tiles'
-//     number.  A tile that several blocks share is joined by the last to arrive, in the
+//   * All k-steps of all tiles are cut into contiguous pieces, one for each block of
+//     the grid: the same number for every tile, or, where that leaves too many SMs idle,
+//     equal ones whatever the tiles' number.  A tile that several blocks share is joined by the last to arrive, in the
 //     pieces' order: the same inputs give the same bits.
 //   * A ring of some 190 KiB of stages is under way on each SM.
-// Measured, in a graph, weights not in L2: one row by 4096 x 14336, 17 us (8.8 at the copy
+// Measured, in a graph, weights not in L2: one row by 4096 x 14336, 16 us (8.8 at the copy
 // bandwidth); 192 rows in 64 groups of 2048 x 1408, 40 us (25.6).  What is left is the start
 // (some 3 us to the first weights), the join of shared tiles (2 to 3 us) and SMs that HBM
-// serves unevenly; tiles in place of equal pieces left a third of the SMs idle.
+// serves unevenly.
 // Roles of a block's 256 threads: warp 0 loads weights, warp 3 activations, warp 2
 // scales, warp 1 issues the MMAs, warps 4-7 take each step's sums out of tensor
 // memory, times the scales, into sums in registers (one output column to a thread).

@@ -142,7 +142,7 @@ def test_two_graphs_on_one_workspace(lib):  # noqa: F811
     assert not ws[:256].any()
 
 
-@pytest.mark.parametrize("counts,h,f", [([50], 4096, 1152), ([130, 0, 300], 2048, 256), ([20, 0, 40], 192, 8192)])
+@pytest.mark.parametrize("counts,h,f", [([30], 1024, 640), ([50], 4096, 1152), ([130, 0, 300], 2048, 256), ([20, 0, 40], 192, 8192)])
 def test_shared_tiles_give_the_same_bits_each_time(lib, counts, h, f):  # noqa: F811
     """Few tiles with a long contraction: pieces of a tile are joined in their order, whichever arrives last."""
     E, R = len(counts), sum(counts)
