@@ -9,8 +9,8 @@
 //     same columns of W1 and W3.
 //   * All k-steps of all tiles are cut into contiguous pieces, one for each block of
 //     the grid: the same number for every tile, or, where that leaves too many SMs idle,
-//     equal ones whatever the tiles' number.  A tile that several blocks share is joined by the last to arrive, in the
-//     pieces' order: the same inputs give the same bits.
+//     equal ones whatever the tiles' number.  A tile that several blocks share is joined
+//     by the last to arrive, in the pieces' order: the same inputs give the same bits.
 //   * A ring of some 190 KiB of stages is under way on each SM.
 // Measured, in a graph, weights not in L2: one row by 4096 x 14336, 16 us (8.8 at the copy
 // bandwidth); 192 rows in 64 groups of 2048 x 1408, 40 us (25.6).  What is left is the start
