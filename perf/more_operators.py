@@ -41,23 +41,23 @@ def listed():
         # the weights of 8 wide experts after an optimiser step
         _weights("quantise 8 wide weights", 8, 4096, 14336),
         # one token through one wide projection: the latency of a dense block's decode step
-        _gemm("product of one row", 1, 4096, 14336, 1),
+        _gemm("product, one row", 1, 4096, 14336, 1),
         # 32 tokens, top 6 of 64 experts: a few rows to each expert, some experts without any
-        _gemm("product of few rows and 64 experts", 192, 2048, 1408, 64, skew=0.5),
+        _gemm("product, 64 experts, few rows", 192, 2048, 1408, 64, skew=0.5),
         # sizes that fill no tile and no block of 128, the transposed weight, float32 sums handed on
-        _gemm("product at odd sizes", 1037, 1104, 720, 5, skew=1.0, trans=True, out="fp32"),
+        _gemm("product, odd sizes", 1037, 1104, 720, 5, skew=1.0, trans=True, out="fp32"),
         # a training step's first projection over 8 wide experts
-        _gemm("product in training", 16384, 4096, 14336, 8),
+        _gemm("product, training", 16384, 4096, 14336, 8),
         # a dense (shared) expert on one user's next token
-        _ffn("feed-forward of one row", "ffn_fwd", 1, 4096, 14336, 1, keep=False),
+        _ffn("feed-forward, one row", "ffn_fwd", 1, 4096, 14336, 1, keep=False),
         # a server's batch through the DeepSeekMoE-shaped experts, skewed
-        _ffn("feed-forward of few rows", "ffn_fwd", 192, 2048, 1408, 64, skew=0.5, keep=False),
+        _ffn("feed-forward, 64 experts", "ffn_fwd", 192, 2048, 1408, 64, skew=0.5, keep=False),
         # a training step of the DeepSeekMoE-shaped layer: 8192 tokens, top 6, activations kept for the backward
-        _ffn("feed-forward in training", "ffn_fwd", 49152, 2048, 1408, 64, skew=0.2),
+        _ffn("feed-forward, training", "ffn_fwd", 49152, 2048, 1408, 64, skew=0.2),
         # a small training step at odd sizes: half blocks of 128, ragged experts
-        _ffn("backward at odd sizes", "ffn_bwd", 1021, 1088, 704, 5, skew=1.0),
+        _ffn("backward, odd sizes", "ffn_bwd", 1021, 1088, 704, 5, skew=1.0),
         # the backward of 8 wide experts in training
-        _ffn("backward in training", "ffn_bwd", 16384, 4096, 14336, 8),
+        _ffn("backward, training", "ffn_bwd", 16384, 4096, 14336, 8),
     ]
 
 
