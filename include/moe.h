@@ -458,7 +458,8 @@ size_t moe_ffn_workspace_bytes(const moe_ffn_dims* dims, int backward);
 /* x [rows, h] bf16 (rows of expert e at offsets[e] .. offsets[e+1]-1), y
  * [rows, h] bf16.  A, B, H [rows, f] bf16 are what the backward takes; all three
  * NULL where none follows.  Rows p >= offsets[E] are neither read nor
- * written.  Offsets and ws as in moe_gemm_fp8_block. */
+ * written.  Offsets and ws as in moe_gemm_fp8_block: with offsets out of order
+ * the groups are those of the offsets clamped into order, in every step. */
 moe_status moe_gated_ffn_fwd(const moe_ffn_dims* dims, const moe_bf16* x,
                              const int32_t* offsets, const uint8_t* W1q,
                              const float* s1, const uint8_t* W3q,

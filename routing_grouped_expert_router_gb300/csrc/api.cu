@@ -1013,7 +1013,7 @@ moe_status moe_layer_fwd_fp8_block(const moe_dims* dims, const moe_bf16* x, cons
     return st;
   // the rows' codes for FC1 and, in the same pass, the bf16 rows of the weight gradients
   MOE_RUN(moe::launch_quant_rows_block(x, psrc, d.k, R, d.T, d.h, Xq, sx, num_sms(), stream,
-                                       offsets + d.E, at<uint16_t>(saved, S.x_perm),
+                                       offsets + d.E, 1, at<uint16_t>(saved, S.x_perm),
                                        at<int>(ws, 0)),
           "permute_quant_x_block");
   if (R > 0) {
@@ -1077,7 +1077,7 @@ moe_status moe_layer_bwd_fp8_block(const moe_dims* dims, const moe_bf16* x, cons
     const moe::BlockRows r = {d.E, offsets, static_cast<int>(R), at<int>(ws, 0), num_sms(),
                               at<float>(ws, L.part)};
     MOE_RUN(moe::launch_quant_rows_block(dO, nullptr, 1, R, R, d.h, dOq, sdo, num_sms(), stream,
-                                         nvalid, nullptr, at<int>(ws, 0)),
+                                         nvalid, 1, nullptr, at<int>(ws, 0)),
             "quant_dO_block");
     MOE_RUN(moe::block_fc2_dgrad(r, {dOq, sdo}, {W2q, s2}, d.h, d.f, at<uint16_t>(saved, S.A),
                                  at<uint16_t>(saved, S.B), dA, dB, dAq, sda, dBq, sdb, stream),

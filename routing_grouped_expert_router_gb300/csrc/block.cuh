@@ -15,12 +15,15 @@ constexpr int kBlock = 128;
 inline int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 
 // Rows of `in` (row idx[p] / div, or p) -> codes [rows, n] and block scales
-// [ceil(n/128), rows], for p < rows (and p < *nvalid where given).  With copy,
-// the bf16 source rows are also written to copy [rows, n].  n a multiple of 16.
+// [ceil(n/128), rows], for p < rows (and, where given, p < the largest of
+// ends[0 .. n_ends-1]: the groups' offsets, or their last alone where they are known
+// to be in order).  With copy, the bf16 source rows are also written to copy [rows, n].
+// n a multiple of 16.
 cudaError_t launch_quant_rows_block(const uint16_t* in, const int32_t* idx, int div,
                                     long long rows, long long src_rows, int n, uint8_t* q,
                                     float* scale, int num_sms, cudaStream_t s,
-                                    const int32_t* nvalid, uint16_t* copy, int* status);
+                                    const int32_t* ends, int n_ends, uint16_t* copy,
+                                    int* status);
 // Weights [E, K, N] -> codes [E, K, N] and scales [E, ceil(K/128), ceil(N/128)].
 cudaError_t launch_quant_weights_block(const uint16_t* W, int E, int K, int N, uint8_t* q,
                                        float* scale, cudaStream_t s);

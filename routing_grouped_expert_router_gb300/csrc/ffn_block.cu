@@ -153,8 +153,7 @@ moe_status moe_gated_ffn_fwd(const moe_ffn_dims* dims, const moe_bf16* x, const 
   uint8_t *xq = at<uint8_t>(ws, L.Xq), *hq = at<uint8_t>(ws, L.Hq);
   float *sx = at<float>(ws, L.sx), *sh = at<float>(ws, L.sh);
   BLOCK_RUN(moe::launch_quant_rows_block(x, nullptr, 1, d.rows, d.rows, d.h, xq, sx, r.num_sms,
-                                         stream, offsets ? offsets + d.E : nullptr, nullptr,
-                                         r.status),
+                                         stream, offsets, d.E + 1, nullptr, r.status),
             "quant_rows_block");
   BLOCK_RUN(moe::block_fc1_fwd(r, {xq, sx}, {W1q, s1}, {W3q, s3}, d.h, d.f, A, B, H, hq, sh,
                                stream),
@@ -196,8 +195,7 @@ moe_status moe_gated_ffn_bwd(const moe_ffn_dims* dims, const moe_bf16* x, const 
   float *sdy = at<float>(ws, L.sx), *sda = at<float>(ws, L.sda), *sdb = at<float>(ws, L.sdb);
   uint16_t *da = at<uint16_t>(ws, L.dA), *db = at<uint16_t>(ws, L.dB);
   BLOCK_RUN(moe::launch_quant_rows_block(dy, nullptr, 1, d.rows, d.rows, d.h, dyq, sdy, r.num_sms,
-                                         stream, offsets ? offsets + d.E : nullptr, nullptr,
-                                         r.status),
+                                         stream, offsets, d.E + 1, nullptr, r.status),
             "quant_rows_block");
   BLOCK_RUN(moe::block_fc2_dgrad(r, {dyq, sdy}, {W2q, s2}, d.h, d.f, A, B, da, db, daq, sda, dbq,
                                  sdb, stream),

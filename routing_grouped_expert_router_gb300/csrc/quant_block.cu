@@ -43,8 +43,8 @@ __device__ __forceinline__ uint32_t top8(const uint4& w) {
 // rows to fill the GPU.
 __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
     const uint4* __restrict__ in, const int32_t* __restrict__ idx, int div, long long rows,
-    long long src_rows, const int32_t* __restrict__ nvalid, int n8, int quads, int quads_each,
-    uint2* __restrict__ q, float* __restrict__ scale, uint4* __restrict__ copy,
+    long long src_rows, const int32_t* __restrict__ ends, int n_ends, int n8, int quads,
+    int quads_each, uint2* __restrict__ q, float* __restrict__ scale, uint4* __restrict__ copy,
     int* __restrict__ status) {
   // The kernel before may have written what is read here.  The next one may start once all
   // before this one are done: it can read what neither this one nor itself writes.
@@ -55,9 +55,12 @@ __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
   const long long warps = (static_cast<long long>(gridDim.x) * kRowThreads) >> 5;
   const long long ld = rows;  // of the scales
   long long last = rows;
-  if (nvalid) {
-    const long long nv = __ldg(nvalid);
-    last = nv < rows ? nv : rows;
+  if (ends) {
+    // the furthest end, as group_tables clamps the groups: offsets out of order leave no row
+    // that a product takes without codes
+    int top = 0;
+    for (int i = lane; i < n_ends; i += 32) top = max(top, __ldg(ends + i));
+    last = min(static_cast<long long>(__reduce_max_sync(kFull, top)), rows);
   }
   const int first_quad = blockIdx.y * quads_each;
   const int end_quad = min(first_quad + quads_each, quads);
@@ -147,7 +150,8 @@ __global__ void __launch_bounds__(kWeightThreads) quant_weights_block_kernel(
 cudaError_t launch_quant_rows_block(const uint16_t* in, const int32_t* idx, int div,
                                     long long rows, long long src_rows, int n, uint8_t* q,
                                     float* scale, int num_sms, cudaStream_t s,
-                                    const int32_t* nvalid, uint16_t* copy, int* status) {
+                                    const int32_t* ends, int n_ends, uint16_t* copy,
+                                    int* status) {
   if (rows == 0) return cudaSuccess;
   const int quads = (n + 4 * kBlock - 1) / (4 * kBlock);
   const long long row_blocks = (rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
@@ -168,7 +172,7 @@ cudaError_t launch_quant_rows_block(const uint16_t* in, const int32_t* idx, int 
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(
       &cfg, quant_rows_block_kernel, reinterpret_cast<const uint4*>(in), idx, idx ? div : 1, rows,
-      src_rows, nvalid, n / 8, quads, each, reinterpret_cast<uint2*>(q), scale,
+      src_rows, ends, n_ends, n / 8, quads, each, reinterpret_cast<uint2*>(q), scale,
       reinterpret_cast<uint4*>(copy), status);
   return e == cudaSuccess ? launched() : e;
 }
@@ -204,7 +208,7 @@ moe_status moe_quantize_rows_fp8_block(const moe_bf16* in, int64_t rows, int32_t
   if (!status) return MOE_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (moe::launch_quant_rows_block(in, idx, div, rows, src_rows, n, q, scale, moe_api::num_sms(),
-                                   s, nullptr, nullptr, status) != cudaSuccess ||
+                                   s, nullptr, 0, nullptr, status) != cudaSuccess ||
       !moe_api::note(s, "quant_rows_block"))
     return MOE_ERR_CUDA;
   return MOE_OK;

@@ -1,0 +1,52 @@
+"""The block-scaled e4m3 operators where a call goes wrong or two ways of making
+it meet: offsets out of order, launches that fail, waits that ran out, streams
+and graphs, and each way in which few rows are cut into pieces.  References and
+tolerances are those of test_gpu_block_fp8.py."""
+import pytest
+import torch
+
+from routing_grouped_expert_router_gb300 import binding as mb
+from tests import block_ref as br
+from tests.test_gpu_block_fp8 import BF, F32, _check_bwd, _check_fwd, _ffn_weights, _normal, _offsets, _product, _quantize_rows, _ws, lib  # noqa: F401
+
+pytestmark = [pytest.mark.gpu]
+
+
+# ---------------------------------------------------------------- offsets out of order
+@pytest.mark.parametrize("R", [9, 300])
+@pytest.mark.parametrize("cuts", ["down", "past the end", "all in the first", "below zero"])
+def test_feed_forward_with_offsets_out_of_order(lib, R, cuts):  # noqa: F811
+    """Clamped into order and recorded: the rows of the groups as clamped, none of what an earlier call left in the workspace."""
+    E, h, f = 4, 256, 320
+    offsets, counts = {
+        "down": ([0, 5, 3, R, 2], [5, 0, R - 5, 0]),
+        "past the end": ([0, 2, 7, R + 1000, 2 ** 31 - 1], [2, 5, R - 7, 0]),
+        "all in the first": ([0, R, 0, 0, 0], [R, 0, 0, 0]),
+        "below zero": ([0, -3, 7, 6, -2 ** 31], [0, 7, 0, 0]),
+    }[cuts]
+    n = sum(counts)
+    w = _ffn_weights(E, h, f, 41)
+    codes = [t for q, s, _ in w for t in (q, s)]
+    x, dy = _normal((R, h), 42), _normal((R, h), 43)
+    A, B, H = (torch.full((R, f), 55.0, dtype=BF, device="cuda") for _ in range(3))
+    y, dx = torch.full_like(x, 55.0), torch.full_like(x, 55.0)
+    dW = [torch.full(v[0].shape, 55.0, dtype=F32, device="cuda") for v in w]
+    fd = mb.ffn_dims(R, h, f, E)
+    ws = _ws(max(mb.moe_ffn_workspace_bytes(fd, b) for b in (0, 1)))
+    # other rows through the same workspace first
+    x0, dy0, o0 = _normal((R, h), 44, 50.0), _normal((R, h), 45, 50.0), _offsets([R, 0, 0, 0])
+    A0, B0, H0 = (torch.empty_like(A) for _ in range(3))
+    o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    mb.moe_gated_ffn_fwd(fd, x0, o0, *codes, A0, B0, H0, torch.empty_like(y), ws)
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK
+    mb.moe_gated_ffn_fwd(fd, x, o, *codes, A, B, H, y, ws)
+    assert mb.moe_read_device_status(ws) == mb.MOE_ERR_DEVICE_INDEX
+    _check_fwd(x, A, B, H, y, w, counts)
+    for t in (A, B, H, y):
+        assert (t[n:] == 55).all()
+    mb.moe_gated_ffn_bwd(fd, x0, dy0, o0, *codes, A0, B0, H0, torch.empty_like(dx), None, None, None, ws)
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK
+    mb.moe_gated_ffn_bwd(fd, x, dy, o, *codes, A, B, H, dx, *dW, ws)
+    assert mb.moe_read_device_status(ws) == mb.MOE_ERR_DEVICE_INDEX
+    _check_bwd(x, dy, A, B, H, w, counts, dx, dW, n)
+    assert (dx[n:] == 55).all()
