@@ -408,7 +408,7 @@ moe_status moe_quantize_weights_fp8_block(const moe_bf16* W, int32_t E,
                                           float* scale, moe_stream_t stream);
 
 typedef struct {
-  int32_t rows;     /* rows of the activations */
+  int32_t rows;     /* rows of the activations, at most 2^31 - 512 */
   int32_t K;        /* contraction, a multiple of 16, at most 2^20 */
   int32_t N;        /* output columns, a multiple of 16, at most 2^20 */
   int32_t E;        /* groups of rows (experts), at most 64 */
@@ -443,7 +443,7 @@ moe_status moe_gemm_fp8_block(const moe_gemm_dims* dims, const uint8_t* aq,
  * in the call; both projections, the activation, the product and H's codes
  * (from its bf16 value) come from one kernel. */
 typedef struct {
-  int32_t rows;
+  int32_t rows;     /* at most 2^31 - 512 */
   int32_t h;        /* a multiple of 64, at most 2^20 */
   int32_t f;        /* a multiple of 64, at most 2^20 */
   int32_t E;        /* groups of rows (experts), at most 64 */
@@ -490,8 +490,8 @@ moe_status moe_gated_ffn_bwd(const moe_ffn_dims* dims, const moe_bf16* x,
 
 /* moe_layer_fwd and moe_layer_bwd with the experts above.  The forward writes
  * the same `saved` context as moe_layer_fwd; the backward takes one from
- * either of the two.  h and f multiples of 64; dims.sar = 1 is
- * MOE_ERR_UNSUPPORTED.  Workspaces: moe_workspace_bytes with
+ * either of the two.  h and f multiples of 64; dims.sar = 1 and more than
+ * 2^31 - 512 assignments T*k are MOE_ERR_UNSUPPORTED.  Workspaces: moe_workspace_bytes with
  * MOE_OP_LAYER_FWD_FP8_BLOCK and MOE_OP_LAYER_BWD_FP8_BLOCK. */
 moe_status moe_layer_fwd_fp8_block(const moe_dims* dims, const moe_bf16* x,
                                    const float* Wg, const float* b,

@@ -133,6 +133,9 @@ Fp8BwdWeightLayout fp8_bwd_weight_layout(const moe_dims& d) {
 
 size_t rows_of(const moe_dims& d) { return static_cast<size_t>(d.T) * d.k; }
 
+// What the layer on block-scaled weights takes of the dims that the others do.
+bool block_ok(const moe_dims& d) { return !d.sar && rows_of(d) <= moe::kMostRows; }
+
 struct SavedLayout {
   size_t topk_idx, gates, counts, offsets, perm_src, perm_dst, x_perm, A, B, H, O, total;
 };
@@ -203,7 +206,7 @@ WsLayout ws_layout(const moe_dims& d, int op) {
   const size_t hb = moe::blocks_of(d.h), fb = moe::blocks_of(d.f);
   switch (op) {
     case MOE_OP_LAYER_FWD_FP8_BLOCK:
-      if (d.sar) return WsLayout{};
+      if (!block_ok(d)) return WsLayout{};
       route();
       dispatch();
       L.Xq = c.take(R * d.h);
@@ -213,7 +216,7 @@ WsLayout ws_layout(const moe_dims& d, int op) {
       L.part = c.take(moe::part_bytes(static_cast<int>(R)));
       break;
     case MOE_OP_LAYER_BWD_FP8_BLOCK:
-      if (d.sar) return WsLayout{};
+      if (!block_ok(d)) return WsLayout{};
       expert_bwd(false);
       L.dOq = c.take(R * d.h);
       L.sdo = c.take(R * hb * 4);
@@ -988,7 +991,7 @@ moe_status moe_layer_fwd_fp8_block(const moe_dims* dims, const moe_bf16* x, cons
   moe_status st = check_dims(dims, true);
   if (st != MOE_OK) return st;
   const moe_dims& d = *dims;
-  if (d.sar) return MOE_ERR_UNSUPPORTED;  // as in moe_layer_fwd_fp8
+  if (!block_ok(d)) return MOE_ERR_UNSUPPORTED;
   const size_t T = d.T;
   if (!buf_ok(x, T) || !ptr_ok(Wg) || !ptr_ok(W1q) || !ptr_ok(s1) || !ptr_ok(W3q) || !ptr_ok(s3) ||
       !ptr_ok(W2q) || !ptr_ok(s2) || !buf_ok(y, T) || (d.has_bias && !ptr_ok(b)) || !saved ||
@@ -1041,7 +1044,7 @@ moe_status moe_layer_bwd_fp8_block(const moe_dims* dims, const moe_bf16* x, cons
   moe_status st = check_dims(dims, true);
   if (st != MOE_OK) return st;
   const moe_dims& d = *dims;
-  if (d.sar) return MOE_ERR_UNSUPPORTED;
+  if (!block_ok(d)) return MOE_ERR_UNSUPPORTED;
   const size_t T = d.T;
   if (!buf_ok(x, T) || !buf_ok(dy, T) || !ptr_ok(Wg) || !ptr_ok(W1q) || !ptr_ok(s1) ||
       !ptr_ok(W3q) || !ptr_ok(s3) || !ptr_ok(W2q) || !ptr_ok(s2) || !saved ||

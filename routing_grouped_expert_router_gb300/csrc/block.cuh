@@ -9,6 +9,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "block_order.h"
+
 namespace moe {
 
 constexpr int kBlock = 128;

@@ -42,8 +42,8 @@ bool tiles_fit(int rows, int E, int n) {
 moe_status check_gemm(const moe_gemm_dims* d) {
   if (!d || d->rows < 0 || d->K <= 0 || d->N <= 0 || d->E <= 0) return MOE_ERR_INVALID_ARG;
   if ((d->trans_b | 1) != 1 || (d->out_f32 | 1) != 1) return MOE_ERR_INVALID_ARG;
-  if (d->E > 64 || d->K % 16 != 0 || d->N % 16 != 0 || d->K > kMaxSide ||
-      d->N > kMaxSide || !tiles_fit(d->rows, d->E, d->N))
+  if (d->rows > moe::kMostRows || d->E > 64 || d->K % 16 != 0 || d->N % 16 != 0 ||
+      d->K > kMaxSide || d->N > kMaxSide || !tiles_fit(d->rows, d->E, d->N))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -51,8 +51,8 @@ moe_status check_gemm(const moe_gemm_dims* d) {
 moe_status check_ffn(const moe_ffn_dims* d) {
   if (!d || d->rows < 0 || d->h <= 0 || d->f <= 0 || d->E <= 0 || (d->dw_bf16 | 1) != 1)
     return MOE_ERR_INVALID_ARG;
-  if (d->E > 64 || d->h % 64 != 0 || d->f % 64 != 0 || d->h > kMaxSide ||
-      d->f > kMaxSide || !tiles_fit(d->rows, d->E, d->h) || !tiles_fit(d->rows, d->E, d->f))
+  if (d->rows > moe::kMostRows || d->E > 64 || d->h % 64 != 0 || d->f % 64 != 0 ||
+      d->h > kMaxSide || d->f > kMaxSide || !tiles_fit(d->rows, d->E, d->h) || !tiles_fit(d->rows, d->E, d->f))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

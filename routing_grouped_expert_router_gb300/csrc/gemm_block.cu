@@ -81,7 +81,7 @@ struct Params {
   uint8_t* codes[2];
   float* scales[2];
   int* status;
-  int raster_n, group;      // tile order (see place)
+  TileOrder order;          // of a group's tiles
   float* part;              // shared tiles' sums
   uint32_t* arrived;        // a byte for each CTA's rows of a shared tile
   int most_pieces;          // of a tile
@@ -150,9 +150,7 @@ struct Tile {
   int e, nb, row0, row_end;
 };
 
-// Tile t: groups in order; within one, bands of p.group row tiles (or, raster_n,
-// column tiles) swept along the other side, so that the tiles under way share
-// what L2 holds.
+// Tile t: groups in order; within one, as p.order has them.
 template <int FORM>
 __device__ __forceinline__ bool place(const Params& p, const int* off, const int* cum, int t,
                                       Tile& tl) {
@@ -167,16 +165,10 @@ __device__ __forceinline__ bool place(const Params& p, const int* off, const int
       hi = mid - 1;
   }
   const int local = t - NT * cum[e];
-  const int MT = cum[e + 1] - cum[e];
-  const int wide = p.raster_n ? NT : MT, along = p.raster_n ? MT : NT;
-  const int band = local / (p.group * along);
-  const int base = band * p.group;
-  const int size = min(p.group, wide - base);
-  const int r = local - band * p.group * along;
-  const int u = base + r % size, v = r / size;
+  const TileAt at = tile_at(p.order, cum[e + 1] - cum[e], NT, local);
   tl.e = e;
-  tl.nb = p.raster_n ? u : v;
-  tl.row0 = off[e] + (p.raster_n ? v : u) * PM;
+  tl.nb = at.n;
+  tl.row0 = off[e] + at.m * PM;
   tl.row_end = off[e + 1];
   return true;
 }
@@ -871,27 +863,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// The smaller operand of a group stays in L2 where it fits, in one band; otherwise
-// bands of sixteen pair tiles.
-constexpr long long kL2ResidentBytes = 48ll << 20;
-void set_raster(Params& p, long long a_bytes, long long b_bytes, long long slab_a, long long slab_b) {
-  auto bands = [](long long slab) {
-    const long long g = slab > 0 ? kL2ResidentBytes / slab : 1;
-    return static_cast<int>(g < 1 ? 1 : (g > 4096 ? 4096 : g));
-  };
-  p.raster_n = 0;
-  p.group = 16;
-  if (a_bytes <= kL2ResidentBytes && a_bytes <= b_bytes) {
-    p.group = bands(slab_a);
-  } else if (b_bytes <= kL2ResidentBytes) {
-    p.raster_n = 1;
-    p.group = bands(slab_b);
-  }
-}
-
 template <int FORM>
 long long column_tiles(const Params& p) {
   return (p.N + Shape<FORM>::OUT_COLS - 1) / Shape<FORM>::OUT_COLS;
+}
+// The order of a group's tiles; a_row, b_col: bytes of a row of A and of a column of the weight
+// (of both, where there are two).
+template <int FORM>
+void set_order(Params& p, long long a_row, long long b_col) {
+  const long long cols = Shape<FORM>::OUT_COLS, rows_each = (p.rows + p.E - 1ll) / p.E;
+  p.order = tile_order(rows_each * a_row, p.N * b_col, PM * a_row, cols * b_col,
+                       (p.rows + PM - 1) / PM, column_tiles<FORM>(p));
 }
 template <int FORM>
 long long most_tiles(const Params& p) {
@@ -978,7 +960,6 @@ Params params_of(const BlockRows& r, int K, int N, bool trans, int products = 1)
   p.sb_n = trans ? p.kblocks : 1;
   return p;
 }
-long long rows_each(const BlockRows& r) { return (r.rows + r.E - 1) / r.E; }
 
 bool map_rows(CUtensorMap* m, const void* q, int K, int rows) {
   return make_map_kmajor(m, q, K, rows, 128, true);
@@ -1004,7 +985,7 @@ cudaError_t block_product(const BlockRows& r, const Coded& a, const Coded& b, in
   if (!map_rows(&m.a[0], a.q, K, r.rows) || !map_weight(&m.b[0], b.q, r.E, K, N, trans, 128) ||
       !make_map_box(&m.o[0], C, out_f32 ? 4 : 2, N, r.rows))
     return cudaErrorInvalidValue;
-  set_raster(p, rows_each(r) * K, 1ll * K * N, 1ll * PM * K, 256ll * K);
+  set_order<PLAIN_BF16>(p, K, K);
   if (out_f32)
     return trans ? launch_pairs<PLAIN_F32, false>(p, m, r.num_sms, s)
                  : launch_pairs<PLAIN_F32, true>(p, m, r.num_sms, s);
@@ -1036,7 +1017,7 @@ cudaError_t block_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, c
             !make_map_box(&m.o[1], B, 2, f, r.rows) ||
             !make_map_box(&m.o[2], H, 2, f, r.rows)))
     return cudaErrorInvalidValue;
-  set_raster(p, rows_each(r) * h, 2ll * h * f, 1ll * PM * h, 256ll * h);
+  set_order<GATED>(p, h, 2ll * h);
   return launch_pairs<GATED, true>(p, m, r.num_sms, s);
 }
 
@@ -1059,7 +1040,7 @@ cudaError_t block_fc2_dgrad(const BlockRows& r, const Coded& dy, const Coded& w2
       !make_map_box(&m.o[0], dA, 2, f, r.rows) || !make_map_box(&m.o[1], dB, 2, f, r.rows) ||
       !make_map_box(&m.i[0], A, 2, f, r.rows) || !make_map_box(&m.i[1], B, 2, f, r.rows))
     return cudaErrorInvalidValue;
-  set_raster(p, rows_each(r) * h, 1ll * h * f, 1ll * PM * h, 128ll * h);
+  set_order<GATED_BWD>(p, h, h);
   return launch_pairs<GATED_BWD, false>(p, m, r.num_sms, s);
 }
 
@@ -1080,7 +1061,7 @@ cudaError_t block_fc1_dgrad(const BlockRows& r, const Coded& da, const Coded& db
       !map_weight(&m.b[1], w3.q, r.E, f, h, true, 128) ||
       !make_map_box(&m.o[0], dX, out_f32 ? 4 : 2, h, r.rows))
     return cudaErrorInvalidValue;
-  set_raster(p, rows_each(r) * 2 * f, 2ll * f * h, 1ll * PM * 2 * f, 256ll * 2 * f);
+  set_order<PLAIN_BF16>(p, 2ll * f, 2ll * f);
   return out_f32 ? launch_pairs<PLAIN_F32, false>(p, m, r.num_sms, s)
                  : launch_pairs<PLAIN_BF16, false>(p, m, r.num_sms, s);
 }
