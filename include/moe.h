@@ -392,17 +392,17 @@ moe_status moe_layer_bwd_fp8(const moe_dims* dims, const moe_bf16* x,
 
 /* Rows: as moe_quantize_rows_fp8 (source row idx[p] / div, or p when idx is
  * NULL), with one scale for each block: scale[b * rows + p] is that of
- * q[p, 128 b ...].  n a multiple of 16.  A source index out of range gives
- * codes 0 with scales 1 and MOE_ERR_DEVICE_INDEX in the per-device status
- * word. */
+ * q[p, 128 b ...].  n a multiple of 16, at most 2^31 - 512.  A source index
+ * out of range gives codes 0 with scales 1 and MOE_ERR_DEVICE_INDEX in the
+ * per-device status word. */
 moe_status moe_quantize_rows_fp8_block(const moe_bf16* in, int64_t rows,
                                        int32_t n, const int32_t* idx,
                                        int32_t div, int64_t src_rows,
                                        uint8_t* q, float* scale,
                                        moe_stream_t stream);
 
-/* Weights W [E, K, N] (also a single matrix, E = 1): K and N multiples of
- * 16. */
+/* Weights W [E, K, N] (also a single matrix, E = 1): K and N multiples of 16,
+ * at most 2^31 - 512, and fewer than 2^31 blocks of 128 x 128. */
 moe_status moe_quantize_weights_fp8_block(const moe_bf16* W, int32_t E,
                                           int32_t K, int32_t N, uint8_t* q,
                                           float* scale, moe_stream_t stream);
@@ -490,8 +490,9 @@ moe_status moe_gated_ffn_bwd(const moe_ffn_dims* dims, const moe_bf16* x,
 
 /* moe_layer_fwd and moe_layer_bwd with the experts above.  The forward writes
  * the same `saved` context as moe_layer_fwd; the backward takes one from
- * either of the two.  h and f multiples of 64; dims.sar = 1 and more than
- * 2^31 - 512 assignments T*k are MOE_ERR_UNSUPPORTED.  Workspaces: moe_workspace_bytes with
+ * either of the two.  h and f multiples of 64, at most 2^20; dims.sar = 1
+ * and more than 2^31 - 512 assignments T*k are MOE_ERR_UNSUPPORTED.
+ * Workspaces: moe_workspace_bytes with
  * MOE_OP_LAYER_FWD_FP8_BLOCK and MOE_OP_LAYER_BWD_FP8_BLOCK. */
 moe_status moe_layer_fwd_fp8_block(const moe_dims* dims, const moe_bf16* x,
                                    const float* Wg, const float* b,

@@ -134,7 +134,10 @@ Fp8BwdWeightLayout fp8_bwd_weight_layout(const moe_dims& d) {
 size_t rows_of(const moe_dims& d) { return static_cast<size_t>(d.T) * d.k; }
 
 // What the layer on block-scaled weights takes of the dims that the others do.
-bool block_ok(const moe_dims& d) { return !d.sar && rows_of(d) <= moe::kMostRows; }
+bool block_ok(const moe_dims& d) {
+  return !d.sar && rows_of(d) <= moe::kMostRows && d.h <= moe::kMostWidth &&
+         d.f <= moe::kMostWidth;
+}
 
 struct SavedLayout {
   size_t topk_idx, gates, counts, offsets, perm_src, perm_dst, x_perm, A, B, H, O, total;

@@ -13,6 +13,8 @@ namespace moe {
 
 // The most rows of a call: a row's number, a tile's 256 rows further on, fits 31 bits.
 constexpr int kMostRows = 2147483647 - 511;
+// The longest contraction and the most columns.
+constexpr int kMostWidth = 1 << 20;
 
 // The tiles of a group of rows: bands of `group` row tiles (or, raster_n, column tiles), each
 // swept along the other side, so that the tiles under way share what L2 holds.

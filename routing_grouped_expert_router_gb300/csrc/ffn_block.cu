@@ -14,7 +14,6 @@
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr int32_t kMaxSide = 1 << 20;
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool ptr_ok(const void* p) { return p && aligned(p, 16); }
@@ -43,7 +42,7 @@ moe_status check_gemm(const moe_gemm_dims* d) {
   if (!d || d->rows < 0 || d->K <= 0 || d->N <= 0 || d->E <= 0) return MOE_ERR_INVALID_ARG;
   if ((d->trans_b | 1) != 1 || (d->out_f32 | 1) != 1) return MOE_ERR_INVALID_ARG;
   if (d->rows > moe::kMostRows || d->E > 64 || d->K % 16 != 0 || d->N % 16 != 0 ||
-      d->K > kMaxSide || d->N > kMaxSide || !tiles_fit(d->rows, d->E, d->N))
+      d->K > moe::kMostWidth || d->N > moe::kMostWidth || !tiles_fit(d->rows, d->E, d->N))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -52,7 +51,8 @@ moe_status check_ffn(const moe_ffn_dims* d) {
   if (!d || d->rows < 0 || d->h <= 0 || d->f <= 0 || d->E <= 0 || (d->dw_bf16 | 1) != 1)
     return MOE_ERR_INVALID_ARG;
   if (d->rows > moe::kMostRows || d->E > 64 || d->h % 64 != 0 || d->f % 64 != 0 ||
-      d->h > kMaxSide || d->f > kMaxSide || !tiles_fit(d->rows, d->E, d->h) || !tiles_fit(d->rows, d->E, d->f))
+      d->h > moe::kMostWidth || d->f > moe::kMostWidth || !tiles_fit(d->rows, d->E, d->h) ||
+      !tiles_fit(d->rows, d->E, d->f))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

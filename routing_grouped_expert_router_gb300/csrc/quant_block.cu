@@ -191,6 +191,8 @@ cudaError_t launch_quant_weights_block(const uint16_t* W, int E, int K, int N, u
 // =================================================================== C ABI
 namespace {
 bool ptr_ok(const void* p) { return p && reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// The longest side: with a step of the kernels (four blocks of 128) on top it fits 31 bits.
+constexpr int32_t kMostSide = 2147483647 - 511;
 }  // namespace
 
 extern "C" {
@@ -200,6 +202,7 @@ moe_status moe_quantize_rows_fp8_block(const moe_bf16* in, int64_t rows, int32_t
                                        uint8_t* q, float* scale, moe_stream_t stream) {
   if (rows < 0 || src_rows < 0 || n <= 0 || n % 16 != 0 || (idx && div <= 0))
     return MOE_ERR_INVALID_ARG;
+  if (n > kMostSide) return MOE_ERR_UNSUPPORTED;
   if (rows > 0 && (!ptr_ok(in) || !ptr_ok(q) || !ptr_ok(scale) || (idx && !ptr_ok(idx))))
     return MOE_ERR_INVALID_ARG;
   if (rows > 0 && !idx && src_rows < rows) return MOE_ERR_INVALID_ARG;
@@ -217,7 +220,8 @@ moe_status moe_quantize_rows_fp8_block(const moe_bf16* in, int64_t rows, int32_t
 moe_status moe_quantize_weights_fp8_block(const moe_bf16* W, int32_t E, int32_t K, int32_t N,
                                           uint8_t* q, float* scale, moe_stream_t stream) {
   if (E <= 0 || K <= 0 || N <= 0 || K % 16 != 0 || N % 16 != 0) return MOE_ERR_INVALID_ARG;
-  if (static_cast<double>(E) * moe::blocks_of(K) * moe::blocks_of(N) > 2147483647.0)
+  if (K > kMostSide || N > kMostSide ||
+      static_cast<double>(E) * moe::blocks_of(K) * moe::blocks_of(N) > 2147483647.0)
     return MOE_ERR_UNSUPPORTED;
   if (!ptr_ok(W) || !ptr_ok(q) || !ptr_ok(scale)) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -110,3 +110,20 @@ def test_calls_of_more_rows_are_refused():
         assert L.moe_gated_ffn_bwd(f, *[at] * 17, room, None) == mb.MOE_ERR_UNSUPPORTED
         assert L.moe_layer_fwd_fp8_block(d, *[at] * 12, room, None) == mb.MOE_ERR_UNSUPPORTED
         assert L.moe_layer_bwd_fp8_block(d, *[at] * 16, room, None) == mb.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake device addresses: host-only check")
+def test_sides_whose_blocks_leave_31_bits_are_refused():
+    """The quantisers' sides, and the layer's as the feed-forward block's."""
+    mbuild.build()
+    L, at, uns = mb.load(), 1 << 20, mb.MOE_ERR_UNSUPPORTED
+    for far in (2 ** 31 - 16, 2 ** 31 - 128, 2 ** 31 - 496):
+        assert L.moe_quantize_rows_fp8_block(at, 1, far, None, 1, 1, at, at, None) == uns
+        assert L.moe_quantize_weights_fp8_block(at, 1, far, 16, at, at, None) == uns
+        assert L.moe_quantize_weights_fp8_block(at, 1, 16, far, at, at, None) == uns
+    for kw in (dict(h=2 ** 20 + 64), dict(f=2 ** 20 + 64), dict(h=2 ** 31 - 64)):
+        d = mb.dims(**{**dict(T=1, h=64, f=64, E=2, k=1), **kw})
+        assert L.moe_layer_fwd_fp8_block(ctypes.byref(d), *[at] * 12, 1 << 60, None) == uns
+        assert L.moe_layer_bwd_fp8_block(ctypes.byref(d), *[at] * 16, 1 << 60, None) == uns
+        assert mb.moe_workspace_bytes(d, mb.OP_LAYER_FWD_FP8_BLOCK) == mb.moe_workspace_bytes(d, mb.OP_LAYER_BWD_FP8_BLOCK) == 0
+    assert mb.moe_workspace_bytes(mb.dims(1, 2 ** 20, 2 ** 20, 2, 1), mb.OP_LAYER_FWD_FP8_BLOCK) > 0
