@@ -428,8 +428,8 @@ size_t moe_gemm_workspace_bytes(const moe_gemm_dims* dims);
  * the status word of ws.
  * The same inputs give the same bits.  Calls that may run at the same time need
  * a workspace each; the first 256 bytes of ws have to be zero before its first
- * use (every call leaves them so, but for the status word; after
- * MOE_ERR_DEVICE_TIMEOUT call moe_clear_device_status). */
+ * use (every call leaves them so, but for the status word; after a wait that
+ * ran out the call that reads MOE_ERR_DEVICE_TIMEOUT does). */
 moe_status moe_gemm_fp8_block(const moe_gemm_dims* dims, const uint8_t* aq,
                               const float* sa, const uint8_t* bq,
                               const float* sb, const int32_t* offsets, void* C,
@@ -647,7 +647,8 @@ void* moe_saved_view(const moe_dims* dims, void* saved, const char* name);
 const char* moe_status_string(moe_status status);
 
 /* Synchronises `stream`, returns the status word at the start of `ws` and
- * clears it.  ws = NULL: the status word of the calls that take no workspace
+ * clears it; with MOE_ERR_DEVICE_TIMEOUT it zeroes the whole 256 bytes, where
+ * kernels that gave up leave what they had counted.  ws = NULL: the status word of the calls that take no workspace
  * (moe_combine, moe_unpermute, moe_quantize_rows_fp8, moe_permute_noalloc,
  * moe_quantize_rows_fp8_block, moe_block_norm_fwd) on the current device.
  * MOE_ERR_CUDA if the synchronisation itself failed. */

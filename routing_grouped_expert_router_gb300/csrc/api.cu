@@ -527,7 +527,13 @@ moe_status moe_read_device_status(void* ws, moe_stream_t stream) {
   int v = 0;
   MOE_CU(cudaStreamSynchronize(s));
   MOE_CU(cudaMemcpy(&v, word, sizeof(int), cudaMemcpyDeviceToHost));
-  MOE_CU(cudaMemset(word, 0, sizeof(int)));
+  if (v != 0) {
+    // blocks that gave up leave counts of their tiles and barriers in a workspace's header too.
+    // On the caller's stream, and done before the call returns: a next call's counts are safe.
+    const size_t n = ws && v == MOE_ERR_DEVICE_TIMEOUT ? kAlign : sizeof(int);
+    MOE_CU(cudaMemsetAsync(word, 0, n, s));
+    MOE_CU(cudaStreamSynchronize(s));
+  }
   return static_cast<moe_status>(v);
 }
 

@@ -50,3 +50,24 @@ def test_feed_forward_with_offsets_out_of_order(lib, R, cuts):  # noqa: F811
     assert mb.moe_read_device_status(ws) == mb.MOE_ERR_DEVICE_INDEX
     _check_bwd(x, dy, A, B, H, w, counts, dx, dW, n)
     assert (dx[n:] == 55).all()
+
+
+# ---------------------------------------------------------------- after a wait that ran out
+@pytest.mark.parametrize("counts,K,N", [([3], 4096, 512), ([2, 0, 5], 4096, 1408), ([70], 4096, 512)])
+def test_a_status_of_a_timeout_read_leaves_the_workspace_as_new(lib, counts, K, N):  # noqa: F811
+    """What blocks that gave up leave in the header: the status, and pieces counted of tiles that nobody joined."""
+    R, E = sum(counts), len(counts)
+    x = _normal((R, K), 51)
+    aq, sa = _quantize_rows(x)
+    bq, sb, w = br.weights(E, K, N, seed=52)
+    gd, o = mb.gemm_dims(R, K, N, E, out_f32=True), _offsets(counts)
+    ws = _ws(mb.moe_gemm_workspace_bytes(gd))
+    want, C = (torch.full((R, N), 77.0, dtype=F32, device="cuda") for _ in range(2))
+    mb.moe_gemm_fp8_block(gd, aq, sa, bq, sb, o, want, ws)
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK and (want != 77).all()
+    ws[64:224] = 100
+    ws[:4] = torch.tensor([mb.MOE_ERR_DEVICE_TIMEOUT, 0, 0, 0], dtype=torch.uint8)
+    assert mb.moe_read_device_status(ws) == mb.MOE_ERR_DEVICE_TIMEOUT
+    mb.moe_gemm_fp8_block(gd, aq, sa, bq, sb, o, C, ws)
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK
+    assert torch.equal(C, want)
