@@ -912,7 +912,7 @@ cudaError_t launch_with(const Params& p, const Maps& m, int num_sms, bool early,
 // 20.4 17.7, its feed-forward block 44.9 41.6; with 64 blocks in turn 70.7 73.8.  In a graph an
 // early launch gains nothing.
 template <int FORM, bool B_MN>
-cudaError_t launch_pairs(const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
+cudaError_t launch_pairs(Params& p, const Maps& m, int num_sms, cudaStream_t s) {
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   const cudaError_t e = cudaStreamIsCapturing(s, &capture);
   if (e != cudaSuccess) return e;
@@ -922,6 +922,9 @@ cudaError_t launch_pairs(const Params& p, const Maps& m, int num_sms, cudaStream
   // the fewest tiles that these rows can make; the kernel counts those there are
   const long long least = column_tiles<FORM>(p) * ((p.rows + PM - 1) / PM);
   const bool shared = p.most_pieces > 1 && 2 * least <= pairs;
+  // a launch that is small for its early start alone shares no tile, however few there are:
+  // in a graph it would not, and the same inputs give the same bits
+  if (!shared) p.most_pieces = 1;
   return shared || (stream && turns * p.kblocks * p.products <= 32)
              ? launch_with<FORM, B_MN, true>(p, m, num_sms, stream, s)
              : launch_with<FORM, B_MN, false>(p, m, num_sms, false, s);

@@ -71,3 +71,25 @@ def test_a_status_of_a_timeout_read_leaves_the_workspace_as_new(lib, counts, K, 
     mb.moe_gemm_fp8_block(gd, aq, sa, bq, sb, o, C, ws)
     assert mb.moe_read_device_status(ws) == mb.MOE_OK
     assert torch.equal(C, want)
+
+
+# ---------------------------------------------------------------- streams and graphs
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("R,n", [(8192, 100), (8192, 300), (9000, 256), (4096, 4000), (300, 40)])
+def test_a_graph_gives_the_bits_of_a_stream(lib, R, n, f32):  # noqa: F811
+    """Also where the rows that there are would make fewer tiles than the rows that there could be."""
+    K, N = 4096, 512
+    aq, sa = _quantize_rows(_normal((R, K), 61))
+    bq, sb, _ = br.weights(1, K, N, seed=62)
+    gd, o = mb.gemm_dims(R, K, N, 1, out_f32=f32), _offsets([n])
+    ws = _ws(mb.moe_gemm_workspace_bytes(gd))
+    C = torch.full((R, N), 77.0, dtype=F32 if f32 else BF, device="cuda")
+    mb.moe_gemm_fp8_block(gd, aq, sa, bq, sb, o, C, ws)
+    torch.cuda.synchronize()
+    want = C.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mb.moe_gemm_fp8_block(gd, aq, sa, bq, sb, o, C, ws)
+    C.fill_(77)
+    graph.replay()
+    assert torch.equal(C, want) and (C[n:] == 77).all()
