@@ -293,14 +293,14 @@ moe_status ws_check(const moe_dims& d, int op, const void* ws, size_t ws_bytes) 
   return MOE_OK;
 }
 
-#define MOE_CU(expr)                                   \
-  do {                                                 \
-    if ((expr) != cudaSuccess) return MOE_ERR_CUDA;    \
+#define MOE_CU(expr)                                         \
+  do {                                                       \
+    if ((expr) != cudaSuccess) return moe_api::cuda_error(); \
   } while (0)
-#define MOE_RUN(expr, name)                            \
-  do {                                                 \
-    if ((expr) != cudaSuccess) return MOE_ERR_CUDA;    \
-    if (!note(stream, name)) return MOE_ERR_CUDA;      \
+#define MOE_RUN(expr, name)                                  \
+  do {                                                       \
+    if ((expr) != cudaSuccess) return moe_api::cuda_error(); \
+    if (!note(stream, name)) return moe_api::cuda_error();   \
   } while (0)
 
 GemmProblem problem(const moe_dims& d, const int32_t* offsets, void* ws) {
@@ -522,7 +522,7 @@ const char* moe_profile_kernel_name(int i) {
 moe_status moe_read_device_status(void* ws, moe_stream_t stream) {
   if (ws && !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
   int* word = ws ? static_cast<int*>(ws) : moe::nows_status_word();
-  if (!word) return MOE_ERR_CUDA;
+  if (!word) return moe_api::cuda_error();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int v = 0;
   MOE_CU(cudaStreamSynchronize(s));
@@ -548,7 +548,7 @@ moe_status moe_selftest_wait_timeout(void* ws, uint32_t limit_us, moe_stream_t s
 moe_status moe_clear_device_status(void* ws, moe_stream_t stream) {
   if (ws && !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
   int* word = ws ? static_cast<int*>(ws) : moe::nows_status_word();
-  if (!word) return MOE_ERR_CUDA;
+  if (!word) return moe_api::cuda_error();
   // a workspace's whole header: the few-token layer keeps its barrier words there
   MOE_CU(cudaMemsetAsync(word, 0, ws ? kAlign : sizeof(int),
                          reinterpret_cast<cudaStream_t>(stream)));
@@ -632,7 +632,7 @@ moe_status moe_unpermute(const moe_dims* dims, const int32_t* perm_dst, const mo
     return MOE_ERR_INVALID_ARG;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   int* status = moe::nows_status_word();
-  if (!status) return MOE_ERR_CUDA;
+  if (!status) return moe_api::cuda_error();
   MOE_RUN(moe::launch_gather_rows(rows_perm, perm_dst, 1, static_cast<long long>(rows_of(d)),
                                   static_cast<long long>(rows_of(d)), d.h, rows_assign, num_sms(),
                                   stream, nullptr, nullptr, nullptr, status),
@@ -674,7 +674,7 @@ moe_status moe_combine(const moe_dims* dims, const moe_bf16* O, const float* gat
     return MOE_ERR_INVALID_ARG;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   int* status = moe::nows_status_word();
-  if (!status) return MOE_ERR_CUDA;
+  if (!status) return moe_api::cuda_error();
   MOE_RUN(moe::launch_combine(O, gates, perm_dst, d.T, d.k, d.h, y, num_sms(), stream, status),
           "combine");
   return MOE_OK;
@@ -825,7 +825,7 @@ moe_status moe_quantize_rows_fp8(const moe_bf16* in, int64_t rows, int32_t n, co
   if (rows > 0 && !idx && src_rows < rows) return MOE_ERR_INVALID_ARG;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   int* status = moe::nows_status_word();
-  if (!status) return MOE_ERR_CUDA;
+  if (!status) return moe_api::cuda_error();
   MOE_RUN(moe::launch_quant_rows(in, idx, idx ? div : 1, rows, src_rows, n, q, scale, num_sms(),
                                  stream, nullptr, nullptr, 0, nullptr, nullptr, nullptr, status),
           "quant_rows");

@@ -20,4 +20,11 @@ int num_sms();
 // named `name` when the hook is armed.  False if recording failed.
 bool note(cudaStream_t s, const char* name);
 
+// MOE_ERR_CUDA for the call that met the error, which is taken from the runtime: left there it
+// would be reported again after the next call's first launch.
+inline moe_status cuda_error() {
+  cudaGetLastError();
+  return MOE_ERR_CUDA;
+}
+
 }  // namespace moe_api

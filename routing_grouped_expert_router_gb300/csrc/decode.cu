@@ -1463,7 +1463,7 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
         !make_map_codes(&m.w1, view("W13q"), h, 2 * f, E, 256) ||
         !make_map_kmajor(&m.h, p.Hq, f, R, 16, true) ||
         !make_map_codes(&m.w2, view("W2q"), f, h, E, 256))
-      return MOE_ERR_CUDA;
+      return moe_api::cuda_error();
     m.w3 = m.w1;
     e = quotient ? launch<true, true>(p, m, plan.smem, blocks, stream)
                  : launch<true, false>(p, m, plan.smem, blocks, stream);
@@ -1471,10 +1471,10 @@ moe_status decode(const moe_dims* dims, const moe_bf16* x, const float* Wg, cons
     if (!make_map_kmajor(&m.x, x, h, d.T, plan.n1, false) || !make_map_columns(&m.w1, W1, f, E * h, 2) ||
         !make_map_columns(&m.w3, W3, f, E * h, 2) || !make_map_kmajor(&m.h, p.H, f, 2 * R, 16, false) ||
         !make_map_columns(&m.w2, W2, h, E * f, 4))
-      return MOE_ERR_CUDA;
+      return moe_api::cuda_error();
     e = launch<false, false>(p, m, plan.smem, blocks, stream);
   }
-  if (e != cudaSuccess || !moe_api::note(stream, "layer_decode")) return MOE_ERR_CUDA;
+  if (e != cudaSuccess || !moe_api::note(stream, "layer_decode")) return moe_api::cuda_error();
   return MOE_OK;
 }
 

@@ -90,10 +90,10 @@ FfnLayout ffn_layout(const moe_ffn_dims& d, bool backward) {
   return L;
 }
 
-#define BLOCK_RUN(expr, name)                                  \
-  do {                                                         \
-    if ((expr) != cudaSuccess) return MOE_ERR_CUDA;            \
-    if (!moe_api::note(stream, name)) return MOE_ERR_CUDA;     \
+#define BLOCK_RUN(expr, name)                                       \
+  do {                                                              \
+    if ((expr) != cudaSuccess) return moe_api::cuda_error();        \
+    if (!moe_api::note(stream, name)) return moe_api::cuda_error(); \
   } while (0)
 
 }  // namespace

@@ -43,13 +43,13 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 // Device address of the scratch array on the current device.
 moe_status scratch_address(void** out) {
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return moe_api::cuda_error();
   if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lock(g_scratch_mu);
   if (!g_scratch_addr[dev]) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || p == nullptr)
-      return MOE_ERR_CUDA;
+      return moe_api::cuda_error();
     g_scratch_addr[dev] = p;
   }
   *out = g_scratch_addr[dev];
@@ -90,7 +90,7 @@ extern "C" moe_status moe_permute_noalloc(const moe_dims* dims, const int32_t* t
   if (st != MOE_OK) return st;
   // index errors go to the per-device status word of the calls without a workspace
   int* status = moe::nows_status_word();
-  if (!status) return MOE_ERR_CUDA;
+  if (!status) return moe_api::cuda_error();
   int32_t* blk_counts = static_cast<int32_t*>(scratch);
   int32_t* bases = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(scratch) + part);
 
@@ -103,11 +103,11 @@ extern "C" moe_status moe_permute_noalloc(const moe_dims* dims, const int32_t* t
       !ran(moe::launch_dispatch_scatter(topk_idx, R, d.E, sel, bases, offsets, perm_src, perm_dst,
                                         s, status),
            s, "dispatch_scatter"))
-    return MOE_ERR_CUDA;
+    return moe_api::cuda_error();
   if (x && x_perm &&
       !ran(moe::launch_gather_rows(x, perm_src, d.k, R, d.T, d.h, x_perm, moe_api::num_sms(), s,
                                    offsets + d.E, nullptr, nullptr, status),
            s, "permute_rows"))
-    return MOE_ERR_CUDA;
+    return moe_api::cuda_error();
   return MOE_OK;
 }

@@ -847,10 +847,10 @@ moe_status moe_block_norm_fwd(const moe_norm_dims* dims, const void* r, const mo
   a.out_r = r_out;
   a.out_u = reinterpret_cast<uint4*>(u);
   a.status = moe::nows_status_word();
-  if (!a.status) return MOE_ERR_CUDA;
+  if (!a.status) return moe_api::cuda_error();
   const Plan p = plan_of(d, false);
   const cudaError_t e = launch(d.res_f32 ? fwd_kernel<true>(p) : fwd_kernel<false>(p), a, p, s);
-  return e == cudaSuccess && moe_api::note(s, "block_norm_fwd") ? MOE_OK : MOE_ERR_CUDA;
+  return e == cudaSuccess && moe_api::note(s, "block_norm_fwd") ? MOE_OK : moe_api::cuda_error();
 }
 
 moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, const moe_bf16* y,
@@ -867,7 +867,7 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
     for (float* p : sums) {
       if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
       if (p && cudaMemsetAsync(p, 0, static_cast<size_t>(d.h) * sizeof(float), s) != cudaSuccess)
-        return MOE_ERR_CUDA;
+        return moe_api::cuda_error();
     }
     return MOE_OK;
   }
@@ -892,7 +892,7 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
   const bool all = y && w_post && w_pre && dr_out;
   const cudaError_t e =
       launch(d.res_f32 ? bwd_kernel<true>(p, all) : bwd_kernel<false>(p, all), a, p, s);
-  if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return MOE_ERR_CUDA;
+  if (e != cudaSuccess || !moe_api::note(s, "block_norm_bwd")) return moe_api::cuda_error();
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
   if (dw_pre || dw_post || channel) {
     const int cols = d.h > 16 * moe_api::num_sms() ? 16 : 8;
@@ -901,7 +901,7 @@ moe_status moe_block_norm_bwd(const moe_norm_dims* dims, const void* r_out, cons
                      channel ? gate : nullptr, d.beta, dw_pre, dw_post,
                      channel ? dgate : nullptr) != cudaSuccess ||
         !moe_api::note(s, "block_norm_cols"))
-      return MOE_ERR_CUDA;
+      return moe_api::cuda_error();
   }
   return MOE_OK;
 }

@@ -208,12 +208,12 @@ moe_status moe_quantize_rows_fp8_block(const moe_bf16* in, int64_t rows, int32_t
   if (rows > 0 && !idx && src_rows < rows) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   int* status = moe::nows_status_word();
-  if (!status) return MOE_ERR_CUDA;
+  if (!status) return moe_api::cuda_error();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (moe::launch_quant_rows_block(in, idx, div, rows, src_rows, n, q, scale, moe_api::num_sms(),
                                    s, nullptr, 0, nullptr, status) != cudaSuccess ||
       !moe_api::note(s, "quant_rows_block"))
-    return MOE_ERR_CUDA;
+    return moe_api::cuda_error();
   return MOE_OK;
 }
 
@@ -227,7 +227,7 @@ moe_status moe_quantize_weights_fp8_block(const moe_bf16* W, int32_t E, int32_t 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (moe::launch_quant_weights_block(W, E, K, N, q, scale, s) != cudaSuccess ||
       !moe_api::note(s, "quant_weights_block"))
-    return MOE_ERR_CUDA;
+    return moe_api::cuda_error();
   return MOE_OK;
 }
 

@@ -2,6 +2,8 @@
 it meet: offsets out of order, launches that fail, waits that ran out, streams
 and graphs, and each way in which few rows are cut into pieces.  References and
 tolerances are those of test_gpu_block_fp8.py."""
+import ctypes
+
 import pytest
 import torch
 
@@ -93,3 +95,46 @@ def test_a_graph_gives_the_bits_of_a_stream(lib, R, n, f32):  # noqa: F811
     C.fill_(77)
     graph.replay()
     assert torch.equal(C, want) and (C[n:] == 77).all()
+
+
+# ---------------------------------------------------------------- launches that fail
+@pytest.mark.parametrize("call", ["rows", "weights", "few", "many", "forward"])
+def test_an_error_of_one_call_is_not_the_next_ones(lib, call):  # noqa: F811
+    """A launch that the runtime refuses (the legacy stream beside a capture of a stream that waits for it) is that call's error;
+    the next call has none."""
+    E, h, f, R = 2, 256, 384, 300 if call == "many" else 5
+    w = _ffn_weights(E, h, f, 71)
+    codes = [t for q, s, _ in w for t in (q, s)]
+    x, o, W = _normal((R, h), 72), _offsets([R - 2, 2]), _normal((E, h, f), 73)
+    aq, sa = _quantize_rows(x)
+    fd, gd = mb.ffn_dims(R, h, f, E), mb.gemm_dims(R, h, f, E)
+    ws = _ws(max(mb.moe_ffn_workspace_bytes(fd, 0), mb.moe_gemm_workspace_bytes(gd)))
+    q, s = torch.empty_like(aq), torch.empty_like(sa)
+    wq, wsc = torch.empty(W.shape, dtype=torch.uint8, device="cuda"), torch.empty((E, 2, 3), dtype=F32, device="cuda")
+    C, y = torch.empty((R, f), dtype=BF, device="cuda"), torch.empty_like(x)
+
+    def run():
+        if call == "rows":
+            mb.moe_quantize_rows_fp8_block(x, R, h, None, 1, R, q, s, stream=0)
+        elif call == "weights":
+            mb.moe_quantize_weights_fp8_block(W, E, h, f, wq, wsc, stream=0)
+        elif call == "forward":
+            mb.moe_gated_ffn_fwd(fd, x, o, *codes, None, None, None, y, ws, stream=0)
+        else:
+            mb.moe_gemm_fp8_block(gd, aq, sa, codes[0], codes[1], o, C, ws, stream=0)
+
+    run()
+    torch.cuda.synchronize()
+    cu = ctypes.CDLL("libcuda.so.1")
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert cu.cuStreamCreate(ctypes.byref(stream), 0) == 0
+    try:
+        assert cu.cuStreamBeginCapture_v2(stream, 2) == 0
+        with pytest.raises(mb.MoeError) as e:
+            run()
+        cu.cuStreamEndCapture(stream, ctypes.byref(graph))
+        assert e.value.status == mb.MOE_ERR_CUDA
+        run()
+        torch.cuda.synchronize()
+    finally:
+        cu.cuStreamDestroy_v2(stream)
