@@ -2,7 +2,7 @@
 // group, as a serving step has them: bound by reading each weight once.
 //
 //   * The product is taken transposed: 128 columns of the weight are the tensor
-//     cores' rows (from the weight's own layout, MN-major or K-major), 16 to 64 rows
+//     cores' rows (from the weight's own layout, MN-major or K-major), 16 or 32 rows
 //     of activations their columns, so that a block of 128 x 128 codes costs one
 //     block's MMAs whatever the number of rows.  A step has two such blocks: side by
 //     side in one weight (256 bytes in a row of it: with 128 HBM moved 10% less), or the
@@ -76,8 +76,8 @@ struct Shape {
   static constexpr int PITCH = (FORM == PLAIN_F32 ? 512 : 256) + 16;  // staging: bytes of a row
   static constexpr int FIT = (232448 - 1024 - NT * PITCH - 3 * 1024) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 12 ? 12 : FIT;
-  static constexpr int BUFS = 4 * UNIT > 256 ? 2 : 4;  // steps whose sums wait in tensor memory
-  static constexpr int TMEM = BUFS * UNIT;           // columns (a power of two, 64 to 256)
+  static constexpr int BUFS = 4;                     // steps whose sums wait in tensor memory
+  static constexpr int TMEM = BUFS * UNIT;           // columns (a power of two, 128 or 256)
   static_assert(X_BYTES % 1024 == 0 && TMEM <= 256 && TMEM >= 32 && STAGES >= 2, "does not fit");
 };
 template <int NT>
@@ -98,7 +98,7 @@ struct alignas(16) Ctrl {
   int cum[kMaxGroups + 1];       // row tiles before each group
   Slot<NT> slots[SLOTS];
 };
-static_assert(2 * 2 * 64 * 128 <= 128 * 256, "a block's two slots fit its part");
+static_assert(2 * 2 * 32 * 128 <= 128 * 256, "a block's two slots fit its part");
 template <int FORM, int NT>
 constexpr int smem_bytes() {
   using S = Shape<FORM, NT>;
@@ -211,13 +211,7 @@ __device__ __forceinline__ void tmem_columns(uint32_t taddr, float (&v)[NT]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
   } else {
-#pragma unroll
-    for (int i = 0; i < NT; i += 32) {
-      float t[32];
-      tmem_ld32(taddr + i, t);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[i + j] = t[j];
-    }
+    tmem_ld32(taddr, v);
   }
 }
 
@@ -587,11 +581,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// Activations to a tile: the least that holds twice a group's mean (one group: all rows).
-int tile_rows(int rows, int E) {
-  const long long want = E == 1 ? rows : 2ll * ((rows + E - 1) / E);
-  return want <= 16 ? 16 : want <= 32 ? 32 : 64;
-}
+// Activations to a tile: 16 where they hold twice a group's mean (one group: all rows), or 32,
+// which do for all that few_rows lets through.
+int tile_rows(int rows, int E) { return (E == 1 ? rows : 2 * ((rows + E - 1) / E)) <= 16 ? 16 : 32; }
 
 template <int FORM, int NT, bool TRANS>
 cudaError_t launch(const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
@@ -615,9 +607,8 @@ cudaError_t launch(const Params& p, const Maps& m, int num_sms, cudaStream_t s) 
 }
 template <int FORM, bool TRANS>
 cudaError_t launch(int nt, const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
-  return nt == 16   ? launch<FORM, 16, TRANS>(p, m, num_sms, s)
-         : nt == 32 ? launch<FORM, 32, TRANS>(p, m, num_sms, s)
-                    : launch<FORM, 64, TRANS>(p, m, num_sms, s);
+  return nt == 16 ? launch<FORM, 16, TRANS>(p, m, num_sms, s)
+                  : launch<FORM, 32, TRANS>(p, m, num_sms, s);
 }
 
 bool fill(Params& p, Maps& m, const BlockRows& r, const Coded& x, int K, int N, bool trans, int nt,
