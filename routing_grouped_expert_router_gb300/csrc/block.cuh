@@ -13,9 +13,6 @@
 
 namespace moe {
 
-constexpr int kBlock = 128;
-inline int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
-
 // Rows of `in` (row idx[p] / div, or p) -> codes [rows, n] and block scales
 // [ceil(n/128), rows], for p < rows (and, where given, p < the largest of
 // ends[0 .. n_ends-1]: the groups' offsets, or their last alone where they are known
@@ -40,39 +37,6 @@ struct BlockRows {
   int num_sms;
   float* part;    // part_bytes(rows) bytes for the sums of tiles that several blocks share
 };
-// Whether a group's rows are so few that gemm_block_few.cu's kernel is the faster one where
-// another of these launches comes before it (whose end its first weights need not wait for).
-// The feed-forward block in a graph, us, that kernel against the pairs':
-//   rows to a group           1          8          16         24         32
-//   4096, 14336, 1 group      41 : 79    43 : 74    45 : 71    53 : 72    55 : 71
-//   4096, 4096, 1 group       23 : 43    25 : 40    27 : 39    35 : 40    37 : 41
-//   2048, 1408, 1 group       16 : 26    17 : 26    18 : 26    23 : 26    24 : 26
-//   2048, 1408, 8 groups      24 : 42    25 : 41    28 : 42    39 : 42    40 : 42
-//   4096, 2048, 4 groups      30 : 50    30 : 49    37 : 49    59 : 49    60 : 49
-//   4096, 14336, 8 groups     283 : 382  289 : 319  294 : 320  316 : 323  318 : 324
-//   2048, 1408, 64 groups     122 : 172  126 : 160  137 : 161  165 : 164  172 : 165
-// The steps of such a launch are counted in 32 bits.
-inline bool few_rows(int rows, int E, int K, int N) {
-  return rows <= (E == 1 ? 32 : 16ll * E) && (rows / 16 + E) * (N / 128 + 1ll) * blocks_of(K) < 2147483647ll;
-}
-// The same for a product by itself, whose weights may be what the launch before writes: the
-// rows have to fit its smallest tile (16, twice a group's mean), or the weights' stream to be
-// long beside the join.  Products in a graph, us, as above:
-//   rows to a group           1          4          8          16         32
-//   4096 x 14336, 1 group     16 : 26    16 : 20    16 : 19    17 : 20    19 : 20
-//   4096 x 4096, 1 group      10 : 17    10 : 16    12 : 15    13 : 15    19 : 15
-//   8192 x 2048, 1 group      13 : 18    12 : 18    15 : 18    18 : 18    28 : 18
-//   14336 x 4096, 1 group     17 : 29    17 : 27    18 : 24    20 : 24    26 : 24
-//   2048 x 1408, 8 groups     12 : 13    12 : 12    12 : 12    14 : 13    19 : 13
-//   4096 x 1024, 8 groups     13 : 18    13 : 18    14 : 18    16 : 18    22 : 18
-//   512 x 2048, 64 groups     23 : 23    23 : 23    24 : 24    27 : 24    33 : 26
-//   2048 x 640, 64 groups     24 : 29    25 : 29    25 : 29    27 : 30    36 : 30
-//   2048 x 1408, 64 groups    40 : 50    41 : 50    43 : 52    46 : 53    55 : 52
-//   4096 x 14336, 8 groups    78 : 120   79 : 92    81 : 93    83 : 95    89 : 97
-inline bool few_rows_alone(int rows, int E, int K, int N) {
-  return few_rows(rows, E, K, N) &&
-         (rows <= (E == 1 ? 16 : 8ll * E) || 1ll * E * K * N > 64ll << 20);
-}
 constexpr int kPartBlocks = 160;  // blocks of a grid that have room for a shared tile's sums
 inline size_t part_bytes(int rows) {  // 128 x 256 sums for each: the most of either kernel
   return rows ? static_cast<size_t>(kPartBlocks) * 128 * 256 * 4 : 0;

@@ -134,53 +134,6 @@ __device__ __forceinline__ Tile place(const Params& p, const int* off, const int
   return tl;
 }
 
-// How all steps, nkb to a tile, are cut into contiguous pieces, one for each block.  Where every
-// tile can have the same number of pieces (per > 0) and enough blocks get one, no block has parts
-// of two tiles, and its first load comes sooner; otherwise all steps are cut into equal pieces.
-// The first `longer` pieces (of each tile, or of all) have a step more than the others' `each`.
-// Enough: three quarters of the blocks stream as fast as all; with fewer, 5 ns a step in the
-// ratio stay below the 3 us that parts of two tiles cost.  In a graph, us, alike and not: one row
-// by 4096 and 14336 (112 tiles of 152) 41 46, 8 experts of 2048 and 1408 (88) 24.6 28.4.
-// In 32 bits (see few_rows).
-constexpr int MIN_STEPS = 4;  // pieces of fewer cost more to join than they save
-struct Share {
-  int nkb, per, each, longer;
-  int t, kb, count;  // this block's first tile and step, its steps
-  __device__ __forceinline__ int lo(int c) const { return each * c + min(c, longer); }
-  __device__ __forceinline__ int owner(int s) const {
-    const int edge = (each + 1) * longer;
-    return s < edge ? s / (each + 1) : longer + (s - edge) / each;
-  }
-};
-__device__ __forceinline__ Share share_of(int tiles, int nkb) {
-  const int grid = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
-  const int steps = tiles * nkb;
-  Share share = {nkb, 0, 0, 0, 0, 0, 0};
-  if (steps == 0) return share;
-  if (tiles <= grid) {
-    const int per = max(1, min(grid / tiles, nkb / MIN_STEPS)), used = tiles * per;
-    if ((per + 1) * MIN_STEPS > nkb ||
-        static_cast<long long>(steps) * (3 * grid - 4 * used) <= 2400ll * used) {
-      share.per = per;
-      share.each = nkb / per;
-      share.longer = nkb - share.each * per;
-      share.t = me / per;
-      const int piece = me - share.t * per;
-      share.kb = share.lo(piece);
-      share.count = share.t < tiles ? share.each + (piece < share.longer) : 0;
-      return share;
-    }
-  }
-  const int blocks = max(1, min(steps / MIN_STEPS, grid));
-  share.each = steps / blocks;
-  share.longer = steps - share.each * blocks;
-  const int lo = min(share.lo(me), steps);  // blocks past the pieces: none
-  share.count = min(share.lo(me + 1), steps) - lo;
-  share.t = lo / nkb;
-  share.kb = lo - share.t * nkb;
-  return share;
-}
-
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* status) {
   bool ok = mbar_try_wait(smem_u32(bar), parity);
   if (__all_sync(0xffffffffu, ok)) return true;
@@ -256,7 +209,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // the kernel before ends (should it write them, L2 has what it wrote).
     if (warp == LOAD_W && p.E == 1) {
       const int row_tiles = (p.rows + NT - 1) / NT;
-      const Share guess = share_of((p.N + S::COLS - 1) / S::COLS * row_tiles, p.nkb);
+      const Share guess = share_of((p.N + S::COLS - 1) / S::COLS * row_tiles, p.nkb, gridDim.x, blockIdx.x);
       const int from = guess.t * p.nkb + guess.kb, to = from + min(guess.count, kEarlySteps);
       if (elect_one())
         for (int i = from; i < to; ++i) {
@@ -279,7 +232,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = c.tmem_base;
   const int nkb = p.nkb;
-  const Share share = share_of((p.N + S::COLS - 1) / S::COLS * c.cum[p.E], nkb);
+  const Share share = share_of((p.N + S::COLS - 1) / S::COLS * c.cum[p.E], nkb, gridDim.x, blockIdx.x);
   const int me = static_cast<int>(blockIdx.x);
   const int count = share.count;
   int t = share.t, kb = share.kb;
@@ -581,10 +534,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// Activations to a tile: 16 where they hold twice a group's mean (one group: all rows), or 32,
-// which do for all that few_rows lets through.
-int tile_rows(int rows, int E) { return (E == 1 ? rows : 2 * ((rows + E - 1) / E)) <= 16 ? 16 : 32; }
-
 template <int FORM, int NT, bool TRANS>
 cudaError_t launch(const Params& p, const Maps& m, int num_sms, cudaStream_t s) {
   auto kern = block_few_kernel<FORM, NT, TRANS>;
@@ -640,7 +589,7 @@ cudaError_t few_product(const BlockRows& r, const Coded& a, const Coded& b, int 
                         bool out_f32, void* C, cudaStream_t s, bool ahead) {
   Params p;
   Maps m;
-  const int nt = tile_rows(r.rows, r.E);
+  const int nt = few_tile_rows(r.rows, r.E);
   if (!fill(p, m, r, a, K, N, trans, nt, ahead) || !map_weight(&m.w[0], b.q, r.E, K, N, trans))
     return cudaErrorInvalidValue;
   p.sb[0] = b.s;
@@ -657,7 +606,7 @@ cudaError_t few_fc1_fwd(const BlockRows& r, const Coded& x, const Coded& w1, con
                         uint8_t* Hq, float* sh, cudaStream_t s) {
   Params p;
   Maps m;
-  const int nt = tile_rows(r.rows, r.E);
+  const int nt = few_tile_rows(r.rows, r.E);
   if (!fill(p, m, r, x, h, f, false, nt, true) || !map_weight(&m.w[0], w1.q, r.E, h, f, false) ||
       !map_weight(&m.w[1], w3.q, r.E, h, f, false))
     return cudaErrorInvalidValue;

@@ -1,6 +1,7 @@
-"""Which tile of a block-scaled product comes when, on the CPU: csrc/block_order.h
-compiled by the host compiler, where an operation that leaves 32 bits ends the
-run, against the same order in Python's integers."""
+"""Which kernel, tile and piece of a block-scaled product comes when, on the CPU:
+csrc/block_order.h compiled by the host compiler, where an operation that leaves
+32 bits ends the run, against the same order in Python's integers; and that the
+GPU tests' sizes reach every variant."""
 import ctypes
 import random
 import subprocess
@@ -11,6 +12,8 @@ import torch
 from oracle import cbuild
 from routing_grouped_expert_router_gb300 import binding as mb
 from routing_grouped_expert_router_gb300 import build as mbuild
+from tests import test_gpu_block_fp8 as near
+from tests import test_gpu_block_fp8_edges as edges
 
 MOST_ROWS = 2 ** 31 - 512
 SOURCE = r"""
@@ -27,6 +30,15 @@ void tile_of(int raster_n, int group, int MT, int NT, int local, int* at) {
   at[1] = t.n;
 }
 int most_rows() { return moe::kMostRows; }
+int few(int rows, int E, int K, int N, int alone) { return alone ? moe::few_rows_alone(rows, E, K, N) : moe::few_rows(rows, E, K, N); }
+int few_tile(int rows, int E) { return moe::few_tile_rows(rows, E); }
+void share(int tiles, int nkb, int grid, int me, int* o) {
+  const moe::Share s = moe::share_of(tiles, nkb, grid, me);
+  const int all[6] = {s.per, s.each, s.longer, s.t, s.kb, s.count};
+  for (int i = 0; i < 6; ++i) o[i] = all[i];
+}
+int owner(int tiles, int nkb, int grid, int step) { return moe::share_of(tiles, nkb, grid, 0).owner(step); }
+int first_of(int tiles, int nkb, int grid, int c) { return moe::share_of(tiles, nkb, grid, 0).lo(c); }
 }
 """
 
@@ -127,3 +139,84 @@ def test_sides_whose_blocks_leave_31_bits_are_refused():
         assert L.moe_layer_bwd_fp8_block(ctypes.byref(d), *[at] * 16, 1 << 60, None) == uns
         assert mb.moe_workspace_bytes(d, mb.OP_LAYER_FWD_FP8_BLOCK) == mb.moe_workspace_bytes(d, mb.OP_LAYER_BWD_FP8_BLOCK) == 0
     assert mb.moe_workspace_bytes(mb.dims(1, 2 ** 20, 2 ** 20, 2, 1), mb.OP_LAYER_FWD_FP8_BLOCK) > 0
+
+
+# ---------------------------------------------------------------- few rows
+SMS = 152
+
+
+def _cut(order, tiles, nkb, grid):
+    """Every block's steps as (tile, first step, steps, slot) and what they are: "whole", "even", or "parts" of tiles."""
+    out, shares, slots = (ctypes.c_int * 6)(), [], False
+    for me in range(grid):
+        order.share(tiles, nkb, grid, me, out)
+        per, each, longer, t, kb, left = out
+        mine = []
+        while left > 0:
+            n, slot = min(nkb - kb, left), None
+            if n < nkb:  # as the kernel finds the pieces of a shared tile, and its own slot
+                if per:
+                    first, last, first_slot = t * per, t * per + per - 1, 0
+                else:
+                    first, last = (order.owner(tiles, nkb, grid, s) for s in (t * nkb, t * nkb + nkb - 1))
+                    first_slot = 0 if order.first_of(tiles, nkb, grid, first) == t * nkb else 1
+                assert first <= me <= last and last - first < 160
+                slot = (first, last, first_slot if me == first else 0)
+                slots = slots or slot[2] == 1
+            mine.append((t, kb, n, slot))
+            left, kb = left - n, kb + n
+            if kb == nkb:
+                t, kb = t + 1, 0
+        shares.append(mine)
+    return shares, ("even" if out[0] > 1 else "whole") if out[0] else ("parts" if slots else "edges")
+
+
+def _check_cut(order, tiles, nkb, grid):
+    shares, kind = _cut(order, tiles, nkb, grid)
+    done = sorted((t, kb, n) for mine in shares for t, kb, n, _ in mine)
+    want = [0] * tiles
+    for t, kb, n in done:  # each tile's steps once, in order
+        assert kb == want[t]
+        want[t] += n
+    assert all(w == nkb for w in want)
+    joins = {}
+    for me, mine in enumerate(shares):
+        at = [s[2] for *_, s in mine if s]
+        assert len(at) == len(set(at)) <= 2  # no slot holds two tiles' sums
+        for t, _, _, s in mine:
+            if s:
+                joins.setdefault(t, []).append((me, s))
+    for t, who in joins.items():  # each piece of a shared tile agrees on which blocks they are
+        first, last = who[0][1][:2]
+        assert [me for me, _ in who] == list(range(first, last + 1)) and all(s[:2] == (first, last) for _, s in who)
+    assert len({who[0][1][0] for who in joins.values()}) == len(joins)  # a counter to a tile
+    return kind
+
+
+def test_steps_of_few_rows_are_cut_once(order):
+    rng = random.Random(3)
+    kinds = {_check_cut(order, rng.choice([1, 2, 11, 56, 88, 112, 151, 152, 153, 384, rng.randint(1, 700)]),
+                        rng.choice([1, 2, 3, 4, 7, 8, 9, 16, 32, rng.randint(1, 200)]), rng.choice([1, 2, 148, 152, 160])) for _ in range(400)}
+    assert kinds >= {"whole", "even", "parts"}
+    assert _check_cut(order, 0, 16, 152) in ("edges", "whole")
+
+
+def test_the_gpu_tests_reach_every_variant(order):
+    """By the rules as they stand: the pair kernel, and the one for few rows with each tile and each cut."""
+    def variant(counts, K, N, alone, cols):
+        R, E = sum(counts), len(counts)
+        if not order.few(R, E, K, N, alone):
+            return "pair"
+        nt = order.few_tile(R, E)
+        tiles = -(-N // cols) * sum(-(-c // nt) for c in counts)
+        return nt, _check_cut(order, tiles, -(-K // 128), SMS)
+
+    products = {variant(c, K, N, 1, 256) for c, K, N in near.SHAPES + edges.FEW}
+    assert products >= {"pair", (16, "whole"), (16, "even"), (16, "parts"), (32, "even"), (32, "parts")}
+    assert {n for n, _ in products - {"pair"}} == {16, 32}
+    first = {variant(c, h, f, 0, 128) for c, h, f in near.FFN + edges.FEW_FFN}
+    assert first >= {"pair", (16, "whole"), (16, "even"), (16, "parts"), (32, "whole"), (32, "parts")}
+    second = {variant(c, f, h, 0, 256) for c, h, f in near.FFN + edges.FEW_FFN}
+    assert second >= {"pair", (16, "whole"), (16, "even"), (16, "parts"), (32, "even"), (32, "parts")}
+    # one group whose rows fill more than one tile of 32
+    assert any(max(c) > 32 and order.few(sum(c), len(c), K, N, 1) for c, K, N in edges.FEW)

@@ -138,3 +138,84 @@ def test_an_error_of_one_call_is_not_the_next_ones(lib, call):  # noqa: F811
         torch.cuda.synchronize()
     finally:
         cu.cuStreamDestroy_v2(stream)
+
+
+@pytest.mark.parametrize("R", [1, 20, 300])
+def test_calls_behind_copies_and_other_streams_in_a_graph(lib, R):  # noqa: F811
+    """Kernels that may begin early, behind a copy, behind a fill and behind two streams that join."""
+    h, f = 512, 384
+    w = _ffn_weights(1, h, f, 81)
+    codes = [t for q, s, _ in w for t in (q, s)]
+    xs = [_normal((R, h), 82 + i) for i in range(4)]
+    x, x2, y, C = (torch.empty_like(xs[0]), torch.empty_like(xs[0]), torch.empty_like(xs[0]), torch.empty((R, f), dtype=BF, device="cuda"))
+    aq, sa = torch.empty((R, h), dtype=torch.uint8, device="cuda"), torch.empty((h // 128, R), dtype=F32, device="cuda")
+    src = torch.empty_like(x)
+    fd, gd = mb.ffn_dims(R, h, f), mb.gemm_dims(R, h, f)
+    wss = [_ws(mb.moe_ffn_workspace_bytes(fd, 0)), _ws(mb.moe_gemm_workspace_bytes(gd))]
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        x.copy_(src)
+        mb.moe_gated_ffn_fwd(fd, x, None, *codes, None, None, None, y, wss[0])
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            x2.copy_(src)
+            mb.moe_quantize_rows_fp8_block(x2, R, h, None, 1, R, aq, sa)
+        C.zero_()
+        here.wait_stream(side)
+        mb.moe_gemm_fp8_block(gd, aq, sa, codes[0], codes[1], None, C, wss[1])
+        x.zero_()
+
+    want = []
+    for t in xs:
+        src.copy_(t)
+        torch.cuda.synchronize()
+        step()
+        torch.cuda.synchronize()
+        want.append((y.clone(), C.clone()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(5):
+        for t, (a, b) in zip(xs, want):
+            src.copy_(t)
+            graph.replay()
+            assert torch.equal(y, a) and torch.equal(C, b)
+
+
+# ---------------------------------------------------------------- few rows: every cut, every tile
+FEW = [([3] * 64, 2048, 1408), ([1] * 8, 4096, 2816), ([9, 0, 1, 16, 0, 2] * 8, 1104, 1552),   # pieces that hold parts of two tiles
+       ([32], 4096, 16512), ([17], 4096, 16512), ([40, 3, 0, 5], 2048, 8320), ([12] * 8, 4096, 2816)]   # the tile of 32 rows
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("counts,K,N", FEW)
+def test_product_of_few_rows(lib, counts, K, N, trans, f32):  # noqa: F811
+    C, ref, bound = _product(counts, K, N, trans, f32, seed=len(counts) + K + N)
+    assert ((C.double() - ref).abs() <= bound).all()
+
+
+FEW_FFN = [([3, 0, 2, 7, 0, 1, 4, 3] * 8, 2048, 1408), ([1] * 8, 4096, 1408), ([9, 0, 30, 2, 0, 2] * 4, 1088, 2112), ([14] * 8, 2816, 4096)]
+
+
+@pytest.mark.parametrize("counts,h,f", FEW_FFN)
+def test_feed_forward_of_few_rows_cut_inside_tiles(lib, counts, h, f):  # noqa: F811
+    E, R = len(counts), sum(counts)
+    w, x, o = _ffn_weights(E, h, f, 91), _normal((R, h), 92), _offsets(counts)
+    codes = [t for q, s, _ in w for t in (q, s)]
+    fd = mb.ffn_dims(R, h, f, E)
+    ws = _ws(mb.moe_ffn_workspace_bytes(fd, 0))
+    A, B, H = (torch.empty(R, f, dtype=BF, device="cuda") for _ in range(3))
+    y = torch.empty_like(x)
+    first = None
+    for _ in range(20):
+        for t in (A, B, H, y):
+            t.fill_(3)
+        mb.moe_gated_ffn_fwd(fd, x, o, *codes, A, B, H, y, ws)
+        got = [t.clone() for t in (A, B, H, y)]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    _check_fwd(x, A, B, H, y, w, counts)
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK and not ws[:256].any()
