@@ -15,7 +15,7 @@ namespace moe {
 
 // Rows of `in` (row idx[p] / div, or p) -> codes [rows, n] and block scales
 // [ceil(n/128), rows], for p < rows (and, where given, p < the largest of
-// ends[0 .. n_ends-1]: the groups' offsets, or their last alone where they are known
+// ends[0 .. n_ends-1], at most 65: the groups' offsets, or their last alone where they are known
 // to be in order).  With copy, the bf16 source rows are also written to copy [rows, n].
 // n a multiple of 16.
 cudaError_t launch_quant_rows_block(const uint16_t* in, const int32_t* idx, int div,

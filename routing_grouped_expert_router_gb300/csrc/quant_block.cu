@@ -58,8 +58,10 @@ __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
   if (ends) {
     // the furthest end, as group_tables clamps the groups: offsets out of order leave no row
     // that a product takes without codes
-    int top = 0;
-    for (int i = lane; i < n_ends; i += 32) top = max(top, __ldg(ends + i));
+    int top = lane < n_ends ? __ldg(ends + lane) : 0;  // n_ends: at most 65
+    if (n_ends > 32 && lane + 32 < n_ends) top = max(top, __ldg(ends + lane + 32));
+    if (n_ends > 64) top = max(top, __ldg(ends + 64));
+    top = max(top, 0);
     last = min(static_cast<long long>(__reduce_max_sync(kFull, top)), rows);
   }
   const int first_quad = blockIdx.y * quads_each;

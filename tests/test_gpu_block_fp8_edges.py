@@ -54,6 +54,22 @@ def test_feed_forward_with_offsets_out_of_order(lib, R, cuts):  # noqa: F811
     assert (dx[n:] == 55).all()
 
 
+@pytest.mark.parametrize("at", [1, 31, 32, 33, 63, 64])
+def test_the_furthest_of_64_ends_in_any_place(lib, at):  # noqa: F811
+    """The group that ends there has all rows; every later offset is smaller."""
+    R, h, f, E = 70, 128, 192, 64
+    w, x = _ffn_weights(E, h, f, 46), _normal((R, h), 47)
+    codes = [t for q, s, _ in w for t in (q, s)]
+    o = torch.tensor([0] * at + [R] + [3] * (E - at), dtype=torch.int32, device="cuda")
+    counts = [0] * (at - 1) + [R] + [0] * (E - at)
+    A, B, H = (torch.full((R, f), 55.0, dtype=BF, device="cuda") for _ in range(3))
+    y, fd = torch.full_like(x, 55.0), mb.ffn_dims(R, h, f, E)
+    ws = _ws(mb.moe_ffn_workspace_bytes(fd, 0))
+    mb.moe_gated_ffn_fwd(fd, x, o, *codes, A, B, H, y, ws)
+    assert mb.moe_read_device_status(ws) == (mb.MOE_OK if at == 64 else mb.MOE_ERR_DEVICE_INDEX)
+    _check_fwd(x, A, B, H, y, w, counts)
+
+
 # ---------------------------------------------------------------- after a wait that ran out
 @pytest.mark.parametrize("counts,K,N", [([3], 4096, 512), ([2, 0, 5], 4096, 1408), ([70], 4096, 512)])
 def test_a_status_of_a_timeout_read_leaves_the_workspace_as_new(lib, counts, K, N):  # noqa: F811
