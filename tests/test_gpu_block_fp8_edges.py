@@ -3,6 +3,7 @@ it meet: offsets out of order, launches that fail, waits that ran out, streams
 and graphs, and each way in which few rows are cut into pieces.  References and
 tolerances are those of test_gpu_block_fp8.py."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -200,6 +201,57 @@ def test_calls_behind_copies_and_other_streams_in_a_graph(lib, R):  # noqa: F811
             assert torch.equal(y, a) and torch.equal(C, b)
 
 
+def test_host_threads_with_a_stream_each(lib):  # noqa: F811
+    """Four threads at once, each with its stream, workspace and sizes: the same bits as alone."""
+    E, h, f = 4, 512, 384
+    w = _ffn_weights(E, h, f, 84)
+    codes = [t for q, s, _ in w for t in (q, s)]
+    jobs = []
+    for i, R in enumerate((3, 30, 200, 600)):
+        fd, gd, o = mb.ffn_dims(R, h, f, E), mb.gemm_dims(R, h, f, E), _offsets([R - 2, 0, 2, 0])
+        x, dy = _normal((R, h), 85 + i), _normal((R, h), 185 + i)
+        outs = [torch.empty(shape, dtype=BF, device="cuda") for shape in [(R, f)] * 4 + [(R, h)] * 2]
+        outs += [torch.empty(q.shape, dtype=F32, device="cuda") for q, _, _ in w]
+        q, s = torch.empty((R, h), dtype=torch.uint8, device="cuda"), torch.empty((h // 128, R), dtype=F32, device="cuda")
+        wss = [_ws(mb.moe_ffn_workspace_bytes(fd, 0)), _ws(mb.moe_ffn_workspace_bytes(fd, 1)), _ws(mb.moe_gemm_workspace_bytes(gd))]
+        jobs.append((R, fd, gd, o, x, dy, outs, q, s, wss, torch.cuda.Stream()))
+
+    def step(R, fd, gd, o, x, dy, outs, q, s, wss, stream):
+        A, B, H, C, y, dx = outs[:6]
+        mb.moe_quantize_rows_fp8_block(x, R, h, None, 1, R, q, s, stream=stream)
+        mb.moe_gemm_fp8_block(gd, q, s, codes[0], codes[1], o, C, wss[2], stream=stream)
+        mb.moe_gated_ffn_fwd(fd, x, o, *codes, A, B, H, y, wss[0], stream=stream)
+        mb.moe_gated_ffn_bwd(fd, x, dy, o, *codes, A, B, H, dx, *outs[6:], wss[1], stream=stream)
+
+    want = []
+    for j in jobs:
+        step(*j)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in j[6]])
+        for t in j[6]:
+            t.fill_(3)
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(j):
+        try:
+            for _ in range(30):
+                step(*j)
+        except Exception as e:  # reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for j, first in zip(jobs, want):
+        assert all(torch.equal(a, b) for a, b in zip(first, j[6]))
+        assert all(mb.moe_read_device_status(ws) == mb.MOE_OK for ws in j[9])
+
+
 # ---------------------------------------------------------------- few rows: every cut, every tile
 FEW = [([3] * 64, 2048, 1408), ([1] * 8, 4096, 2816), ([9, 0, 1, 16, 0, 2] * 8, 1104, 1552),   # pieces that hold parts of two tiles
        ([32], 4096, 16512), ([17], 4096, 16512), ([40, 3, 0, 5], 2048, 8320), ([12] * 8, 4096, 2816)]   # the tile of 32 rows
@@ -235,3 +287,51 @@ def test_feed_forward_of_few_rows_cut_inside_tiles(lib, counts, h, f):  # noqa: 
         assert all(torch.equal(a, b) for a, b in zip(first, got))
     _check_fwd(x, A, B, H, y, w, counts)
     assert mb.moe_read_device_status(ws) == mb.MOE_OK and not ws[:256].any()
+
+
+# ---------------------------------------------------------------- the gate at its ends
+@pytest.mark.parametrize("R", [1, 16, 30, 300])
+def test_gate_values_from_one_end_to_the_other(lib, R):  # noqa: F811
+    """A from -1e37 to 1e37.  Past A = -87.3 the sigmoid's quotient is 0: silu is off by less than 88.8 * 2^-126 there.  In the
+    backward a value of dA or dB that rounds to the other side is off by one bf16 step, 2^-7 of it at most."""
+    h, f = 64, 320
+    gate = torch.empty(f, device="cuda")  # the values of a block of 128 columns are codes under one scale
+    gate[:128] = torch.linspace(-300, -1, 128)
+    gate[128:256] = torch.logspace(32, 37, 128) * torch.tensor([1.0, -1.0]).repeat(64)
+    gate[256:] = torch.logspace(-6, -1, 64) * torch.tensor([1.0, -1.0]).repeat(32)
+    W1 = torch.zeros((1, h, f), dtype=BF, device="cuda")
+    W1[0, 0] = gate.to(BF)
+    q1, s1, v1 = br.code_weights(W1)
+    q3, s3, v3 = br.weights(1, h, f, seed=95)
+    q2, s2, v2 = br.weights(1, f, h, seed=96)
+    codes = (q1, s1, q3, s3, q2, s2)
+    x = _normal((R, h), 97, 2.0 ** -10)
+    x[:, 0] = 1 + torch.arange(R, device="cuda") % 128 * 2.0 ** -7
+    fd = mb.ffn_dims(R, h, f)
+    ws = _ws(max(mb.moe_ffn_workspace_bytes(fd, b) for b in (0, 1)))
+    A, B, H = (torch.empty((R, f), dtype=BF, device="cuda") for _ in range(3))
+    y = torch.empty_like(x)
+    mb.moe_gated_ffn_fwd(fd, x, None, *codes, A, B, H, y, ws)
+    v = br.coded_rows(x.double())
+    a, b = v @ v1[0], v @ v3[0]
+    ea, eb = (11 * 2.0 ** -23 * (v.abs() @ w[0].abs()) for w in (v1, v3))
+    hh = br.silu(a) * b
+    off = 1.1 * (b.abs() + eb) * ea + br.silu(a).abs() * eb + (16 + a.abs().clamp(max=200)) * 2.0 ** -23 * hh.abs() + 88.8 * 2.0 ** -126 * (b.abs() + eb)
+    assert torch.isfinite(H).all() and torch.isfinite(y).all()
+    assert ((H.double() - hh).abs() <= off + 2.0 ** -8 * (hh.abs() + off) + 2.0 ** -134).all()
+    assert (H[a < -1000] == 0).all()
+    # the backward, from A at once
+    A[:] = torch.cat([-torch.logspace(36, -3, f // 2, device="cuda"), torch.logspace(-3, 36, f // 2, device="cuda")]).to(BF)
+    A[:, :40] = torch.linspace(-120, -60, 40, device="cuda").to(BF)
+    B, dy = _normal((R, f), 98), _normal((R, h), 99)
+    H = torch.zeros_like(A)
+    dx, dW = torch.empty_like(x), [torch.empty(t.shape, dtype=F32, device="cuda") for t in (q1, q3, q2)]
+    mb.moe_gated_ffn_bwd(fd, x, dy, None, *codes, A, B, H, dx, *dW, ws)
+    assert mb.moe_read_device_status(ws) == mb.MOE_OK
+    dh, aa = br.coded_rows(dy.double()) @ v2[0].t(), A.double()
+    sg = torch.sigmoid(aa)
+    da, db = br.kept(dh * B.double() * sg * (1 + aa * (1 - sg))), br.kept(dh * aa * sg)
+    assert all(torch.isfinite(t).all() for t in (dx, *dW))
+    for got, ref in ((dW[0][0], x.double().t() @ da), (dW[1][0], x.double().t() @ db)):
+        n = ref.norm(dim=0)  # each column by itself: its A sets its size
+        assert ((got.double() - ref).norm(dim=0) <= (2.0 ** -7 + 1e-4) * n + 1e-30).all()
