@@ -58,10 +58,11 @@
  *     skipped (an assignment not placed, a zero row, a slot that adds
  *     nothing), so nothing is read or written out of bounds.  The calls that
  *     take no workspace (moe_combine, moe_unpermute, moe_quantize_rows_fp8,
- *     moe_quantize_rows_fp8_block, moe_permute_noalloc, moe_block_norm_fwd) record into one status word per device that the
- *     library keeps (its address is looked up on the first such call on a
- *     device and kept until the process exits); moe_read_device_status(NULL,
- *     stream) reports that one.
+ *     moe_quantize_rows_fp8_block, moe_permute_noalloc, moe_block_norm_fwd)
+ *     record into one status word per device that the library keeps (its
+ *     address is looked up on the first such call on a device and kept until
+ *     the process exits); moe_read_device_status(NULL, stream) reports that
+ *     one.
  *   - Supported shapes: 1 <= k <= 8, E <= 64, T*k < 2^31, h and f multiples
  *     of 64 (the GEMMs' K blocks are 64 wide).  Calls that choose experts
  *     (moe_route, moe_layer_fwd/bwd, moe_saved_bytes) also need k <= E; the
@@ -388,7 +389,9 @@ moe_status moe_layer_bwd_fp8(const moe_dims* dims, const moe_bf16* x,
  *   weights [E, K, N]:  codes uint8 [E, K, N], scales
  *                       float [E, ceil(K/128), ceil(N/128)]
  * Products are summed block by block: the 128 products of a block in fp32 in
- * tensor memory, then times both scales and added in fp32 registers. */
+ * tensor memory, then times the product of both scales and added in fp32
+ * registers.  Where the product of the scales leaves float32's normal range,
+ * 2^-126 to 2^128, the block's sum loses digits or is not finite. */
 
 /* Rows: as moe_quantize_rows_fp8 (source row idx[p] / div, or p when idx is
  * NULL), with one scale for each block: scale[b * rows + p] is that of

@@ -27,10 +27,12 @@
 // each pair takes a piece of a tile's contraction; the last to arrive adds the pieces' sums in
 // their order (20 to 128 rows by 14336 x 4096: 23 to 29 us, 50 in one piece; see pieces_of).
 //
-// Measured: 16384 x 4096 x 14336 in eight groups, bf16 out, 716 us, 2.69 PFLOP/s, 0.67 of
-// twice the measured bf16 rate.  No one part bounds it: 666 us without the multiply-adds, 603
-// without the loads from tensor memory too, 516 without operand loads as well; a block takes
-// some 900 cycles, 512 of them the tensor cores'.  One CTA instead of a pair, four accumulators
+// Measured: 16384 x 4096 x 14336 in eight groups, bf16 out, 716 us after a pause (2.69 PFLOP/s,
+// 0.67 of twice the measured bf16 rate); in a row of calls, under the power cap, 786 to 826 us
+// (2.3 to 2.4).  After a pause: 666 us without the multiply-adds, 603 without the loads from
+// tensor memory too, 516 without operand loads as well.  A block takes some 900 cycles, 512 of
+// them the tensor cores'; no unit is busy for more than 62% of them (the tensor pipe), and what
+// holds up the others is not known.  One CTA instead of a pair, four accumulators
 // of 128 columns (818 us), sixteen sum warps of half the columns (799), a block's first columns
 // asked for during the block before (740) and two issuing warps were all slower; packed
 // multiply-adds made no difference.
@@ -203,7 +205,8 @@ __device__ __forceinline__ void add_32(const float (&v)[32], float scale, float*
   for (int i = 0; i < 32; ++i) sums[i] = fmaf(v[i], scale, sums[i]);
 }
 // sigmoid and silu with the fast exponential and quotient: their few ulps are far below the
-// bf16 rounding of all that is stored.  (Two sigmoids with one reciprocal were slower.)
+// bf16 rounding of all that is stored.  Past a = -87.3 the quotient is 0, which loses 88.8 *
+// 2^-126 of silu at most.  (Two sigmoids with one reciprocal were slower.)
 __device__ __forceinline__ float sigmoid_f(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
 __device__ __forceinline__ float silu_f(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 

@@ -39,8 +39,8 @@ __device__ __forceinline__ uint32_t top8(const uint4& w) {
 // A warp takes a row's blocks four at a time, eight lanes of two 16-byte pieces to a
 // block, with kRowAhead such quads under way: sixteen values share the arithmetic of a
 // block's scale, which with eight took as many instructions as all else (16384 x 4096
-// rows gathered twice: 90 us); with quotients and maxima of one value at a time it was 70.  blockIdx.y splits a row's quads where there are too few
-// rows to fill the GPU.
+// rows gathered twice: 90 us); with quotients and maxima of one value at a time it was 70.
+// blockIdx.y splits a row's quads where there are too few rows to fill the GPU.
 __global__ void __launch_bounds__(kRowThreads) quant_rows_block_kernel(
     const uint4* __restrict__ in, const int32_t* __restrict__ idx, int div, long long rows,
     long long src_rows, const int32_t* __restrict__ ends, int n_ends, int n8, int quads,
