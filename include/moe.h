@@ -391,7 +391,8 @@ moe_status moe_layer_bwd_fp8(const moe_dims* dims, const moe_bf16* x,
  * Products are summed block by block: the 128 products of a block in fp32 in
  * tensor memory, then times the product of both scales and added in fp32
  * registers.  Where the product of the scales leaves float32's normal range,
- * 2^-126 to 2^128, the block's sum loses digits or is not finite. */
+ * 2^-126 to 2^128, the block's sum loses digits or is not finite.
+ * No output of these calls may overlap an input, another output or ws. */
 
 /* Rows: as moe_quantize_rows_fp8 (source row idx[p] / div, or p when idx is
  * NULL), with one scale for each block: scale[b * rows + p] is that of
